@@ -65,6 +65,9 @@ enum {
 };
 
 enum { MOE_RENORM = 1u };                       /* moe_route flag */
+enum { MOE_GROUP_TOP2 = 2u };                   /* moe_route_select flag */
+enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
+enum { MOE_SCALE_POW2 = 1u };                   /* moe_quantize_fp8 flag */
 enum { MOE_REGIME_AUTO = 0, MOE_REGIME_DECODE = 1, MOE_REGIME_BATCHED = 2, MOE_REGIME_SMALL = 3 };
 /* OR'd into the regime of moe_expert_ffn_plan / moe_expert_ffn_w4a16: y rows
  * in token order (row t*k + j) instead of sorted order; see below. */
@@ -76,8 +79,9 @@ enum { MOE_Y_TOKEN_ORDER = 0x100 };
  * of the router's pinned logit sum lie side by side, so a reader that owns
  * partial j reads whole lines.  Needs C <= 64 or C a multiple of 64. */
 enum { MOE_Y_PARTIAL_ORDER = 0x400 };
-/* y dtypes: fp16, fp32 (decode slices), fp32 in partial-major column order. */
-enum { MOE_DTYPE_F16 = 0, MOE_DTYPE_F32 = 1, MOE_DTYPE_F32_PM = 2 };
+/* y dtypes: fp16, fp32 (decode slices), fp32 in partial-major column order;
+ * bf16 where a call names it (moe_route_select, moe_quantize_fp8, moe_gemm_fp8). */
+enum { MOE_DTYPE_F16 = 0, MOE_DTYPE_F32 = 1, MOE_DTYPE_F32_PM = 2, MOE_DTYPE_BF16 = 3 };
 /* Expert blob formats: symmetric codes, or codes with a zero point per group
  * (lucashiago.com.br explainer, step 1: each block carries a scale and a zero
  * point).  MOE_W4_ZERO_POINT is OR'd into the regime of moe_expert_ffn_plan /
@@ -481,6 +485,130 @@ int moe_expert_ffn_w4a16_routed(const void *x_f16, const float *logit_partials,
                                 const void *const *d_expert_blobs, int T, int H, int I,
                                 int group, int regime, void *y, int y_dtype, int y_slices,
                                 hipStream_t stream);
+
+/* ------------------------------------------- routing by scores and groups */
+/*
+ * Router logits alone: the logits that moe_route selects from (same summation
+ * order, same bits), for a selection the caller runs itself or with
+ * moe_route_select.
+ *   x_f16 device fp16 [T][H], w_router_f16 device fp16 [E][H] (16-byte
+ *   aligned), logit_bias device fp32 [E] or NULL; logits device fp32 [T][E].
+ * H in {256, 512, 1024, 2048}, E <= 1024 (MOE_EUNSUPPORTED).  T = 0: no-op.
+ */
+int moe_router_logits(const void *x_f16, const void *w_router_f16, const float *logit_bias, int T,
+                      int H, int E, float *logits, hipStream_t stream);
+
+/*
+ * Expert selection from logits in hand, in the forms of current sparse
+ * models.  With l the logits of a token:
+ *   s_e = softmax(l)_e (MOE_SCORE_SOFTMAX) or 1 / (1 + exp(-l_e))
+ *         (MOE_SCORE_SIGMOID);
+ *   c_e = s_e + select_bias[e]  -- a balancing bias decides, it does not weigh;
+ *   the experts are n_group equal runs of E / n_group; a group counts by its
+ *   largest c, or with MOE_GROUP_TOP2 by the sum of its two largest; only the
+ *   topk_group groups that count most (ties: lower group) can be chosen from;
+ *   topk_idx: the k largest c in descending order (ties: lower expert);
+ *   topk_w:   scale * s at those experts, with MOE_RENORM divided by the sum
+ *             of the k chosen s (all zero when that sum is zero).
+ * A logit of -inf or NaN masks its expert: s = 0, and it ranks behind every
+ * other expert of the kept groups (by index) and does not count for its
+ * group; a row that is masked throughout gives the lowest experts of the
+ * lowest groups with weight 0.  A logit of +inf counts as the largest finite
+ * value, a choice that is NaN ranks as masked.  Scores and choices are formed
+ * in fp64; topk_w is rounded once.
+ *   logits      device [T] rows of E values of logits_dtype (MOE_DTYPE_F32,
+ *               F16 or BF16), ld elements apart (ld >= E), element-aligned
+ *   select_bias device fp32 [E] or NULL
+ *   topk_idx    device int32 [T][k];  topk_w device fp32 [T][k]
+ * Errors: MOE_EINVAL for bad sizes (n_group must divide E; the kept groups
+ * must hold k experts; ld < E), an unknown dtype, score or flag, a scale that
+ * is not finite, null or misaligned pointers; MOE_EUNSUPPORTED for E > 1024,
+ * k > 16 or more than 64 groups.  T = 0: no-op.
+ * The permute form also writes moe_permute's outputs of topk_idx: in the same
+ * launch for at most 16 tokens (with T * E <= 8192), else on ws, a device
+ * scratch of moe_route_select_workspace_bytes(T, k, E) bytes (may be 0; no
+ * initialisation needed); MOE_ENOMEM if too small.
+ */
+int moe_route_select(const void *logits, int logits_dtype, int64_t ld, const float *select_bias,
+                     int T, int E, int k, int score, int n_group, int topk_group, unsigned flags,
+                     float scale, int32_t *topk_idx, float *topk_w, hipStream_t stream);
+size_t moe_route_select_workspace_bytes(int T, int k, int E);
+int moe_route_select_permute(const void *logits, int logits_dtype, int64_t ld,
+                             const float *select_bias, int T, int E, int k, int score, int n_group,
+                             int topk_group, unsigned flags, float scale, int32_t *topk_idx,
+                             float *topk_w, int32_t *counts, int32_t *offsets, int32_t *perm,
+                             int32_t *inv_perm, void *ws, size_t ws_bytes, hipStream_t stream);
+
+/* --------------------------------------------- FP8 with block scales (W8A8) */
+/*
+ * e4m3 (OCP: 1 sign, 4 exponent, 3 mantissa bits, largest value 448) with one
+ * fp32 scale per block: x is about q * s.
+ * moe_quantize_fp8: blocks of block_rows x 128 (block_rows 1: activations,
+ * one scale per row and 128 columns; 128: weights), the last ones partial.
+ *   a = max |x| of the block; s = a / 448 in fp32, at least 2^-126 (0 when
+ *   a = 0); with MOE_SCALE_POW2 the smallest power of two not below that (then
+ *   x / s is exact); q = e4m3(x / s), nearest even (0 when s = 0).
+ *   x       device [rows] of cols values of dtype (F16, BF16, F32), ldx
+ *           elements apart, element-aligned (fastest 16-byte aligned)
+ *   q       device e4m3 [rows], ldq bytes apart (fastest 8-byte aligned)
+ *   scales  device fp32 [ceil(rows / block_rows)][ceil(cols / 128)]
+ * A block that holds a NaN or an infinity gives codes or a scale that make
+ * every product with it NaN or infinite.  Errors: MOE_EINVAL for bad sizes,
+ * dtype, block_rows or flags, null or misaligned pointers; rows = 0: no-op.
+ */
+int moe_quantize_fp8(const void *x, int dtype, int64_t ldx, int64_t rows, int cols, int block_rows,
+                     unsigned flags, void *q, int64_t ldq, float *scales, hipStream_t stream);
+
+/*
+ * Dense product of two such matrices, y = x w^T:
+ *   y[m][n] = sum_b xs[m][b] * ws[n/128][b] * sum_{j in block b} xq[m][j] wq[n][j]
+ * products and sums of a block in fp32 on the matrix cores, scaled once per
+ * block, accumulated in fp32 in a fixed order, rounded once to out_dtype.
+ *   xq  device e4m3 [M], ldx bytes apart;  x_scales device fp32 [M][ceil(K/128)]
+ *   wq  device e4m3 [N], ldw bytes apart;  w_scales [ceil(N/128)][ceil(K/128)]
+ *   out device [M] rows of N values (F16, BF16 or F32), ldo elements apart
+ * Any M and N.  K, ldx and ldw multiples of 16, K <= 16384 (MOE_EUNSUPPORTED);
+ * xq and wq 16-byte aligned (MOE_EINVAL).  out must not overlap the inputs.
+ * M = 0: no-op.  No workspace.
+ */
+int moe_gemm_fp8(const void *xq, int64_t ldx, const float *x_scales, const void *wq, int64_t ldw,
+                 const float *w_scales, int M, int N, int K, void *out, int out_dtype, int64_t ldo,
+                 hipStream_t stream);
+
+/*
+ * FP8 expert blob: six sections, each 256-byte aligned: gate_q[I][H],
+ * up_q[I][H], down_q[H][I] (e4m3, row-major) then gate_s, up_s
+ * [ceil(I/128)][ceil(H/128)] and down_s[ceil(H/128)][ceil(I/128)] (fp32, one
+ * per 128 x 128 block) -- moe_quantize_fp8 with block_rows = 128 writes such
+ * sections.  The kernels read this layout as it is.  Host-only.
+ */
+int moe_fp8_blob_layout(int H, int I, int64_t offsets[6], int64_t *total_bytes);
+
+/*
+ * Routed SwiGLU experts from FP8 blobs.  For each sorted row p of expert e and
+ * token t = perm[p] / k:
+ *   (xq, xs) = quantised x_t,  g = Wg[e] x, u = Wu[e] x (products as above),
+ *   h = silu(g) * u in fp32,   (hq, hs) = quantised h,   y_p = Wd[e] h -> fp16
+ * the activations quantised per row and 128 columns with power-of-two scales
+ * (MOE_SCALE_POW2).
+ *   x_f16, perm, offsets, d_expert_blobs as moe_expert_ffn_w4a16 (a NULL entry
+ *   leaves that expert's rows of y unwritten); blobs in the layout above,
+ *   16-byte aligned
+ *   y_f16  device fp16 [T*k][H], row p holds sorted row p (moe_combine with
+ *          MOE_DTYPE_F16, one slice)
+ *   ws     device scratch of the plan's size, 16-byte aligned, no
+ *          initialisation; calls that share it must not overlap
+ * Rows behind offsets[E] are left as they were.  Regimes: DECODE (T <= 4: two
+ * launches over the weights' stream, activations quantised inside them) and
+ * BATCHED (any T); AUTO picks by T.  Both give the same sums up to the order
+ * of the blocks.  H and I multiples of 64, at most 8192; E <= 1024; k <= 16
+ * (MOE_EUNSUPPORTED).  x, y and ws 16-byte aligned (MOE_EINVAL).  T = 0: no-op.
+ */
+int moe_expert_ffn_w8a8_plan(int T, int H, int I, int E, int k, int regime, int *resolved_regime,
+                             size_t *ws_bytes);
+int moe_expert_ffn_w8a8(const void *x_f16, const int32_t *perm, const int32_t *offsets,
+                        const void *const *d_expert_blobs, int T, int H, int I, int E, int k,
+                        int regime, void *y_f16, void *ws, size_t ws_bytes, hipStream_t stream);
 
 /* ------------------------------------------------- expert slot pool */
 /*

@@ -10,7 +10,8 @@ __all__ = [
     "MoEError", "lib", "MOE_OK", "MOE_EINVAL", "MOE_EUNSUPPORTED", "MOE_ENOMEM", "MOE_EHIP",
     "MOE_ECAPACITY", "MOE_ESTATE", "MOE_RENORM", "MOE_REGIME_AUTO", "MOE_REGIME_DECODE",
     "MOE_REGIME_BATCHED", "MOE_REGIME_SMALL", "MOE_Y_TOKEN_ORDER", "MOE_Y_PARTIAL_ORDER",
-    "MOE_DTYPE_F16", "MOE_DTYPE_F32", "MOE_DTYPE_F32_PM", "MOE_FMT_SYM", "MOE_FMT_ZP", "MOE_W4_ZERO_POINT", "EXPORTS",
+    "MOE_DTYPE_F16", "MOE_DTYPE_F32", "MOE_DTYPE_F32_PM", "MOE_DTYPE_BF16",
+    "MOE_GROUP_TOP2", "MOE_SCORE_SOFTMAX", "MOE_SCORE_SIGMOID", "MOE_SCALE_POW2", "MOE_FMT_SYM", "MOE_FMT_ZP", "MOE_W4_ZERO_POINT", "EXPORTS",
     "moe_blob_layout_fmt", "moe_quantize_experts_fmt", "moe_prepack_experts_fmt",
     "moe_unpack_experts_fmt", "moe_prepack_expert_host", "moe_unpack_expert_host",
     "moe_last_error", "moe_workspace_clear", "moe_blob_layout", "moe_quantize_experts",
@@ -23,6 +24,9 @@ __all__ = [
     "moe_combine_route_permute_workspace_bytes", "moe_combine_route_permute",
     "moe_logit_partials_bytes", "moe_logit_partials", "moe_combine_route_partials",
     "moe_expert_ffn_w4a16_routed",
+    "moe_router_logits", "moe_route_select", "moe_route_select_workspace_bytes",
+    "moe_route_select_permute", "moe_quantize_fp8", "moe_gemm_fp8", "moe_fp8_blob_layout",
+    "moe_expert_ffn_w8a8_plan", "moe_expert_ffn_w8a8",
     "PoolConfig",
     "PoolStats", "PoolLayerArgs",
     "moe_pool_create", "moe_pool_prepare", "moe_pool_layer_forward", "moe_pool_pin",
@@ -36,7 +40,10 @@ MOE_RENORM = 1
 MOE_REGIME_AUTO, MOE_REGIME_DECODE, MOE_REGIME_BATCHED, MOE_REGIME_SMALL = 0, 1, 2, 3
 MOE_Y_TOKEN_ORDER = 0x100   # OR'd into a regime: decode y rows in token order
 MOE_Y_PARTIAL_ORDER = 0x400  # OR'd into a regime: decode y columns in partial-major order
-MOE_DTYPE_F16, MOE_DTYPE_F32, MOE_DTYPE_F32_PM = 0, 1, 2
+MOE_DTYPE_F16, MOE_DTYPE_F32, MOE_DTYPE_F32_PM, MOE_DTYPE_BF16 = 0, 1, 2, 3
+MOE_GROUP_TOP2 = 2          # moe_route_select flag: a group counts by its two best experts
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+MOE_SCALE_POW2 = 1          # moe_quantize_fp8 flag: power-of-two scales
 MOE_FMT_SYM, MOE_FMT_ZP = 0, 1   # expert blob formats (zero point per group)
 MOE_W4_ZERO_POINT = 0x200        # OR'd into a regime: the blobs are MOE_FMT_ZP
 
@@ -53,6 +60,9 @@ EXPORTS = [
     "moe_combine_route_permute_workspace_bytes", "moe_combine_route_permute",
     "moe_logit_partials_bytes", "moe_logit_partials", "moe_combine_route_partials",
     "moe_expert_ffn_w4a16_routed",
+    "moe_router_logits", "moe_route_select", "moe_route_select_workspace_bytes",
+    "moe_route_select_permute", "moe_quantize_fp8", "moe_gemm_fp8", "moe_fp8_blob_layout",
+    "moe_expert_ffn_w8a8_plan", "moe_expert_ffn_w8a8",
     "moe_pool_create",
     "moe_pool_prepare",
     "moe_pool_layer_forward", "moe_pool_pin",
@@ -141,6 +151,19 @@ def _declare(L):
         "moe_expert_ffn_w4a16_routed": (i32, [vp, vp, vp, i32, i32, C.c_uint, vp, vp, vp, vp,
                                               vp, vp, vp, i32, i32, i32, i32, i32, vp, i32, i32,
                                               vp]),
+        "moe_router_logits": (i32, [vp, vp, vp, i32, i32, i32, vp, vp]),
+        "moe_route_select": (i32, [vp, i32, i64, vp, i32, i32, i32, i32, i32, i32, C.c_uint,
+                                   C.c_float, vp, vp, vp]),
+        "moe_route_select_workspace_bytes": (sz, [i32, i32, i32]),
+        "moe_route_select_permute": (i32, [vp, i32, i64, vp, i32, i32, i32, i32, i32, i32,
+                                           C.c_uint, C.c_float, vp, vp, vp, vp, vp, vp, vp, sz,
+                                           vp]),
+        "moe_quantize_fp8": (i32, [vp, i32, i64, i64, i32, i32, C.c_uint, vp, i64, vp, vp]),
+        "moe_gemm_fp8": (i32, [vp, i64, vp, vp, i64, vp, i32, i32, i32, vp, i32, i64, vp]),
+        "moe_fp8_blob_layout": (i32, [i32, i32, vp, vp]),
+        "moe_expert_ffn_w8a8_plan": (i32, [i32, i32, i32, i32, i32, i32, vp, vp]),
+        "moe_expert_ffn_w8a8": (i32, [vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, vp, vp, sz,
+                                      vp]),
         "moe_pool_create": (i32, [C.POINTER(PoolConfig), vp, C.POINTER(vp)]),
         "moe_pool_prepare": (i32, [vp, i32, vp, i32, vp, C.POINTER(vp), C.POINTER(PoolStats)]),
         "moe_pool_layer_forward": (i32, [vp, i32, C.POINTER(PoolLayerArgs), vp,
@@ -390,6 +413,62 @@ def moe_expert_ffn_w4a16_routed(x, logit_partials, logit_bias, E, k, flags, topk
         _p(x), _p(logit_partials), _p(logit_bias), E, k, flags, _p(topk_idx), _p(topk_w),
         _p(counts), _p(offsets), _p(perm), _p(inv_perm), _p(d_expert_blobs), T, H, I, group,
         regime, _p(y), y_dtype, y_slices, _s(stream)))
+
+
+def moe_router_logits(x_f16, w_router, logit_bias, T, H, E, logits, stream=None):
+    return _check(lib().moe_router_logits(_p(x_f16), _p(w_router), _p(logit_bias), T, H, E,
+                                          _p(logits), _s(stream)))
+
+
+def moe_route_select(logits, logits_dtype, ld, select_bias, T, E, k, score, n_group, topk_group,
+                     flags, scale, topk_idx, topk_w, stream=None):
+    return _check(lib().moe_route_select(_p(logits), logits_dtype, ld, _p(select_bias), T, E, k,
+                                         score, n_group, topk_group, flags, scale, _p(topk_idx),
+                                         _p(topk_w), _s(stream)))
+
+
+def moe_route_select_workspace_bytes(T, k, E):
+    return lib().moe_route_select_workspace_bytes(T, k, E)
+
+
+def moe_route_select_permute(logits, logits_dtype, ld, select_bias, T, E, k, score, n_group,
+                             topk_group, flags, scale, topk_idx, topk_w, counts, offsets, perm,
+                             inv_perm, ws=None, ws_bytes=0, stream=None):
+    return _check(lib().moe_route_select_permute(
+        _p(logits), logits_dtype, ld, _p(select_bias), T, E, k, score, n_group, topk_group, flags,
+        scale, _p(topk_idx), _p(topk_w), _p(counts), _p(offsets), _p(perm), _p(inv_perm), _p(ws),
+        ws_bytes, _s(stream)))
+
+
+def moe_quantize_fp8(x, dtype, ldx, rows, cols, block_rows, flags, q, ldq, scales, stream=None):
+    return _check(lib().moe_quantize_fp8(_p(x), dtype, ldx, rows, cols, block_rows, flags, _p(q),
+                                         ldq, _p(scales), _s(stream)))
+
+
+def moe_gemm_fp8(xq, ldx, x_scales, wq, ldw, w_scales, M, N, K, out, out_dtype, ldo, stream=None):
+    return _check(lib().moe_gemm_fp8(_p(xq), ldx, _p(x_scales), _p(wq), ldw, _p(w_scales), M, N, K,
+                                     _p(out), out_dtype, ldo, _s(stream)))
+
+
+def moe_fp8_blob_layout(H, I):
+    """Returns (offsets[6], total_bytes) of an FP8 expert blob."""
+    off = (C.c_int64 * 6)()
+    tot = C.c_int64()
+    _check(lib().moe_fp8_blob_layout(H, I, off, C.byref(tot)))
+    return list(off), tot.value
+
+
+def moe_expert_ffn_w8a8_plan(T, H, I, E, k, regime=MOE_REGIME_AUTO):
+    """Returns (resolved_regime, ws_bytes); y is fp16 [T*k, H]."""
+    r, ws = C.c_int(), C.c_size_t()
+    _check(lib().moe_expert_ffn_w8a8_plan(T, H, I, E, k, regime, C.byref(r), C.byref(ws)))
+    return r.value, ws.value
+
+
+def moe_expert_ffn_w8a8(x, perm, offsets, d_expert_blobs, T, H, I, E, k, regime, y, ws=None,
+                        ws_bytes=0, stream=None):
+    return _check(lib().moe_expert_ffn_w8a8(_p(x), _p(perm), _p(offsets), _p(d_expert_blobs), T, H,
+                                            I, E, k, regime, _p(y), _p(ws), ws_bytes, _s(stream)))
 
 
 def moe_pool_create(cfg: PoolConfig, pinned_src_ptrs):

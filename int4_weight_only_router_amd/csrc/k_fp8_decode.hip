@@ -1,0 +1,293 @@
+// k_fp8_decode.hip -- block-scaled FP8 products of few rows: decode tokens
+// through the routed experts, and dense products of up to 64 rows.
+//
+//   y[m, n] = sum_b xs[m, b] ws[n / 128, b] sum_{j in block b} xq[m, j] wq[n, j]
+//
+// Bound by the weights' stream from memory: each weight byte is used for one
+// row tile only, so the kernel's task is to have many bytes in flight.  A
+// workgroup owns 32 weight rows (gate/up: 16 gate rows and the same 16 up
+// rows, so that it also forms h) and its four waves take every fourth
+// 128-long block of K each; a wave issues the loads of four blocks (16 KB) at
+// once, before it touches the tokens.  The waves' sums meet in LDS in wave
+// order, so results do not depend on timing.  The tokens are the matrix
+// core's second operand, 16 to a fragment; its idle columns cost nothing here.
+//
+// Decode experts quantise their rows in the workgroup (gate/up: the fp16
+// tokens; down: the fp32 h the first launch left in the workspace), hidden
+// behind the weight loads: no launch of its own.
+#include "k_fp8_frag.h"
+
+namespace moe {
+
+constexpr int F8D_KPD = 4;   // K blocks a wave has in flight
+
+// One row's 128-blocks to e4m3 in LDS by 16-lane groups.
+template <typename XT>
+__device__ __forceinline__ void quant_row_lds(const XT *src, int K, int kb, int c, uint8_t *dst,
+                                              float *sc)
+{
+    float v[8];
+    const int at = kb * 128 + c * 8;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        v[i] = 0.0f;
+    if (at < K) {   // K is a multiple of 64: eight values are all in or all out
+        if constexpr (sizeof(XT) == 2) {
+            const half8_t h = *reinterpret_cast<const half8_t *>(src + at);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v[i] = (float)h[i];
+        } else {
+            const float4_t a = *reinterpret_cast<const float4_t *>(src + at);
+            const float4_t b = *reinterpret_cast<const float4_t *>(src + at + 4);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[i] = a[i];
+                v[4 + i] = b[i];
+            }
+        }
+    }
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        m = fmaxf(m, fabsf(v[i]));
+    const float s = fp8_scale(row16_max(m), true);
+    const float inv = fp8_inv_pow2(s);
+    int2_t q;
+    q[0] = fp8_pack4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
+    q[1] = fp8_pack4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv);
+    *reinterpret_cast<int2_t *>(dst + kb * 128 + c * 8) = q;
+    if (c == 0)
+        sc[kb] = s;
+}
+
+// MODE F8_DENSE: grid (32-column tiles, 16*MT-row tiles).  F8_GATEUP /
+// F8_DOWN: grid (tiles of 16 intermediate / 32 output columns, sorted rows);
+// the workgroup at an expert's first row serves its T rows (an expert has at
+// most one row per token), the others leave at once.
+template <int MODE, int MT>
+__global__ __launch_bounds__(256) void fp8_rows_kernel(Fp8Args a)
+{
+    static_assert(MODE == F8_DENSE || MT == 1, "decode experts: one row fragment");
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ __align__(16) float red[4][2 * MT][64][4];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int col = lane & 15, q = lane >> 4;
+    const int K = a.K, nkb = (K + 127) / 128;
+
+    int row0 = blockIdx.y * 16 * MT, rows = min(16 * MT, a.M - row0);
+    const uint8_t *w0 = a.w, *w1 = a.w;
+    const float *s0 = a.ws, *s1 = a.ws;
+    if constexpr (MODE != F8_DENSE) {
+        const int p = blockIdx.y;
+        // the expert of sorted row p: the experts that end at or before it
+        int e = 0;
+        for (int b = 0; b < a.E; b += 64) {
+            const int o = b + lane < a.E ? a.offsets[b + lane + 1] : 0x7fffffff;
+            e += __popcll(__ballot(o <= p));
+        }
+        if (e >= a.E)
+            return;   // behind the last routed row
+        // T rows to a workgroup (all of them, unless a token chose an expert twice)
+        if ((p - a.offsets[e]) % a.T)
+            return;
+        row0 = p;
+        rows = min(a.T, a.offsets[e + 1] - p);
+        const uint8_t *blob = static_cast<const uint8_t *>(a.blobs[e]);
+        if (!blob)
+            return;
+        w0 = blob + a.off_w0;
+        w1 = blob + a.off_w1;
+        s0 = reinterpret_cast<const float *>(blob + a.off_s0);
+        s1 = reinterpret_cast<const float *>(blob + a.off_s1);
+    }
+    // this lane's weight rows of the two fragments
+    const int n0 = MODE == F8_GATEUP ? blockIdx.x * 16 : blockIdx.x * 32;
+    const int na = n0 + col, nb = MODE == F8_GATEUP ? na : na + 16;
+    const int64_t ldw = MODE == F8_DENSE ? a.ldw : K;
+    const uint8_t *wr[2] = {w0 + (int64_t)min(na, a.N - 1) * ldw,
+                            w1 + (int64_t)min(nb, a.N - 1) * ldw};
+    s0 += (int64_t)(n0 >> 7) * nkb;
+    s1 += (int64_t)((MODE == F8_GATEUP ? n0 : n0 + 16) >> 7) * nkb;
+    const int64_t last = K - 16;   // K is a multiple of 16: the last whole piece of a row
+
+    float4_t acc[2][MT];
+#pragma unroll
+    for (int f = 0; f < 2; ++f)
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+            acc[f][m] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+
+    uint8_t *xl = smem;                                              // decode: [rows][nkb*128]
+    float *sl = reinterpret_cast<float *>(smem + (size_t)a.T * nkb * 128);   // [rows][nkb]
+
+    for (int kc = 0; kc < nkb; kc += 4 * F8D_KPD) {
+        int4_t wf[F8D_KPD][2][2];
+        float wsc[F8D_KPD][2];
+#pragma unroll
+        for (int j = 0; j < F8D_KPD; ++j) {
+            const int kb = min(kc + 4 * j + wave, nkb - 1);
+#pragma unroll
+            for (int f = 0; f < 2; ++f) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int64_t at = min((int64_t)kb * 128 + h * 64 + q * 16, last);
+                    wf[j][f][h] = ldg_nt(reinterpret_cast<const int4_t *>(wr[f] + at));
+                }
+            }
+            wsc[j][0] = s0[kb];
+            wsc[j][1] = s1[kb];
+        }
+        if constexpr (MODE != F8_DENSE) {
+            if (kc == 0) {   // quantise this expert's rows while the weights arrive
+                const int g = threadIdx.x >> 4, c = threadIdx.x & 15;
+                for (int i = g; i < rows * nkb; i += 16) {
+                    const int r = i / nkb, kb = i - r * nkb;
+                    if constexpr (MODE == F8_GATEUP) {
+                        const int t = a.perm[row0 + r] / a.k;
+                        quant_row_lds(static_cast<const f16 *>(a.src) + (int64_t)t * K, K, kb, c,
+                                      xl + (size_t)r * nkb * 128, sl + r * nkb);
+                    } else {
+                        quant_row_lds(static_cast<const float *>(a.src) + (int64_t)(row0 + r) * K,
+                                      K, kb, c, xl + (size_t)r * nkb * 128, sl + r * nkb);
+                    }
+                }
+                lds_barrier();
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < F8D_KPD; ++j) {
+            const int kb = kc + 4 * j + wave;
+            if (kb >= nkb)
+                break;
+            half32 wh[2];
+#pragma unroll
+            for (int f = 0; f < 2; ++f)
+                wh[f] = f8_to_f16(join16(wf[j][f][0], wf[j][f][1]));
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                int4_t x0 = {0, 0, 0, 0}, x1 = {0, 0, 0, 0};
+                float xs = 0.0f;
+                const int r = m * 16 + col;
+                const int c0 = kb * 128 + q * 16;
+                if (r < rows) {   // rows and bytes past the end count as zeros
+                    if constexpr (MODE == F8_DENSE) {
+                        const uint8_t *xr = a.x + (int64_t)(row0 + r) * a.ldx;
+                        if (c0 < K)
+                            x0 = ldg(reinterpret_cast<const int4_t *>(xr + c0));
+                        if (c0 + 64 < K)
+                            x1 = ldg(reinterpret_cast<const int4_t *>(xr + c0 + 64));
+                        xs = a.xs[(int64_t)(row0 + r) * nkb + kb];
+                    } else {
+                        const uint8_t *xr = xl + (size_t)r * nkb * 128;
+                        x0 = *reinterpret_cast<const int4_t *>(xr + c0);
+                        x1 = *reinterpret_cast<const int4_t *>(xr + c0 + 64);
+                        xs = sl[r * nkb + kb];
+                    }
+                }
+                const half32 xf = f8_to_f16(join16(x0, x1));
+#pragma unroll
+                for (int f = 0; f < 2; ++f) {
+                    const float4_t t = mfma_f16(wh[f], xf);
+                    const float s = xs * wsc[j][f];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        acc[f][m][i] = __builtin_fmaf(t[i], s, acc[f][m][i]);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int f = 0; f < 2; ++f)
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+            *reinterpret_cast<float4_t *>(red[wave][f * MT + m][lane]) = acc[f][m];
+    __syncthreads();
+    // fragment (f, m) is summed and stored by wave (f * MT + m) % 4; gate and
+    // up of a fragment meet in one wave
+    auto total = [&](int i) {
+        float4_t v = *reinterpret_cast<const float4_t *>(red[0][i][lane]);
+#pragma unroll
+        for (int w = 1; w < 4; ++w)
+            v += *reinterpret_cast<const float4_t *>(red[w][i][lane]);
+        return v;
+    };
+    if constexpr (MODE == F8_GATEUP) {
+        if (wave == 0 && col < rows) {
+            const float4_t g = total(0), u = total(1);
+            float4_t h;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                h[i] = swiglu_fast(g[i], u[i]);
+            *reinterpret_cast<float4_t *>(static_cast<float *>(a.out) + (int64_t)(row0 + col) * a.N +
+                                          n0 + q * 4) = h;
+        }
+    } else {
+        for (int i = wave; i < 2 * MT; i += 4) {
+            const int f = i / MT, m = i - f * MT;
+            const int r = m * 16 + col, n = n0 + f * 16 + q * 4;
+            const float4_t v = total(i);
+            if (r < rows && n < a.N)
+                store4(a.out, MODE == F8_DOWN ? MOE_DTYPE_F16 : a.odt,
+                       (int64_t)(row0 + r) * a.ldo + n, v, a.N - n,
+                       MODE == F8_DOWN || (a.ldo % 4 == 0 && ((uintptr_t)a.out & 15) == 0));
+        }
+    }
+}
+
+template <int MODE, int MT>
+static int launch_rows(const Fp8Args &a, dim3 grid, size_t lds, hipStream_t s)
+{
+    if (lds) {
+        static bool attr_set = false;   // raising the LDS limit is idempotent
+        if (!attr_set) {
+            MOE_HIP_TRY(hipFuncSetAttribute((const void *)fp8_rows_kernel<MODE, MT>,
+                                            hipFuncAttributeMaxDynamicSharedMemorySize,
+                                            FP8_DECODE_MAX_T * 64 * (128 + 4)));
+            attr_set = true;
+        }
+    }
+    hipLaunchKernelGGL((fp8_rows_kernel<MODE, MT>), grid, dim3(256), lds, s, a);
+    MOE_LAUNCH_CHECK("fp8_rows_kernel");
+    return MOE_OK;
+}
+
+// Dense, any M (in row tiles of 16, 32 or 64).
+int launch_fp8_rows_dense(const Fp8Args &a, hipStream_t s)
+{
+    const unsigned nt = (unsigned)((a.N + 31) / 32);
+    if (a.M <= 16)
+        return launch_rows<F8_DENSE, 1>(a, dim3(nt, 1), 0, s);
+    if (a.M <= 32)
+        return launch_rows<F8_DENSE, 2>(a, dim3(nt, 1), 0, s);
+    return launch_rows<F8_DENSE, 4>(a, dim3(nt, (unsigned)((a.M + 63) / 64)), 0, s);
+}
+
+// Decode experts: gate/up with SwiGLU into fp32 h, then down.
+int launch_fp8_decode(Fp8Args a, const void *x_f16, float *h, int H, int I, const int64_t off[6],
+                      void *y, hipStream_t s)
+{
+    auto lds = [&](int K) { return (size_t)a.T * ((K + 127) / 128) * (128 + 4); };
+    a.src = x_f16;
+    a.out = h;
+    a.N = I;
+    a.K = H;
+    a.off_w0 = off[0];
+    a.off_w1 = off[1];
+    a.off_s0 = off[3];
+    a.off_s1 = off[4];
+    const unsigned n = (unsigned)(a.T * a.k);
+    const int rc = launch_rows<F8_GATEUP, 1>(a, dim3((I + 15) / 16, n), lds(H), s);
+    if (rc)
+        return rc;
+    a.src = h;
+    a.out = y;
+    a.N = H;
+    a.K = I;
+    a.ldo = H;
+    a.off_w0 = a.off_w1 = off[2];
+    a.off_s0 = a.off_s1 = off[5];
+    return launch_rows<F8_DOWN, 1>(a, dim3((H + 31) / 32, n), lds(I), s);
+}
+
+}  // namespace moe

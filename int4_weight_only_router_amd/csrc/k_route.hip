@@ -269,11 +269,10 @@ __global__ __launch_bounds__(RT_WAVES * 64) void route_topk_kernel(
 
 size_t route_batched_ws_bytes(int T, int E) { return (size_t)al256((int64_t)T * E * 4); }
 
-// T > 8: logits into ws (T*E fp32), then top-k.
-int launch_route_batched(const void *x, const void *wr, const float *bias, int T, int H, int E,
-                         int k, unsigned flags, int32_t *idx, float *w, void *ws, hipStream_t s)
+// Logits alone, any T.
+int launch_route_batched_logits(const void *x, const void *wr, const float *bias, int T, int H,
+                                int E, float *lg, hipStream_t s)
 {
-    float *lg = static_cast<float *>(ws);
     const f16 *xh = static_cast<const f16 *>(x), *wh = static_cast<const f16 *>(wr);
     const dim3 grid((T + 7) / 8, (E + 8 * RL_WAVES - 1) / (8 * RL_WAVES)), block(RL_WAVES * 64);
     switch (H) {
@@ -284,6 +283,17 @@ int launch_route_batched(const void *x, const void *wr, const float *bias, int T
     default: return set_error(MOE_EUNSUPPORTED, "route: H=%d not instantiated", H);
     }
     MOE_LAUNCH_CHECK("route_logits_kernel");
+    return MOE_OK;
+}
+
+// T > 8: logits into ws (T*E fp32), then top-k.
+int launch_route_batched(const void *x, const void *wr, const float *bias, int T, int H, int E,
+                         int k, unsigned flags, int32_t *idx, float *w, void *ws, hipStream_t s)
+{
+    float *lg = static_cast<float *>(ws);
+    const int rc = launch_route_batched_logits(x, wr, bias, T, H, E, lg, s);
+    if (rc)
+        return rc;
     const size_t lds = (size_t)RT_WAVES * ((((size_t)E * sizeof(float) + 15) & ~(size_t)15) +
                                            topk_scratch_bytes(E) + 16 * sizeof(Cand));
     hipLaunchKernelGGL(route_topk_kernel, dim3((T + RT_WAVES - 1) / RT_WAVES),
