@@ -26,8 +26,8 @@ int launch_fp8_rows_dense(const Fp8Args &, hipStream_t);
 int launch_fp8_tile_dense(const Fp8Args &, hipStream_t);
 int launch_fp8_decode(Fp8Args, const void *, float *, int, int, const int64_t *, void *,
                       hipStream_t);
-int fp8_pick_mf(int64_t rows, int E);
-int64_t fp8_tile_bound(int64_t rows, int E, int mf);
+int fp8_pick_rows(int64_t rows, int E);
+int64_t fp8_tile_bound(int64_t rows, int E, int bm);
 int launch_fp8_experts(Fp8Args, int, uint8_t *, float *, int, int, const int64_t *, void *,
                        hipStream_t);
 
@@ -83,7 +83,7 @@ static Fp8Ws fp8_ws(int T, int H, int I, int E, int k, bool decode)
         w.xs = o;    o = al256(o + (int64_t)T * ((H + 127) / 128) * 4);
         w.hq = o;    o = al256(o + n * I);
         w.hs = o;    o = al256(o + n * ((I + 127) / 128) * 4);
-        w.tiles = o; o = al256(o + (2 + 2 * fp8_tile_bound(n, E, fp8_pick_mf(n, E))) * 4);
+        w.tiles = o; o = al256(o + (2 + 2 * fp8_tile_bound(n, E, fp8_pick_rows(n, E))) * 4);
     }
     w.total = o;
     return w;
@@ -269,10 +269,10 @@ int moe_gemm_fp8(const void *xq, int64_t ldx, const float *x_scales, const void 
     a.out = out;
     a.ldo = ldo;
     a.odt = out_dtype;
-    // 128 x 256 tiles once they occupy most compute units, else the kernel of
-    // few rows, which has 16 times as many workgroups
-    const int64_t tiles = (int64_t)((M + 127) / 128) * ((N + 255) / 256);
-    if (M > 64 && tiles >= 192)
+    // 256 x 256 tiles once they occupy most compute units, else the kernel of
+    // few rows, which has 32 times as many workgroups
+    const int64_t tiles = (int64_t)((M + 255) / 256) * ((N + 255) / 256);
+    if (M > 64 && tiles >= 96)
         return launch_fp8_tile_dense(a, stream);
     return launch_fp8_rows_dense(a, stream);
 }
@@ -342,18 +342,18 @@ int moe_expert_ffn_w8a8(const void *x_f16, const int32_t *perm, const int32_t *o
         return launch_fp8_decode(a, x_f16, reinterpret_cast<float *>(base + w.h), H, I, off, y_f16,
                                  stream);
     const int64_t n = (int64_t)T * k;
-    const int mf = fp8_pick_mf(n, E);
+    const int bm = fp8_pick_rows(n, E);
     int32_t *tiles = reinterpret_cast<int32_t *>(base + w.tiles);
     float *xs = reinterpret_cast<float *>(base + w.xs);
     rc = launch_quant_fp8(x_f16, MOE_DTYPE_F16, H, T, H, 1, true, base + w.xq, H, xs, stream);
     if (!rc)
-        rc = launch_fp8_tiles(offsets, E, 16 * mf, tiles, stream);
+        rc = launch_fp8_tiles(offsets, E, bm, tiles, stream);
     if (rc)
         return rc;
     a.x = base + w.xq;
     a.xs = xs;
     a.tiles = tiles;
-    return launch_fp8_experts(a, mf, base + w.hq, reinterpret_cast<float *>(base + w.hs), H, I, off,
+    return launch_fp8_experts(a, bm, base + w.hq, reinterpret_cast<float *>(base + w.hs), H, I, off,
                               y_f16, stream);
 }
 

@@ -9,18 +9,38 @@
 // registers, and the fma's (4 per matrix instruction of 32 cycles) run in the
 // shadow of the matrix pipe.
 //
-// A workgroup of four waves owns 16*MF rows x 256 weight rows; wave w owns 64
-// of the weight rows and reads them straight from memory into registers (no
-// other wave needs them, so LDS would only add traffic), one block ahead.
-// MF = 8: the rows' blocks pass through a three-stage LDS ring filled by
-// direct-to-LDS loads and are shared by the waves.  MF <= 4: few rows, each
-// wave loads them itself, and there is no barrier in the loop.
+// Two forms of a block's sum:
+//  - v_mfma_f32_16x16x128_f8f6f4, the full FP8 rate.  It first adds
+//    neighbouring products and drops there what lies 13 bits or more below the
+//    larger one (measured: 1 + 2^-14 of neighbours gives 1, of others 1 +
+//    2^-14), 1.4e-5 relative on random data.  Used where the output is rounded
+//    to 16 bits anyway.
+//  - EX: both operands as fp16 (exactly) on v_mfma_f32_16x16x32_f16, half the
+//    rate, errors of fp32 sums.  Used for fp32 outputs, and for gate/up, whose
+//    result is quantised again: an error of 1e-5 there would send 1 element of
+//    2000 to a neighbouring code.
+//
+// fp8_tile_kernel: eight waves own 64*MF rows x 256 weight rows, wave w the
+// 16*MF rows of row group w / 2 and 128 of the weight rows.  Both operands'
+// blocks travel to LDS by direct-to-LDS loads, 8 lanes per 128-byte row block,
+// into a ring of two or three stages: one barrier per block, and a block has
+// the whole work of another to arrive.  (Read straight into registers in the
+// matrix instruction's layout, consecutive lanes are consecutive rows, and the
+// L1 then serves 16 bytes a cycle instead of 64: measured 4 times slower.)  A
+// wave holds its row fragments of the block and walks its eight weight
+// fragments; each sum enters its accumulator by one fma two sums later.  The
+// fma's and the fp16 conversions run in the shadow of the matrix pipe.
+//
+// fp8_rows16_kernel: at most 16 rows to a tile, where the weights' stream from
+// memory is the bound: four waves of 64 weight rows each, everything straight
+// to registers one block ahead, no barrier.
 //
 // gate/up: the 256 weight rows are 128 gate rows and the same 128 up rows (a
-// wave holds 32 + 32), so a workgroup forms 128 columns of h, exactly one
-// scale block: h's largest magnitudes meet in LDS, h is quantised with a
+// wave holds as many of each), so a workgroup forms 128 columns of h, exactly
+// one scale block: h's largest magnitudes meet in LDS, h is quantised with a
 // power-of-two scale and leaves as e4m3.
 #include <algorithm>
+#include <type_traits>
 
 #include "k_fp8_frag.h"
 
@@ -28,294 +48,312 @@ namespace moe {
 
 constexpr int F8_NXCD = 8;
 
-template <int MF>
-constexpr int f8_stage() { return MF * 16 * 128; }
-// LDS: three stages of rows and their scales (MF = 8), or the epilogue's
-// h tile and maxima (gate/up); never both at once.
-template <int MODE, int MF, bool EX>
-size_t f8_lds(int nkb)
+// The work item of a workgroup: column tile nt of row tile mt.  Workgroup i
+// runs on XCD i % 8; each XCD takes a contiguous run of items, so that the
+// tiles that share weights or rows share an L2.
+struct F8Item {
+    int mt, nt;
+};
+template <int MODE>
+__device__ __forceinline__ bool f8_item(int MT, int NT, F8Item &it)
 {
-    const size_t loop = MF == 8 ? 3 * (size_t)f8_stage<MF>() + (size_t)nkb * MF * 16 * 4 : 0;
-    const size_t epi = MODE == F8_GATEUP ? (size_t)MF * 16 * (128 + 16) : 0;
-    return loop > epi ? loop : epi;
-}
-
-template <int MODE, int MF, bool EX>
-__global__ __launch_bounds__(256, MF >= 4 ? 1 : 2) void fp8_tile_kernel(Fp8Args a)
-{
-    constexpr bool XLDS = MF == 8;
-    constexpr int BM = 16 * MF;
-    extern __shared__ __align__(16) uint8_t smem[];
-    const int tid = threadIdx.x;
-    const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int col = lane & 15, q = lane >> 4;
-    const int K = a.K, nkb = (K + 127) / 128;
-
-    // work item: column tile nt of row tile mt.  Workgroup i runs on XCD
-    // i % 8; each XCD takes a contiguous run of items.
-    const int NT = MODE == F8_GATEUP ? (a.N + 127) / 128 : (a.N + 255) / 256;
-    const int MT = MODE == F8_DENSE ? (a.M + BM - 1) / BM : a.tiles[0];
     const int total = MT * NT;
     const int run = (total + F8_NXCD - 1) / F8_NXCD;
     const int li = blockIdx.x / F8_NXCD;
     const int item = (int)(blockIdx.x % F8_NXCD) * run + li;
     if (li >= run || item >= total)
-        return;
-    const int mt = MODE == F8_DENSE ? item % MT : item / NT;
-    const int nt = MODE == F8_DENSE ? item / MT : item % NT;
+        return false;
+    it.mt = MODE == F8_DENSE ? item % MT : item / NT;
+    it.nt = MODE == F8_DENSE ? item / MT : item % NT;
+    return true;
+}
 
+// Rows and weights of a row tile; false: nothing to do.
+struct F8Tile {
     int row0, rows;
-    const uint8_t *w0 = a.w, *w1 = a.w;
-    const float *s0 = a.ws, *s1 = a.ws;
+    const uint8_t *w0, *w1;
+    const float *s0, *s1;
+};
+template <int MODE, int BM>
+__device__ __forceinline__ bool f8_tile(const Fp8Args &a, int mt, F8Tile &t)
+{
+    t.w0 = t.w1 = a.w;
+    t.s0 = t.s1 = a.ws;
     if constexpr (MODE == F8_DENSE) {
-        row0 = mt * BM;
-        rows = min(BM, a.M - row0);
+        t.row0 = mt * BM;
+        t.rows = min(BM, a.M - t.row0);
     } else {
         const int e = a.tiles[2 + 2 * mt];
-        row0 = a.tiles[3 + 2 * mt];
-        rows = min(BM, a.offsets[e + 1] - row0);
+        t.row0 = a.tiles[3 + 2 * mt];
+        t.rows = min(BM, a.offsets[e + 1] - t.row0);
         const uint8_t *blob = static_cast<const uint8_t *>(a.blobs[e]);
         if (!blob)
-            return;
-        w0 = blob + a.off_w0;
-        w1 = blob + a.off_w1;
-        s0 = reinterpret_cast<const float *>(blob + a.off_s0);
-        s1 = reinterpret_cast<const float *>(blob + a.off_s1);
+            return false;
+        t.w0 = blob + a.off_w0;
+        t.w1 = blob + a.off_w1;
+        t.s0 = reinterpret_cast<const float *>(blob + a.off_s0);
+        t.s1 = reinterpret_cast<const float *>(blob + a.off_s1);
     }
+    return true;
+}
 
-    // weights: fragment f of this wave, lane row col
+// Source row of a tile's row r (rows past the end repeat the last one).
+template <int MODE>
+__device__ __forceinline__ int64_t f8_xrow(const Fp8Args &a, const F8Tile &t, int r)
+{
+    const int p = t.row0 + min(r, t.rows - 1);
+    return MODE == F8_GATEUP ? a.perm[p] / a.k : p;
+}
+
+// Blocks 0..nkb-1, two per round so that buffers have fixed names; the last
+// one apart (true_type), where K may end inside it.
+template <typename F>
+__device__ __forceinline__ void f8_blocks(int nkb, F &&body)
+{
+    int kb = 0;
+    for (; kb + 2 < nkb; kb += 2) {
+        body(kb, 0, std::false_type());
+        body(kb + 1, 1, std::false_type());
+    }
+    if (kb + 1 < nkb) {
+        body(kb, 0, std::false_type());
+        body(kb + 1, 1, std::true_type());
+    } else {
+        body(kb, 0, std::true_type());
+    }
+}
+
+// Bytes of the last block past K count as zeros on the rows' side (the
+// weights' side holds bytes of the same weight row there).
+__device__ __forceinline__ int8_8 f8_cut(int8_8 x, int kb, int q, int K)
+{
+    const int c = kb * 128 + q * 16;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[i] = c < K ? x[i] : 0;
+        x[4 + i] = c + 64 < K ? x[4 + i] : 0;
+    }
+    return x;
+}
+
+constexpr int F8_SCW = 8;   // blocks of row scales in LDS at a time (two windows)
+
+template <int MF>
+constexpr int f8_stages() { return MF == 4 ? 2 : 3; }
+template <int MF>
+constexpr int f8_stage_bytes() { return (64 * MF + 256) * 128; }
+// LDS: the ring, two windows of row scales, the weight scales; gate/up's h
+// tile and maxima take the ring's place afterwards.
+template <int MF>
+constexpr int f8_lds(int nkb)
+{
+    return f8_stages<MF>() * f8_stage_bytes<MF>() + 2 * F8_SCW * 64 * MF * 4 + 2 * nkb * 4;
+}
+
+template <int MODE, int MF, bool EX>
+__global__ __launch_bounds__(512, 1) void fp8_tile_kernel(Fp8Args a)
+{
+    constexpr int NTH = 512;
+    constexpr int BM = 64 * MF;
+    constexpr int NS = f8_stages<MF>();
+    constexpr int STAGE = f8_stage_bytes<MF>();
+    constexpr int XB = BM * 128;
+    constexpr int PX = MF, PW = 4;   // 16-byte loads per thread and stage
+    static_assert(PX * 16 * NTH == XB && PW * 16 * NTH == 256 * 128, "whole loads");
+    extern __shared__ __align__(16) uint8_t smem[];
+    const int tid = threadIdx.x;
+    const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int m0 = (wave >> 1) * 16 * MF, wn = wave & 1;
+    const int col = lane & 15, q = lane >> 4;
+    const int K = a.K, nkb = (K + 127) / 128;
+
+    const int NT = MODE == F8_GATEUP ? (a.N + 127) / 128 : (a.N + 255) / 256;
+    const int MT = MODE == F8_DENSE ? (a.M + BM - 1) / BM : a.tiles[0];
+    F8Item it;
+    F8Tile t;
+    if (!f8_item<MODE>(MT, NT, it) || !f8_tile<MODE, BM>(a, it.mt, t))
+        return;
     const int64_t ldw = MODE == F8_DENSE ? a.ldw : K;
-    const uint8_t *wr[4];
+    // first column: of h (gate/up), of the output
+    const int n0 = it.nt * (MODE == F8_GATEUP ? 128 : 256);
+
+    // Load i of a wave covers 8 rows; lane L fills slot L % 8 of its row, with
+    // piece (L % 8) ^ f(row), f(r) = (r >> 1) & 7: the 16 rows of a fragment
+    // read hit distinct banks.
+    const int lr = wave * 8 + (lane >> 3);            // its row within 64
+    const int pc = ((lane & 7) ^ ((lr >> 1) & 7)) * 16;   // 64 divides f's period
+    // Rows as indexes and 32-bit offsets from the tile's first weight row
+    // (256 ldw < 2^32): the registers are short.
+    int xr[PX];
+    unsigned wo[PW];
+    const uint8_t *wb0 = t.w0 + (int64_t)n0 * ldw, *wb1 = t.w1 + (int64_t)n0 * ldw;
 #pragma unroll
-    for (int f = 0; f < 4; ++f) {
-        const uint8_t *base;
-        int n;
-        if constexpr (MODE == F8_GATEUP) {
-            base = f < 2 ? w0 : w1;
-            n = nt * 128 + wave * 32 + (f & 1) * 16 + col;
-        } else {
-            base = w0;
-            n = nt * 256 + wave * 64 + f * 16 + col;
-        }
-        wr[f] = base + (int64_t)min(n, a.N - 1) * ldw;
+    for (int i = 0; i < PX; ++i)
+        xr[i] = (int)f8_xrow<MODE>(a, t, i * 64 + lr);
+#pragma unroll
+    for (int i = 0; i < PW; ++i) {   // gate/up: rows 0..127 gate, 128..255 up
+        const int r = MODE == F8_GATEUP ? (i & 1) * 64 + lr : i * 64 + lr;
+        wo[i] = (unsigned)min(r, a.N - 1 - n0) * (unsigned)ldw;
     }
-    // the wave's columns lie in one 128-column scale block (two for gate/up:
-    // one of each matrix)
-    const int sb = MODE == F8_GATEUP ? nt : min(nt * 256 + wave * 64, a.N - 1) >> 7;
-    s0 += (int64_t)sb * nkb;
-    s1 += (int64_t)sb * nkb;
-
-    // source row of the tile's row r (rows past the end repeat the last one)
-    auto xrow = [&](int r) -> int64_t {
-        const int p = row0 + min(r, rows - 1);
-        return MODE == F8_GATEUP ? a.perm[p] / a.k : p;
-    };
-    const int klast = K - 16;
-    int4_t wf[2][4][2];
-    float wsc[2][2];
-    auto load_w = [&](int kb, int b) {
-        kb = min(kb, nkb - 1);
+    auto issue = [&](int kb) {   // past the end re-reads the last block
+        uint8_t *st = smem + (kb % NS) * STAGE + wave * 1024;
+        const int at = min(min(kb, nkb - 1) * 128 + pc, K - 16);
 #pragma unroll
-        for (int f = 0; f < 4; ++f)
+        for (int i = 0; i < PX; ++i)
+            dma16(a.x + xr[i] * a.ldx + at, st + i * 8192);
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-                wf[b][f][h] =
-                    ldg(reinterpret_cast<const int4_t *>(wr[f] + min(kb * 128 + h * 64 + q * 16, klast)));
-        wsc[b][0] = s0[kb];
-        wsc[b][1] = MODE == F8_GATEUP ? s1[kb] : 0.0f;
+        for (int i = 0; i < PW; ++i)
+            dma16((MODE == F8_GATEUP && i >= 2 ? wb1 : wb0) + (wo[i] + (unsigned)at),
+                  st + XB + i * 8192);
     };
+    float *xsc = reinterpret_cast<float *>(smem + NS * STAGE);   // [2][F8_SCW][BM]
+    float *wsc = xsc + 2 * F8_SCW * BM;                          // [2][nkb]
+    // window v of the row scales, transposed
+    auto scales = [&](int v) {
+        for (int i = tid; i < BM * F8_SCW; i += NTH) {
+            const int r = i / F8_SCW, j = i % F8_SCW, kb = v * F8_SCW + j;
+            if (kb < nkb)
+                xsc[((v & 1) * F8_SCW + j) * BM + r] =
+                    a.xs[f8_xrow<MODE>(a, t, r) * nkb + kb];
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < NS - 1; ++i)
+        issue(i);
+    scales(0);
+    {
+        // the two 128-row scale blocks (gate/up: one of each matrix)
+        const float *s1 = MODE == F8_GATEUP ? t.s1 + (int64_t)(n0 >> 7) * nkb
+                                            : t.s0 + (int64_t)min((n0 >> 7) + 1, (a.N - 1) >> 7) * nkb;
+        const float *s0 = t.s0 + (int64_t)(n0 >> 7) * nkb;
+        for (int i = tid; i < 2 * nkb; i += NTH)
+            wsc[i] = i < nkb ? s0[i] : s1[i - nkb];
+    }
 
-    float4_t acc[MF][4];
+    float4_t acc[MF][8];
 #pragma unroll
     for (int m = 0; m < MF; ++m)
 #pragma unroll
-        for (int f = 0; f < 4; ++f)
+        for (int f = 0; f < 8; ++f)
             acc[m][f] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
-    half32 wh[4];   // EX: the block's weights as fp16
-    auto begin = [&](int b) {
-        if constexpr (EX) {
-#pragma unroll
-            for (int f = 0; f < 4; ++f)
-                wh[f] = f8_to_f16(join16(wf[b][f][0], wf[b][f][1]));
-        }
+    const int sw = (col >> 1) & 7;
+    const int o0 = (q ^ sw) * 16, o1 = ((q + 4) ^ sw) * 16;
+    // LDS row of weight fragment f: gate/up waves take 64 rows of each matrix
+    auto wrow = [&](int f) {
+        return (MODE == F8_GATEUP ? (f >> 2) * 128 + wn * 64 + (f & 3) * 16 : wn * 128 + f * 16) + col;
     };
-    auto step = [&](int m, int b, int8_8 xf, float xs) {
-        half32 xh;
-        if constexpr (EX)
-            xh = f8_to_f16(xf);
-        const float sg = xs * wsc[b][0];
-        const float su = MODE == F8_GATEUP ? xs * wsc[b][1] : sg;
-#pragma unroll
-        for (int f = 0; f < 4; ++f) {
-            float4_t t;
-            if constexpr (EX)
-                t = mfma_f16(wh[f], xh);
-            else
-                t = mfma_f8(join16(wf[b][f][0], wf[b][f][1]), xf);
-            const float s = f < 2 ? sg : su;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                acc[m][f][i] = __builtin_fmaf(t[i], s, acc[m][f][i]);
-        }
-    };
-    // bytes of the last block past K count as zeros (the weights' side reads
-    // bytes of the same row there instead)
-    auto cut = [&](int8_8 xf, int kb) {
-        const int c = kb * 128 + q * 16;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            xf[i] = c < K ? xf[i] : 0;
-            xf[4 + i] = c + 64 < K ? xf[4 + i] : 0;
-        }
-        return xf;
-    };
-    const bool ragged = (K & 127) != 0;
+    const bool idle = m0 >= t.rows;   // no row of this wave's group exists
 
-    if constexpr (XLDS) {
-        constexpr int STAGE = f8_stage<MF>();
-        constexpr int PX = STAGE / 4096;   // 16-byte loads per thread per stage
-        float *sl = reinterpret_cast<float *>(smem + 3 * STAGE);   // [nkb][BM]
-        // load i of wave w covers rows 8 (4 i + w) ..+7; lane L fills slot
-        // L % 8 of its row, i.e. piece (L % 8) ^ f(row), f(r) = (r >> 1) & 7:
-        // the 16 rows of a fragment read hit distinct banks
-        const uint8_t *src[PX];
-        int pc[PX];
-#pragma unroll
-        for (int i = 0; i < PX; ++i) {
-            const int r = (i * 4 + wave) * 8 + (lane >> 3);
-            pc[i] = ((lane & 7) ^ ((r >> 1) & 7)) * 16;
-            src[i] = a.x + xrow(r) * a.ldx;
-        }
-        auto issue = [&](int kb) {   // past the end re-reads the last block
-            uint8_t *st = smem + (kb % 3) * STAGE;
-            kb = min(kb, nkb - 1);
-#pragma unroll
-            for (int i = 0; i < PX; ++i)
-                dma16(src[i] + min(kb * 128 + pc[i], klast), st + (i * 4 + wave) * 1024);
+    auto block = [&](int kb, auto tail) {
+        // this wave's loads of block kb have landed (those of the NS - 2
+        // blocks after it may be pending); after the barrier everyone's have,
+        // and the stage of block kb - 1 is read by all
+        wait_vm<(NS - 2) * (PX + PW)>();
+        lds_barrier();
+        if ((kb & (F8_SCW - 1)) == F8_SCW - 2)
+            scales(kb / F8_SCW + 1);   // before the ring loads: their wait covers it
+        issue(kb + NS - 1);
+        if (idle)
+            return;
+        const uint8_t *st = smem + (kb % NS) * STAGE;
+        auto frag = [&](const uint8_t *r) {
+            return join16(*reinterpret_cast<const int4_t *>(r + o0),
+                          *reinterpret_cast<const int4_t *>(r + o1));
         };
-        // rows' scales, transposed
-        for (int i = tid; i < BM * nkb; i += 256) {
-            const int r = i / nkb, kb = i - r * nkb;
-            sl[kb * BM + r] = a.xs[xrow(r) * nkb + kb];
-        }
-        load_w(0, 0);
-        issue(0);
-        issue(1);
-        const int sw = (col >> 1) & 7;
-        const int o0 = (q ^ sw) * 16, o1 = ((q + 4) ^ sw) * 16;
-        auto body = [&](int kb, int b) {
-            // this wave's weights and row loads of block kb have landed (only
-            // the PX row loads of block kb + 1 may be pending); after the
-            // barrier everyone's have, and block kb - 1 is read by all
-            wait_vm<PX>();
-            lds_barrier();
-            begin(b);
-            load_w(kb + 1, b ^ 1);
-            issue(kb + 2);
-            const uint8_t *st = smem + (kb % 3) * STAGE;
-            const bool tail = ragged && kb == nkb - 1;
-#pragma unroll
-            for (int m = 0; m < MF; ++m) {
-                const uint8_t *r = st + (m * 16 + col) * 128;
-                int8_8 xf = join16(*reinterpret_cast<const int4_t *>(r + o0),
-                                   *reinterpret_cast<const int4_t *>(r + o1));
-                if (tail)
-                    xf = cut(xf, kb);
-                step(m, b, xf, sl[kb * BM + m * 16 + col]);
-            }
-        };
-        for (int kb = 0; kb < nkb; kb += 2) {
-            body(kb, 0);
-            if (kb + 1 < nkb)
-                body(kb + 1, 1);
-        }
-        wait_vm<0>();   // trailing loads into LDS are done before it is reused
-    } else {
-        const uint8_t *xr[MF];
-        const float *xsr[MF];
+        int8_8 x[MF];
+        half32 xh[MF];
+        float sc[MF][2];
+        const float *xs = xsc + (kb & (2 * F8_SCW - 1)) * BM + m0 + col;
+        const float wg = wsc[MODE == F8_GATEUP ? kb : wn * nkb + kb];
+        const float wu = MODE == F8_GATEUP ? wsc[nkb + kb] : wg;
 #pragma unroll
         for (int m = 0; m < MF; ++m) {
-            const int64_t r = xrow(m * 16 + col);
-            xr[m] = a.x + r * a.ldx;
-            xsr[m] = a.xs + r * nkb;
+            x[m] = frag(st + (m0 + m * 16 + col) * 128);
+            if constexpr (decltype(tail)::value)
+                x[m] = f8_cut(x[m], kb, q, K);
+            if constexpr (EX)
+                xh[m] = f8_to_f16(x[m]);
+            sc[m][0] = xs[m * 16] * wg;
+            sc[m][1] = MODE == F8_GATEUP ? xs[m * 16] * wu : sc[m][0];
         }
-        int4_t xf[2][MF][2];
-        float xs[2][MF];
-        auto load_x = [&](int kb, int b) {
-            kb = min(kb, nkb - 1);
+        float4_t s[4];
+        auto add = [&](int i) {
+            const int f = i / MF, m = i % MF;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                acc[m][f][j] = __builtin_fmaf(s[i & 3][j], sc[m][f >> 2], acc[m][f][j]);
+        };
+        int8_8 w[2];
+        w[0] = frag(st + XB + wrow(0) * 128);
+#pragma unroll
+        for (int f = 0; f < 8; ++f) {
+            if (f + 1 < 8)
+                w[(f + 1) & 1] = frag(st + XB + wrow(f + 1) * 128);
+            half32 wh;
+            if constexpr (EX)
+                wh = f8_to_f16(w[f & 1]);
 #pragma unroll
             for (int m = 0; m < MF; ++m) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    xf[b][m][h] = ldg(reinterpret_cast<const int4_t *>(
-                        xr[m] + min(kb * 128 + h * 64 + q * 16, klast)));
-                xs[b][m] = xsr[m][kb];
+                const int i = f * MF + m;
+                if constexpr (EX)
+                    s[i & 3] = mfma_f16(wh, xh[m]);
+                else
+                    s[i & 3] = mfma_f8(w[f & 1], x[m]);
+                if (i >= 2)
+                    add(i - 2);
+                // keeps the steps in order: left to itself the scheduler
+                // hoists reads and sums until the registers run out
+                __builtin_amdgcn_sched_barrier(0);
             }
-        };
-        auto body = [&](int kb, int b) {
-            begin(b);
-            load_w(kb + 1, b ^ 1);
-            load_x(kb + 1, b ^ 1);
-            const bool tail = ragged && kb == nkb - 1;
-#pragma unroll
-            for (int m = 0; m < MF; ++m) {
-                int8_8 v = join16(xf[b][m][0], xf[b][m][1]);
-                if (tail)
-                    v = cut(v, kb);
-                step(m, b, v, xs[b][m]);
-            }
-        };
-        load_w(0, 0);
-        load_x(0, 0);
-        for (int kb = 0; kb < nkb; kb += 2) {
-            body(kb, 0);
-            if (kb + 1 < nkb)
-                body(kb + 1, 1);
         }
-    }
+        add(8 * MF - 2);
+        add(8 * MF - 1);
+    };
+    for (int kb = 0; kb + 1 < nkb; ++kb)
+        block(kb, std::false_type());
+    block(nkb - 1, std::true_type());
+    wait_vm<0>();   // trailing loads into LDS are done before it is reused
 
     if constexpr (MODE == F8_GATEUP) {
         uint8_t *ht = smem;                                              // [BM][128]
-        float *mx = reinterpret_cast<float *>(smem + (size_t)BM * 128);   // [4][BM]
+        float *mx = reinterpret_cast<float *>(smem + (size_t)BM * 128);   // [2][BM]
         __syncthreads();   // the ring is read by all
-        const int i0 = nt * 128 + wave * 32;   // I is a multiple of 64: a wave is in or out
-        const bool in = i0 < a.N;
+        const bool in = n0 + wn * 64 < a.N;   // I is a multiple of 64: a wave is in or out
 #pragma unroll
         for (int m = 0; m < MF; ++m) {
             float top = 0.0f;
 #pragma unroll
-            for (int f = 0; f < 2; ++f)
+            for (int f = 0; f < 4; ++f)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float h = in ? swiglu_fast(acc[m][f][i], acc[m][2 + f][i]) : 0.0f;
+                    const float h = in ? swiglu_fast(acc[m][f][i], acc[m][4 + f][i]) : 0.0f;
                     acc[m][f][i] = h;
                     top = fmaxf(top, fabsf(h));
                 }
             top = fmaxf(top, __shfl_xor(top, 16, 64));
             top = fmaxf(top, __shfl_xor(top, 32, 64));
             if (q == 0)
-                mx[wave * BM + m * 16 + col] = top;
+                mx[wn * BM + m0 + m * 16 + col] = top;
         }
         __syncthreads();
 #pragma unroll
         for (int m = 0; m < MF; ++m) {
-            const int r = m * 16 + col;
-            const float top = fmaxf(fmaxf(mx[r], mx[BM + r]), fmaxf(mx[2 * BM + r], mx[3 * BM + r]));
-            const float s = fp8_scale(top, true), inv = fp8_inv_pow2(s);
+            const int r = m0 + m * 16 + col;
+            const float sc = fp8_scale(fmaxf(mx[r], mx[BM + r]), true), inv = fp8_inv_pow2(sc);
 #pragma unroll
-            for (int f = 0; f < 2; ++f)
-                *reinterpret_cast<int *>(ht + r * 128 + wave * 32 + f * 16 + q * 4) =
+            for (int f = 0; f < 4; ++f)
+                *reinterpret_cast<int *>(ht + r * 128 + wn * 64 + f * 16 + q * 4) =
                     fp8_pack4(acc[m][f][0] * inv, acc[m][f][1] * inv, acc[m][f][2] * inv,
                               acc[m][f][3] * inv);
-            if (wave == 0 && q == 0 && r < rows)
-                a.hs[(int64_t)(row0 + r) * NT + nt] = s;
+            if (wn == 0 && q == 0 && r < t.rows)
+                a.hs[(int64_t)(t.row0 + r) * NT + it.nt] = sc;
         }
         __syncthreads();
-        for (int i = tid; i < BM * 8; i += 256) {
+        for (int i = tid; i < BM * 8; i += NTH) {
             const int r = i >> 3, c = (i & 7) * 16;
-            if (r < rows && nt * 128 + c < a.N)
+            if (r < t.rows && n0 + c < a.N)
                 *reinterpret_cast<int4_t *>(static_cast<uint8_t *>(a.out) +
-                                            (int64_t)(row0 + r) * a.N + nt * 128 + c) =
+                                            (int64_t)(t.row0 + r) * a.N + n0 + c) =
                     *reinterpret_cast<const int4_t *>(ht + r * 128 + c);
         }
     } else {
@@ -323,33 +361,149 @@ __global__ __launch_bounds__(256, MF >= 4 ? 1 : 2) void fp8_tile_kernel(Fp8Args 
         const bool vec = MODE == F8_DOWN || (a.ldo % 4 == 0 && ((uintptr_t)a.out & 15) == 0);
 #pragma unroll
         for (int m = 0; m < MF; ++m) {
-            const int r = m * 16 + col;
-            if (r >= rows)
+            const int r = m0 + m * 16 + col;
+            if (r >= t.rows)
                 continue;
 #pragma unroll
-            for (int f = 0; f < 4; ++f) {
-                const int n = nt * 256 + wave * 64 + f * 16 + q * 4;
+            for (int f = 0; f < 8; ++f) {
+                const int n = n0 + wn * 128 + f * 16 + q * 4;
                 if (n < a.N)
-                    store4(a.out, dt, (int64_t)(row0 + r) * a.ldo + n, acc[m][f], a.N - n, vec);
+                    store4(a.out, dt, (int64_t)(t.row0 + r) * a.ldo + n, acc[m][f], a.N - n, vec);
             }
         }
     }
 }
 
+// At most 16 rows to a tile; four waves of 64 weight rows (gate/up: 32 + 32).
+template <int MODE>
+__global__ __launch_bounds__(256, 2) void fp8_rows16_kernel(Fp8Args a)
+{
+    constexpr int BM = 16;
+    __shared__ __align__(16) uint8_t ht[BM * 128];   // gate/up: h
+    __shared__ float mx[4][BM];
+    const int tid = threadIdx.x;
+    const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int col = lane & 15, q = lane >> 4;
+    const int K = a.K, nkb = (K + 127) / 128;
+    const int NT = MODE == F8_GATEUP ? (a.N + 127) / 128 : (a.N + 255) / 256;
+    F8Item it;
+    F8Tile t;
+    if (!f8_item<MODE>(a.tiles[0], NT, it) || !f8_tile<MODE, BM>(a, it.mt, t))
+        return;
+    const int nw = MODE == F8_GATEUP ? it.nt * 128 + wave * 32 : it.nt * 256 + wave * 64;
+    const int nb = min(nw, a.N - 1);
+    const uint8_t *wb0 = t.w0 + (int64_t)nb * K, *wb1 = t.w1 + (int64_t)nb * K;
+    int wo[4];   // lane offsets of the fragments' rows
+#pragma unroll
+    for (int f = 0; f < 4; ++f)
+        wo[f] = (min(nw + (MODE == F8_GATEUP ? f & 1 : f) * 16 + col, a.N - 1) - nb) * K;
+    const float *s0 = t.s0 + (int64_t)(nb >> 7) * nkb, *s1 = t.s1 + (int64_t)(nb >> 7) * nkb;
+    const int64_t r = f8_xrow<MODE>(a, t, col);
+    const uint8_t *xr = a.x + r * a.ldx;
+    const float *xsr = a.xs + r * nkb;
+
+    int4_t wf[2][4][2], xf[2][2];
+    float wsc[2][2], xs[2];
+    auto load = [&](int kb, int b) {   // past the end re-reads the last block
+        kb = min(kb, nkb - 1);
+        const int o0 = min(kb * 128 + q * 16, K - 16), o1 = min(kb * 128 + 64 + q * 16, K - 16);
+#pragma unroll
+        for (int f = 0; f < 4; ++f) {
+            const uint8_t *base = MODE == F8_GATEUP && f >= 2 ? wb1 : wb0;
+            wf[b][f][0] = ldg(reinterpret_cast<const int4_t *>(base + (unsigned)(wo[f] + o0)));
+            wf[b][f][1] = ldg(reinterpret_cast<const int4_t *>(base + (unsigned)(wo[f] + o1)));
+        }
+        xf[b][0] = ldg(reinterpret_cast<const int4_t *>(xr + o0));
+        xf[b][1] = ldg(reinterpret_cast<const int4_t *>(xr + o1));
+        wsc[b][0] = s0[kb];
+        wsc[b][1] = MODE == F8_GATEUP ? s1[kb] : 0.0f;
+        xs[b] = xsr[kb];
+    };
+    float4_t acc[4];
+#pragma unroll
+    for (int f = 0; f < 4; ++f)
+        acc[f] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    load(0, 0);
+    f8_blocks(nkb, [&](int kb, int b, auto tail) {
+        load(kb + 1, b ^ 1);
+        int8_8 x = join16(xf[b][0], xf[b][1]);
+        if constexpr (decltype(tail)::value)
+            x = f8_cut(x, kb, q, K);
+        const half32 xh = f8_to_f16(x);
+#pragma unroll
+        for (int f = 0; f < 4; ++f) {
+            const float4_t s = mfma_f16(f8_to_f16(join16(wf[b][f][0], wf[b][f][1])), xh);
+            const float c = xs[b] * (MODE == F8_GATEUP && f >= 2 ? wsc[b][1] : wsc[b][0]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                acc[f][i] = __builtin_fmaf(s[i], c, acc[f][i]);
+        }
+    });
+    if constexpr (MODE == F8_GATEUP) {
+        float top = 0.0f;
+#pragma unroll
+        for (int f = 0; f < 2; ++f)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float h = nw < a.N ? swiglu_fast(acc[f][i], acc[2 + f][i]) : 0.0f;
+                acc[f][i] = h;
+                top = fmaxf(top, fabsf(h));
+            }
+        top = fmaxf(top, __shfl_xor(top, 16, 64));
+        top = fmaxf(top, __shfl_xor(top, 32, 64));
+        if (q == 0)
+            mx[wave][col] = top;
+        __syncthreads();
+        const float sc = fp8_scale(fmaxf(fmaxf(mx[0][col], mx[1][col]), fmaxf(mx[2][col], mx[3][col])),
+                                   true);
+        const float inv = fp8_inv_pow2(sc);
+#pragma unroll
+        for (int f = 0; f < 2; ++f)
+            *reinterpret_cast<int *>(ht + col * 128 + wave * 32 + f * 16 + q * 4) =
+                fp8_pack4(acc[f][0] * inv, acc[f][1] * inv, acc[f][2] * inv, acc[f][3] * inv);
+        if (tid < t.rows)   // wave 0, q = 0: lane = row
+            a.hs[(int64_t)(t.row0 + tid) * NT + it.nt] = sc;
+        __syncthreads();
+        const int rr = tid >> 3, c = (tid & 7) * 16;
+        if (rr < t.rows && it.nt * 128 + c < a.N)
+            *reinterpret_cast<int4_t *>(static_cast<uint8_t *>(a.out) +
+                                        (int64_t)(t.row0 + rr) * a.N + it.nt * 128 + c) =
+                *reinterpret_cast<const int4_t *>(ht + rr * 128 + c);
+    } else if (col < t.rows) {
+#pragma unroll
+        for (int f = 0; f < 4; ++f) {
+            const int n = nw + f * 16 + q * 4;
+            if (n < a.N)
+                store4(a.out, MOE_DTYPE_F16, (int64_t)(t.row0 + col) * a.ldo + n, acc[f], a.N - n,
+                       true);
+        }
+    }
+}
+
+static int f8_grid(int64_t items, unsigned *grid)
+{
+    const int64_t g = (items + F8_NXCD - 1) / F8_NXCD * F8_NXCD;
+    if (g > 0x7fffffffLL)
+        return set_error(MOE_EUNSUPPORTED, "FP8 product: more than 2^31 - 1 tiles");
+    *grid = (unsigned)g;
+    return MOE_OK;
+}
+
 template <int MODE, int MF, bool EX>
 static int launch_tile(const Fp8Args &a, int64_t items, hipStream_t s)
 {
-    const size_t lds = f8_lds<MODE, MF, EX>((a.K + 127) / 128);
     static bool attr_set = false;   // raising the LDS limit is idempotent
-    if (lds > 65536 && !attr_set) {
+    if (!attr_set) {
         MOE_HIP_TRY(hipFuncSetAttribute((const void *)fp8_tile_kernel<MODE, MF, EX>,
                                         hipFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024));
         attr_set = true;
     }
-    const int64_t grid = (items + F8_NXCD - 1) / F8_NXCD * F8_NXCD;
-    if (grid > 0x7fffffffLL)
-        return set_error(MOE_EUNSUPPORTED, "FP8 product: more than 2^31 - 1 tiles");
-    hipLaunchKernelGGL((fp8_tile_kernel<MODE, MF, EX>), dim3((unsigned)grid), dim3(256), lds, s, a);
+    unsigned grid;
+    const int rc = f8_grid(items, &grid);
+    if (rc)
+        return rc;
+    hipLaunchKernelGGL((fp8_tile_kernel<MODE, MF, EX>), dim3(grid), dim3(512),
+                       f8_lds<MF>((a.K + 127) / 128), s, a);
     MOE_LAUNCH_CHECK("fp8_tile_kernel");
     return MOE_OK;
 }
@@ -360,37 +514,49 @@ static int launch_tile_mf(const Fp8Args &a, int mf, int64_t items, hipStream_t s
     switch (mf) {
     case 1: return launch_tile<MODE, 1, EX>(a, items, s);
     case 2: return launch_tile<MODE, 2, EX>(a, items, s);
-    case 4: return launch_tile<MODE, 4, EX>(a, items, s);
-    default: return launch_tile<MODE, 8, EX>(a, items, s);
+    default: return launch_tile<MODE, 4, EX>(a, items, s);
     }
+}
+
+template <int MODE>
+static int launch_rows16(const Fp8Args &a, int64_t items, hipStream_t s)
+{
+    unsigned grid;
+    const int rc = f8_grid(items, &grid);
+    if (rc)
+        return rc;
+    hipLaunchKernelGGL((fp8_rows16_kernel<MODE>), dim3(grid), dim3(256), 0, s, a);
+    MOE_LAUNCH_CHECK("fp8_rows16_kernel");
+    return MOE_OK;
 }
 
 int launch_fp8_tile_dense(const Fp8Args &a, hipStream_t s)
 {
-    const int64_t items = (int64_t)((a.M + 127) / 128) * ((a.N + 255) / 256);
+    const int mf = 4;
+    const int64_t items = (int64_t)((a.M + 64 * mf - 1) / (64 * mf)) * ((a.N + 255) / 256);
     if (a.odt == MOE_DTYPE_F32)
-        return launch_tile<F8_DENSE, 8, true>(a, items, s);
-    return launch_tile<F8_DENSE, 8, false>(a, items, s);
+        return launch_tile_mf<F8_DENSE, true>(a, mf, items, s);
+    return launch_tile_mf<F8_DENSE, false>(a, mf, items, s);
 }
 
-// Row-tile height (16 MF rows) from the mean rows of an expert.
-int fp8_pick_mf(int64_t rows, int E)
+// Rows of a row tile from the mean rows of an expert: 16, 64, 128 or 256.
+int fp8_pick_rows(int64_t rows, int E)
 {
     const int64_t avg = rows / std::max<int64_t>(1, std::min<int64_t>(E, rows));
-    return avg <= 12 ? 1 : avg <= 24 ? 2 : avg <= 64 ? 4 : 8;
+    return avg <= 16 ? 16 : avg <= 48 ? 64 : avg <= 96 ? 128 : 256;
 }
 
 // Upper bound of row tiles: every expert adds at most one partial tile.
-int64_t fp8_tile_bound(int64_t rows, int E, int mf)
+int64_t fp8_tile_bound(int64_t rows, int E, int bm)
 {
-    return (rows + 16 * mf - 1) / (16 * mf) + std::min<int64_t>(E, rows);
+    return (rows + bm - 1) / bm + std::min<int64_t>(E, rows);
 }
 
 // Routed experts over the tile table: gate/up into hq/hs, then down into y.
-int launch_fp8_experts(Fp8Args a, int mf, uint8_t *hq, float *hs, int H, int I,
+int launch_fp8_experts(Fp8Args a, int bm, uint8_t *hq, float *hs, int H, int I,
                        const int64_t off[6], void *y, hipStream_t s)
 {
-    const int64_t bound = fp8_tile_bound((int64_t)a.T * a.k, a.E, mf);
+    const int64_t bound = fp8_tile_bound((int64_t)a.T * a.k, a.E, bm);
     a.ldx = H;
     a.N = I;
     a.K = H;
@@ -400,7 +566,9 @@ int launch_fp8_experts(Fp8Args a, int mf, uint8_t *hq, float *hs, int H, int I,
     a.off_w1 = off[1];
     a.off_s0 = off[3];
     a.off_s1 = off[4];
-    const int rc = launch_tile_mf<F8_GATEUP, true>(a, mf, bound * ((I + 127) / 128), s);
+    int64_t items = bound * ((I + 127) / 128);
+    const int rc = bm == 16 ? launch_rows16<F8_GATEUP>(a, items, s)
+                            : launch_tile_mf<F8_GATEUP, true>(a, bm / 64, items, s);
     if (rc)
         return rc;
     a.x = hq;
@@ -412,7 +580,9 @@ int launch_fp8_experts(Fp8Args a, int mf, uint8_t *hq, float *hs, int H, int I,
     a.ldo = H;
     a.off_w0 = off[2];
     a.off_s0 = off[5];
-    return launch_tile_mf<F8_DOWN, false>(a, mf, bound * ((H + 255) / 256), s);
+    items = bound * ((H + 255) / 256);
+    return bm == 16 ? launch_rows16<F8_DOWN>(a, items, s)
+                    : launch_tile_mf<F8_DOWN, false>(a, bm / 64, items, s);
 }
 
 }  // namespace moe
