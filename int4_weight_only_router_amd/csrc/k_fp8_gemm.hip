@@ -10,15 +10,17 @@
 // shadow of the matrix pipe.
 //
 // Two forms of a block's sum:
-//  - v_mfma_f32_16x16x128_f8f6f4, the full FP8 rate.  It first adds
-//    neighbouring products and drops there what lies 13 bits or more below the
-//    larger one (measured: 1 + 2^-14 of neighbours gives 1, of others 1 +
-//    2^-14), 1.4e-5 relative on random data.  Used where the output is rounded
-//    to 16 bits anyway.
+//  - v_mfma_f32_16x16x128_f8f6f4, the full FP8 rate.  It first adds runs of
+//    eight products and drops there what lies 13 bits or more below the
+//    largest (measured: 1 + 2^-14 in one run gives 1, in two runs 1 + 2^-14;
+//    the smaller v_mfma_f32_16x16x32_fp8_fp8 gives the same bits), 1.4e-5
+//    relative on random data.  Used where the output is rounded to 16 bits
+//    anyway.
 //  - EX: both operands as fp16 (exactly) on v_mfma_f32_16x16x32_f16, half the
 //    rate, errors of fp32 sums.  Used for fp32 outputs, and for gate/up, whose
-//    result is quantised again: an error of 1e-5 there would send 1 element of
-//    2000 to a neighbouring code.
+//    result is quantised again: an error of 1e-5 there sends 1 element of 2000
+//    to a neighbouring code (measured: the experts' error against 64 bits goes
+//    from 3e-4 to 1.1e-3).
 //
 // fp8_tile_kernel: eight waves own 64*MF rows x 256 weight rows, wave w the
 // 16*MF rows of row group w / 2 and 128 of the weight rows.  Both operands'
@@ -29,7 +31,7 @@
 // L1 then serves 16 bytes a cycle instead of 64: measured 4 times slower.)  A
 // wave holds its row fragments of the block and walks its eight weight
 // fragments; each sum enters its accumulator by one fma two sums later.  The
-// fma's and the fp16 conversions run in the shadow of the matrix pipe.
+// fma's run in the shadow of the matrix pipe.
 //
 // fp8_rows16_kernel: at most 16 rows to a tile, where the weights' stream from
 // memory is the bound: four waves of 64 weight rows each, everything straight
@@ -139,7 +141,7 @@ __device__ __forceinline__ int8_8 f8_cut(int8_8 x, int kb, int q, int K)
 constexpr int F8_SCW = 8;   // blocks of row scales in LDS at a time (two windows)
 
 template <int MF>
-constexpr int f8_stages() { return MF == 4 ? 2 : 3; }
+constexpr int f8_stages() { return MF >= 3 ? 2 : 3; }
 template <int MF>
 constexpr int f8_stage_bytes() { return (64 * MF + 256) * 128; }
 // LDS: the ring, two windows of row scales, the weight scales; gate/up's h
@@ -195,32 +197,41 @@ __global__ __launch_bounds__(512, 1) void fp8_tile_kernel(Fp8Args a)
         const int r = MODE == F8_GATEUP ? (i & 1) * 64 + lr : i * 64 + lr;
         wo[i] = (unsigned)min(r, a.N - 1 - n0) * (unsigned)ldw;
     }
-    auto issue = [&](int kb) {   // past the end re-reads the last block
+    // load i of block kb's PX + PW (past the end re-reads the last block)
+    auto issue1 = [&](int kb, int i) {
         uint8_t *st = smem + (kb % NS) * STAGE + wave * 1024;
         const int at = min(min(kb, nkb - 1) * 128 + pc, K - 16);
+        if (i < PX)
+            dma16(a.x + xr[i < PX ? i : 0] * a.ldx + at, st + i * 8192);
+        else
+            dma16((MODE == F8_GATEUP && i - PX >= 2 ? wb1 : wb0) +
+                      (wo[i < PX ? 0 : i - PX] + (unsigned)at),
+                  st + XB + (i - PX) * 8192);
+    };
+    auto issue = [&](int kb) {
 #pragma unroll
-        for (int i = 0; i < PX; ++i)
-            dma16(a.x + xr[i] * a.ldx + at, st + i * 8192);
-#pragma unroll
-        for (int i = 0; i < PW; ++i)
-            dma16((MODE == F8_GATEUP && i >= 2 ? wb1 : wb0) + (wo[i] + (unsigned)at),
-                  st + XB + i * 8192);
+        for (int i = 0; i < PX + PW; ++i)
+            issue1(kb, i);
     };
     float *xsc = reinterpret_cast<float *>(smem + NS * STAGE);   // [2][F8_SCW][BM]
     float *wsc = xsc + 2 * F8_SCW * BM;                          // [2][nkb]
-    // window v of the row scales, transposed
+    // window v of the row scales, transposed; thread t's MF values all in flight
+    static_assert(BM * F8_SCW == MF * NTH, "MF scales per thread and window");
     auto scales = [&](int v) {
-        for (int i = tid; i < BM * F8_SCW; i += NTH) {
-            const int r = i / F8_SCW, j = i % F8_SCW, kb = v * F8_SCW + j;
-            if (kb < nkb)
-                xsc[((v & 1) * F8_SCW + j) * BM + r] =
-                    a.xs[f8_xrow<MODE>(a, t, r) * nkb + kb];
-        }
+        float c[MF];
+#pragma unroll
+        for (int i = 0; i < MF; ++i)
+            c[i] = a.xs[f8_xrow<MODE>(a, t, (i * NTH + tid) / F8_SCW) * nkb +
+                        min(v * F8_SCW + tid % F8_SCW, nkb - 1)];
+#pragma unroll
+        for (int i = 0; i < MF; ++i)
+            xsc[((v & 1) * F8_SCW + tid % F8_SCW) * BM + (i * NTH + tid) / F8_SCW] = c[i];
     };
 #pragma unroll
     for (int i = 0; i < NS - 1; ++i)
         issue(i);
     scales(0);
+    scales(1);
     {
         // the two 128-row scale blocks (gate/up: one of each matrix)
         const float *s1 = MODE == F8_GATEUP ? t.s1 + (int64_t)(n0 >> 7) * nkb
@@ -250,32 +261,47 @@ __global__ __launch_bounds__(512, 1) void fp8_tile_kernel(Fp8Args a)
         // and the stage of block kb - 1 is read by all
         wait_vm<(NS - 2) * (PX + PW)>();
         lds_barrier();
-        if ((kb & (F8_SCW - 1)) == F8_SCW - 2)
-            scales(kb / F8_SCW + 1);   // before the ring loads: their wait covers it
-        issue(kb + NS - 1);
-        if (idle)
+        if (kb && kb % F8_SCW == 0 && (kb / F8_SCW + 1) * F8_SCW < nkb)
+            scales(kb / F8_SCW + 1);   // the window before this one is read by all
+        if (idle) {
+            issue(kb + NS - 1);
             return;
+        }
         const uint8_t *st = smem + (kb % NS) * STAGE;
         auto frag = [&](const uint8_t *r) {
             return join16(*reinterpret_cast<const int4_t *>(r + o0),
                           *reinterpret_cast<const int4_t *>(r + o1));
         };
-        int8_8 x[MF];
+        // in the order of use, so that the first sum waits for the first reads
+        // only
+        constexpr int WD = EX && MF == 4 ? 1 : 2;   // weight fragments read ahead
+        constexpr bool WC = EX && WD == 2;          // and converted one ahead
+        int8_8 x[MF], w[WD + 1];
         half32 xh[MF];
         float sc[MF][2];
         const float *xs = xsc + (kb & (2 * F8_SCW - 1)) * BM + m0 + col;
-        const float wg = wsc[MODE == F8_GATEUP ? kb : wn * nkb + kb];
-        const float wu = MODE == F8_GATEUP ? wsc[nkb + kb] : wg;
+        w[0] = frag(st + XB + wrow(0) * 128);
 #pragma unroll
         for (int m = 0; m < MF; ++m) {
             x[m] = frag(st + (m0 + m * 16 + col) * 128);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        if constexpr (WD == 2)
+            w[1] = frag(st + XB + wrow(1) * 128);
+        const float wg = wsc[MODE == F8_GATEUP ? kb : wn * nkb + kb];
+        const float wu = MODE == F8_GATEUP ? wsc[nkb + kb] : wg;
+        float xv[MF];
+#pragma unroll
+        for (int m = 0; m < MF; ++m)
+            xv[m] = xs[m * 16];
+        __builtin_amdgcn_sched_barrier(0);
+        auto ready = [&](int m) {   // before fragment m's first sum
             if constexpr (decltype(tail)::value)
                 x[m] = f8_cut(x[m], kb, q, K);
             if constexpr (EX)
                 xh[m] = f8_to_f16(x[m]);
-            sc[m][0] = xs[m * 16] * wg;
-            sc[m][1] = MODE == F8_GATEUP ? xs[m * 16] * wu : sc[m][0];
-        }
+        };
+        half32 wh[WC ? 2 : 1];
         float4_t s[4];
         auto add = [&](int i) {
             const int f = i / MF, m = i % MF;
@@ -283,28 +309,44 @@ __global__ __launch_bounds__(512, 1) void fp8_tile_kernel(Fp8Args a)
             for (int j = 0; j < 4; ++j)
                 acc[m][f][j] = __builtin_fmaf(s[i & 3][j], sc[m][f >> 2], acc[m][f][j]);
         };
-        int8_8 w[2];
-        w[0] = frag(st + XB + wrow(0) * 128);
 #pragma unroll
         for (int f = 0; f < 8; ++f) {
-            if (f + 1 < 8)
-                w[(f + 1) & 1] = frag(st + XB + wrow(f + 1) * 128);
-            half32 wh;
+            if (f + WD < 8)
+                w[(f + WD) % (WD + 1)] = frag(st + XB + wrow(f + WD) * 128);
+            // the next block's loads go out over the first four fragments: all
+            // at once they would hold every wave until the address unit had
+            // taken them
+#pragma unroll
+            for (int i = 0; i < PX + PW; ++i)
+                if (i * 4 / (PX + PW) == f)
+                    issue1(kb + NS - 1, i);
             if constexpr (EX)
-                wh = f8_to_f16(w[f & 1]);
+                if (!WC || f == 0)
+                    wh[WC ? f & 1 : 0] = f8_to_f16(w[f % (WD + 1)]);
+            __builtin_amdgcn_s_setprio(1);
 #pragma unroll
             for (int m = 0; m < MF; ++m) {
                 const int i = f * MF + m;
+                if (f == 0)
+                    ready(m);
                 if constexpr (EX)
-                    s[i & 3] = mfma_f16(wh, xh[m]);
+                    s[i & 3] = mfma_f16(wh[WC ? f & 1 : 0], xh[m]);
                 else
-                    s[i & 3] = mfma_f8(w[f & 1], x[m]);
+                    s[i & 3] = mfma_f8(w[f % (WD + 1)], x[m]);
+                if (f == 0) {
+                    sc[m][0] = xv[m] * wg;
+                    sc[m][1] = MODE == F8_GATEUP ? xv[m] * wu : sc[m][0];
+                }
                 if (i >= 2)
                     add(i - 2);
                 // keeps the steps in order: left to itself the scheduler
                 // hoists reads and sums until the registers run out
                 __builtin_amdgcn_sched_barrier(0);
+                if constexpr (WC)
+                    if (m == 0 && f + 1 < 8)
+                        wh[(f + 1) & 1] = f8_to_f16(w[(f + 1) % (WD + 1)]);
             }
+            __builtin_amdgcn_s_setprio(0);
         }
         add(8 * MF - 2);
         add(8 * MF - 1);
@@ -357,18 +399,49 @@ __global__ __launch_bounds__(512, 1) void fp8_tile_kernel(Fp8Args a)
                     *reinterpret_cast<const int4_t *>(ht + r * 128 + c);
         }
     } else {
+        // through LDS, so that rows leave in whole lines (a lane holds four
+        // columns of a row: stored from there, 16 rows by 32 bytes at a time,
+        // the 4096 x 11264 product spent a quarter of its time on them)
         const int dt = MODE == F8_DOWN ? MOE_DTYPE_F16 : a.odt;
-        const bool vec = MODE == F8_DOWN || (a.ldo % 4 == 0 && ((uintptr_t)a.out & 15) == 0);
+        constexpr int es = EX ? 4 : 2;               // EX is the fp32 output
+        constexpr int LR = 256 * es + 16;            // LDS row, off the banks' period
+        constexpr int PASS = EX && MF > 2 ? (MF == 4 ? 2 : 3) : 1;   // parts of the row fragments that fit
+        constexpr int gp = 16 / es;                  // columns of a 16-byte piece
+        const bool vec = (a.ldo * es) % 16 == 0 && ((uintptr_t)a.out & 15) == 0;
 #pragma unroll
-        for (int m = 0; m < MF; ++m) {
-            const int r = m0 + m * 16 + col;
-            if (r >= t.rows)
-                continue;
+        for (int h = 0; h < PASS; ++h) {
+            constexpr int MH = MF / PASS;
+            __syncthreads();   // the ring, or the first half, is read by all
 #pragma unroll
-            for (int f = 0; f < 8; ++f) {
-                const int n = n0 + wn * 128 + f * 16 + q * 4;
-                if (n < a.N)
-                    store4(a.out, dt, (int64_t)(t.row0 + r) * a.ldo + n, acc[m][f], a.N - n, vec);
+            for (int mm = 0; mm < MH; ++mm) {
+                const int m = h * MH + mm;
+                const int r = (wave >> 1) * 16 * MH + mm * 16 + col;
+#pragma unroll
+                for (int f = 0; f < 8; ++f)
+                    store4(smem + r * LR, dt, wn * 128 + f * 16 + q * 4, acc[m][f], 4, true);
+            }
+            __syncthreads();
+            constexpr int np = 256 / gp;   // pieces of a row
+            for (int i = tid; i < 64 * MH * np; i += NTH) {
+                const int lr2 = i / np, c = (i % np) * gp;
+                const int r = (lr2 / (16 * MH)) * 16 * MF + h * 16 * MH + lr2 % (16 * MH);
+                const int n = n0 + c;
+                if (r >= t.rows || n >= a.N)
+                    continue;
+                uint8_t *to = static_cast<uint8_t *>(a.out) + ((t.row0 + r) * a.ldo + n) * es;
+                const uint8_t *from = smem + lr2 * LR + c * es;
+                if (vec && n + gp <= a.N) {
+                    *reinterpret_cast<int4_t *>(to) = *reinterpret_cast<const int4_t *>(from);
+                } else {
+                    for (int j = 0; j < gp && n + j < a.N; ++j) {
+                        if constexpr (EX)
+                            reinterpret_cast<uint32_t *>(to)[j] =
+                                reinterpret_cast<const uint32_t *>(from)[j];
+                        else
+                            reinterpret_cast<uint16_t *>(to)[j] =
+                                reinterpret_cast<const uint16_t *>(from)[j];
+                    }
+                }
             }
         }
     }
@@ -514,6 +587,7 @@ static int launch_tile_mf(const Fp8Args &a, int mf, int64_t items, hipStream_t s
     switch (mf) {
     case 1: return launch_tile<MODE, 1, EX>(a, items, s);
     case 2: return launch_tile<MODE, 2, EX>(a, items, s);
+    case 3: return launch_tile<MODE, 3, EX>(a, items, s);
     default: return launch_tile<MODE, 4, EX>(a, items, s);
     }
 }
