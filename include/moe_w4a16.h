@@ -524,10 +524,12 @@ int moe_router_logits(const void *x_f16, const void *w_router_f16, const float *
  * must hold k experts; ld < E), an unknown dtype, score or flag, a scale that
  * is not finite, null or misaligned pointers; MOE_EUNSUPPORTED for E > 1024,
  * k > 16 or more than 64 groups.  T = 0: no-op.
- * The permute form also writes moe_permute's outputs of topk_idx: in the same
- * launch for at most 16 tokens (with T * E <= 8192), else on ws, a device
- * scratch of moe_route_select_workspace_bytes(T, k, E) bytes (may be 0; no
- * initialisation needed); MOE_ENOMEM if too small.
+ * The permute form also writes moe_permute's outputs of topk_idx, in the same
+ * launch for one token (and up to 16 with T * E <= 8192), in one more up to
+ * 8192 tokens of 768 experts, else by moe_permute's launches.
+ *   ws  device scratch of moe_route_select_workspace_bytes(T, k, E) bytes (may
+ *       be 0; no initialisation needed); MOE_ENOMEM if too small.  Calls that
+ *       share it must not overlap.
  */
 int moe_route_select(const void *logits, int logits_dtype, int64_t ld, const float *select_bias,
                      int T, int E, int k, int score, int n_group, int topk_group, unsigned flags,
@@ -598,7 +600,7 @@ int moe_fp8_blob_layout(int H, int I, int64_t offsets[6], int64_t *total_bytes);
  *          MOE_DTYPE_F16, one slice)
  *   ws     device scratch of the plan's size, 16-byte aligned, no
  *          initialisation; calls that share it must not overlap
- * Rows behind offsets[E] are left as they were.  Regimes: DECODE (T <= 4: two
+ * Rows behind offsets[E] are left as they were.  Regimes: DECODE (T <= 16: two
  * launches over the weights' stream, activations quantised inside them) and
  * BATCHED (any T); AUTO picks by T.  Both give the same sums up to the order
  * of the blocks.  H and I multiples of 64, at most 8192; E <= 1024; k <= 16

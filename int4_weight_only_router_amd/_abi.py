@@ -220,10 +220,28 @@ def _p(t):
     return t.data_ptr()
 
 
+_raw_stream = None
+
+
+def _current_stream():
+    """torch's current stream of the current device as an address.  The raw
+    lookup spares the 2.5 us of building a Stream object, half of a small
+    call's time on the host."""
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        device = torch.cuda.current_device
+        if raw is None:
+            _raw_stream = lambda: torch.cuda.current_stream().cuda_stream   # noqa: E731
+        else:
+            _raw_stream = lambda: raw(device())   # noqa: E731
+    return _raw_stream()
+
+
 def _s(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

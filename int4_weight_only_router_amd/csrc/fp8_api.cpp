@@ -12,21 +12,19 @@ int launch_route_batched_logits(const void *, const void *, const float *, int, 
                                 hipStream_t);
 int launch_route_logits_rows(const void *, const void *, const float *, int, int, int, float *,
                              hipStream_t);
-bool route_select_sorts(int T, int E);
+size_t route_select_ws_bytes(int T, int k, int E);
 int launch_route_select(const void *, int, int64_t, const float *, int, int, int, int, int, int,
                         unsigned, float, int32_t *, float *, int32_t *, int32_t *, int32_t *,
-                        int32_t *, hipStream_t);
-size_t permute_ws_bytes(int T, int k, int E);
-int launch_permute(const int32_t *, int, int, int, int32_t *, int32_t *, int32_t *, int32_t *,
-                   void *, hipStream_t);
+                        int32_t *, void *, hipStream_t);
 int launch_quant_fp8(const void *, int, int64_t, int64_t, int, int, bool, void *, int64_t, float *,
                      hipStream_t);
-int launch_fp8_tiles(const int32_t *, int, int, int32_t *, hipStream_t);
+int launch_fp8_tokens(const void *, int64_t, int, uint8_t *, float *, const int32_t *,
+                      const void *const *, int, int, Fp8TileRec *, hipStream_t);
 int launch_fp8_rows_dense(const Fp8Args &, hipStream_t);
 int launch_fp8_tile_dense(const Fp8Args &, hipStream_t);
 int launch_fp8_decode(Fp8Args, const void *, float *, int, int, const int64_t *, void *,
                       hipStream_t);
-int fp8_pick_rows(int64_t rows, int E);
+int fp8_pick_rows(int64_t rows, int E, int I);
 int64_t fp8_tile_bound(int64_t rows, int E, int bm);
 int launch_fp8_experts(Fp8Args, int, uint8_t *, float *, int, int, const int64_t *, void *,
                        hipStream_t);
@@ -83,7 +81,7 @@ static Fp8Ws fp8_ws(int T, int H, int I, int E, int k, bool decode)
         w.xs = o;    o = al256(o + (int64_t)T * ((H + 127) / 128) * 4);
         w.hq = o;    o = al256(o + n * I);
         w.hs = o;    o = al256(o + n * ((I + 127) / 128) * 4);
-        w.tiles = o; o = al256(o + (2 + 2 * fp8_tile_bound(n, E, fp8_pick_rows(n, E))) * 4);
+        w.tiles = o; o = al256(o + (1 + fp8_tile_bound(n, E, fp8_pick_rows(n, E, I))) * sizeof(Fp8TileRec));
     }
     w.total = o;
     return w;
@@ -166,14 +164,14 @@ int moe_route_select(const void *logits, int logits_dtype, int64_t ld, const flo
         return rc;
     return launch_route_select(logits, logits_dtype, ld, select_bias, T, E, k, score, n_group,
                                topk_group, flags, scale, topk_idx, topk_w, nullptr, nullptr,
-                               nullptr, nullptr, stream);
+                               nullptr, nullptr, nullptr, stream);
 }
 
 size_t moe_route_select_workspace_bytes(int T, int k, int E)
 {
-    if (T < 0 || k <= 0 || E <= 0 || route_select_sorts(T, E))
+    if (T < 0 || k <= 0 || E <= 0)
         return 0;
-    return permute_ws_bytes(T, k, E);
+    return route_select_ws_bytes(T, k, E);
 }
 
 int moe_route_select_permute(const void *logits, int logits_dtype, int64_t ld,
@@ -194,15 +192,11 @@ int moe_route_select_permute(const void *logits, int logits_dtype, int64_t ld,
     const size_t need = moe_route_select_workspace_bytes(T, k, E);
     if (need && (!ws || ws_bytes < need))
         return set_error(MOE_ENOMEM, "%s: workspace %zu < %zu bytes", fn, ws_bytes, need);
-    const bool sorts = route_select_sorts(T, E);
-    if (T > 0) {
-        rc = launch_route_select(logits, logits_dtype, ld, select_bias, T, E, k, score, n_group,
-                                 topk_group, flags, scale, topk_idx, topk_w,
-                                 sorts ? counts : nullptr, offsets, perm, inv_perm, stream);
-        if (rc || sorts)
-            return rc;
-    }
-    return launch_permute(topk_idx, T, k, E, counts, offsets, perm, inv_perm, ws, stream);
+    if (need && (uintptr_t)ws % 4)
+        return set_error(MOE_EINVAL, "%s: misaligned workspace", fn);
+    return launch_route_select(logits, logits_dtype, ld, select_bias, T, E, k, score, n_group,
+                               topk_group, flags, scale, topk_idx, topk_w, counts, offsets, perm,
+                               inv_perm, ws, stream);
 }
 
 int moe_quantize_fp8(const void *x, int dtype, int64_t ldx, int64_t rows, int cols, int block_rows,
@@ -296,9 +290,13 @@ int moe_expert_ffn_w8a8_plan(int T, int H, int I, int E, int k, int regime, int 
         return rc;
     if (regime != MOE_REGIME_AUTO && regime != MOE_REGIME_DECODE && regime != MOE_REGIME_BATCHED)
         return set_error(MOE_EINVAL, "%s: bad regime %d", fn, regime);
+    // decode up to 32 routed rows: its workgroups then stream weights that few
+    // others share (measured: 64 experts, top-8, us decode / batched: 1 token
+    // 16 / 32, 2: 28 / 32, 4: 44 / 36, 6: 57 / 63, 8: 68 / 65; 8 experts,
+    // top-2: 16 tokens 26 / 31)
     const int r = regime != MOE_REGIME_AUTO ? regime
-                  : T <= FP8_DECODE_MAX_T   ? MOE_REGIME_DECODE
-                                            : MOE_REGIME_BATCHED;
+                  : T <= FP8_DECODE_MAX_T && T * k <= 32 ? MOE_REGIME_DECODE
+                                                         : MOE_REGIME_BATCHED;
     if (r == MOE_REGIME_DECODE && T > FP8_DECODE_MAX_T)
         return set_error(MOE_EUNSUPPORTED, "%s: the decode regime takes T <= %d (T=%d)", fn,
                          FP8_DECODE_MAX_T, T);
@@ -342,12 +340,11 @@ int moe_expert_ffn_w8a8(const void *x_f16, const int32_t *perm, const int32_t *o
         return launch_fp8_decode(a, x_f16, reinterpret_cast<float *>(base + w.h), H, I, off, y_f16,
                                  stream);
     const int64_t n = (int64_t)T * k;
-    const int bm = fp8_pick_rows(n, E);
-    int32_t *tiles = reinterpret_cast<int32_t *>(base + w.tiles);
+    const int bm = fp8_pick_rows(n, E, I);
+    Fp8TileRec *tiles = reinterpret_cast<Fp8TileRec *>(base + w.tiles);
     float *xs = reinterpret_cast<float *>(base + w.xs);
-    rc = launch_quant_fp8(x_f16, MOE_DTYPE_F16, H, T, H, 1, true, base + w.xq, H, xs, stream);
-    if (!rc)
-        rc = launch_fp8_tiles(offsets, E, bm, tiles, stream);
+    rc = launch_fp8_tokens(x_f16, T, H, base + w.xq, xs, offsets, d_expert_blobs, E, bm, tiles,
+                           stream);
     if (rc)
         return rc;
     a.x = base + w.xq;

@@ -7,8 +7,8 @@
 // row tile only, so the kernel's task is to have many bytes in flight.  A
 // workgroup owns 32 weight rows (gate/up: 16 gate rows and the same 16 up
 // rows, so that it also forms h) and its four waves take every fourth
-// 128-long block of K each; a wave issues the loads of four blocks (16 KB) at
-// once, before it touches the tokens.  The waves' sums meet in LDS in wave
+// 128-long block of K each; a wave issues the loads of up to four blocks (16 KB)
+// at once, before it touches the tokens.  The waves' sums meet in LDS in wave
 // order, so results do not depend on timing.  The tokens are the matrix
 // core's second operand, 16 to a fragment; its idle columns cost nothing here.
 //
@@ -18,8 +18,6 @@
 #include "k_fp8_frag.h"
 
 namespace moe {
-
-constexpr int F8D_KPD = 4;   // K blocks a wave has in flight
 
 // One row's 128-blocks to e4m3 in LDS by 16-lane groups.
 template <typename XT>
@@ -64,14 +62,19 @@ __device__ __forceinline__ void quant_row_lds(const XT *src, int K, int kb, int 
 // MODE F8_DENSE: grid (32-column tiles, 16*MT-row tiles).  F8_GATEUP /
 // F8_DOWN: grid (tiles of 16 intermediate / 32 output columns, sorted rows);
 // the workgroup at an expert's first row serves its T rows (an expert has at
-// most one row per token), the others leave at once.
-template <int MODE, int MT>
+// most one row per token), the others leave at once.  A wave has KP blocks of
+// K in flight at a time.  Nothing is predicated between a matrix instruction
+// and the use of its result: rows past the end repeat the last one (their
+// columns are not stored), blocks past the end repeat the last one with a
+// weight scale of zero.
+template <int MODE, int MT, int KP>
 __global__ __launch_bounds__(256) void fp8_rows_kernel(Fp8Args a)
 {
     static_assert(MODE == F8_DENSE || MT == 1, "decode experts: one row fragment");
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ __align__(16) float red[4][2 * MT][64][4];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int col = lane & 15, q = lane >> 4;
     const int K = a.K, nkb = (K + 127) / 128;
 
@@ -109,7 +112,7 @@ __global__ __launch_bounds__(256) void fp8_rows_kernel(Fp8Args a)
                             w1 + (int64_t)min(nb, a.N - 1) * ldw};
     s0 += (int64_t)(n0 >> 7) * nkb;
     s1 += (int64_t)((MODE == F8_GATEUP ? n0 : n0 + 16) >> 7) * nkb;
-    const int64_t last = K - 16;   // K is a multiple of 16: the last whole piece of a row
+    const int last = K - 16;   // K is a multiple of 16: the last whole piece of a row
 
     float4_t acc[2][MT];
 #pragma unroll
@@ -118,25 +121,38 @@ __global__ __launch_bounds__(256) void fp8_rows_kernel(Fp8Args a)
         for (int m = 0; m < MT; ++m)
             acc[f][m] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
 
-    uint8_t *xl = smem;                                              // decode: [rows][nkb*128]
-    float *sl = reinterpret_cast<float *>(smem + (size_t)a.T * nkb * 128);   // [rows][nkb]
-
-    for (int kc = 0; kc < nkb; kc += 4 * F8D_KPD) {
-        int4_t wf[F8D_KPD][2][2];
-        float wsc[F8D_KPD][2];
+    uint8_t *xl = smem;                                              // decode: [T][nkb*128]
+    float *sl = reinterpret_cast<float *>(smem + (size_t)a.T * nkb * 128);   // [T][nkb]
+    const uint8_t *xr[MT];
+    const float *xsr[MT];
 #pragma unroll
-        for (int j = 0; j < F8D_KPD; ++j) {
+    for (int m = 0; m < MT; ++m) {
+        const int r = min(m * 16 + col, rows - 1);
+        if constexpr (MODE == F8_DENSE) {
+            xr[m] = a.x + (int64_t)(row0 + r) * a.ldx;
+            xsr[m] = a.xs + (int64_t)(row0 + r) * nkb;
+        } else {
+            xr[m] = xl + r * nkb * 128;
+            xsr[m] = sl + r * nkb;
+        }
+    }
+
+    for (int kc = 0; kc < nkb; kc += 4 * KP) {
+        int4_t wf[KP][2][2];
+        float wsc[KP][2];
+#pragma unroll
+        for (int j = 0; j < KP; ++j) {
             const int kb = min(kc + 4 * j + wave, nkb - 1);
 #pragma unroll
             for (int f = 0; f < 2; ++f) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int64_t at = min((int64_t)kb * 128 + h * 64 + q * 16, last);
-                    wf[j][f][h] = ldg_nt(reinterpret_cast<const int4_t *>(wr[f] + at));
-                }
+                for (int h = 0; h < 2; ++h)
+                    wf[j][f][h] = ldg_nt(reinterpret_cast<const int4_t *>(
+                        wr[f] + min(kb * 128 + h * 64 + q * 16, last)));
             }
-            wsc[j][0] = s0[kb];
-            wsc[j][1] = s1[kb];
+            const bool in = kc + 4 * j + wave < nkb;
+            wsc[j][0] = in ? s0[kb] : 0.0f;
+            wsc[j][1] = in ? s1[kb] : 0.0f;
         }
         if constexpr (MODE != F8_DENSE) {
             if (kc == 0) {   // quantise this expert's rows while the weights arrive
@@ -156,35 +172,29 @@ __global__ __launch_bounds__(256) void fp8_rows_kernel(Fp8Args a)
             }
         }
 #pragma unroll
-        for (int j = 0; j < F8D_KPD; ++j) {
-            const int kb = kc + 4 * j + wave;
-            if (kb >= nkb)
-                break;
+        for (int j = 0; j < KP; ++j) {
+            const int kb = min(kc + 4 * j + wave, nkb - 1);
+            const int c0 = kb * 128 + q * 16;
             half32 wh[2];
 #pragma unroll
             for (int f = 0; f < 2; ++f)
                 wh[f] = f8_to_f16(join16(wf[j][f][0], wf[j][f][1]));
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
-                int4_t x0 = {0, 0, 0, 0}, x1 = {0, 0, 0, 0};
-                float xs = 0.0f;
-                const int r = m * 16 + col;
-                const int c0 = kb * 128 + q * 16;
-                if (r < rows) {   // rows and bytes past the end count as zeros
-                    if constexpr (MODE == F8_DENSE) {
-                        const uint8_t *xr = a.x + (int64_t)(row0 + r) * a.ldx;
-                        if (c0 < K)
-                            x0 = ldg(reinterpret_cast<const int4_t *>(xr + c0));
-                        if (c0 + 64 < K)
-                            x1 = ldg(reinterpret_cast<const int4_t *>(xr + c0 + 64));
-                        xs = a.xs[(int64_t)(row0 + r) * nkb + kb];
-                    } else {
-                        const uint8_t *xr = xl + (size_t)r * nkb * 128;
-                        x0 = *reinterpret_cast<const int4_t *>(xr + c0);
-                        x1 = *reinterpret_cast<const int4_t *>(xr + c0 + 64);
-                        xs = sl[r * nkb + kb];
+                int4_t x0, x1;
+                if constexpr (MODE == F8_DENSE) {
+                    x0 = ldg(reinterpret_cast<const int4_t *>(xr[m] + min(c0, last)));
+                    x1 = ldg(reinterpret_cast<const int4_t *>(xr[m] + min(c0 + 64, last)));
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {   // bytes past K count as zeros
+                        x0[i] = c0 < K ? x0[i] : 0;
+                        x1[i] = c0 + 64 < K ? x1[i] : 0;
                     }
+                } else {   // zero-filled to whole blocks
+                    x0 = *reinterpret_cast<const int4_t *>(xr[m] + c0);
+                    x1 = *reinterpret_cast<const int4_t *>(xr[m] + c0 + 64);
                 }
+                const float xs = xsr[m][kb];
                 const half32 xf = f8_to_f16(join16(x0, x1));
 #pragma unroll
                 for (int f = 0; f < 2; ++f) {
@@ -235,19 +245,19 @@ __global__ __launch_bounds__(256) void fp8_rows_kernel(Fp8Args a)
     }
 }
 
-template <int MODE, int MT>
+template <int MODE, int MT, int KP>
 static int launch_rows(const Fp8Args &a, dim3 grid, size_t lds, hipStream_t s)
 {
     if (lds) {
         static bool attr_set = false;   // raising the LDS limit is idempotent
         if (!attr_set) {
-            MOE_HIP_TRY(hipFuncSetAttribute((const void *)fp8_rows_kernel<MODE, MT>,
+            MOE_HIP_TRY(hipFuncSetAttribute((const void *)fp8_rows_kernel<MODE, MT, KP>,
                                             hipFuncAttributeMaxDynamicSharedMemorySize,
                                             FP8_DECODE_MAX_T * 64 * (128 + 4)));
             attr_set = true;
         }
     }
-    hipLaunchKernelGGL((fp8_rows_kernel<MODE, MT>), grid, dim3(256), lds, s, a);
+    hipLaunchKernelGGL((fp8_rows_kernel<MODE, MT, KP>), grid, dim3(256), lds, s, a);
     MOE_LAUNCH_CHECK("fp8_rows_kernel");
     return MOE_OK;
 }
@@ -257,10 +267,23 @@ int launch_fp8_rows_dense(const Fp8Args &a, hipStream_t s)
 {
     const unsigned nt = (unsigned)((a.N + 31) / 32);
     if (a.M <= 16)
-        return launch_rows<F8_DENSE, 1>(a, dim3(nt, 1), 0, s);
+        return launch_rows<F8_DENSE, 1, 4>(a, dim3(nt, 1), 0, s);
     if (a.M <= 32)
-        return launch_rows<F8_DENSE, 2>(a, dim3(nt, 1), 0, s);
-    return launch_rows<F8_DENSE, 4>(a, dim3(nt, (unsigned)((a.M + 63) / 64)), 0, s);
+        return launch_rows<F8_DENSE, 2, 4>(a, dim3(nt, 1), 0, s);
+    return launch_rows<F8_DENSE, 4, 4>(a, dim3(nt, (unsigned)((a.M + 63) / 64)), 0, s);
+}
+
+// The fewest blocks in flight that cover K in one round, at most four: a round
+// past the end re-reads the last block.
+template <int MODE>
+static int launch_rows_kp(const Fp8Args &a, dim3 grid, size_t lds, hipStream_t s)
+{
+    switch ((a.K + 511) / 512) {
+    case 1: return launch_rows<MODE, 1, 1>(a, grid, lds, s);
+    case 2: return launch_rows<MODE, 1, 2>(a, grid, lds, s);
+    case 3: return launch_rows<MODE, 1, 3>(a, grid, lds, s);
+    default: return launch_rows<MODE, 1, 4>(a, grid, lds, s);
+    }
 }
 
 // Decode experts: gate/up with SwiGLU into fp32 h, then down.
@@ -277,7 +300,7 @@ int launch_fp8_decode(Fp8Args a, const void *x_f16, float *h, int H, int I, cons
     a.off_s0 = off[3];
     a.off_s1 = off[4];
     const unsigned n = (unsigned)(a.T * a.k);
-    const int rc = launch_rows<F8_GATEUP, 1>(a, dim3((I + 15) / 16, n), lds(H), s);
+    const int rc = launch_rows_kp<F8_GATEUP>(a, dim3((I + 15) / 16, n), lds(H), s);
     if (rc)
         return rc;
     a.src = h;
@@ -287,7 +310,7 @@ int launch_fp8_decode(Fp8Args a, const void *x_f16, float *h, int H, int I, cons
     a.ldo = H;
     a.off_w0 = a.off_w1 = off[2];
     a.off_s0 = a.off_s1 = off[5];
-    return launch_rows<F8_DOWN, 1>(a, dim3((H + 31) / 32, n), lds(I), s);
+    return launch_rows_kp<F8_DOWN>(a, dim3((H + 31) / 32, n), lds(I), s);
 }
 
 }  // namespace moe

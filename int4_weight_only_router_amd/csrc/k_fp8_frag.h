@@ -105,7 +105,14 @@ __device__ __forceinline__ float row16_max(float a)
 }
 
 enum { F8_DENSE = 0, F8_GATEUP = 1, F8_DOWN = 2 };
-constexpr int FP8_DECODE_MAX_T = 4;   // routed experts: decode kernels up to this many tokens
+constexpr int FP8_DECODE_MAX_T = 16;   // routed experts: decode kernels up to this many tokens
+
+// One row tile of the routed experts: its expert's blob, first sorted row and
+// rows.  Entry 0 of a table holds the number of tiles in `rows`.
+struct Fp8TileRec {
+    const uint8_t *blob;
+    int32_t row0, rows;
+};
 
 struct Fp8Args {
     // tokens: e4m3 rows of ldx bytes and their scales, xkb per row
@@ -120,7 +127,7 @@ struct Fp8Args {
     const void *const *blobs;
     int64_t off_w0, off_w1, off_s0, off_s1;
     const int32_t *offsets, *perm;
-    const int32_t *tiles;   // [0] count, then (expert, first sorted row) from [2]
+    const Fp8TileRec *tiles;
     const void *src;        // decode: fp16 tokens (gate/up) or fp32 h (down)
     int E, k, T;
     int M, N, K;            // rows, output columns (gate/up: I), contraction length

@@ -33,10 +33,6 @@
 // fragments; each sum enters its accumulator by one fma two sums later.  The
 // fma's run in the shadow of the matrix pipe.
 //
-// fp8_rows16_kernel: at most 16 rows to a tile, where the weights' stream from
-// memory is the bound: four waves of 64 weight rows each, everything straight
-// to registers one block ahead, no barrier.
-//
 // gate/up: the 256 weight rows are 128 gate rows and the same 128 up rows (a
 // wave holds as many of each), so a workgroup forms 128 columns of h, exactly
 // one scale block: h's largest magnitudes meet in LDS, h is quantised with a
@@ -85,12 +81,12 @@ __device__ __forceinline__ bool f8_tile(const Fp8Args &a, int mt, F8Tile &t)
         t.row0 = mt * BM;
         t.rows = min(BM, a.M - t.row0);
     } else {
-        const int e = a.tiles[2 + 2 * mt];
-        t.row0 = a.tiles[3 + 2 * mt];
-        t.rows = min(BM, a.offsets[e + 1] - t.row0);
-        const uint8_t *blob = static_cast<const uint8_t *>(a.blobs[e]);
+        const Fp8TileRec r = a.tiles[1 + mt];
+        const uint8_t *blob = r.blob;
         if (!blob)
             return false;
+        t.row0 = r.row0;
+        t.rows = r.rows;
         t.w0 = blob + a.off_w0;
         t.w1 = blob + a.off_w1;
         t.s0 = reinterpret_cast<const float *>(blob + a.off_s0);
@@ -105,24 +101,6 @@ __device__ __forceinline__ int64_t f8_xrow(const Fp8Args &a, const F8Tile &t, in
 {
     const int p = t.row0 + min(r, t.rows - 1);
     return MODE == F8_GATEUP ? a.perm[p] / a.k : p;
-}
-
-// Blocks 0..nkb-1, two per round so that buffers have fixed names; the last
-// one apart (true_type), where K may end inside it.
-template <typename F>
-__device__ __forceinline__ void f8_blocks(int nkb, F &&body)
-{
-    int kb = 0;
-    for (; kb + 2 < nkb; kb += 2) {
-        body(kb, 0, std::false_type());
-        body(kb + 1, 1, std::false_type());
-    }
-    if (kb + 1 < nkb) {
-        body(kb, 0, std::false_type());
-        body(kb + 1, 1, std::true_type());
-    } else {
-        body(kb, 0, std::true_type());
-    }
 }
 
 // Bytes of the last block past K count as zeros on the rows' side (the
@@ -170,7 +148,7 @@ __global__ __launch_bounds__(512, 1) void fp8_tile_kernel(Fp8Args a)
     const int K = a.K, nkb = (K + 127) / 128;
 
     const int NT = MODE == F8_GATEUP ? (a.N + 127) / 128 : (a.N + 255) / 256;
-    const int MT = MODE == F8_DENSE ? (a.M + BM - 1) / BM : a.tiles[0];
+    const int MT = MODE == F8_DENSE ? (a.M + BM - 1) / BM : a.tiles[0].rows;
     F8Item it;
     F8Tile t;
     if (!f8_item<MODE>(MT, NT, it) || !f8_tile<MODE, BM>(a, it.mt, t))
@@ -447,112 +425,6 @@ __global__ __launch_bounds__(512, 1) void fp8_tile_kernel(Fp8Args a)
     }
 }
 
-// At most 16 rows to a tile; four waves of 64 weight rows (gate/up: 32 + 32).
-template <int MODE>
-__global__ __launch_bounds__(256, 2) void fp8_rows16_kernel(Fp8Args a)
-{
-    constexpr int BM = 16;
-    __shared__ __align__(16) uint8_t ht[BM * 128];   // gate/up: h
-    __shared__ float mx[4][BM];
-    const int tid = threadIdx.x;
-    const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int col = lane & 15, q = lane >> 4;
-    const int K = a.K, nkb = (K + 127) / 128;
-    const int NT = MODE == F8_GATEUP ? (a.N + 127) / 128 : (a.N + 255) / 256;
-    F8Item it;
-    F8Tile t;
-    if (!f8_item<MODE>(a.tiles[0], NT, it) || !f8_tile<MODE, BM>(a, it.mt, t))
-        return;
-    const int nw = MODE == F8_GATEUP ? it.nt * 128 + wave * 32 : it.nt * 256 + wave * 64;
-    const int nb = min(nw, a.N - 1);
-    const uint8_t *wb0 = t.w0 + (int64_t)nb * K, *wb1 = t.w1 + (int64_t)nb * K;
-    int wo[4];   // lane offsets of the fragments' rows
-#pragma unroll
-    for (int f = 0; f < 4; ++f)
-        wo[f] = (min(nw + (MODE == F8_GATEUP ? f & 1 : f) * 16 + col, a.N - 1) - nb) * K;
-    const float *s0 = t.s0 + (int64_t)(nb >> 7) * nkb, *s1 = t.s1 + (int64_t)(nb >> 7) * nkb;
-    const int64_t r = f8_xrow<MODE>(a, t, col);
-    const uint8_t *xr = a.x + r * a.ldx;
-    const float *xsr = a.xs + r * nkb;
-
-    int4_t wf[2][4][2], xf[2][2];
-    float wsc[2][2], xs[2];
-    auto load = [&](int kb, int b) {   // past the end re-reads the last block
-        kb = min(kb, nkb - 1);
-        const int o0 = min(kb * 128 + q * 16, K - 16), o1 = min(kb * 128 + 64 + q * 16, K - 16);
-#pragma unroll
-        for (int f = 0; f < 4; ++f) {
-            const uint8_t *base = MODE == F8_GATEUP && f >= 2 ? wb1 : wb0;
-            wf[b][f][0] = ldg(reinterpret_cast<const int4_t *>(base + (unsigned)(wo[f] + o0)));
-            wf[b][f][1] = ldg(reinterpret_cast<const int4_t *>(base + (unsigned)(wo[f] + o1)));
-        }
-        xf[b][0] = ldg(reinterpret_cast<const int4_t *>(xr + o0));
-        xf[b][1] = ldg(reinterpret_cast<const int4_t *>(xr + o1));
-        wsc[b][0] = s0[kb];
-        wsc[b][1] = MODE == F8_GATEUP ? s1[kb] : 0.0f;
-        xs[b] = xsr[kb];
-    };
-    float4_t acc[4];
-#pragma unroll
-    for (int f = 0; f < 4; ++f)
-        acc[f] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
-    load(0, 0);
-    f8_blocks(nkb, [&](int kb, int b, auto tail) {
-        load(kb + 1, b ^ 1);
-        int8_8 x = join16(xf[b][0], xf[b][1]);
-        if constexpr (decltype(tail)::value)
-            x = f8_cut(x, kb, q, K);
-        const half32 xh = f8_to_f16(x);
-#pragma unroll
-        for (int f = 0; f < 4; ++f) {
-            const float4_t s = mfma_f16(f8_to_f16(join16(wf[b][f][0], wf[b][f][1])), xh);
-            const float c = xs[b] * (MODE == F8_GATEUP && f >= 2 ? wsc[b][1] : wsc[b][0]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                acc[f][i] = __builtin_fmaf(s[i], c, acc[f][i]);
-        }
-    });
-    if constexpr (MODE == F8_GATEUP) {
-        float top = 0.0f;
-#pragma unroll
-        for (int f = 0; f < 2; ++f)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float h = nw < a.N ? swiglu_fast(acc[f][i], acc[2 + f][i]) : 0.0f;
-                acc[f][i] = h;
-                top = fmaxf(top, fabsf(h));
-            }
-        top = fmaxf(top, __shfl_xor(top, 16, 64));
-        top = fmaxf(top, __shfl_xor(top, 32, 64));
-        if (q == 0)
-            mx[wave][col] = top;
-        __syncthreads();
-        const float sc = fp8_scale(fmaxf(fmaxf(mx[0][col], mx[1][col]), fmaxf(mx[2][col], mx[3][col])),
-                                   true);
-        const float inv = fp8_inv_pow2(sc);
-#pragma unroll
-        for (int f = 0; f < 2; ++f)
-            *reinterpret_cast<int *>(ht + col * 128 + wave * 32 + f * 16 + q * 4) =
-                fp8_pack4(acc[f][0] * inv, acc[f][1] * inv, acc[f][2] * inv, acc[f][3] * inv);
-        if (tid < t.rows)   // wave 0, q = 0: lane = row
-            a.hs[(int64_t)(t.row0 + tid) * NT + it.nt] = sc;
-        __syncthreads();
-        const int rr = tid >> 3, c = (tid & 7) * 16;
-        if (rr < t.rows && it.nt * 128 + c < a.N)
-            *reinterpret_cast<int4_t *>(static_cast<uint8_t *>(a.out) +
-                                        (int64_t)(t.row0 + rr) * a.N + it.nt * 128 + c) =
-                *reinterpret_cast<const int4_t *>(ht + rr * 128 + c);
-    } else if (col < t.rows) {
-#pragma unroll
-        for (int f = 0; f < 4; ++f) {
-            const int n = nw + f * 16 + q * 4;
-            if (n < a.N)
-                store4(a.out, MOE_DTYPE_F16, (int64_t)(t.row0 + col) * a.ldo + n, acc[f], a.N - n,
-                       true);
-        }
-    }
-}
-
 static int f8_grid(int64_t items, unsigned *grid)
 {
     const int64_t g = (items + F8_NXCD - 1) / F8_NXCD * F8_NXCD;
@@ -587,37 +459,33 @@ static int launch_tile_mf(const Fp8Args &a, int mf, int64_t items, hipStream_t s
     switch (mf) {
     case 1: return launch_tile<MODE, 1, EX>(a, items, s);
     case 2: return launch_tile<MODE, 2, EX>(a, items, s);
-    case 3: return launch_tile<MODE, 3, EX>(a, items, s);
-    default: return launch_tile<MODE, 4, EX>(a, items, s);
+    default: return launch_tile<MODE, 3, EX>(a, items, s);
     }
-}
-
-template <int MODE>
-static int launch_rows16(const Fp8Args &a, int64_t items, hipStream_t s)
-{
-    unsigned grid;
-    const int rc = f8_grid(items, &grid);
-    if (rc)
-        return rc;
-    hipLaunchKernelGGL((fp8_rows16_kernel<MODE>), dim3(grid), dim3(256), 0, s, a);
-    MOE_LAUNCH_CHECK("fp8_rows16_kernel");
-    return MOE_OK;
 }
 
 int launch_fp8_tile_dense(const Fp8Args &a, hipStream_t s)
 {
-    const int mf = 4;
+    constexpr int mf = 4;
     const int64_t items = (int64_t)((a.M + 64 * mf - 1) / (64 * mf)) * ((a.N + 255) / 256);
     if (a.odt == MOE_DTYPE_F32)
-        return launch_tile_mf<F8_DENSE, true>(a, mf, items, s);
-    return launch_tile_mf<F8_DENSE, false>(a, mf, items, s);
+        return launch_tile<F8_DENSE, mf, true>(a, items, s);
+    return launch_tile<F8_DENSE, mf, false>(a, items, s);
 }
 
-// Rows of a row tile from the mean rows of an expert: 16, 64, 128 or 256.
-int fp8_pick_rows(int64_t rows, int E)
+// Rows of a row tile, 64, 128 or 192, from the mean rows of an expert; fewer
+// where that leaves under half the compute units a tile.  Measured (us, H =
+// 2048; 64 / 128 / 192 rows): 64 experts of I = 1024, top-8, at 64 tokens 91 /
+// 97 / 110, at 256: 97 / 101 / 115, at 512: 126 / 116 / 121, at 1024: 203 /
+// 167 / 150, at 4096: 617 / 448 / 389; 8 experts, top-2, at 256: 43 / 52 / 49,
+// at 1024: 79 / 57 / 68, at 4096: 184 / 153 / 130.  (256-row tiles lost
+// everywhere: the registers of the fp16 form do not suffice.)
+int fp8_pick_rows(int64_t rows, int E, int I)
 {
     const int64_t avg = rows / std::max<int64_t>(1, std::min<int64_t>(E, rows));
-    return avg <= 16 ? 16 : avg <= 48 ? 64 : avg <= 96 ? 128 : 256;
+    int bm = avg <= 32 ? 64 : avg <= 96 ? 128 : 192;
+    while (bm > 64 && (rows + bm - 1) / bm * ((I + 127) / 128) < 128)
+        bm -= 64;
+    return bm;
 }
 
 // Upper bound of row tiles: every expert adds at most one partial tile.
@@ -641,8 +509,7 @@ int launch_fp8_experts(Fp8Args a, int bm, uint8_t *hq, float *hs, int H, int I,
     a.off_s0 = off[3];
     a.off_s1 = off[4];
     int64_t items = bound * ((I + 127) / 128);
-    const int rc = bm == 16 ? launch_rows16<F8_GATEUP>(a, items, s)
-                            : launch_tile_mf<F8_GATEUP, true>(a, bm / 64, items, s);
+    const int rc = launch_tile_mf<F8_GATEUP, true>(a, bm / 64, items, s);
     if (rc)
         return rc;
     a.x = hq;
@@ -655,8 +522,7 @@ int launch_fp8_experts(Fp8Args a, int bm, uint8_t *hq, float *hs, int H, int I,
     a.off_w0 = off[2];
     a.off_s0 = off[5];
     items = bound * ((H + 255) / 256);
-    return bm == 16 ? launch_rows16<F8_DOWN>(a, items, s)
-                    : launch_tile_mf<F8_DOWN, false>(a, bm / 64, items, s);
+    return launch_tile_mf<F8_DOWN, false>(a, bm / 64, items, s);
 }
 
 }  // namespace moe

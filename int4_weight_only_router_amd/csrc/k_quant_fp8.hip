@@ -187,40 +187,78 @@ int launch_quant_fp8(const void *x, int dtype, int64_t ldx, int64_t rows, int co
                           scales, s);
 }
 
-// Row tiles of the routed experts: tiles[0] = count, then (expert, first
-// sorted row) pairs from tiles[2], experts in order.  One workgroup; E <= 1024.
-__global__ __launch_bounds__(1024) void fp8_tiles_kernel(const int32_t *__restrict__ offsets,
-                                                         int E, int bm, int32_t *__restrict__ tiles)
+// Before the routed experts' tile kernels, in one launch: the tokens to e4m3
+// (power-of-two scales; cols a multiple of 64), and in the last workgroup the
+// table of row tiles of at most bm rows, experts in order.  E <= 1024.
+__global__ __launch_bounds__(256) void fp8_tokens_kernel(
+    const f16 *__restrict__ x, int64_t rows, int cols, uint8_t *__restrict__ q,
+    float *__restrict__ scales, const int32_t *__restrict__ offsets,
+    const void *const *__restrict__ blobs, int E, int bm, Fp8TileRec *__restrict__ tiles)
 {
-    __shared__ int wsum[16];
-    const int e = threadIdx.x, lane = e & 63, wave = e >> 6;
-    const int o = e < E ? offsets[e] : 0;
-    const int c = e < E ? (offsets[e + 1] - o + bm - 1) / bm : 0;
-    int incl = c;
+    if (blockIdx.x == gridDim.x - 1) {
+        __shared__ int wsum[4];
+        const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+        int o[5], c[4], n = 0;   // thread t: experts 4t..4t+3
 #pragma unroll
-    for (int st = 1; st < 64; st <<= 1) {
-        const int v = __shfl_up(incl, st, 64);
-        if (lane >= st)
-            incl += v;
+        for (int i = 0; i < 5; ++i)
+            o[i] = offsets[min((int)threadIdx.x * 4 + i, E)];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            c[i] = (o[i + 1] - o[i] + bm - 1) / bm;
+            n += c[i];
+        }
+        int incl = n;
+#pragma unroll
+        for (int st = 1; st < 64; st <<= 1) {
+            const int v = __shfl_up(incl, st, 64);
+            if (lane >= st)
+                incl += v;
+        }
+        if (lane == 63)
+            wsum[wave] = incl;
+        __syncthreads();
+        int at = incl - n;
+        for (int i = 0; i < wave; ++i)
+            at += wsum[i];
+        if (threadIdx.x == 255)
+            tiles[0] = Fp8TileRec{nullptr, 0, at + n};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (!c[i])
+                continue;
+            const uint8_t *b = static_cast<const uint8_t *>(blobs[threadIdx.x * 4 + i]);
+            for (int j = 0; j < c[i]; ++j)
+                tiles[1 + at++] =
+                    Fp8TileRec{b, o[i] + j * bm, min(bm, o[i + 1] - o[i] - j * bm)};
+        }
+        return;
     }
-    if (lane == 63)
-        wsum[wave] = incl;
-    __syncthreads();
-    int at = incl - c;
-    for (int i = 0; i < wave; ++i)
-        at += wsum[i];
-    for (int i = 0; i < c; ++i) {
-        tiles[2 + 2 * (at + i)] = e;
-        tiles[3 + 2 * (at + i)] = o + i * bm;
-    }
-    if (e == 1023)
-        tiles[0] = at + c;
+    const int nb = (cols + 127) / 128;
+    const int64_t b = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> 4;
+    if (b >= rows * nb)
+        return;
+    const int64_t r = b / nb;
+    const int kb = (int)(b - r * nb);
+    const int c = kb * 128 + (threadIdx.x & 15) * 8;
+    float v[8];
+    load8<f16, true>(x + r * cols, c, cols, v);
+    const float s = fp8_scale(row16_max(max8(v)), true);
+    if ((threadIdx.x & 15) == 0)
+        scales[b] = s;
+    store8(q + r * cols, c, cols, v, s, true, true);
 }
 
-int launch_fp8_tiles(const int32_t *offsets, int E, int bm, int32_t *tiles, hipStream_t s)
+int launch_fp8_tokens(const void *x, int64_t rows, int cols, uint8_t *q, float *scales,
+                      const int32_t *offsets, const void *const *blobs, int E, int bm,
+                      Fp8TileRec *tiles, hipStream_t s)
 {
-    hipLaunchKernelGGL(fp8_tiles_kernel, dim3(1), dim3(1024), 0, s, offsets, E, bm, tiles);
-    MOE_LAUNCH_CHECK("fp8_tiles_kernel");
+    const int64_t grid = (rows * ((cols + 127) / 128) + 15) / 16 + 1;
+    if (grid > 0x7fffffffLL)
+        return set_error(MOE_EUNSUPPORTED, "FP8 experts: more than 2^31 - 1 workgroups");
+    hipLaunchKernelGGL(fp8_tokens_kernel, dim3((unsigned)grid), dim3(256), 0, s,
+                       static_cast<const f16 *>(x), rows, cols, q, scales, offsets, blobs, E, bm,
+                       tiles);
+    MOE_LAUNCH_CHECK("fp8_tokens_kernel");
     return MOE_OK;
 }
 

@@ -12,18 +12,25 @@
 // expert of the kept groups.  Scores, choices and group scores are held in
 // fp64: two experts then rank as their exact scores do except within about
 // 1e-15 of each other, and the choice does not depend on the order in which a
-// softmax sum is formed.  An fp64 exp costs about 40 vector instructions,
-// small beside the selection; measured with the rest below.
+// softmax sum is formed.  exp and the reciprocal are written out for the range
+// that occurs (20 and 6 fp64 instructions, at the full vector rate).
 //
 // One wave owns a token.  Lane l holds experts l*NV .. l*NV+NV-1 as 64-bit
 // keys whose unsigned order is the order of the choices (0: not selectable,
 // 1: masked), so a lower lane always holds lower indices.  Selection:
-//  1. each lane's largest key is ranked among the 64 lanes by counting larger
-//     ones; the k-th largest of them is a lower bound of the k-th largest key;
+//  1. the lanes' largest keys, cut to their high words, are ranked among the
+//     64 lanes by counting larger ones; the k-th largest is a lower bound of
+//     the k-th largest key;
 //  2. the keys not below that bound (k plus a few) are compacted, one per
-//     lane, and ranked by counting; ranks below k are the answer, in order.
+//     lane, and ranked in full by counting; ranks below k are the answer, in
+//     order.
 // More than 64 candidates (long ties, few lanes in the kept groups) take k
 // rounds of a wave-wide maximum instead.
+//
+// The grouping by expert follows in the same launch for a few tokens.  For
+// more, a workgroup selects for 16 tokens and leaves how often it chose each
+// expert; in a second launch each workgroup adds up what the others left (its
+// own start in every expert's run) and places its elements, without atomics.
 #include "k_sort_common.h"
 
 namespace moe {
@@ -31,10 +38,18 @@ namespace moe {
 constexpr int RS_WAVES = 4;          // waves (tokens) per workgroup
 constexpr int RSP_MAX_T = 16;        // one-workgroup select + sort up to this T
 constexpr int RSP_MAX_KEYS = 8192;   // and up to this T*E: 64 KB of keys beside 34 KB of scratch
+constexpr int RSC_WAVES = 16;        // chunked form: waves per workgroup,
+constexpr int RSC_TOK = 16;          // tokens of a chunk,
+constexpr int RSC_MAX_T = 8192;      // tokens up to which it is used,
+constexpr size_t RSC_KEY_BYTES = 96 * 1024;   // LDS for group keys beside its scratch
+
+size_t permute_ws_bytes(int T, int k, int E);
+int launch_permute(const int32_t *, int, int, int, int32_t *, int32_t *, int32_t *, int32_t *,
+                   void *, hipStream_t);
 
 // Per-wave LDS of the selection.
 struct SelScratch {
-    uint64_t key[64];
+    uint32_t key[64];
     double score[64];
     uint64_t ckey[64];
     int cidx[64];
@@ -67,9 +82,80 @@ __device__ __forceinline__ double key_choice(uint64_t k)
     return __builtin_bit_cast(double, b);
 }
 
-__device__ __forceinline__ double shfl_xor_f64(double v, int m)
+// exp(x) for x <= 709 (0 below -745): x = n ln 2 + r, |r| <= ln 2 / 2, Taylor
+// to r^13 (next term 4e-18).
+__device__ __forceinline__ double exp_f64(double x)
 {
-    return __shfl_xor(v, m, 64);
+    x = fmax(x, -746.0);
+    const double n = __builtin_rint(x * 1.4426950408889634074);
+    double r = __builtin_fma(n, -6.93147180369123816490e-01, x);
+    r = __builtin_fma(n, -1.90821492927058770002e-10, r);
+    double p = 1.0 / 6227020800.0;
+    p = __builtin_fma(p, r, 1.0 / 479001600.0);
+    p = __builtin_fma(p, r, 1.0 / 39916800.0);
+    p = __builtin_fma(p, r, 1.0 / 3628800.0);
+    p = __builtin_fma(p, r, 1.0 / 362880.0);
+    p = __builtin_fma(p, r, 1.0 / 40320.0);
+    p = __builtin_fma(p, r, 1.0 / 5040.0);
+    p = __builtin_fma(p, r, 1.0 / 720.0);
+    p = __builtin_fma(p, r, 1.0 / 120.0);
+    p = __builtin_fma(p, r, 1.0 / 24.0);
+    p = __builtin_fma(p, r, 1.0 / 6.0);
+    p = __builtin_fma(p, r, 0.5);
+    p = __builtin_fma(p, r, 1.0);
+    p = __builtin_fma(p, r, 1.0);
+    return __builtin_amdgcn_ldexp(p, (int)n);
+}
+
+// 1 / x for 1 <= x < 2^1000: the hardware's estimate and two Newton steps.
+__device__ __forceinline__ double rcp_f64(double x)
+{
+    double y = __builtin_amdgcn_rcp(x);
+    y = __builtin_fma(__builtin_fma(-x, y, 1.0), y, y);
+    return __builtin_fma(__builtin_fma(-x, y, 1.0), y, y);
+}
+
+// Wave-wide fp64 sum and fp32 maximum in a fixed order, without LDS: steps
+// inside the 16-lane rows, then the four rows by reading their lanes.
+template <int CTRL>
+__device__ __forceinline__ double dpp_f64(double a)
+{
+    const uint64_t u = __builtin_bit_cast(uint64_t, a);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, 0xF, 0xF, false);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, 0xF, 0xF, false);
+    return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+__device__ __forceinline__ double readlane_f64(double a, int l)
+{
+    const uint64_t u = __builtin_bit_cast(uint64_t, a);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, l);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), l);
+    return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+__device__ __forceinline__ double wave_sum_f64(double a)
+{
+    a += dpp_f64<0xB1>(a);
+    a += dpp_f64<0x4E>(a);
+    a += dpp_f64<0x141>(a);
+    a += dpp_f64<0x140>(a);
+    return (readlane_f64(a, 0) + readlane_f64(a, 16)) + (readlane_f64(a, 32) + readlane_f64(a, 48));
+}
+__device__ __forceinline__ float wave_max_f32(float a)
+{
+#define MOE_MAX_STEP(C)                                                                       \
+    a = fmaxf(a, __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(                       \
+                     0, __builtin_bit_cast(int, a), C, 0xF, 0xF, false)))
+    MOE_MAX_STEP(0xB1);
+    MOE_MAX_STEP(0x4E);
+    MOE_MAX_STEP(0x141);
+    MOE_MAX_STEP(0x140);
+#undef MOE_MAX_STEP
+    float m = a;
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+        m = fmaxf(m, __builtin_bit_cast(
+                         float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, a), 16 * r)));
+    return m;
 }
 
 __device__ __forceinline__ uint64_t readlane_u64(uint64_t v, int l)
@@ -111,24 +197,51 @@ __device__ __forceinline__ uint64_t group_key(Top2 t, bool top2)
     return choice_key(key_choice(t.a) + key_choice(t.b), false);
 }
 
+// What one token's selection left for its grouping: lane's rank (>= k: none).
+struct SelOut {
+    int rank, e;
+};
+
 // Selection of token t by one wave.  gk: LDS of E keys, only read when the
 // groups do not fall on whole power-of-two runs of lanes.  sidx (LDS) also
 // receives the chosen experts when given.
 template <int NV, typename LT>
-__device__ __forceinline__ void select_token(const SelArgs &a, int t, int lane, SelScratch *sc,
+__device__ __forceinline__ SelOut select_token(const SelArgs &a, int t, int lane, SelScratch *sc,
                                              uint64_t *gk, int *sidx)
 {
     const LT *row = static_cast<const LT *>(a.logits) + (int64_t)t * a.ld;
     const int e0 = lane * NV;
     const int E = a.E, k = a.k;
-    float l[NV];
+    float l[NV], b[NV];
+    // a full row of 64 NV experts in 16-byte loads where it is aligned, else
+    // one by one (past the end the last expert's, then masked: nothing is
+    // predicated)
+    constexpr int VW = 16 / (int)sizeof(LT);
+    if (NV % VW == 0 && E == 64 * NV && ((uintptr_t)row & 15) == 0) {
+        typedef LT lvec __attribute__((ext_vector_type(VW)));
+#pragma unroll
+        for (int i = 0; i < NV / VW; ++i) {
+            const lvec v = *reinterpret_cast<const lvec *>(row + e0 + i * VW);
+#pragma unroll
+            for (int j = 0; j < VW; ++j)
+                l[(i * VW + j) % NV] = logit_f32<LT>(v[j]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            l[i] = logit_f32<LT>(row[min(e0 + i, E - 1)]);
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            l[i] = e0 + i < E ? l[i] : -__builtin_inff();
+    }
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-        l[i] = e0 + i < E ? logit_f32<LT>(row[e0 + i]) : -__builtin_inff();
-    float b[NV];
+        b[i] = 0.0f;
+    if (a.bias) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-        b[i] = (a.bias && e0 + i < E) ? a.bias[e0 + i] : 0.0f;
+        for (int i = 0; i < NV; ++i)
+            b[i] = a.bias[min(e0 + i, E - 1)];
+    }
 
     // masked: -inf or NaN; +inf counts as the largest finite value
     bool live[NV];
@@ -143,26 +256,25 @@ __device__ __forceinline__ void select_token(const SelArgs &a, int t, int lane, 
 #pragma unroll
         for (int i = 0; i < NV; ++i)
             m = live[i] ? fmaxf(m, l[i]) : m;
-#pragma unroll
-        for (int o = 32; o; o >>= 1)
-            m = fmaxf(m, __shfl_xor(m, o, 64));
+        m = wave_max_f32(m);
         double sum = 0.0;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            s[i] = live[i] ? exp((double)l[i] - (double)m) : 0.0;
+            s[i] = live[i] ? exp_f64((double)l[i] - (double)m) : 0.0;
             sum += s[i];
         }
-#pragma unroll
-        for (int o = 32; o; o >>= 1)
-            sum += shfl_xor_f64(sum, o);
-        const double inv = sum > 0.0 ? 1.0 / sum : 0.0;
+        sum = wave_sum_f64(sum);
+        const double inv = sum > 0.0 ? rcp_f64(sum) : 0.0;   // sum is 0 or at least 1
 #pragma unroll
         for (int i = 0; i < NV; ++i)
             s[i] *= inv;
     } else {
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-            s[i] = live[i] ? 1.0 / (1.0 + exp(-(double)l[i])) : 0.0;
+        for (int i = 0; i < NV; ++i) {
+            // with t = exp(-|l|) <= 1 nothing overflows at either end
+            const double t = exp_f64(-fabs((double)l[i])), r = rcp_f64(1.0 + t);
+            s[i] = !live[i] ? 0.0 : l[i] < 0.0f ? t * r : r;
+        }
     }
     uint64_t key[NV];
 #pragma unroll
@@ -173,8 +285,9 @@ __device__ __forceinline__ void select_token(const SelArgs &a, int t, int lane, 
         const int size = E / a.n_group;
         const int per = size / NV;   // lanes per group, if whole
         const bool top2 = (a.flags & MOE_GROUP_TOP2) != 0;
+        const bool whole = size % NV == 0 && (per & (per - 1)) == 0;
         uint64_t mine;               // lane g < n_group: group g's rank key
-        if (size % NV == 0 && (per & (per - 1)) == 0) {
+        if (whole) {
             Top2 p{0ull, 0ull};
 #pragma unroll
             for (int i = 0; i < NV; ++i)
@@ -204,33 +317,43 @@ __device__ __forceinline__ void select_token(const SelArgs &a, int t, int lane, 
             rank += (o > mine || (o == mine && g < lane)) ? 1 : 0;
         }
         const uint64_t kept = __ballot(lane < a.n_group && rank < a.keep);
+        if (whole) {   // a lane's experts are of one group
+            const bool in = (kept >> min(e0 / size, 63)) & 1ull;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int e = e0 + i;
-            if (e < E && !((kept >> (e / size)) & 1ull))
-                key[i] = 0ull;
+            for (int i = 0; i < NV; ++i)
+                key[i] = in ? key[i] : 0ull;
+        } else {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int e = e0 + i;
+                if (e < E && !((kept >> (e / size)) & 1ull))
+                    key[i] = 0ull;
+            }
         }
     }
 
-    // 1. a bound from the lanes' largest keys
+    // 1. a bound from the lanes' largest keys: their high words, made unique
+    // (and cut a little lower) by the lane
     uint64_t mk = key[0];
 #pragma unroll
     for (int i = 1; i < NV; ++i)
         mk = key[i] > mk ? key[i] : mk;
-    sc->key[lane] = mk;
+    const uint32_t mine32 = ((uint32_t)(mk >> 32) & ~63u) | (uint32_t)(63 - lane);
+    sc->key[lane] = mine32;
     wave_lds_sync();
     int r0 = 0, r1 = 0;
 #pragma unroll
-    for (int j = 0; j < 64; j += 2) {
-        const uint4_t q = *reinterpret_cast<const uint4_t *>(&sc->key[j]);
-        const uint64_t ka = ((uint64_t)q.y << 32) | q.x, kb = ((uint64_t)q.w << 32) | q.z;
-        r0 += (ka > mk || (ka == mk && j < lane)) ? 1 : 0;
-        r1 += (kb > mk || (kb == mk && j + 1 < lane)) ? 1 : 0;
+    for (int j = 0; j < 64; j += 4) {
+        const uint4_t v = *reinterpret_cast<const uint4_t *>(&sc->key[j]);
+        r0 += v.x > mine32 ? 1 : 0;
+        r1 += v.y > mine32 ? 1 : 0;
+        r0 += v.z > mine32 ? 1 : 0;
+        r1 += v.w > mine32 ? 1 : 0;
     }
-    const int lrank = r0 + r1;
-    const uint64_t at = __ballot(lrank == k - 1);   // exactly one lane
-    uint64_t bound = readlane_u64(mk, __ffsll((long long)at) - 1);
-    bound = bound ? bound : 1ull;
+    const uint64_t at = __ballot(r0 + r1 == k - 1);   // exactly one lane
+    const uint32_t cut = (uint32_t)__builtin_amdgcn_readlane((int)mine32,
+                                                             __ffsll((long long)at) - 1) & ~63u;
+    const uint64_t bound = cut ? (uint64_t)cut << 32 : 1ull;
 
     // 2. candidates, compacted in index order within each register
     const uint64_t below = (lane == 0) ? 0ull : (~0ull >> (64 - lane));
@@ -301,10 +424,7 @@ __device__ __forceinline__ void select_token(const SelArgs &a, int t, int lane, 
     const bool sel = rank < k;
     double w = sel ? sv : 0.0;
     if (a.flags & MOE_RENORM) {
-        double sum = w;
-#pragma unroll
-        for (int o = 32; o; o >>= 1)
-            sum += shfl_xor_f64(sum, o);
+        const double sum = wave_sum_f64(w);
         w = sum > 0.0 ? w / sum : 0.0;
     }
     if (sel) {
@@ -314,6 +434,7 @@ __device__ __forceinline__ void select_token(const SelArgs &a, int t, int lane, 
             sidx[rank] = e;
     }
     wave_lds_sync();   // the scratch may be reused for the wave's next token
+    return SelOut{sel ? rank : k, e};
 }
 
 // LDS of keys per wave for groups that do not fall on whole runs of lanes.
@@ -361,6 +482,153 @@ __global__ __launch_bounds__(RSP_MAX_T * 64) void route_select_sort_kernel(
     }
 }
 
+// One token: its experts' places by marking them in LDS, without a sort.
+template <int NV, typename LT>
+__global__ __launch_bounds__(64) void route_select_one_kernel(
+    SelArgs a, int32_t *__restrict__ counts, int32_t *__restrict__ offsets,
+    int32_t *__restrict__ perm, int32_t *__restrict__ inv_perm)
+{
+    extern __shared__ __align__(16) uint64_t gkeys[];
+    __shared__ __align__(16) SelScratch sc;
+    __shared__ int mark[64 * NV];   // rank + 1 of a chosen expert
+    const int lane = threadIdx.x;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+        mark[lane * NV + i] = 0;
+    const SelOut o = select_token<NV, LT>(a, 0, lane, &sc, gkeys, nullptr);
+    if (o.rank < a.k)
+        mark[o.e] = o.rank + 1;
+    wave_lds_sync();
+    int m[NV], n = 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        m[i] = mark[lane * NV + i];
+        n += m[i] != 0;
+    }
+    int at = n;
+#pragma unroll
+    for (int st = 1; st < 64; st <<= 1) {
+        const int v = __shfl_up(at, st, 64);
+        if (lane >= st)
+            at += v;
+    }
+    at -= n;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int e = lane * NV + i;
+        if (e < a.E) {
+            counts[e] = m[i] != 0;
+            offsets[e] = at;
+        }
+        if (m[i]) {
+            perm[at] = m[i] - 1;
+            inv_perm[m[i] - 1] = at;
+            ++at;
+        }
+    }
+    if (lane == 0)
+        offsets[a.E] = a.k;
+}
+
+// Chunked form, first launch: selection of RSC_TOK tokens per workgroup and
+// how often they chose each expert (at most once per token: a byte).
+template <int NV, typename LT>
+__global__ __launch_bounds__(RSC_WAVES * 64) void route_select_count_kernel(
+    SelArgs a, uint8_t *__restrict__ hist)
+{
+    extern __shared__ __align__(16) uint64_t gkeys[];
+    __shared__ __align__(16) SelScratch sc[RSC_WAVES];
+    __shared__ int cnt[1024];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    cnt[threadIdx.x] = 0;
+    lds_barrier();
+    for (int i = 0; i < RSC_TOK / RSC_WAVES; ++i) {
+        const int t = blockIdx.x * RSC_TOK + i * RSC_WAVES + wave;
+        if (t < a.T) {
+            const SelOut o = select_token<NV, LT>(a, t, lane, &sc[wave],
+                                                  gkeys + (size_t)wave * a.E, nullptr);
+            if (o.rank < a.k)
+                atomicAdd(&cnt[o.e], 1);
+        }
+    }
+    lds_barrier();
+    const int pitch = (a.E + 3) & ~3;
+    if ((int)threadIdx.x < pitch)   // cnt past E is zero
+        hist[(size_t)blockIdx.x * pitch + threadIdx.x] = (uint8_t)cnt[threadIdx.x];
+}
+
+// Second launch: workgroup b places chunk b's elements.  Thread (g, e) adds up
+// every G-th chunk's counts of experts 4e..4e+3, in all chunks and in those
+// before b (16-bit lanes: at most 16 * RSC_MAX_T / RSC_TOK / G).
+__global__ __launch_bounds__(1024) void route_place_kernel(
+    const int32_t *__restrict__ idx, const uint32_t *__restrict__ hist, int T, int k, int E,
+    int chunks, int32_t *__restrict__ counts, int32_t *__restrict__ offsets,
+    int32_t *__restrict__ perm, int32_t *__restrict__ inv_perm)
+{
+    __shared__ int tot[1024], pre[1024], wsum[16];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int mine = blockIdx.x;
+    tot[tid] = 0;
+    pre[tid] = 0;
+    lds_barrier();
+    const int E4 = (E + 3) / 4, G = 1024 / E4, g = tid / E4, e = tid - g * E4;
+    if (g < G) {
+        uint32_t all0 = 0, all1 = 0, pre0 = 0, pre1 = 0;   // experts 4e, 4e+2; 4e+1, 4e+3
+        for (int b0 = g; b0 < chunks; b0 += 8 * G) {
+            uint32_t h[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                h[i] = hist[(size_t)min(b0 + i * G, chunks - 1) * E4 + e];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int b = b0 + i * G;
+                const uint32_t v = b < chunks ? h[i] : 0u, u = b < mine ? v : 0u;
+                all0 += v & 0x00ff00ffu;
+                all1 += (v >> 8) & 0x00ff00ffu;
+                pre0 += u & 0x00ff00ffu;
+                pre1 += (u >> 8) & 0x00ff00ffu;
+            }
+        }
+        atomicAdd(&tot[4 * e], (int)(all0 & 0xffffu));
+        atomicAdd(&tot[4 * e + 1], (int)(all1 & 0xffffu));
+        atomicAdd(&tot[4 * e + 2], (int)(all0 >> 16));
+        atomicAdd(&tot[4 * e + 3], (int)(all1 >> 16));
+        atomicAdd(&pre[4 * e], (int)(pre0 & 0xffffu));
+        atomicAdd(&pre[4 * e + 1], (int)(pre1 & 0xffffu));
+        atomicAdd(&pre[4 * e + 2], (int)(pre0 >> 16));
+        atomicAdd(&pre[4 * e + 3], (int)(pre1 >> 16));
+    }
+    lds_barrier();
+    const int c = tid < E ? tot[tid] : 0;
+    int incl = c;
+#pragma unroll
+    for (int st = 1; st < 64; st <<= 1) {
+        const int v = __shfl_up(incl, st, 64);
+        if (lane >= st)
+            incl += v;
+    }
+    if (lane == 63)
+        wsum[wave] = incl;
+    lds_barrier();
+    int off = incl - c;
+    for (int i = 0; i < wave; ++i)
+        off += wsum[i];
+    if (tid < E) {
+        if (mine == 0) {
+            counts[tid] = c;
+            offsets[tid] = off;
+        }
+        pre[tid] += off;
+    }
+    if (mine == 0 && tid == E - 1)
+        offsets[E] = off + c;
+    lds_barrier();
+    if (wave == 0) {
+        const int f0 = mine * RSC_TOK * k, f1 = min(T * k, f0 + RSC_TOK * k);
+        wave_scatter(idx, f0, f1, E, pre, perm, inv_perm, lane);
+    }
+}
+
 template <typename LT, typename F>
 static int for_width(int E, F &&f)
 {
@@ -372,23 +640,52 @@ static int for_width(int E, F &&f)
     return f(std::integral_constant<int, 16>());
 }
 
+// Raises a kernel's LDS limit for group keys (idempotent).
+static int raise_lds(const void *kernel, size_t group_bytes)
+{
+    if (group_bytes)
+        MOE_HIP_TRY(hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize,
+                                        (int)RSC_KEY_BYTES));
+    return MOE_OK;
+}
+
+// The grouping's outputs (counts NULL: selection alone); hist: the chunked form.
+struct SelSort {
+    int32_t *counts, *offsets, *perm, *inv_perm;
+    uint8_t *hist;
+};
+
 template <typename LT>
-static int launch_select_t(const SelArgs &a, int32_t *counts, int32_t *offsets, int32_t *perm,
-                           int32_t *inv_perm, hipStream_t st)
+static int launch_select_t(const SelArgs &a, const SelSort &how, hipStream_t st)
 {
     return for_width<LT>(a.E, [&](auto nv) -> int {
         constexpr int NV = decltype(nv)::value;
         const size_t g = group_lds(a, NV);
-        if (counts) {
-            static bool attr_set = false;   // raising the LDS limit is idempotent
-            if (g && !attr_set) {
-                MOE_HIP_TRY(hipFuncSetAttribute(
-                    (const void *)route_select_sort_kernel<NV, LT>,
-                    hipFuncAttributeMaxDynamicSharedMemorySize, RSP_MAX_KEYS * 8));
-                attr_set = true;
-            }
+        if (how.counts && a.T == 1) {
+            hipLaunchKernelGGL((route_select_one_kernel<NV, LT>), dim3(1), dim3(64), g, st, a,
+                               how.counts, how.offsets, how.perm, how.inv_perm);
+            MOE_LAUNCH_CHECK("route_select_one_kernel");
+            return MOE_OK;
+        }
+        if (how.counts && how.hist) {
+            if (const int rc = raise_lds((const void *)route_select_count_kernel<NV, LT>, g))
+                return rc;
+            const int chunks = (a.T + RSC_TOK - 1) / RSC_TOK;
+            hipLaunchKernelGGL((route_select_count_kernel<NV, LT>), dim3(chunks),
+                               dim3(RSC_WAVES * 64), g * RSC_WAVES, st, a, how.hist);
+            MOE_LAUNCH_CHECK("route_select_count_kernel");
+            hipLaunchKernelGGL(route_place_kernel, dim3(chunks), dim3(1024), 0, st, a.idx,
+                               reinterpret_cast<const uint32_t *>(how.hist),
+                               a.T, a.k, a.E, chunks, how.counts, how.offsets, how.perm,
+                               how.inv_perm);
+            MOE_LAUNCH_CHECK("route_place_kernel");
+            return MOE_OK;
+        }
+        if (how.counts) {
+            if (const int rc = raise_lds((const void *)route_select_sort_kernel<NV, LT>, g))
+                return rc;
             hipLaunchKernelGGL((route_select_sort_kernel<NV, LT>), dim3(1), dim3(a.T * 64),
-                               g * a.T, st, a, counts, offsets, perm, inv_perm);
+                               g * a.T, st, a, how.counts, how.offsets, how.perm, how.inv_perm);
             MOE_LAUNCH_CHECK("route_select_sort_kernel");
             return MOE_OK;
         }
@@ -399,26 +696,53 @@ static int launch_select_t(const SelArgs &a, int32_t *counts, int32_t *offsets, 
     });
 }
 
-bool route_select_sorts(int T, int E)
+// How the grouping is formed: inside the selecting workgroup, in chunks over
+// two launches, or by the permutation's own launches behind the selection.
+// Measured at 4096 tokens of 512 experts, top-10: 2 launches against 4.
+enum { SORT_INSIDE, SORT_CHUNKS, SORT_AFTER };
+static int sort_kind(int T, int E)
 {
-    return T > 0 && T <= RSP_MAX_T && T * E <= RSP_MAX_KEYS;
+    if (T <= RSP_MAX_T && (T == 1 || T * E <= RSP_MAX_KEYS))
+        return SORT_INSIDE;
+    // the chunked form's 16 waves must fit their group keys in LDS
+    if (T <= RSC_MAX_T && (size_t)E * 8 * RSC_WAVES <= RSC_KEY_BYTES)
+        return SORT_CHUNKS;
+    return SORT_AFTER;
 }
 
-// counts != NULL (route_select_sorts): with the sort, in one launch.
+size_t route_select_ws_bytes(int T, int k, int E)
+{
+    switch (sort_kind(T, E)) {
+    case SORT_INSIDE: return T > 0 ? 0 : permute_ws_bytes(T, k, E);
+    case SORT_CHUNKS: return (size_t)al256((int64_t)((T + RSC_TOK - 1) / RSC_TOK) * ((E + 3) & ~3));
+    default: return permute_ws_bytes(T, k, E);
+    }
+}
+
+// counts NULL: selection alone.
 int launch_route_select(const void *logits, int dtype, int64_t ld, const float *bias, int T, int E,
                         int k, int score, int n_group, int keep, unsigned flags, float scale,
                         int32_t *idx, float *w, int32_t *counts, int32_t *offsets, int32_t *perm,
-                        int32_t *inv_perm, hipStream_t st)
+                        int32_t *inv_perm, void *ws, hipStream_t st)
 {
     const SelArgs a{logits, ld, bias, T, E, k, score, n_group, keep, flags, scale, idx, w};
-    if (dtype == MOE_DTYPE_F32)
-        return launch_select_t<float>(a, counts, offsets, perm, inv_perm, st);
-    if (dtype == MOE_DTYPE_F16)
-        return launch_select_t<f16>(a, counts, offsets, perm, inv_perm, st);
-    return launch_select_t<uint16_t>(a, counts, offsets, perm, inv_perm, st);
+    const int kind = sort_kind(T, E);
+    SelSort how{counts, offsets, perm, inv_perm, nullptr};
+    if (counts && kind == SORT_CHUNKS)
+        how.hist = static_cast<uint8_t *>(ws);
+    if (kind == SORT_AFTER)
+        how.counts = nullptr;
+    if (T > 0) {
+        const int rc = dtype == MOE_DTYPE_F32   ? launch_select_t<float>(a, how, st)
+                       : dtype == MOE_DTYPE_F16 ? launch_select_t<f16>(a, how, st)
+                                                : launch_select_t<uint16_t>(a, how, st);
+        if (rc || !counts || kind != SORT_AFTER)
+            return rc;
+    }
+    return counts ? launch_permute(idx, T, k, E, counts, offsets, perm, inv_perm, ws, st) : MOE_OK;
 }
 
-// Router logits of at most 8 tokens, one wave per expert: the summation order
+// Router logits of at most 4 tokens, one wave per expert: the summation order
 // of every other router kernel (partial j in lane j, then the xor butterfly),
 // so the same bits.
 template <int H, int TT>

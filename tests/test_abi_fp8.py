@@ -101,7 +101,7 @@ def test_product_no_rows():
     ((1, 8256, 1024, 64, 8), EUNSUP), ((1, 2048, 1024, 2048, 8), EUNSUP),
     ((1, 2048, 1024, 64, 17), EUNSUP), ((1, 2048, 1024, 64, 8, M.MOE_REGIME_SMALL), EINVAL),
     ((1, 2048, 1024, 64, 8, M.MOE_REGIME_AUTO | M.MOE_Y_TOKEN_ORDER), EINVAL),
-    ((5, 2048, 1024, 64, 8, M.MOE_REGIME_DECODE), EUNSUP)])
+    ((17, 2048, 1024, 64, 8, M.MOE_REGIME_DECODE), EUNSUP)])
 def test_plan_refusals(args, code):
     assert _code(M.moe_expert_ffn_w8a8_plan, *args) == code
 
@@ -109,6 +109,8 @@ def test_plan_refusals(args, code):
 def test_plan_and_layout():
     assert M.moe_expert_ffn_w8a8_plan(4, 2048, 1024, 64, 8)[0] == M.MOE_REGIME_DECODE
     assert M.moe_expert_ffn_w8a8_plan(5, 2048, 1024, 64, 8)[0] == M.MOE_REGIME_BATCHED
+    assert M.moe_expert_ffn_w8a8_plan(16, 2048, 1024, 8, 2)[0] == M.MOE_REGIME_DECODE
+    assert M.moe_expert_ffn_w8a8_plan(17, 2048, 1024, 8, 1)[0] == M.MOE_REGIME_BATCHED
     r, n = M.moe_expert_ffn_w8a8_plan(4096, 2048, 1024, 64, 8)
     assert r == M.MOE_REGIME_BATCHED and n >= 4096 * (2048 + 8 * 1024)
     off, total = M.moe_fp8_blob_layout(320, 192)
@@ -118,7 +120,7 @@ def test_plan_and_layout():
 
 def test_experts_refusals():
     a = (P, P, P, P, 8, 256, 128, 8, 2, M.MOE_REGIME_BATCHED, P, P)
-    need = M.moe_expert_ffn_w8a8_plan(8, 256, 128, 8, 2)[1]
+    need = M.moe_expert_ffn_w8a8_plan(8, 256, 128, 8, 2, M.MOE_REGIME_BATCHED)[1]
     assert _code(M.moe_expert_ffn_w8a8, *a, need - 1, stream=0) == ENOMEM
     for i in (0, 1, 2, 3, 10):
         b = list(a)

@@ -248,7 +248,8 @@ def _check_ffn(y, x, perm, offsets, vals, k, skip=()):
 FFN = [   # T, H, I, E, k, regime
     (1, 256, 512, 8, 2, 0), (1, 2048, 1024, 16, 8, 0), (4, 256, 192, 8, 2, 0),
     (3, 320, 64, 5, 3, 0), (1, 64, 64, 1, 1, 0), (4, 256, 192, 8, 2, M.MOE_REGIME_BATCHED),
-    (5, 256, 192, 8, 2, 0), (16, 320, 64, 5, 3, 0), (40, 512, 320, 8, 4, 0),
+    (5, 256, 192, 8, 2, 0), (16, 320, 64, 5, 3, M.MOE_REGIME_DECODE), (16, 320, 64, 5, 3, 0),
+    (11, 2048, 1408, 6, 2, 0), (1, 8192, 64, 2, 1, 0), (16, 64, 8192, 2, 2, 0), (40, 512, 320, 8, 4, 0),
     (100, 256, 192, 4, 2, 0), (300, 512, 448, 3, 1, 0), (70, 2048, 512, 70, 4, 0)]
 
 
@@ -264,7 +265,7 @@ def test_experts(T, H, I, E, k, regime):
     _check_ffn(y, x, perm, offsets, vals, k)
 
 
-@pytest.mark.parametrize("T", [2, 4, 30])
+@pytest.mark.parametrize("T", [2, 4, 16, 30])
 def test_experts_uneven(T):
     """Every token with the same expert twice, ids that route nowhere (rows
     behind the last sorted row stay as they were), and an absent expert."""

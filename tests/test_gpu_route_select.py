@@ -62,7 +62,9 @@ CASES = [   # T, E, k, groups, keep, top2
     (3, 60, 4, 6, 3, False), (16, 512, 10, 8, 4, True), (17, 512, 10, 8, 4, True),
     (5, 1024, 16, 64, 9, True), (33, 1000, 16, 8, 3, True), (9, 65, 16, 5, 2, True),
     (130, 256, 8, 8, 4, True), (67, 96, 6, 4, 4, False), (2, 129, 1, 3, 1, True),
-    (1025, 60, 4, 60, 4, False), (12, 640, 7, 10, 1, False), (8, 1024, 16, 1, 1, False)]
+    (1025, 60, 4, 60, 4, False), (12, 640, 7, 10, 1, False), (8, 1024, 16, 1, 1, False),
+    (1, 1024, 16, 64, 2, True), (1, 130, 5, 2, 1, False), (9, 1000, 3, 8, 2, True),
+    (8192, 64, 2, 8, 3, True), (8193, 16, 2, 1, 1, False), (40, 768, 9, 3, 2, True)]
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
