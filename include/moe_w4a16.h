@@ -87,6 +87,9 @@ enum { MOE_DTYPE_F16 = 0, MOE_DTYPE_F32 = 1, MOE_DTYPE_F32_PM = 2, MOE_DTYPE_BF1
  * point).  MOE_W4_ZERO_POINT is OR'd into the regime of moe_expert_ffn_plan /
  * moe_expert_ffn_w4a16 / moe_pool_layer_args when the blobs are FMT_ZP. */
 enum { MOE_FMT_SYM = 0, MOE_FMT_ZP = 1 };
+/* Name of the FP8 blobs' format (moe_fp8_blob_layout) for programs that hold
+ * layers of several formats; the _fmt calls refuse it (MOE_EINVAL). */
+enum { MOE_FMT_FP8 = 2 };
 enum { MOE_W4_ZERO_POINT = 0x200 };
 
 /* Thread-local text of the last error on this thread ("" if none). */

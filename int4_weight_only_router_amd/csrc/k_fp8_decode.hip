@@ -83,19 +83,27 @@ __global__ __launch_bounds__(256) void fp8_rows_kernel(Fp8Args a)
     const float *s0 = a.ws, *s1 = a.ws;
     if constexpr (MODE != F8_DENSE) {
         const int p = blockIdx.y;
-        // the expert of sorted row p: the experts that end at or before it
-        int e = 0;
+        // the expert of sorted row p: the experts that end at or before it;
+        // its run's bounds come from the same lanes
+        int e = 0, first = 0, end = 0;
         for (int b = 0; b < a.E; b += 64) {
             const int o = b + lane < a.E ? a.offsets[b + lane + 1] : 0x7fffffff;
-            e += __popcll(__ballot(o <= p));
+            const int n = __popcll(__ballot(o <= p));
+            if (n)
+                first = __builtin_amdgcn_readlane(o, n - 1);
+            e += n;
+            if (n < 64) {
+                end = __builtin_amdgcn_readlane(o, n);
+                break;
+            }
         }
         if (e >= a.E)
             return;   // behind the last routed row
         // T rows to a workgroup (all of them, unless a token chose an expert twice)
-        if ((p - a.offsets[e]) % a.T)
+        if ((p - first) % a.T)
             return;
         row0 = p;
-        rows = min(a.T, a.offsets[e + 1] - p);
+        rows = min(a.T, end - p);
         const uint8_t *blob = static_cast<const uint8_t *>(a.blobs[e]);
         if (!blob)
             return;

@@ -37,6 +37,37 @@ def load_experts(weights, H, I, group, device="cuda", stream=None, fmt=A.MOE_FMT
     return dev, canon
 
 
+def load_experts_fp8(weights, H, I, device="cuda", stream=None):
+    """Quantise experts to e4m3 with a scale per 128 x 128 block on the device.
+
+    weights: iterable of (wg [I,H], wu [I,H], wd [H,I]) float32 arrays (numpy
+    or torch).  Returns a uint8 device tensor [n, blob_bytes] in the layout of
+    moe_fp8_blob_layout, which the kernels read as it is."""
+    weights = list(weights)
+    off, total = A.moe_fp8_blob_layout(H, I)
+    blobs = torch.zeros((len(weights), total), dtype=torch.uint8, device=device)
+    for e, w in enumerate(weights):
+        base = blobs[e].data_ptr()
+        for j, (m, (rows, cols)) in enumerate(zip(w, ((I, H), (I, H), (H, I)))):
+            m = torch.as_tensor(m).to(device=device, dtype=torch.float32).contiguous()
+            A.moe_quantize_fp8(m, A.MOE_DTYPE_F32, cols, rows, cols, 128, 0, base + off[j], cols,
+                               base + off[3 + j], stream)
+    return blobs
+
+
+@dataclass
+class ScoreRouting:
+    """Expert selection by moe_route_select instead of moe_route's softmax
+    top-k: scores (MOE_SCORE_*), a bias that decides but does not weigh, expert
+    groups of which topk_group are kept, and a factor on the weights."""
+    score: int = A.MOE_SCORE_SIGMOID
+    select_bias: torch.Tensor | None = None   # fp32 [E] device
+    n_group: int = 1
+    topk_group: int = 1
+    group_top2: bool = False                  # a group counts by its two best experts
+    scale: float = 1.0
+
+
 def blob_table(blobs: torch.Tensor) -> torch.Tensor:
     """Device array of per-expert blob addresses for a [E, bytes] tensor."""
     E, nbytes = blobs.shape
@@ -63,14 +94,17 @@ class LayerBuffers:
     shared_out: torch.Tensor | None
     shared_ws: torch.Tensor | None
     out: torch.Tensor
+    logits: torch.Tensor | None = None
 
 
 class MoELayer:
-    """One W4A16 MoE layer resident on the device."""
+    """One MoE layer resident on the device: W4A16 experts (fmt MOE_FMT_SYM or
+    MOE_FMT_ZP) or FP8 experts (MOE_FMT_FP8: blobs of load_experts_fp8, `group`
+    unused), routed by softmax top-k or, with `routing`, by scores and groups."""
 
     def __init__(self, H, I, E, k, group, router, table, bias=None, shared=None,
                  renorm=False, device="cuda", shared_gate=None, overlap_shared=False,
-                 fmt=A.MOE_FMT_SYM):
+                 fmt=A.MOE_FMT_SYM, routing: ScoreRouting | None = None):
         self.H, self.I, self.E, self.k, self.g = H, I, E, k, group
         self.fmt = fmt                  # blob format of the routed experts
         self.router = router            # fp16 [E, H] device
@@ -83,15 +117,24 @@ class MoELayer:
         if shared_gate is not None and shared is None:
             raise ValueError("a shared-expert gate needs a shared expert")
         self.flags = A.MOE_RENORM if renorm else 0
+        self.routing = routing
         self.device = device
+
+    @property
+    def fp8(self) -> bool:
+        return self.fmt == A.MOE_FMT_FP8
 
     def buffers(self, T, regime=A.MOE_REGIME_AUTO, partial_order=True) -> LayerBuffers:
         """partial_order: decode partials in partial-major column order, which
         the fused combine + next route reads in whole lines."""
         d = self.device
-        r, ydt, ysl, ffn_ws = A.moe_expert_ffn_plan(T, self.H, self.I, self.E, self.k, self.g,
-                                                    regime)
-        if r == A.MOE_REGIME_DECODE:
+        if self.fp8:
+            r, ffn_ws = A.moe_expert_ffn_w8a8_plan(T, self.H, self.I, self.E, self.k, regime)
+            ydt, ysl = A.MOE_DTYPE_F16, 1
+        else:
+            r, ydt, ysl, ffn_ws = A.moe_expert_ffn_plan(T, self.H, self.I, self.E, self.k, self.g,
+                                                        regime)
+        if not self.fp8 and r == A.MOE_REGIME_DECODE:
             # decode partials straight in token order: the combine then reads
             # them without inv_perm (one dependent round trip less)
             r |= A.MOE_Y_TOKEN_ORDER
@@ -105,6 +148,10 @@ class MoELayer:
         pws = max(A.moe_permute_workspace_bytes(T, self.k, self.E),
                   A.moe_route_permute_workspace_bytes(T, self.k, self.E),
                   A.moe_combine_route_permute_workspace_bytes(T, self.k, self.E))
+        logits = None
+        if self.routing is not None:
+            pws = max(pws, A.moe_route_select_workspace_bytes(T, self.k, self.E))
+            logits = torch.empty((T, self.E), dtype=torch.float32, device=d)
         n = T * self.k
         ytype = torch.float16 if ydt == A.MOE_DTYPE_F16 else torch.float32
         sh_out = sh_ws = None
@@ -128,11 +175,21 @@ class MoELayer:
             ffn_ws=torch.empty(ffn_ws, dtype=torch.uint8, device=d) if ffn_ws else None,
             shared_out=sh_out, shared_ws=sh_ws,
             out=torch.empty((T, self.H), dtype=torch.float16, device=d),
+            logits=logits,
         )
 
     def route_permute(self, x, b: LayerBuffers, stream=None, fused=True):
         T = b.T
         nws = 0 if b.perm_ws is None else b.perm_ws.numel()
+        if self.routing is not None:
+            s = self.routing
+            A.moe_router_logits(x, self.router, self.bias, T, self.H, self.E, b.logits, stream)
+            A.moe_route_select_permute(
+                b.logits, A.MOE_DTYPE_F32, self.E, s.select_bias, T, self.E, self.k, s.score,
+                s.n_group, s.topk_group, self.flags | (A.MOE_GROUP_TOP2 if s.group_top2 else 0),
+                s.scale, b.topk_idx, b.topk_w, b.counts, b.offsets, b.perm, b.inv_perm, b.perm_ws,
+                nws, stream)
+            return
         if fused:
             A.moe_route_permute(x, self.router, self.bias, T, self.H, self.E, self.k,
                                 self.flags, b.topk_idx, b.topk_w, b.counts, b.offsets, b.perm,
@@ -149,6 +206,13 @@ class MoELayer:
                              b.shared_ws, b.shared_ws.numel(), stream)
 
     def experts(self, x, b: LayerBuffers, table=None, stream=None, shared=True):
+        if self.fp8:
+            A.moe_expert_ffn_w8a8(x, b.perm, b.offsets, self.table if table is None else table,
+                                  b.T, self.H, self.I, self.E, self.k, b.regime, b.y, b.ffn_ws,
+                                  0 if b.ffn_ws is None else b.ffn_ws.numel(), stream)
+            if shared and self.shared is not None:
+                self.shared_ffn(x, b, stream)
+            return
         A.moe_expert_ffn_w4a16(x, b.perm, b.offsets, self.table if table is None else table,
                                b.T, self.H, self.I, self.E, self.k, self.g, b.regime, b.y,
                                b.y_dtype, b.y_slices, b.ffn_ws,
@@ -177,6 +241,8 @@ class MoELayer:
         decode token of at most 64 experts, else the two calls)."""
         if nxt.H != self.H or b_next.T != b.T:
             raise ValueError("the next layer must have the same H and batch")
+        if nxt.routing is not None:
+            raise ValueError("the fused call routes by softmax top-k only")
         out = b.out if out is None else out
         inv = None if b.regime & A.MOE_Y_TOKEN_ORDER else b.inv_perm
         gate = self.shared_gate
@@ -196,7 +262,8 @@ class MoELayer:
         partials (moe_combine_route_partials): one decode token, at most 64
         experts in the next layer, fp32 slice partials here."""
         return (b.T == 1 and nxt.E <= 64 and nxt.H == self.H and b.y_slices > 1 and
-                b.y_dtype in (A.MOE_DTYPE_F32, A.MOE_DTYPE_F32_PM))
+                b.y_dtype in (A.MOE_DTYPE_F32, A.MOE_DTYPE_F32_PM) and not nxt.fp8 and
+                nxt.routing is None)
 
     def combine_partials_next(self, b: LayerBuffers, nxt: "MoELayer", parts,
                               residual=None, out=None, stream=None, x=None):
@@ -216,7 +283,8 @@ class MoELayer:
     def route_from_partials_ok(self, b: LayerBuffers) -> bool:
         """Whether this layer's expert launch can route from logit partials
         (moe_expert_ffn_w4a16_routed): one decode token, at most 64 experts."""
-        return b.T == 1 and self.E <= 64 and b.regime & 0xFF == A.MOE_REGIME_DECODE
+        return (b.T == 1 and self.E <= 64 and b.regime & 0xFF == A.MOE_REGIME_DECODE and
+                not self.fp8 and self.routing is None)
 
     def logit_partials(self, x, parts, stream=None):
         """This layer's logit partials of an input row in hand (the first
@@ -239,6 +307,8 @@ class MoELayer:
         b's buffers; x_f16 / residual_f16 / out_f16 are set per call."""
         if self.shared is not None:
             raise ValueError("pooled layers carry no shared expert")
+        if self.fp8 or self.routing is not None:
+            raise ValueError("pooled layers are W4A16 with the softmax router")
         z = lambda t: 0 if t is None else t.data_ptr()
         a = A.PoolLayerArgs()
         a.w_router_f16, a.logit_bias = z(self.router), z(self.bias)
@@ -305,14 +375,15 @@ def stack_forward(layers, bufs, acts, stream=None, fuse=True, parts=None):
     else:
         layers[0].route_permute(acts[0], bufs[0], stream)
     for l, lay in enumerate(layers):
-        if l > 0 and not fuse:
+        # a layer routed by scores is routed on its own, never with a combine
+        if l > 0 and (not fuse or lay.routing is not None):
             lay.route_permute(acts[l], bufs[l], stream)
         if routed:
             lay.experts_routed(acts[l], bufs[l], parts, stream=stream)
         else:
             lay.experts(acts[l], bufs[l], stream=stream)
         routed = False
-        if fuse and l + 1 < L:
+        if fuse and l + 1 < L and layers[l + 1].routing is None:
             nxt = layers[l + 1]
             if parts is not None and lay.split_route_ok(bufs[l], nxt) and \
                     bufs[l + 1].regime & 0xFF == A.MOE_REGIME_DECODE:
