@@ -603,9 +603,10 @@ int moe_fp8_blob_layout(int H, int I, int64_t offsets[6], int64_t *total_bytes);
  *          MOE_DTYPE_F16, one slice)
  *   ws     device scratch of the plan's size, 16-byte aligned, no
  *          initialisation; calls that share it must not overlap
- * Rows behind offsets[E] are left as they were.  Regimes: DECODE (T <= 16: two
- * launches over the weights' stream, activations quantised inside them) and
- * BATCHED (any T); AUTO picks by T.  Both give the same sums up to the order
+ * Rows behind offsets[E] are left as they were.  Regimes: DECODE (T <= 16 and
+ * T * ceil(max(H, I) / 128) <= 600, else MOE_EUNSUPPORTED: two launches over
+ * the weights' stream, activations quantised inside them) and BATCHED (any T);
+ * AUTO takes DECODE where it can up to T * k = 64.  Both give the same sums up to the order
  * of the blocks.  H and I multiples of 64, at most 8192; E <= 1024; k <= 16
  * (MOE_EUNSUPPORTED).  x, y and ws 16-byte aligned (MOE_EINVAL).  T = 0: no-op.
  */

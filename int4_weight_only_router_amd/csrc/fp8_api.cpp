@@ -21,7 +21,7 @@ int launch_quant_fp8(const void *, int, int64_t, int64_t, int, int, bool, void *
 int launch_fp8_tokens(const void *, int64_t, int, uint8_t *, float *, const int32_t *,
                       const void *const *, int, int, Fp8TileRec *, hipStream_t);
 int launch_fp8_rows_dense(const Fp8Args &, hipStream_t);
-int launch_fp8_tile_dense(const Fp8Args &, hipStream_t);
+int launch_fp8_tile_dense(const Fp8Args &, int mf, hipStream_t);
 int launch_fp8_decode(Fp8Args, const void *, float *, int, int, const int64_t *, void *,
                       hipStream_t);
 int fp8_pick_rows(int64_t rows, int E, int I);
@@ -85,6 +85,30 @@ static Fp8Ws fp8_ws(int T, int H, int I, int E, int k, bool decode)
     }
     w.total = o;
     return w;
+}
+
+// Kernel of a dense product: 64*mf x 256 tiles, or 0 for the kernel of few rows
+// (32 x 32 tiles).  The least of the times that were measured for one round of
+// tiles over the 256 compute units at K = 2048 (every form grows with K alike),
+// in us: 64-, 128-, 192- and 256-row tiles 13.5, 21, 27, 31, and 26, 37, 46,
+// 54 with fp32 outputs (the fp16 form); the kernel of few rows 2.5 and 9.8 for
+// every 1000 workgroups.  Against each form on 17 shapes from 64 x 5632 to
+// 4096 x 11264 the choice is the fastest or within 10% of it.
+static int dense_tile(int M, int N, bool f32)
+{
+    static const double round_us[2][4] = {{13.5, 21, 27, 31}, {26, 37, 46, 54}};
+    const int64_t few = (int64_t)((M + 31) / 32) * ((N + 31) / 32);
+    double best = 2.5 + 9.8e-3 * (double)few;
+    int mf = 0;
+    for (int i = 1; i <= 4; ++i) {
+        const int64_t tiles = (int64_t)((M + 64 * i - 1) / (64 * i)) * ((N + 255) / 256);
+        const double t = 3 + (double)((tiles + 255) / 256) * (round_us[f32][i - 1] - 3);
+        if (M > 32 && t < best) {
+            best = t;
+            mf = i;
+        }
+    }
+    return mf;
 }
 
 static int check_select(const char *fn, const void *logits, int dtype, int64_t ld, int T, int E,
@@ -263,11 +287,12 @@ int moe_gemm_fp8(const void *xq, int64_t ldx, const float *x_scales, const void 
     a.out = out;
     a.ldo = ldo;
     a.odt = out_dtype;
-    // 256 x 256 tiles once they occupy most compute units, else the kernel of
-    // few rows, which has 32 times as many workgroups
-    const int64_t tiles = (int64_t)((M + 255) / 256) * ((N + 255) / 256);
-    if (M > 64 && tiles >= 96)
-        return launch_fp8_tile_dense(a, stream);
+    const int mf = dense_tile(M, N, out_dtype == MOE_DTYPE_F32);
+    // (the tile kernel's offsets inside 256 weight rows are 32 bits wide)
+    if (mf && ldw < (int64_t)1 << 22)
+        return launch_fp8_tile_dense(a, mf, stream);
+    if ((M + 31) / 32 > 65535)
+        return set_error(MOE_EUNSUPPORTED, "%s: M=%d with ldw=%lld", fn, M, (long long)ldw);
     return launch_fp8_rows_dense(a, stream);
 }
 
@@ -290,16 +315,19 @@ int moe_expert_ffn_w8a8_plan(int T, int H, int I, int E, int k, int regime, int 
         return rc;
     if (regime != MOE_REGIME_AUTO && regime != MOE_REGIME_DECODE && regime != MOE_REGIME_BATCHED)
         return set_error(MOE_EINVAL, "%s: bad regime %d", fn, regime);
-    // decode up to 32 routed rows: its workgroups then stream weights that few
-    // others share (measured: 64 experts, top-8, us decode / batched: 1 token
-    // 16 / 32, 2: 28 / 32, 4: 44 / 36, 6: 57 / 63, 8: 68 / 65; 8 experts,
-    // top-2: 16 tokens 26 / 31)
+    // decode up to 64 routed rows (measured, us decode / batched: 64 experts,
+    // top-8, 1 token 15 / 32, 4: 32 / 36, 8: 48 / 64, 12: 73 / 75, 16: 92 / 78;
+    // 512 experts, top-10, 4: 21 / 31, 8: 32 / 32, 16: 54 / 37; 60 experts,
+    // top-4, 8: 41 / 60, 16: 77 / 74; 8 experts, top-2, 16: 19 / 31)
+    const bool fits = T <= FP8_DECODE_MAX_T &&
+                      T * ((std::max(H, I) + 127) / 128) <= FP8_DECODE_BLOCKS;
     const int r = regime != MOE_REGIME_AUTO ? regime
-                  : T <= FP8_DECODE_MAX_T && T * k <= 32 ? MOE_REGIME_DECODE
-                                                         : MOE_REGIME_BATCHED;
-    if (r == MOE_REGIME_DECODE && T > FP8_DECODE_MAX_T)
-        return set_error(MOE_EUNSUPPORTED, "%s: the decode regime takes T <= %d (T=%d)", fn,
-                         FP8_DECODE_MAX_T, T);
+                  : fits && T * k <= 64     ? MOE_REGIME_DECODE
+                                            : MOE_REGIME_BATCHED;
+    if (r == MOE_REGIME_DECODE && !fits)
+        return set_error(MOE_EUNSUPPORTED,
+                         "%s: the decode regime takes T <= %d and T * ceil(max(H, I) / 128) <= %d "
+                         "(T=%d H=%d I=%d)", fn, FP8_DECODE_MAX_T, FP8_DECODE_BLOCKS, T, H, I);
     if (resolved_regime)
         *resolved_regime = r;
     if (ws_bytes)

@@ -7,10 +7,15 @@
 // row tile only, so the kernel's task is to have many bytes in flight.  A
 // workgroup owns 32 weight rows (gate/up: 16 gate rows and the same 16 up
 // rows, so that it also forms h) and its four waves take every fourth
-// 128-long block of K each; a wave issues the loads of up to four blocks (16 KB)
-// at once, before it touches the tokens.  The waves' sums meet in LDS in wave
-// order, so results do not depend on timing.  The tokens are the matrix
-// core's second operand, 16 to a fragment; its idle columns cost nothing here.
+// 128-long block of K each.  A wave has one block in flight, in a stage of its own in
+// LDS filled by direct-to-LDS loads of 8 lanes per 128-byte row block (loaded
+// straight into the matrix instruction's layout, consecutive lanes are
+// consecutive rows, and the L1 serves 16 bytes a cycle instead of 64), and six
+// workgroups share a compute unit: many small stages beat few deep ones (64
+// experts, 4 tokens: 31.5 us with one stage per wave, 35 with two, 50 with
+// four, at a floor of 30.5).  No barrier is needed until the waves' sums meet
+// in LDS, in wave order, so that results do not depend on timing.  The tokens are the matrix core's second
+// operand, 16 to a fragment; its idle columns cost nothing here.
 //
 // Decode experts quantise their rows in the workgroup (gate/up: the fp16
 // tokens; down: the fp32 h the first launch left in the workspace), hidden
@@ -59,18 +64,25 @@ __device__ __forceinline__ void quant_row_lds(const XT *src, int K, int kb, int 
         sc[kb] = s;
 }
 
+// Bytes of a wave's stage: 32 weight rows, dense also 16 MT token rows, and
+// the scales.
+template <int MODE, int MT>
+constexpr int f8_rows_stage()
+{
+    return (4 + (MODE == F8_DENSE ? 2 * MT : 0)) * 1024 + 256;
+}
+
 // MODE F8_DENSE: grid (32-column tiles, 16*MT-row tiles).  F8_GATEUP /
 // F8_DOWN: grid (tiles of 16 intermediate / 32 output columns, sorted rows);
 // the workgroup at an expert's first row serves its T rows (an expert has at
-// most one row per token), the others leave at once.  A wave has KP blocks of
-// K in flight at a time.  Nothing is predicated between a matrix instruction
-// and the use of its result: rows past the end repeat the last one (their
-// columns are not stored), blocks past the end repeat the last one with a
-// weight scale of zero.
-template <int MODE, int MT, int KP>
+// most one row per token), the others leave at once.  Nothing is predicated
+// between a matrix instruction and the use of its result: rows past the end
+// repeat the last one (their columns are not stored), blocks past the end
+// repeat the last one with a weight scale of zero.
+template <int MODE, int MT>
 __global__ __launch_bounds__(256) void fp8_rows_kernel(Fp8Args a)
 {
-    static_assert(MODE == F8_DENSE || MT == 1, "decode experts: one row fragment");
+    static_assert(MT == 1 || (MODE == F8_DENSE && MT == 2), "at most 32 rows; experts 16");
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ __align__(16) float red[4][2 * MT][64][4];
     const int lane = threadIdx.x & 63;
@@ -112,15 +124,45 @@ __global__ __launch_bounds__(256) void fp8_rows_kernel(Fp8Args a)
         s0 = reinterpret_cast<const float *>(blob + a.off_s0);
         s1 = reinterpret_cast<const float *>(blob + a.off_s1);
     }
-    // this lane's weight rows of the two fragments
     const int n0 = MODE == F8_GATEUP ? blockIdx.x * 16 : blockIdx.x * 32;
-    const int na = n0 + col, nb = MODE == F8_GATEUP ? na : na + 16;
     const int64_t ldw = MODE == F8_DENSE ? a.ldw : K;
-    const uint8_t *wr[2] = {w0 + (int64_t)min(na, a.N - 1) * ldw,
-                            w1 + (int64_t)min(nb, a.N - 1) * ldw};
     s0 += (int64_t)(n0 >> 7) * nkb;
-    s1 += (int64_t)((MODE == F8_GATEUP ? n0 : n0 + 16) >> 7) * nkb;
-    const int last = K - 16;   // K is a multiple of 16: the last whole piece of a row
+    s1 += (int64_t)(n0 >> 7) * nkb;   // 32 columns never leave their scale block
+
+    // The wave's stage: 32 weight rows (gate/up: 16 + 16), and dense also the
+    // 16 MT token rows, of 128 bytes.  Load i covers rows 8i..8i+7; lane L
+    // fills slot L % 8 of its row with piece (L % 8) ^ f(row), f(r) = (r >> 1)
+    // & 7, so that the 16 rows of a fragment read hit distinct banks.
+    constexpr int XR = MODE == F8_DENSE ? 2 * MT : 0;   // loads of token rows
+    // then the block's scales, one lane each: dense rows 0.., from 32 the weights'
+    constexpr int STAGE = f8_rows_stage<MODE, MT>();
+    uint8_t *const st = smem + wave * STAGE;
+    const uint8_t *src[4 + XR];
+    int pc[4 + XR];
+#pragma unroll
+    for (int i = 0; i < 4 + XR; ++i) {
+        const int r = (i < 4 ? i : i - 4) * 8 + (lane >> 3);
+        pc[i] = ((lane & 7) ^ ((r >> 1) & 7)) * 16;
+        if (i >= 4)
+            src[i] = a.x + (int64_t)(row0 + min(r, rows - 1)) * a.ldx;
+        else if (MODE == F8_GATEUP)
+            src[i] = (i < 2 ? w0 : w1) + (int64_t)(n0 + (r & 15)) * ldw;
+        else
+            src[i] = w0 + (int64_t)min(n0 + r, a.N - 1) * ldw;
+    }
+    const float *scp = lane == 32 ? s0 : s1;
+    if (MODE == F8_DENSE && lane < 16 * MT)
+        scp = a.xs + (int64_t)(row0 + min(lane, rows - 1)) * nkb;
+    // this wave's block j (past the end the last one again)
+    auto block_of = [&](int j) { return min(4 * j + wave, nkb - 1); };
+    auto issue = [&](int j) {
+        const int at = block_of(j) * 128;
+#pragma unroll
+        for (int i = 0; i < 4 + XR; ++i)
+            dma16(src[i] + min(at + pc[i], K - 16), st + i * 1024);
+        dma4(scp + block_of(j), st + (4 + XR) * 1024);
+    };
+    issue(0);
 
     float4_t acc[2][MT];
 #pragma unroll
@@ -129,92 +171,79 @@ __global__ __launch_bounds__(256) void fp8_rows_kernel(Fp8Args a)
         for (int m = 0; m < MT; ++m)
             acc[f][m] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
 
-    uint8_t *xl = smem;                                              // decode: [T][nkb*128]
-    float *sl = reinterpret_cast<float *>(smem + (size_t)a.T * nkb * 128);   // [T][nkb]
-    const uint8_t *xr[MT];
-    const float *xsr[MT];
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        const int r = min(m * 16 + col, rows - 1);
-        if constexpr (MODE == F8_DENSE) {
-            xr[m] = a.x + (int64_t)(row0 + r) * a.ldx;
-            xsr[m] = a.xs + (int64_t)(row0 + r) * nkb;
-        } else {
-            xr[m] = xl + r * nkb * 128;
-            xsr[m] = sl + r * nkb;
+    uint8_t *xl = smem + 4 * STAGE;                                        // decode: [T][nkb*128]
+    float *sl = reinterpret_cast<float *>(xl + (size_t)a.T * nkb * 128);   // [T][nkb]
+    if constexpr (MODE != F8_DENSE) {
+        // quantise this expert's rows while the weights arrive
+        const int g = threadIdx.x >> 4, c = threadIdx.x & 15;
+        for (int i = g; i < rows * nkb; i += 16) {
+            const int r = i / nkb, kb = i - r * nkb;
+            if constexpr (MODE == F8_GATEUP) {
+                const int t = a.perm[row0 + r] / a.k;
+                quant_row_lds(static_cast<const f16 *>(a.src) + (int64_t)t * K, K, kb, c,
+                              xl + (size_t)r * nkb * 128, sl + r * nkb);
+            } else {
+                quant_row_lds(static_cast<const float *>(a.src) + (int64_t)(row0 + r) * K, K, kb,
+                              c, xl + (size_t)r * nkb * 128, sl + r * nkb);
+            }
         }
+        lds_barrier();
     }
-
-    for (int kc = 0; kc < nkb; kc += 4 * KP) {
-        int4_t wf[KP][2][2];
-        float wsc[KP][2];
+    const int rl = min(col, rows - 1);   // decode: this lane's row
+    const uint8_t *xr = xl + rl * nkb * 128;
+    const float *xsr = sl + rl * nkb;
+    const int sw = (col >> 1) & 7;   // f of every fragment's row col
+    const int o0 = (q ^ sw) * 16, o1 = ((q + 4) ^ sw) * 16;
+    const int rounds = (nkb + 3) / 4;
+    for (int j = 0; j < rounds; ++j) {
+        const int kb = block_of(j);
+        const bool in = 4 * j + wave < nkb;
+        wait_vm<0>();   // block j has landed
+        const float *scl = reinterpret_cast<const float *>(st + (4 + XR) * 1024);
+        float sc[2] = {scl[32], scl[33]}, xs[MT];
+        sc[0] = in ? sc[0] : 0.0f;
+        sc[1] = in ? sc[1] : 0.0f;
 #pragma unroll
-        for (int j = 0; j < KP; ++j) {
-            const int kb = min(kc + 4 * j + wave, nkb - 1);
+        for (int m = 0; m < MT; ++m)
+            xs[m] = MODE == F8_DENSE ? scl[m * 16 + col] : xsr[kb];
+        half32 wh[2];
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+            const uint8_t *r = st + (f * 16 + col) * 128;
+            wh[f] = f8_to_f16(join16(*reinterpret_cast<const int4_t *>(r + o0),
+                                     *reinterpret_cast<const int4_t *>(r + o1)));
+        }
+        const int c0 = kb * 128 + q * 16;
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            int4_t x0, x1;
+            if constexpr (MODE == F8_DENSE) {
+                const uint8_t *r = st + 4096 + (m * 16 + col) * 128;
+                x0 = *reinterpret_cast<const int4_t *>(r + o0);
+                x1 = *reinterpret_cast<const int4_t *>(r + o1);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {   // bytes past K count as zeros
+                    x0[i] = c0 < K ? x0[i] : 0;
+                    x1[i] = c0 + 64 < K ? x1[i] : 0;
+                }
+            } else {   // zero-filled to whole blocks
+                x0 = *reinterpret_cast<const int4_t *>(xr + c0);
+                x1 = *reinterpret_cast<const int4_t *>(xr + c0 + 64);
+            }
+            const half32 xf = f8_to_f16(join16(x0, x1));
 #pragma unroll
             for (int f = 0; f < 2; ++f) {
+                const float4_t t = mfma_f16(wh[f], xf);
+                const float s = xs[m] * sc[f];
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    wf[j][f][h] = ldg_nt(reinterpret_cast<const int4_t *>(
-                        wr[f] + min(kb * 128 + h * 64 + q * 16, last)));
-            }
-            const bool in = kc + 4 * j + wave < nkb;
-            wsc[j][0] = in ? s0[kb] : 0.0f;
-            wsc[j][1] = in ? s1[kb] : 0.0f;
-        }
-        if constexpr (MODE != F8_DENSE) {
-            if (kc == 0) {   // quantise this expert's rows while the weights arrive
-                const int g = threadIdx.x >> 4, c = threadIdx.x & 15;
-                for (int i = g; i < rows * nkb; i += 16) {
-                    const int r = i / nkb, kb = i - r * nkb;
-                    if constexpr (MODE == F8_GATEUP) {
-                        const int t = a.perm[row0 + r] / a.k;
-                        quant_row_lds(static_cast<const f16 *>(a.src) + (int64_t)t * K, K, kb, c,
-                                      xl + (size_t)r * nkb * 128, sl + r * nkb);
-                    } else {
-                        quant_row_lds(static_cast<const float *>(a.src) + (int64_t)(row0 + r) * K,
-                                      K, kb, c, xl + (size_t)r * nkb * 128, sl + r * nkb);
-                    }
-                }
-                lds_barrier();
+                for (int i = 0; i < 4; ++i)
+                    acc[f][m][i] = __builtin_fmaf(t[i], s, acc[f][m][i]);
             }
         }
-#pragma unroll
-        for (int j = 0; j < KP; ++j) {
-            const int kb = min(kc + 4 * j + wave, nkb - 1);
-            const int c0 = kb * 128 + q * 16;
-            half32 wh[2];
-#pragma unroll
-            for (int f = 0; f < 2; ++f)
-                wh[f] = f8_to_f16(join16(wf[j][f][0], wf[j][f][1]));
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                int4_t x0, x1;
-                if constexpr (MODE == F8_DENSE) {
-                    x0 = ldg(reinterpret_cast<const int4_t *>(xr[m] + min(c0, last)));
-                    x1 = ldg(reinterpret_cast<const int4_t *>(xr[m] + min(c0 + 64, last)));
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {   // bytes past K count as zeros
-                        x0[i] = c0 < K ? x0[i] : 0;
-                        x1[i] = c0 + 64 < K ? x1[i] : 0;
-                    }
-                } else {   // zero-filled to whole blocks
-                    x0 = *reinterpret_cast<const int4_t *>(xr[m] + c0);
-                    x1 = *reinterpret_cast<const int4_t *>(xr[m] + c0 + 64);
-                }
-                const float xs = xsr[m][kb];
-                const half32 xf = f8_to_f16(join16(x0, x1));
-#pragma unroll
-                for (int f = 0; f < 2; ++f) {
-                    const float4_t t = mfma_f16(wh[f], xf);
-                    const float s = xs * wsc[j][f];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        acc[f][m][i] = __builtin_fmaf(t[i], s, acc[f][m][i]);
-                }
-            }
-        }
+        wave_lds_sync();   // the stage is read
+        issue(j + 1);      // without a branch: past the end the last block again
     }
+    wait_vm<0>();
 #pragma unroll
     for (int f = 0; f < 2; ++f)
 #pragma unroll
@@ -253,45 +282,33 @@ __global__ __launch_bounds__(256) void fp8_rows_kernel(Fp8Args a)
     }
 }
 
-template <int MODE, int MT, int KP>
+template <int MODE, int MT>
 static int launch_rows(const Fp8Args &a, dim3 grid, size_t lds, hipStream_t s)
 {
-    if (lds) {
-        static bool attr_set = false;   // raising the LDS limit is idempotent
-        if (!attr_set) {
-            MOE_HIP_TRY(hipFuncSetAttribute((const void *)fp8_rows_kernel<MODE, MT, KP>,
-                                            hipFuncAttributeMaxDynamicSharedMemorySize,
-                                            FP8_DECODE_MAX_T * 64 * (128 + 4)));
-            attr_set = true;
-        }
+    lds += (size_t)4 * f8_rows_stage<MODE, MT>();
+    static bool attr_set = false;   // raising the LDS limit is idempotent
+    if (!attr_set) {
+        MOE_HIP_TRY(hipFuncSetAttribute((const void *)fp8_rows_kernel<MODE, MT>,
+                                        hipFuncAttributeMaxDynamicSharedMemorySize,
+                                        (160 - 8 * MT) * 1024));   // beside the waves' sums
+        attr_set = true;
     }
-    hipLaunchKernelGGL((fp8_rows_kernel<MODE, MT, KP>), grid, dim3(256), lds, s, a);
+    static_assert(4 * f8_rows_stage<MODE, MT>() +
+                      (MODE == F8_DENSE ? 0 : FP8_DECODE_BLOCKS * 132) <= (160 - 8 * MT) * 1024,
+                  "LDS of one workgroup");
+    hipLaunchKernelGGL((fp8_rows_kernel<MODE, MT>), grid, dim3(256), lds, s, a);
     MOE_LAUNCH_CHECK("fp8_rows_kernel");
     return MOE_OK;
 }
 
-// Dense, any M (in row tiles of 16, 32 or 64).
+// Dense, any M, in row tiles of 16 or 32 (64-row tiles: 333 x 1408 x 2000
+// takes 12 us against 7).
 int launch_fp8_rows_dense(const Fp8Args &a, hipStream_t s)
 {
     const unsigned nt = (unsigned)((a.N + 31) / 32);
     if (a.M <= 16)
-        return launch_rows<F8_DENSE, 1, 4>(a, dim3(nt, 1), 0, s);
-    if (a.M <= 32)
-        return launch_rows<F8_DENSE, 2, 4>(a, dim3(nt, 1), 0, s);
-    return launch_rows<F8_DENSE, 4, 4>(a, dim3(nt, (unsigned)((a.M + 63) / 64)), 0, s);
-}
-
-// The fewest blocks in flight that cover K in one round, at most four: a round
-// past the end re-reads the last block.
-template <int MODE>
-static int launch_rows_kp(const Fp8Args &a, dim3 grid, size_t lds, hipStream_t s)
-{
-    switch ((a.K + 511) / 512) {
-    case 1: return launch_rows<MODE, 1, 1>(a, grid, lds, s);
-    case 2: return launch_rows<MODE, 1, 2>(a, grid, lds, s);
-    case 3: return launch_rows<MODE, 1, 3>(a, grid, lds, s);
-    default: return launch_rows<MODE, 1, 4>(a, grid, lds, s);
-    }
+        return launch_rows<F8_DENSE, 1>(a, dim3(nt, 1), 0, s);
+    return launch_rows<F8_DENSE, 2>(a, dim3(nt, (unsigned)((a.M + 31) / 32)), 0, s);
 }
 
 // Decode experts: gate/up with SwiGLU into fp32 h, then down.
@@ -308,7 +325,7 @@ int launch_fp8_decode(Fp8Args a, const void *x_f16, float *h, int H, int I, cons
     a.off_s0 = off[3];
     a.off_s1 = off[4];
     const unsigned n = (unsigned)(a.T * a.k);
-    const int rc = launch_rows_kp<F8_GATEUP>(a, dim3((I + 15) / 16, n), lds(H), s);
+    const int rc = launch_rows<F8_GATEUP, 1>(a, dim3((I + 15) / 16, n), lds(H), s);
     if (rc)
         return rc;
     a.src = h;
@@ -318,7 +335,7 @@ int launch_fp8_decode(Fp8Args a, const void *x_f16, float *h, int H, int I, cons
     a.ldo = H;
     a.off_w0 = a.off_w1 = off[2];
     a.off_s0 = a.off_s1 = off[5];
-    return launch_rows_kp<F8_DOWN>(a, dim3((H + 31) / 32, n), lds(I), s);
+    return launch_rows<F8_DOWN, 1>(a, dim3((H + 31) / 32, n), lds(I), s);
 }
 
 }  // namespace moe

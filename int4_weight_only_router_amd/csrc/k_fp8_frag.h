@@ -106,6 +106,7 @@ __device__ __forceinline__ float row16_max(float a)
 
 enum { F8_DENSE = 0, F8_GATEUP = 1, F8_DOWN = 2 };
 constexpr int FP8_DECODE_MAX_T = 16;   // routed experts: decode kernels up to this many tokens
+constexpr int FP8_DECODE_BLOCKS = 600;   // and 128-blocks of quantised rows in LDS (132 bytes each)
 
 // One row tile of the routed experts: its expert's blob, first sorted row and
 // rows.  Entry 0 of a table holds the number of tiles in `rows`.

@@ -463,13 +463,23 @@ static int launch_tile_mf(const Fp8Args &a, int mf, int64_t items, hipStream_t s
     }
 }
 
-int launch_fp8_tile_dense(const Fp8Args &a, hipStream_t s)
+template <int MF>
+static int launch_tile_dense(const Fp8Args &a, hipStream_t s)
 {
-    constexpr int mf = 4;
-    const int64_t items = (int64_t)((a.M + 64 * mf - 1) / (64 * mf)) * ((a.N + 255) / 256);
+    const int64_t items = (int64_t)((a.M + 64 * MF - 1) / (64 * MF)) * ((a.N + 255) / 256);
     if (a.odt == MOE_DTYPE_F32)
-        return launch_tile<F8_DENSE, mf, true>(a, items, s);
-    return launch_tile<F8_DENSE, mf, false>(a, items, s);
+        return launch_tile<F8_DENSE, MF, true>(a, items, s);
+    return launch_tile<F8_DENSE, MF, false>(a, items, s);
+}
+
+int launch_fp8_tile_dense(const Fp8Args &a, int mf, hipStream_t s)
+{
+    switch (mf) {
+    case 1: return launch_tile_dense<1>(a, s);
+    case 2: return launch_tile_dense<2>(a, s);
+    case 3: return launch_tile_dense<3>(a, s);
+    default: return launch_tile_dense<4>(a, s);
+    }
 }
 
 // Rows of a row tile, 64, 128 or 192, from the mean rows of an expert; fewer

@@ -141,7 +141,8 @@ def _product(M_, N, K, dtype, ldx=None, ldw=None, ldo=None, seed=0):
 
 SHAPES = [(1, 1, 16), (1, 32, 128), (1, 5632, 2048), (3, 33, 48), (16, 100, 192), (17, 130, 144),
           (33, 64, 2048), (64, 257, 1040), (65, 31, 80), (333, 1408, 2000), (100, 2048, 4096)]
-TILES = [(1600, 4000, 64), (1531, 4117, 400), (4096, 1536, 256), (130, 24700, 144)]
+TILES = [(1600, 4000, 64), (1531, 4117, 400), (4096, 1536, 256), (130, 24700, 144),
+         (1000, 1500, 272), (700, 5000, 144), (2500, 5000, 80), (2000, 9000, 48)]
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
@@ -249,7 +250,7 @@ FFN = [   # T, H, I, E, k, regime
     (1, 256, 512, 8, 2, 0), (1, 2048, 1024, 16, 8, 0), (4, 256, 192, 8, 2, 0),
     (3, 320, 64, 5, 3, 0), (1, 64, 64, 1, 1, 0), (4, 256, 192, 8, 2, M.MOE_REGIME_BATCHED),
     (5, 256, 192, 8, 2, 0), (16, 320, 64, 5, 3, M.MOE_REGIME_DECODE), (16, 320, 64, 5, 3, 0),
-    (11, 2048, 1408, 6, 2, 0), (1, 8192, 64, 2, 1, 0), (16, 64, 8192, 2, 2, 0), (40, 512, 320, 8, 4, 0),
+    (11, 2048, 1408, 6, 2, 0), (1, 8192, 64, 2, 1, 0), (9, 64, 8192, 2, 2, 0), (10, 64, 8192, 2, 2, 0), (40, 512, 320, 8, 4, 0),
     (100, 256, 192, 4, 2, 0), (300, 512, 448, 3, 1, 0), (70, 2048, 512, 70, 4, 0)]
 
 
