@@ -531,8 +531,8 @@ int moe_router_logits(const void *x_f16, const void *w_router_f16, const float *
  * launch for one token (and up to 16 with T * E <= 8192), in one more up to
  * 8192 tokens of 768 experts, else by moe_permute's launches.
  *   ws  device scratch of moe_route_select_workspace_bytes(T, k, E) bytes (may
- *       be 0; no initialisation needed); MOE_ENOMEM if too small.  Calls that
- *       share it must not overlap.
+ *       be 0; no initialisation needed), 16-byte aligned; MOE_ENOMEM if too
+ *       small.  Calls that share it must not overlap.
  */
 int moe_route_select(const void *logits, int logits_dtype, int64_t ld, const float *select_bias,
                      int T, int E, int k, int score, int n_group, int topk_group, unsigned flags,
@@ -572,7 +572,8 @@ int moe_quantize_fp8(const void *x, int dtype, int64_t ldx, int64_t rows, int co
  *   xq  device e4m3 [M], ldx bytes apart;  x_scales device fp32 [M][ceil(K/128)]
  *   wq  device e4m3 [N], ldw bytes apart;  w_scales [ceil(N/128)][ceil(K/128)]
  *   out device [M] rows of N values (F16, BF16 or F32), ldo elements apart
- * Any M and N.  K, ldx and ldw multiples of 16, K <= 16384 (MOE_EUNSUPPORTED);
+ * Any M and N (M <= 2097120 where ldw >= 2^22).  K, ldx and ldw multiples of
+ * 16, K <= 16384 (MOE_EUNSUPPORTED);
  * xq and wq 16-byte aligned (MOE_EINVAL).  out must not overlap the inputs.
  * M = 0: no-op.  No workspace.
  */

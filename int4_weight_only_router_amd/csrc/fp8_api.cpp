@@ -216,7 +216,7 @@ int moe_route_select_permute(const void *logits, int logits_dtype, int64_t ld,
     const size_t need = moe_route_select_workspace_bytes(T, k, E);
     if (need && (!ws || ws_bytes < need))
         return set_error(MOE_ENOMEM, "%s: workspace %zu < %zu bytes", fn, ws_bytes, need);
-    if (need && (uintptr_t)ws % 4)
+    if (need && (uintptr_t)ws % 16)
         return set_error(MOE_EINVAL, "%s: misaligned workspace", fn);
     return launch_route_select(logits, logits_dtype, ld, select_bias, T, E, k, score, n_group,
                                topk_group, flags, scale, topk_idx, topk_w, counts, offsets, perm,
@@ -289,9 +289,10 @@ int moe_gemm_fp8(const void *xq, int64_t ldx, const float *x_scales, const void 
     a.odt = out_dtype;
     const int mf = dense_tile(M, N, out_dtype == MOE_DTYPE_F32);
     // (the tile kernel's offsets inside 256 weight rows are 32 bits wide)
-    if (mf && ldw < (int64_t)1 << 22)
-        return launch_fp8_tile_dense(a, mf, stream);
-    if ((M + 31) / 32 > 65535)
+    const bool few_rows = (M + 31) / 32 <= 65535;   // its grid's second dimension
+    if (ldw < (int64_t)1 << 22 && (mf || !few_rows))
+        return launch_fp8_tile_dense(a, mf ? mf : 4, stream);
+    if (!few_rows)
         return set_error(MOE_EUNSUPPORTED, "%s: M=%d with ldw=%lld", fn, M, (long long)ldw);
     return launch_fp8_rows_dense(a, stream);
 }

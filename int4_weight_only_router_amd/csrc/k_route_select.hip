@@ -51,7 +51,7 @@ int launch_permute(const int32_t *, int, int, int, int32_t *, int32_t *, int32_t
 struct SelScratch {
     uint32_t key[64];
     double score[64];
-    uint64_t ckey[64];
+    uint64_t ckey[64 + 4];   // and four zeros behind the last candidate
     int cidx[64];
 };
 
@@ -377,18 +377,29 @@ __device__ __forceinline__ SelOut select_token(const SelArgs &a, int t, int lane
             }
             base += __popcll(m);
         }
+        if (lane < 4)
+            sc->ckey[n + lane] = 0ull;
         wave_lds_sync();
-        if (lane < n) {
-            const uint64_t me = sc->ckey[lane];
-            e = sc->cidx[lane];
-            sv = sc->score[lane];
-            int r = 0;
-            for (int j = 0; j < n; ++j) {
-                const uint64_t o = sc->ckey[j];
-                r += (o > me || (o == me && sc->cidx[j] < e)) ? 1 : 0;
+        const uint64_t me = lane < n ? sc->ckey[lane] : ~0ull;
+        e = sc->cidx[lane];
+        sv = sc->score[lane];
+        int above = 0, same = 0;
+        for (int j = 0; j < n; j += 4) {
+            const uint4_t u = *reinterpret_cast<const uint4_t *>(&sc->ckey[j]);
+            const uint4_t v = *reinterpret_cast<const uint4_t *>(&sc->ckey[j + 2]);
+            const uint64_t o[4] = {((uint64_t)u.y << 32) | u.x, ((uint64_t)u.w << 32) | u.z,
+                                   ((uint64_t)v.y << 32) | v.x, ((uint64_t)v.w << 32) | v.z};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                above += o[i] > me ? 1 : 0;
+                same += o[i] == me ? 1 : 0;
             }
-            rank = r;
         }
+        if (__any(lane < n && same > 1)) {   // ties: the lower expert first
+            for (int j = 0; j < n; ++j)
+                above += sc->ckey[j] == me && sc->cidx[j] < e ? 1 : 0;
+        }
+        rank = lane < n ? above : 64;
     } else {
         for (int j = 0; j < k; ++j) {
             uint64_t best = key[0];
@@ -552,16 +563,16 @@ __global__ __launch_bounds__(RSC_WAVES * 64) void route_select_count_kernel(
         }
     }
     lds_barrier();
-    const int pitch = (a.E + 3) & ~3;
+    const int pitch = (a.E + 15) & ~15;
     if ((int)threadIdx.x < pitch)   // cnt past E is zero
         hist[(size_t)blockIdx.x * pitch + threadIdx.x] = (uint8_t)cnt[threadIdx.x];
 }
 
 // Second launch: workgroup b places chunk b's elements.  Thread (g, e) adds up
-// every G-th chunk's counts of experts 4e..4e+3, in all chunks and in those
-// before b (16-bit lanes: at most 16 * RSC_MAX_T / RSC_TOK / G).
+// every G-th chunk's counts of experts 16e..16e+15, in all chunks and in those
+// before b (16-bit lanes: at most 16 * RSC_MAX_T / RSC_TOK).
 __global__ __launch_bounds__(1024) void route_place_kernel(
-    const int32_t *__restrict__ idx, const uint32_t *__restrict__ hist, int T, int k, int E,
+    const int32_t *__restrict__ idx, const uint4_t *__restrict__ hist, int T, int k, int E,
     int chunks, int32_t *__restrict__ counts, int32_t *__restrict__ offsets,
     int32_t *__restrict__ perm, int32_t *__restrict__ inv_perm)
 {
@@ -571,32 +582,43 @@ __global__ __launch_bounds__(1024) void route_place_kernel(
     tot[tid] = 0;
     pre[tid] = 0;
     lds_barrier();
-    const int E4 = (E + 3) / 4, G = 1024 / E4, g = tid / E4, e = tid - g * E4;
-    if (g < G) {
-        uint32_t all0 = 0, all1 = 0, pre0 = 0, pre1 = 0;   // experts 4e, 4e+2; 4e+1, 4e+3
-        for (int b0 = g; b0 < chunks; b0 += 8 * G) {
-            uint32_t h[8];
+    const int EV = (E + 15) / 16, G = 1024 / EV, g = tid / EV, e = tid - g * EV;
+    if (g < G && g < chunks) {
+        uint32_t all[8], bef[8];   // [2 w + h]: experts 4w + h and 4w + h + 2
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                h[i] = hist[(size_t)min(b0 + i * G, chunks - 1) * E4 + e];
+        for (int i = 0; i < 8; ++i)
+            all[i] = bef[i] = 0u;
+        for (int b0 = g; b0 < chunks; b0 += 4 * G) {
+            uint4_t h[4];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < 4; ++i)
+                h[i] = hist[(size_t)min(b0 + i * G, chunks - 1) * EV + e];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
                 const int b = b0 + i * G;
-                const uint32_t v = b < chunks ? h[i] : 0u, u = b < mine ? v : 0u;
-                all0 += v & 0x00ff00ffu;
-                all1 += (v >> 8) & 0x00ff00ffu;
-                pre0 += u & 0x00ff00ffu;
-                pre1 += (u >> 8) & 0x00ff00ffu;
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    const uint32_t v = b < chunks ? h[i][w] : 0u, u = b < mine ? v : 0u;
+                    all[2 * w] += v & 0x00ff00ffu;
+                    all[2 * w + 1] += (v >> 8) & 0x00ff00ffu;
+                    bef[2 * w] += u & 0x00ff00ffu;
+                    bef[2 * w + 1] += (u >> 8) & 0x00ff00ffu;
+                }
             }
         }
-        atomicAdd(&tot[4 * e], (int)(all0 & 0xffffu));
-        atomicAdd(&tot[4 * e + 1], (int)(all1 & 0xffffu));
-        atomicAdd(&tot[4 * e + 2], (int)(all0 >> 16));
-        atomicAdd(&tot[4 * e + 3], (int)(all1 >> 16));
-        atomicAdd(&pre[4 * e], (int)(pre0 & 0xffffu));
-        atomicAdd(&pre[4 * e + 1], (int)(pre1 & 0xffffu));
-        atomicAdd(&pre[4 * e + 2], (int)(pre0 >> 16));
-        atomicAdd(&pre[4 * e + 3], (int)(pre1 >> 16));
+        // zeros are most of a chunk's counts: only the others meet in LDS
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int at = 16 * e + 4 * (i >> 1) + (i & 1);
+            if (all[i] & 0xffffu)
+                atomicAdd(&tot[at], (int)(all[i] & 0xffffu));
+            if (all[i] >> 16)
+                atomicAdd(&tot[at + 2], (int)(all[i] >> 16));
+            if (bef[i] & 0xffffu)
+                atomicAdd(&pre[at], (int)(bef[i] & 0xffffu));
+            if (bef[i] >> 16)
+                atomicAdd(&pre[at + 2], (int)(bef[i] >> 16));
+        }
     }
     lds_barrier();
     const int c = tid < E ? tot[tid] : 0;
@@ -675,7 +697,7 @@ static int launch_select_t(const SelArgs &a, const SelSort &how, hipStream_t st)
                                dim3(RSC_WAVES * 64), g * RSC_WAVES, st, a, how.hist);
             MOE_LAUNCH_CHECK("route_select_count_kernel");
             hipLaunchKernelGGL(route_place_kernel, dim3(chunks), dim3(1024), 0, st, a.idx,
-                               reinterpret_cast<const uint32_t *>(how.hist),
+                               reinterpret_cast<const uint4_t *>(how.hist),
                                a.T, a.k, a.E, chunks, how.counts, how.offsets, how.perm,
                                how.inv_perm);
             MOE_LAUNCH_CHECK("route_place_kernel");
@@ -714,7 +736,7 @@ size_t route_select_ws_bytes(int T, int k, int E)
 {
     switch (sort_kind(T, E)) {
     case SORT_INSIDE: return T > 0 ? 0 : permute_ws_bytes(T, k, E);
-    case SORT_CHUNKS: return (size_t)al256((int64_t)((T + RSC_TOK - 1) / RSC_TOK) * ((E + 3) & ~3));
+    case SORT_CHUNKS: return (size_t)al256((int64_t)((T + RSC_TOK - 1) / RSC_TOK) * ((E + 15) & ~15));
     default: return permute_ws_bytes(T, k, E);
     }
 }

@@ -45,6 +45,7 @@ def test_select_permute_refusals():
     assert need > 0
     assert _code(M.moe_route_select_permute, *big, P, P, P, P, P, need - 1, stream=0) == ENOMEM
     assert _code(M.moe_route_select_permute, *big, P, P, P, P, None, need, stream=0) == ENOMEM
+    assert _code(M.moe_route_select_permute, *big, P, P, P, P, P + 8, need, stream=0) == EINVAL
     assert M.moe_route_select_workspace_bytes(1, 8, 64) == 0
     M.moe_route_select(*_select(T=0, logits=None, idx=None, w=None), stream=0)   # no-op
 
@@ -86,7 +87,8 @@ def _gemm(xq=P, ldx=256, xs=P, wq=P, ldw=256, ws=P, m=4, n=64, k=256, out=P, dt=
     (dict(k=16400, ldx=16400, ldw=16400), EUNSUP), (dict(xq=None), EINVAL), (dict(xs=None), EINVAL),
     (dict(wq=None), EINVAL), (dict(ws=None), EINVAL), (dict(out=None), EINVAL),
     (dict(xq=P + 8), EINVAL), (dict(wq=P + 4), EINVAL), (dict(xs=P + 2), EINVAL),
-    (dict(out=P + 1), EINVAL), (dict(out=P + 2, dt=F32), EINVAL)])
+    (dict(out=P + 1), EINVAL), (dict(out=P + 2, dt=F32), EINVAL),
+    (dict(m=2097121, ldw=1 << 22), EUNSUP)])
 def test_product_refusals(kw, code):
     assert _code(M.moe_gemm_fp8, *_gemm(**kw), stream=0) == code
 
