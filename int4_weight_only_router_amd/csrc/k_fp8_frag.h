@@ -35,17 +35,20 @@ __device__ __forceinline__ int8_8 join16(int4_t lo, int4_t hi)
 struct half32 {
     half8_t v[4];
 };
+// Pair u (0..15) of them: one conversion.
+__device__ __forceinline__ void f8_pair(half32 &r, int8_8 x, int u)
+{
+    const half2_t a = u & 1 ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(x[u >> 1], 1.0f, true)
+                            : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(x[u >> 1], 1.0f, false);
+    r.v[u >> 2][2 * (u & 3)] = a[0];
+    r.v[u >> 2][2 * (u & 3) + 1] = a[1];
+}
 __device__ __forceinline__ half32 f8_to_f16(int8_8 x)
 {
     half32 r;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const half2_t a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(x[2 * j], 1.0f, false);
-        const half2_t b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(x[2 * j], 1.0f, true);
-        const half2_t c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(x[2 * j + 1], 1.0f, false);
-        const half2_t d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(x[2 * j + 1], 1.0f, true);
-        r.v[j] = half8_t{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
-    }
+    for (int u = 0; u < 16; ++u)
+        f8_pair(r, x, u);
     return r;
 }
 

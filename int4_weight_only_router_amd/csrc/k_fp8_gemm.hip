@@ -22,8 +22,8 @@
 //    to a neighbouring code (measured: the experts' error against 64 bits goes
 //    from 3e-4 to 1.1e-3).
 //
-// fp8_tile_kernel: eight waves own 64*MF rows x 256 weight rows, wave w the
-// 16*MF rows of row group w / 2 and 128 of the weight rows.  Both operands'
+// fp8_tile_kernel: eight waves own 64*MF rows x 256 weight rows, wave w 16 of
+// each 64 rows (MF row fragments) and 128 of the weight rows.  Both operands'
 // blocks travel to LDS by direct-to-LDS loads, 8 lanes per 128-byte row block,
 // into a ring of two or three stages: one barrier per block, and a block has
 // the whole work of another to arrive.  (Read straight into registers in the
@@ -45,6 +45,11 @@
 namespace moe {
 
 constexpr int F8_NXCD = 8;
+// Dense items go through F8_GROUP row tiles before the next column tile: the
+// tiles in flight on an XCD (one per compute unit, 32) then make a patch of
+// 4 x 8, whose rows and weights together stay in its L2.  4096 x 11264 x 2048,
+// cold: 117 us, against 122 in groups of 8 and 131 through all 16 row tiles.
+constexpr int F8_GROUP = 4;
 
 // The work item of a workgroup: column tile nt of row tile mt.  Workgroup i
 // runs on XCD i % 8; each XCD takes a contiguous run of items, so that the
@@ -61,8 +66,15 @@ __device__ __forceinline__ bool f8_item(int MT, int NT, F8Item &it)
     const int item = (int)(blockIdx.x % F8_NXCD) * run + li;
     if (li >= run || item >= total)
         return false;
-    it.mt = MODE == F8_DENSE ? item % MT : item / NT;
-    it.nt = MODE == F8_DENSE ? item / MT : item % NT;
+    if constexpr (MODE == F8_DENSE) {
+        const int g = item / (F8_GROUP * NT), r = item - g * F8_GROUP * NT;
+        const int gm = min(F8_GROUP, MT - g * F8_GROUP);
+        it.mt = g * F8_GROUP + r % gm;
+        it.nt = r / gm;
+    } else {
+        it.mt = item / NT;
+        it.nt = item % NT;
+    }
     return true;
 }
 
@@ -143,7 +155,7 @@ __global__ __launch_bounds__(512, 1) void fp8_tile_kernel(Fp8Args a)
     extern __shared__ __align__(16) uint8_t smem[];
     const int tid = threadIdx.x;
     const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int m0 = (wave >> 1) * 16 * MF, wn = wave & 1;
+    const int m0 = (wave >> 1) * 16, wn = wave & 1;   // fragment m: rows m0 + 64 m
     const int col = lane & 15, q = lane >> 4;
     const int K = a.K, nkb = (K + 127) / 128;
 
@@ -231,9 +243,9 @@ __global__ __launch_bounds__(512, 1) void fp8_tile_kernel(Fp8Args a)
     auto wrow = [&](int f) {
         return (MODE == F8_GATEUP ? (f >> 2) * 128 + wn * 64 + (f & 3) * 16 : wn * 128 + f * 16) + col;
     };
-    const bool idle = m0 >= t.rows;   // no row of this wave's group exists
-
-    auto block = [&](int kb, auto tail) {
+    // MA: the wave's row fragments that hold a row of the tile
+    auto block = [&](int kb, auto tail, auto ma) {
+        constexpr int MA = decltype(ma)::value;
         // this wave's loads of block kb have landed (those of the NS - 2
         // blocks after it may be pending); after the barrier everyone's have,
         // and the stage of block kb - 1 is read by all
@@ -241,10 +253,10 @@ __global__ __launch_bounds__(512, 1) void fp8_tile_kernel(Fp8Args a)
         lds_barrier();
         if (kb && kb % F8_SCW == 0 && (kb / F8_SCW + 1) * F8_SCW < nkb)
             scales(kb / F8_SCW + 1);   // the window before this one is read by all
-        if (idle) {
+        if constexpr (MA == 0) {
             issue(kb + NS - 1);
             return;
-        }
+        } else {
         const uint8_t *st = smem + (kb % NS) * STAGE;
         auto frag = [&](const uint8_t *r) {
             return join16(*reinterpret_cast<const int4_t *>(r + o0),
@@ -254,38 +266,40 @@ __global__ __launch_bounds__(512, 1) void fp8_tile_kernel(Fp8Args a)
         // only
         constexpr int WD = EX && MF == 4 ? 1 : 2;   // weight fragments read ahead
         constexpr bool WC = EX && WD == 2;          // and converted one ahead
-        int8_8 x[MF], w[WD + 1];
-        half32 xh[MF];
-        float sc[MF][2];
+        int8_8 x[MA], w[WD + 1];
+        half32 xh[MA];
+        float sc[MA][2];
         const float *xs = xsc + (kb & (2 * F8_SCW - 1)) * BM + m0 + col;
         w[0] = frag(st + XB + wrow(0) * 128);
 #pragma unroll
-        for (int m = 0; m < MF; ++m) {
-            x[m] = frag(st + (m0 + m * 16 + col) * 128);
+        for (int m = 0; m < MA; ++m) {
+            x[m] = frag(st + (m * 64 + m0 + col) * 128);
             __builtin_amdgcn_sched_barrier(0);
         }
         if constexpr (WD == 2)
             w[1] = frag(st + XB + wrow(1) * 128);
         const float wg = wsc[MODE == F8_GATEUP ? kb : wn * nkb + kb];
         const float wu = MODE == F8_GATEUP ? wsc[nkb + kb] : wg;
-        float xv[MF];
+        float xv[MA];
 #pragma unroll
-        for (int m = 0; m < MF; ++m)
-            xv[m] = xs[m * 16];
+        for (int m = 0; m < MA; ++m)
+            xv[m] = xs[m * 64];
         __builtin_amdgcn_sched_barrier(0);
-        auto ready = [&](int m) {   // before fragment m's first sum
-            if constexpr (decltype(tail)::value)
+        if constexpr (decltype(tail)::value) {
+#pragma unroll
+            for (int m = 0; m < MA; ++m)
                 x[m] = f8_cut(x[m], kb, q, K);
-            if constexpr (EX)
-                xh[m] = f8_to_f16(x[m]);
-        };
+        }
         half32 wh[WC ? 2 : 1];
         float4_t s[4];
+        auto add1 = [&](int i, int j) {
+            const int f = i / MA, m = i % MA;
+            acc[m][f][j] = __builtin_fmaf(s[i & 3][j], sc[m][f >> 2], acc[m][f][j]);
+        };
         auto add = [&](int i) {
-            const int f = i / MF, m = i % MF;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                acc[m][f][j] = __builtin_fmaf(s[i & 3][j], sc[m][f >> 2], acc[m][f][j]);
+                add1(i, j);
         };
 #pragma unroll
         for (int f = 0; f < 8; ++f) {
@@ -298,40 +312,76 @@ __global__ __launch_bounds__(512, 1) void fp8_tile_kernel(Fp8Args a)
             for (int i = 0; i < PX + PW; ++i)
                 if (i * 4 / (PX + PW) == f)
                     issue1(kb + NS - 1, i);
-            if constexpr (EX)
+            if constexpr (EX) {
                 if (!WC || f == 0)
                     wh[WC ? f & 1 : 0] = f8_to_f16(w[f % (WD + 1)]);
+                if (f == 0)
+                    xh[0] = f8_to_f16(x[0]);
+            }
             __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-            for (int m = 0; m < MF; ++m) {
-                const int i = f * MF + m;
-                if (f == 0)
-                    ready(m);
-                if constexpr (EX)
-                    s[i & 3] = mfma_f16(wh[WC ? f & 1 : 0], xh[m]);
-                else
-                    s[i & 3] = mfma_f8(w[f % (WD + 1)], x[m]);
+            for (int m = 0; m < MA; ++m) {
+                const int i = f * MA + m;
                 if (f == 0) {
                     sc[m][0] = xv[m] * wg;
                     sc[m][1] = MODE == F8_GATEUP ? xv[m] * wu : sc[m][0];
                 }
-                if (i >= 2)
-                    add(i - 2);
-                // keeps the steps in order: left to itself the scheduler
-                // hoists reads and sums until the registers run out
-                __builtin_amdgcn_sched_barrier(0);
-                if constexpr (WC)
-                    if (m == 0 && f + 1 < 8)
-                        wh[(f + 1) & 1] = f8_to_f16(w[(f + 1) % (WD + 1)]);
+                if constexpr (EX) {
+                    // three vector instructions fit behind each of the four
+                    // matrix instructions of a sum: an earlier sum's scaling
+                    // and the conversions of the fragments that come next
+                    s[i & 3] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        s[i & 3] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                            wh[WC ? f & 1 : 0].v[j], xh[m].v[j], s[i & 3], 0, 0, 0);
+                        if (i >= 2)
+                            add1(i - 2, j);
+                        if (f == 0 && m + 1 < MA)
+#pragma unroll
+                            for (int u = 4 * j; u < 4 * j + 4; ++u)
+                                f8_pair(xh[m + 1 < MA ? m + 1 : 0], x[m + 1 < MA ? m + 1 : 0], u);
+                        if constexpr (WC)
+                            if (f + 1 < 8)
+#pragma unroll
+                                for (int u = (4 * m + j) * 4 / MA; u < (4 * m + j + 1) * 4 / MA; ++u)
+                                    f8_pair(wh[(f + 1) & 1], w[(f + 1) % (WD + 1)], u);
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                } else {
+                    s[i & 3] = mfma_f8(w[f % (WD + 1)], x[m]);
+                    if (i >= 2)
+                        add(i - 2);
+                    // keeps the steps in order: left to itself the scheduler
+                    // hoists reads and sums until the registers run out
+                    __builtin_amdgcn_sched_barrier(0);
+                }
             }
             __builtin_amdgcn_s_setprio(0);
         }
-        add(8 * MF - 2);
-        add(8 * MF - 1);
+        add(8 * MA - 2);
+        add(8 * MA - 1);
+        }
     };
-    for (int kb = 0; kb + 1 < nkb; ++kb)
-        block(kb, std::false_type());
-    block(nkb - 1, std::true_type());
+    auto blocks = [&](auto ma) {
+        for (int kb = 0; kb + 1 < nkb; ++kb)
+            block(kb, std::false_type(), ma);
+        block(nkb - 1, std::true_type(), ma);
+    };
+    // A short tile's fragments are dealt out over the waves, and each takes the
+    // loop of as many as it has: an expert's last tile costs what it holds
+    // (rounded up to 64 rows), not its full height.
+    const int act = t.rows > m0 ? min(MF, (t.rows - m0 + 63) >> 6) : 0;
+    if (act == MF)
+        blocks(std::integral_constant<int, MF>());
+    else if (MF > 3 && act == 3)
+        blocks(std::integral_constant<int, std::min(MF, 3)>());
+    else if (MF > 2 && act == 2)
+        blocks(std::integral_constant<int, std::min(MF, 2)>());
+    else if (MF > 1 && act == 1)
+        blocks(std::integral_constant<int, 1>());
+    else
+        blocks(std::integral_constant<int, 0>());
     wait_vm<0>();   // trailing loads into LDS are done before it is reused
 
     if constexpr (MODE == F8_GATEUP) {
@@ -353,12 +403,12 @@ __global__ __launch_bounds__(512, 1) void fp8_tile_kernel(Fp8Args a)
             top = fmaxf(top, __shfl_xor(top, 16, 64));
             top = fmaxf(top, __shfl_xor(top, 32, 64));
             if (q == 0)
-                mx[wn * BM + m0 + m * 16 + col] = top;
+                mx[wn * BM + m * 64 + m0 + col] = top;
         }
         __syncthreads();
 #pragma unroll
         for (int m = 0; m < MF; ++m) {
-            const int r = m0 + m * 16 + col;
+            const int r = m * 64 + m0 + col;
             const float sc = fp8_scale(fmaxf(mx[r], mx[BM + r]), true), inv = fp8_inv_pow2(sc);
 #pragma unroll
             for (int f = 0; f < 4; ++f)
@@ -393,7 +443,7 @@ __global__ __launch_bounds__(512, 1) void fp8_tile_kernel(Fp8Args a)
 #pragma unroll
             for (int mm = 0; mm < MH; ++mm) {
                 const int m = h * MH + mm;
-                const int r = (wave >> 1) * 16 * MH + mm * 16 + col;
+                const int r = mm * 64 + m0 + col;
 #pragma unroll
                 for (int f = 0; f < 8; ++f)
                     store4(smem + r * LR, dt, wn * 128 + f * 16 + q * 4, acc[m][f], 4, true);
@@ -402,7 +452,7 @@ __global__ __launch_bounds__(512, 1) void fp8_tile_kernel(Fp8Args a)
             constexpr int np = 256 / gp;   // pieces of a row
             for (int i = tid; i < 64 * MH * np; i += NTH) {
                 const int lr2 = i / np, c = (i % np) * gp;
-                const int r = (lr2 / (16 * MH)) * 16 * MF + h * 16 * MH + lr2 % (16 * MH);
+                const int r = h * 64 * MH + lr2;
                 const int n = n0 + c;
                 if (r >= t.rows || n >= a.N)
                     continue;
