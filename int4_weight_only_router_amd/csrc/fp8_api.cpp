@@ -89,7 +89,7 @@ static Fp8Ws fp8_ws(int T, int H, int I, int E, int k, bool decode)
 
 // Kernel of a dense product: 64*mf x 256 tiles, or 0 for the kernel of few rows
 // (32 x 32 tiles).  The least of the times that were measured for one round of
-// tiles over the 256 compute units at K = 2048 (every form grows with K alike),
+// tiles over the 256 compute units at K = 2048 (every form grows alike with K),
 // in us: 64-, 128-, 192- and 256-row tiles 13.5, 21, 27, 31, and 26, 37, 46,
 // 54 with fp32 outputs (the fp16 form); the kernel of few rows 2.5 and 9.8 for
 // every 1000 workgroups.  Against each form on 17 shapes from 64 x 5632 to
@@ -113,7 +113,7 @@ static int dense_tile(int M, int N, bool f32)
 
 static int check_select(const char *fn, const void *logits, int dtype, int64_t ld, int T, int E,
                         int k, int score, int n_group, int topk_group, unsigned flags, float scale,
-                        const int32_t *topk_idx, const float *topk_w)
+                        const float *bias, const int32_t *topk_idx, const float *topk_w)
 {
     if (T < 0 || E <= 0 || k <= 0 || k > E)
         return set_error(MOE_EINVAL, "%s: need T >= 0, E > 0, 0 < k <= E (T=%d E=%d k=%d)", fn, T,
@@ -139,12 +139,13 @@ static int check_select(const char *fn, const void *logits, int dtype, int64_t l
         return set_error(MOE_EUNSUPPORTED,
                          "%s: E <= 1024, k <= 16 and at most 64 groups required (E=%d k=%d "
                          "groups=%d)", fn, E, k, n_group);
-    if ((int64_t)T * k >= (int64_t)1 << 31)
-        return set_error(MOE_EUNSUPPORTED, "%s: T*k too large", fn);
+    if (T > 1 << 25)   // a wave per token, and a launch has fewer than 2^32 threads
+        return set_error(MOE_EUNSUPPORTED, "%s: T=%d above 2^25", fn, T);
     if (T > 0 && (!logits || !topk_idx || !topk_w))
         return set_error(MOE_EINVAL, "%s: null pointer", fn);
-    if ((uintptr_t)logits % dtype_size(dtype))
-        return set_error(MOE_EINVAL, "%s: misaligned logits", fn);
+    if ((uintptr_t)logits % dtype_size(dtype) ||
+        ((uintptr_t)bias | (uintptr_t)topk_idx | (uintptr_t)topk_w) % 4)
+        return set_error(MOE_EINVAL, "%s: misaligned pointer", fn);
     return MOE_OK;
 }
 
@@ -183,7 +184,7 @@ int moe_route_select(const void *logits, int logits_dtype, int64_t ld, const flo
     MOE_API_RANGE();
     clear_error();
     const int rc = check_select("moe_route_select", logits, logits_dtype, ld, T, E, k, score,
-                                n_group, topk_group, flags, scale, topk_idx, topk_w);
+                                n_group, topk_group, flags, scale, select_bias, topk_idx, topk_w);
     if (rc || T == 0)
         return rc;
     return launch_route_select(logits, logits_dtype, ld, select_bias, T, E, k, score, n_group,
@@ -208,11 +209,13 @@ int moe_route_select_permute(const void *logits, int logits_dtype, int64_t ld,
     clear_error();
     const char *fn = "moe_route_select_permute";
     int rc = check_select(fn, logits, logits_dtype, ld, T, E, k, score, n_group, topk_group, flags,
-                          scale, topk_idx, topk_w);
+                          scale, select_bias, topk_idx, topk_w);
     if (rc)
         return rc;
     if (!counts || !offsets || (T > 0 && (!perm || !inv_perm)))
         return set_error(MOE_EINVAL, "%s: null pointer", fn);
+    if (((uintptr_t)counts | (uintptr_t)offsets | (uintptr_t)perm | (uintptr_t)inv_perm) % 4)
+        return set_error(MOE_EINVAL, "%s: misaligned pointer", fn);
     const size_t need = moe_route_select_workspace_bytes(T, k, E);
     if (need && (!ws || ws_bytes < need))
         return set_error(MOE_ENOMEM, "%s: workspace %zu < %zu bytes", fn, ws_bytes, need);
@@ -239,6 +242,9 @@ int moe_quantize_fp8(const void *x, int dtype, int64_t ldx, int64_t rows, int co
         return set_error(MOE_EINVAL, "%s: blocks of %d rows (1 or 128)", fn, block_rows);
     if (flags & ~(unsigned)MOE_SCALE_POW2)
         return set_error(MOE_EINVAL, "%s: unknown flags 0x%x", fn, flags);
+    // a row of blocks must fit one launch, and the blocks' number 64 bits
+    if (cols > 1 << 30 || rows > (1LL << 36) / ((cols + 127) / 128))
+        return set_error(MOE_EUNSUPPORTED, "%s: rows=%lld cols=%d", fn, (long long)rows, cols);
     if (rows == 0)
         return MOE_OK;
     if (!x || !q || !scales)
@@ -266,6 +272,8 @@ int moe_gemm_fp8(const void *xq, int64_t ldx, const float *x_scales, const void 
         return set_error(MOE_EUNSUPPORTED,
                          "%s: K (at most 16384), ldx and ldw must be multiples of 16 (K=%d "
                          "ldx=%lld ldw=%lld)", fn, K, (long long)ldx, (long long)ldw);
+    if (M > 0x7fffff00 || N > 0x7fffff00)   // whole tiles stay within an int
+        return set_error(MOE_EUNSUPPORTED, "%s: M=%d N=%d", fn, M, N);
     if (M == 0)
         return MOE_OK;
     if (!xq || !x_scales || !wq || !w_scales || !out)
@@ -289,11 +297,12 @@ int moe_gemm_fp8(const void *xq, int64_t ldx, const float *x_scales, const void 
     a.odt = out_dtype;
     const int mf = dense_tile(M, N, out_dtype == MOE_DTYPE_F32);
     // (the tile kernel's offsets inside 256 weight rows are 32 bits wide)
-    const bool few_rows = (M + 31) / 32 <= 65535;   // its grid's second dimension
+    const bool few_rows = (M + 31) / 32 <= 65535 && N <= 1 << 28;   // its grid's limits
     if (ldw < (int64_t)1 << 22 && (mf || !few_rows))
         return launch_fp8_tile_dense(a, mf ? mf : 4, stream);
     if (!few_rows)
-        return set_error(MOE_EUNSUPPORTED, "%s: M=%d with ldw=%lld", fn, M, (long long)ldw);
+        return set_error(MOE_EUNSUPPORTED, "%s: M=%d N=%d with ldw=%lld", fn, M, N,
+                         (long long)ldw);
     return launch_fp8_rows_dense(a, stream);
 }
 

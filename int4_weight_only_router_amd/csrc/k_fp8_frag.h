@@ -12,6 +12,8 @@
 // holds four consecutive output columns of one token.
 #pragma once
 
+#include <atomic>
+
 #include "moe_common.h"
 
 namespace moe {
@@ -107,6 +109,23 @@ __device__ __forceinline__ float row16_max(float a)
     return a;
 }
 
+// Raises a kernel's dynamic LDS limit once on each device that launches it.
+struct LdsLimit {
+    std::atomic<uint64_t> done{0};
+    int raise(const void *kernel, int bytes)
+    {
+        int dev = 0;
+        MOE_HIP_TRY(hipGetDevice(&dev));
+        const uint64_t bit = 1ull << (dev & 63);
+        if (!(done.load(std::memory_order_relaxed) & bit)) {
+            MOE_HIP_TRY(hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize,
+                                            bytes));
+            done.fetch_or(bit, std::memory_order_relaxed);
+        }
+        return MOE_OK;
+    }
+};
+
 enum { F8_DENSE = 0, F8_GATEUP = 1, F8_DOWN = 2 };
 constexpr int FP8_DECODE_MAX_T = 16;   // routed experts: decode kernels up to this many tokens
 constexpr int FP8_DECODE_BLOCKS = 600;   // and 128-blocks of quantised rows in LDS (132 bytes each)
@@ -119,7 +138,7 @@ struct Fp8TileRec {
 };
 
 struct Fp8Args {
-    // tokens: e4m3 rows of ldx bytes and their scales, xkb per row
+    // tokens: e4m3 rows of ldx bytes and their scales, one per 128 columns
     const uint8_t *x;
     const float *xs;
     int64_t ldx;

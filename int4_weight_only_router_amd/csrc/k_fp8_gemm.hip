@@ -478,8 +478,8 @@ __global__ __launch_bounds__(512, 1) void fp8_tile_kernel(Fp8Args a)
 static int f8_grid(int64_t items, unsigned *grid)
 {
     const int64_t g = (items + F8_NXCD - 1) / F8_NXCD * F8_NXCD;
-    if (g > 0x7fffffffLL)
-        return set_error(MOE_EUNSUPPORTED, "FP8 product: more than 2^31 - 1 tiles");
+    if (g >= (1LL << 32) / 512)   // a launch has fewer than 2^32 threads
+        return set_error(MOE_EUNSUPPORTED, "FP8 product: 2^23 or more tiles");
     *grid = (unsigned)g;
     return MOE_OK;
 }
@@ -487,14 +487,11 @@ static int f8_grid(int64_t items, unsigned *grid)
 template <int MODE, int MF, bool EX>
 static int launch_tile(const Fp8Args &a, int64_t items, hipStream_t s)
 {
-    static bool attr_set = false;   // raising the LDS limit is idempotent
-    if (!attr_set) {
-        MOE_HIP_TRY(hipFuncSetAttribute((const void *)fp8_tile_kernel<MODE, MF, EX>,
-                                        hipFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024));
-        attr_set = true;
-    }
+    static LdsLimit limit;
     unsigned grid;
-    const int rc = f8_grid(items, &grid);
+    int rc = f8_grid(items, &grid);
+    if (!rc)
+        rc = limit.raise((const void *)fp8_tile_kernel<MODE, MF, EX>, 160 * 1024);
     if (rc)
         return rc;
     hipLaunchKernelGGL((fp8_tile_kernel<MODE, MF, EX>), dim3(grid), dim3(512),
@@ -534,15 +531,16 @@ int launch_fp8_tile_dense(const Fp8Args &a, int mf, hipStream_t s)
 
 // Rows of a row tile, 64, 128 or 192, from the mean rows of an expert; fewer
 // where that leaves under half the compute units a tile.  Measured (us, H =
-// 2048; 64 / 128 / 192 rows): 64 experts of I = 1024, top-8, at 64 tokens 91 /
-// 97 / 110, at 256: 97 / 101 / 115, at 512: 126 / 116 / 121, at 1024: 203 /
-// 167 / 150, at 4096: 617 / 448 / 389; 8 experts, top-2, at 256: 43 / 52 / 49,
-// at 1024: 79 / 57 / 68, at 4096: 184 / 153 / 130.  (256-row tiles lost
+// 2048; 64 / 128 / 192 rows): 64 experts of I = 1024, top-8, at 64 tokens 88 /
+// 92 / 103, at 256: 95 / 99 / 112, at 512: 121 / 107 / 120, at 1024: 208 /
+// 171 / 141, at 4096: 572 / 440 / 378; 60 of I = 1408, top-4, at 512 (34 rows
+// an expert): 121 / 125 / 147; 8 of I = 1024, top-2, at 256: 39 / 45 / 47, at
+// 1024: 73 / 54 / 63, at 4096: 170 / 148 / 123.  (256-row tiles lost
 // everywhere: the registers of the fp16 form do not suffice.)
 int fp8_pick_rows(int64_t rows, int E, int I)
 {
     const int64_t avg = rows / std::max<int64_t>(1, std::min<int64_t>(E, rows));
-    int bm = avg <= 32 ? 64 : avg <= 96 ? 128 : 192;
+    int bm = avg <= 48 ? 64 : avg <= 96 ? 128 : 192;
     while (bm > 64 && (rows + bm - 1) / bm * ((I + 127) / 128) < 128)
         bm -= 64;
     return bm;

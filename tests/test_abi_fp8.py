@@ -29,6 +29,8 @@ def _select(logits=P, dtype=F32, ld=64, bias=None, T=2, E=64, k=8, score=0, n=4,
     (dict(scale=float("inf")), EINVAL), (dict(scale=float("nan")), EINVAL),
     (dict(logits=None), EINVAL), (dict(idx=None), EINVAL), (dict(w=None), EINVAL),
     (dict(logits=P + 2), EINVAL), (dict(logits=P + 1, dtype=F16), EINVAL),
+    (dict(bias=P + 2), EINVAL), (dict(idx=P + 2), EINVAL), (dict(w=P + 1), EINVAL),
+    (dict(T=(1 << 25) + 1), EUNSUP),
     (dict(E=2048, ld=2048), EUNSUP), (dict(k=17, n=1, keep=1), EUNSUP),
     (dict(E=130, ld=130, n=65, keep=65), EUNSUP)])
 def test_select_refusals(kw, code):
@@ -46,6 +48,7 @@ def test_select_permute_refusals():
     assert _code(M.moe_route_select_permute, *big, P, P, P, P, P, need - 1, stream=0) == ENOMEM
     assert _code(M.moe_route_select_permute, *big, P, P, P, P, None, need, stream=0) == ENOMEM
     assert _code(M.moe_route_select_permute, *big, P, P, P, P, P + 8, need, stream=0) == EINVAL
+    assert _code(M.moe_route_select_permute, *big, P, P, P + 2, P, P, need, stream=0) == EINVAL
     assert M.moe_route_select_workspace_bytes(1, 8, 64) == 0
     M.moe_route_select(*_select(T=0, logits=None, idx=None, w=None), stream=0)   # no-op
 
@@ -67,7 +70,8 @@ def _quant(x=P, dtype=F16, ldx=256, rows=3, cols=256, block=1, flags=0, q=P, ldq
     (dict(dtype=2), EINVAL), (dict(rows=-1), EINVAL), (dict(cols=0), EINVAL),
     (dict(ldx=255), EINVAL), (dict(ldq=255), EINVAL), (dict(block=64), EINVAL),
     (dict(flags=2), EINVAL), (dict(x=None), EINVAL), (dict(q=None), EINVAL), (dict(s=None), EINVAL),
-    (dict(x=P + 1), EINVAL), (dict(s=P + 2), EINVAL), (dict(rows=1 << 40), EUNSUP)])
+    (dict(x=P + 1), EINVAL), (dict(s=P + 2), EINVAL), (dict(rows=1 << 40), EUNSUP),
+    (dict(cols=(1 << 30) + 1, ldx=1 << 31, ldq=1 << 31), EUNSUP)])
 def test_quantize_refusals(kw, code):
     assert _code(M.moe_quantize_fp8, *_quant(**kw), stream=0) == code
 
@@ -88,7 +92,10 @@ def _gemm(xq=P, ldx=256, xs=P, wq=P, ldw=256, ws=P, m=4, n=64, k=256, out=P, dt=
     (dict(wq=None), EINVAL), (dict(ws=None), EINVAL), (dict(out=None), EINVAL),
     (dict(xq=P + 8), EINVAL), (dict(wq=P + 4), EINVAL), (dict(xs=P + 2), EINVAL),
     (dict(out=P + 1), EINVAL), (dict(out=P + 2, dt=F32), EINVAL),
-    (dict(m=2097121, ldw=1 << 22), EUNSUP)])
+    (dict(m=2097121, ldw=1 << 22), EUNSUP), (dict(m=0x7fffff01), EUNSUP),
+    (dict(n=0x7fffff01, ldo=1 << 31), EUNSUP),
+    (dict(n=(1 << 28) + 1, ldo=1 << 31, ldw=1 << 22), EUNSUP),
+    (dict(m=1 << 24, n=1 << 24, ldo=1 << 24), EUNSUP)])
 def test_product_refusals(kw, code):
     assert _code(M.moe_gemm_fp8, *_gemm(**kw), stream=0) == code
 

@@ -91,6 +91,21 @@ def test_quantize_non_finite():
         assert bool(v[2].isfinite().all())
 
 
+def test_quantize_more_rows_than_a_launch():
+    """2^28 + 5 rows of one column: more than one launch."""
+    say("quantize many rows")
+    n = (1 << 28) + 5
+    x = torch.randint(-3, 4, (n,), dtype=torch.int8, device=DEV).to(torch.float16)
+    q = torch.full((n,), 9, dtype=torch.uint8, device=DEV)
+    s = torch.full((n,), -1.0, device=DEV)
+    M.moe_quantize_fp8(x, M.MOE_DTYPE_F16, 1, n, 1, 1, 0, q, 1, s)
+    # a lone value takes the largest code, and 448 s gives it back
+    code = torch.where(x > 0, 0x7E, 0).to(torch.uint8) + torch.where(x < 0, 0xFE, 0).to(torch.uint8)
+    want = torch.from_numpy(np.arange(4, dtype=np.float32) / np.float32(448)).to(DEV)
+    wrong = (q != code).sum() + (s != want[x.abs().int()]).sum()
+    assert wrong.item() == 0
+
+
 def test_quantize_far_rows():
     """Rows whose element offsets pass 32 bits."""
     say("quantize far rows")
@@ -122,7 +137,7 @@ def _product(M_, N, K, dtype, ldx=None, ldw=None, ldo=None, seed=0):
     M.moe_gemm_fp8(xb, ldx, torch.from_numpy(xs).to(DEV), wb, ldw, torch.from_numpy(ws).to(DEV),
                    M_, N, K, out, dt, ldo)
     torch.cuda.synchronize()
-    y, bound = R.product(xv, xs, wv, ws, pairs=dtype != "f32")
+    y, bound = R.product(xv, xs, wv, ws, runs=dtype != "f32")
     got = out[:M_, :N].double().cpu().numpy()
     half = R.HALF_STEP[tt]
     tol = bound + half * (np.abs(y) + bound)
@@ -132,10 +147,14 @@ def _product(M_, N, K, dtype, ldx=None, ldw=None, ldo=None, seed=0):
     assert np.all(off <= 0), "off by %g over the bound at %s" % (
         off.max(), np.unravel_index(off.argmax(), off.shape))
     # over many outputs the errors are not all at their bound: the output's own
-    # rounding and PAIR of the root sum of squares of the products
+    # rounding and, of a run's seven losses below GRID of its largest, each of
+    # its product's random sign and a third of its greatest square on average,
+    # sqrt(7 / 3) GRID of the root sum of squares of the runs' largest products,
+    # which is at most that of all products
     rms = np.sqrt((np.square(xv * R.spread(xs, 1, *xv.shape)) @
                    np.square(wv * R.spread(ws, 128, *wv.shape)).T).mean())
-    assert np.sqrt(np.square(got - y).mean()) <= half * np.sqrt(np.square(y).mean()) + R.PAIR * rms
+    assert np.sqrt(np.square(got - y).mean()) <= half * np.sqrt(np.square(y).mean()) \
+        + np.sqrt(7 / 3) * R.GRID * rms
     assert bool((out[:M_, N:] == -7.0).all()) and bool((out[M_] == -7.0).all())
 
 
@@ -282,6 +301,23 @@ def test_experts_uneven(T):
     table[5] = 0
     y = _ffn(x, perm, offsets, table, T, H, I, E, k)
     _check_ffn(y, x, perm, offsets, vals, k, skip=(5,))
+
+
+def test_experts_short_tiles():
+    """Tiles of 192 rows whose last one holds one, two or three row fragments
+    of each wave, or none of some; ragged fragments; an expert of one row."""
+    say("experts short tiles")
+    H, I, k = 192, 4096, 1
+    rows = [193, 300, 129, 1, 64, 192, 241]
+    E, T = len(rows), sum(rows)
+    r = np.random.default_rng(5)
+    dev, vals, table = _blobs(r, E, H, I)
+    x = torch.from_numpy(r.normal(0, 1, (T, H)).astype(np.float16)).to(DEV)
+    idx = np.repeat(np.arange(E), rows)
+    r.shuffle(idx)
+    perm, offsets = _grouping(idx.reshape(T, 1), E)
+    y = _ffn(x, perm, offsets, table, T, H, I, E, k)
+    _check_ffn(y, x, perm, offsets, vals, k)
 
 
 def test_experts_no_rows():
