@@ -611,6 +611,7 @@ int moe_fp8_blob_layout(int H, int I, int64_t offsets[6], int64_t *total_bytes);
  *          MOE_DTYPE_F16, one slice)
  *   ws     device scratch of the plan's size, 16-byte aligned, no
  *          initialisation; calls that share it must not overlap
+ * A token with a NaN or an infinity has no finite value in its rows.
  * Rows behind offsets[E] are left as they were.  Regimes: DECODE (T <= 16 and
  * T * ceil(max(H, I) / 128) <= 600, else MOE_EUNSUPPORTED: two launches over
  * the weights' stream, activations quantised inside them) and BATCHED

@@ -320,6 +320,26 @@ def test_experts_short_tiles():
     _check_ffn(y, x, perm, offsets, vals, k)
 
 
+@pytest.mark.parametrize("T", [3, 40])
+def test_experts_non_finite_tokens(T):
+    """A token with a NaN or an infinity has rows without a finite value; every
+    other row keeps its bits."""
+    say("experts non-finite T=%d" % T)
+    H, I, E, k = 256, 192, 5, 2
+    r = np.random.default_rng(T)
+    dev, vals, table = _blobs(r, E, H, I)
+    x = torch.from_numpy(r.normal(0, 1, (T, H)).astype(np.float16)).to(DEV)
+    perm, offsets = _grouping(np.argsort(r.normal(0, 1, (T, E)), 1)[:, :k], E)
+    clean = _ffn(x, perm, offsets, table, T, H, I, E, k)
+    for v in (float("nan"), float("inf"), -float("inf")):
+        bad = x.clone()
+        bad[1, 70] = v
+        y = _ffn(bad, perm, offsets, table, T, H, I, E, k)
+        hit = torch.cat([perm // k == 1, torch.zeros(2, dtype=torch.bool, device=DEV)])
+        assert not bool(torch.isfinite(y[hit]).any())
+        assert torch.equal(y[~hit], clean[~hit])
+
+
 def test_experts_no_rows():
     """Nothing routed: nothing written."""
     say("experts no rows")
