@@ -50,8 +50,12 @@ def load_experts_fp8(weights, H, I, device="cuda", stream=None):
         base = blobs[e].data_ptr()
         for j, (m, (rows, cols)) in enumerate(zip(w, ((I, H), (I, H), (H, I)))):
             m = torch.as_tensor(m).to(device=device, dtype=torch.float32).contiguous()
+            if stream is not None:   # the copy was made on torch's current stream
+                torch.cuda.synchronize()
             A.moe_quantize_fp8(m, A.MOE_DTYPE_F32, cols, rows, cols, 128, 0, base + off[j], cols,
                                base + off[3 + j], stream)
+            if stream is not None:   # and its memory is free for the next one there
+                torch.cuda.synchronize()
     return blobs
 
 

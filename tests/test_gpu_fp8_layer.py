@@ -141,3 +141,17 @@ def test_layer_captured(T):
         want = lay.forward(x, eb)
         torch.cuda.synchronize()
         assert torch.equal(b.out, want)
+
+
+def test_load_on_another_stream():
+    """Loading on a side stream, by object or address, gives the same blobs."""
+    H, I = 1024, 512
+    r = np.random.default_rng(3)
+    w = [tuple(r.normal(0, 0.02, s).astype(np.float32) for s in ((I, H), (I, H), (H, I)))
+         for _ in range(4)]
+    want = load_experts_fp8(w, H, I, DEV)
+    side = torch.cuda.Stream()
+    for s in (side, side.cuda_stream):
+        got = load_experts_fp8(w, H, I, DEV, s)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
