@@ -22,14 +22,14 @@
 //    to a neighbouring code (measured: the experts' error against 64 bits goes
 //    from 3e-4 to 1.1e-3).
 //
-// fp8_tile_kernel: eight waves own 64*MF rows x 256 weight rows, wave w 16 of
-// each 64 rows (MF row fragments) and 128 of the weight rows.  Both operands'
+// fp8_tile_kernel: eight waves own 64*MF rows x 256 weight rows, as RG groups of
+// rows x 8 / RG groups of weight rows.  Both operands'
 // blocks travel to LDS by direct-to-LDS loads, 8 lanes per 128-byte row block,
 // into a ring of two or three stages: one barrier per block, and a block has
 // the whole work of another to arrive.  (Read straight into registers in the
 // matrix instruction's layout, consecutive lanes are consecutive rows, and the
 // L1 then serves 16 bytes a cycle instead of 64: measured 4 times slower.)  A
-// wave holds its row fragments of the block and walks its eight weight
+// wave holds its row fragments of the block and walks its weight
 // fragments; each sum enters its accumulator by one fma two sums later.  The
 // fma's run in the shadow of the matrix pipe.
 //
@@ -132,6 +132,12 @@ constexpr int F8_SCW = 8;   // blocks of row scales in LDS at a time (two window
 
 template <int MF>
 constexpr int f8_stages() { return MF >= 3 ? 2 : 3; }
+// The eight waves as groups of rows x groups of weight rows.  A wave converts
+// and reads 4 MF / RG row and 2 RG weight fragments for 8 MF sums: 6, 8, 11 and
+// 12 of them for MF = 1, 2, 3, 4 (with four groups of rows 9, 10, 11, 12); 6 + 4
+// for MF = 3 would be one less, in more registers than there are.
+template <int MF>
+constexpr int f8_row_groups() { return MF >= 3 ? 4 : MF; }
 template <int MF>
 constexpr int f8_stage_bytes() { return (64 * MF + 256) * 128; }
 // LDS: the ring, two windows of row scales, the weight scales; gate/up's h
@@ -151,11 +157,15 @@ __global__ __launch_bounds__(512, 1) void fp8_tile_kernel(Fp8Args a)
     constexpr int STAGE = f8_stage_bytes<MF>();
     constexpr int XB = BM * 128;
     constexpr int PX = MF, PW = 4;   // 16-byte loads per thread and stage
+    constexpr int RG = f8_row_groups<MF>(), CG = 8 / RG;   // of the eight waves
+    constexpr int XF = 4 * MF / RG, WF = 16 / CG;   // a wave's row and weight fragments
+    constexpr int WH = WF / 2;                      // gate/up: of each matrix
     static_assert(PX * 16 * NTH == XB && PW * 16 * NTH == 256 * 128, "whole loads");
     extern __shared__ __align__(16) uint8_t smem[];
     const int tid = threadIdx.x;
     const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int m0 = (wave >> 1) * 16, wn = wave & 1;   // fragment m: rows m0 + 64 m
+    // row fragment m: rows m0 + 16 RG m
+    const int m0 = wave / CG * 16, wn = wave % CG;
     const int col = lane & 15, q = lane >> 4;
     const int K = a.K, nkb = (K + 127) / 128;
 
@@ -231,17 +241,18 @@ __global__ __launch_bounds__(512, 1) void fp8_tile_kernel(Fp8Args a)
             wsc[i] = i < nkb ? s0[i] : s1[i - nkb];
     }
 
-    float4_t acc[MF][8];
+    float4_t acc[XF][WF];
 #pragma unroll
-    for (int m = 0; m < MF; ++m)
+    for (int m = 0; m < XF; ++m)
 #pragma unroll
-        for (int f = 0; f < 8; ++f)
+        for (int f = 0; f < WF; ++f)
             acc[m][f] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
     const int sw = (col >> 1) & 7;
     const int o0 = (q ^ sw) * 16, o1 = ((q + 4) ^ sw) * 16;
-    // LDS row of weight fragment f: gate/up waves take 64 rows of each matrix
+    // LDS row of weight fragment f: gate/up waves take as many of each matrix
     auto wrow = [&](int f) {
-        return (MODE == F8_GATEUP ? (f >> 2) * 128 + wn * 64 + (f & 3) * 16 : wn * 128 + f * 16) + col;
+        return (MODE == F8_GATEUP ? f / WH * 128 + wn * (WH * 16) + f % WH * 16
+                                  : wn * (WF * 16) + f * 16) + col;
     };
     // MA: the wave's row fragments that hold a row of the tile
     auto block = [&](int kb, auto tail, auto ma) {
@@ -264,6 +275,7 @@ __global__ __launch_bounds__(512, 1) void fp8_tile_kernel(Fp8Args a)
         };
         // in the order of use, so that the first sum waits for the first reads
         // only
+        constexpr int LF = std::min(4, WF);
         constexpr int WD = EX && MF == 4 ? 1 : 2;   // weight fragments read ahead
         constexpr bool WC = EX && WD == 2;          // and converted one ahead
         int8_8 x[MA], w[WD + 1];
@@ -273,17 +285,17 @@ __global__ __launch_bounds__(512, 1) void fp8_tile_kernel(Fp8Args a)
         w[0] = frag(st + XB + wrow(0) * 128);
 #pragma unroll
         for (int m = 0; m < MA; ++m) {
-            x[m] = frag(st + (m * 64 + m0 + col) * 128);
+            x[m] = frag(st + (m * 16 * RG + m0 + col) * 128);
             __builtin_amdgcn_sched_barrier(0);
         }
         if constexpr (WD == 2)
             w[1] = frag(st + XB + wrow(1) * 128);
-        const float wg = wsc[MODE == F8_GATEUP ? kb : wn * nkb + kb];
+        const float wg = wsc[MODE == F8_GATEUP ? kb : wn * 2 / CG * nkb + kb];
         const float wu = MODE == F8_GATEUP ? wsc[nkb + kb] : wg;
         float xv[MA];
 #pragma unroll
         for (int m = 0; m < MA; ++m)
-            xv[m] = xs[m * 64];
+            xv[m] = xs[m * 16 * RG];
         __builtin_amdgcn_sched_barrier(0);
         if constexpr (decltype(tail)::value) {
 #pragma unroll
@@ -294,7 +306,7 @@ __global__ __launch_bounds__(512, 1) void fp8_tile_kernel(Fp8Args a)
         float4_t s[4];
         auto add1 = [&](int i, int j) {
             const int f = i / MA, m = i % MA;
-            acc[m][f][j] = __builtin_fmaf(s[i & 3][j], sc[m][f >> 2], acc[m][f][j]);
+            acc[m][f][j] = __builtin_fmaf(s[i & 3][j], sc[m][f / WH], acc[m][f][j]);
         };
         auto add = [&](int i) {
 #pragma unroll
@@ -302,15 +314,14 @@ __global__ __launch_bounds__(512, 1) void fp8_tile_kernel(Fp8Args a)
                 add1(i, j);
         };
 #pragma unroll
-        for (int f = 0; f < 8; ++f) {
-            if (f + WD < 8)
+        for (int f = 0; f < WF; ++f) {
+            if (f + WD < WF)
                 w[(f + WD) % (WD + 1)] = frag(st + XB + wrow(f + WD) * 128);
-            // the next block's loads go out over the first four fragments: all
-            // at once they would hold every wave until the address unit had
-            // taken them
+            // the next block's loads go out over several fragments: all at once
+            // they would hold every wave until the address unit had taken them
 #pragma unroll
             for (int i = 0; i < PX + PW; ++i)
-                if (i * 4 / (PX + PW) == f)
+                if (i * LF / (PX + PW) == f)
                     issue1(kb + NS - 1, i);
             if constexpr (EX) {
                 if (!WC || f == 0)
@@ -342,7 +353,7 @@ __global__ __launch_bounds__(512, 1) void fp8_tile_kernel(Fp8Args a)
                             for (int u = 4 * j; u < 4 * j + 4; ++u)
                                 f8_pair(xh[m + 1 < MA ? m + 1 : 0], x[m + 1 < MA ? m + 1 : 0], u);
                         if constexpr (WC)
-                            if (f + 1 < 8)
+                            if (f + 1 < WF)
 #pragma unroll
                                 for (int u = (4 * m + j) * 4 / MA; u < (4 * m + j + 1) * 4 / MA; ++u)
                                     f8_pair(wh[(f + 1) & 1], w[(f + 1) % (WD + 1)], u);
@@ -359,8 +370,8 @@ __global__ __launch_bounds__(512, 1) void fp8_tile_kernel(Fp8Args a)
             }
             __builtin_amdgcn_s_setprio(0);
         }
-        add(8 * MA - 2);
-        add(8 * MA - 1);
+        add(WF * MA - 2);
+        add(WF * MA - 1);
         }
     };
     auto blocks = [&](auto ma) {
@@ -368,17 +379,17 @@ __global__ __launch_bounds__(512, 1) void fp8_tile_kernel(Fp8Args a)
             block(kb, std::false_type(), ma);
         block(nkb - 1, std::true_type(), ma);
     };
-    // A short tile's fragments are dealt out over the waves, and each takes the
-    // loop of as many as it has: an expert's last tile costs what it holds
-    // (rounded up to 64 rows), not its full height.
-    const int act = t.rows > m0 ? min(MF, (t.rows - m0 + 63) >> 6) : 0;
-    if (act == MF)
-        blocks(std::integral_constant<int, MF>());
-    else if (MF > 3 && act == 3)
-        blocks(std::integral_constant<int, std::min(MF, 3)>());
-    else if (MF > 2 && act == 2)
-        blocks(std::integral_constant<int, std::min(MF, 2)>());
-    else if (MF > 1 && act == 1)
+    // A short tile's fragments are dealt out over the row groups, and each takes
+    // the loop of as many as it has: an expert's last tile costs what it holds
+    // (rounded up to 16 RG rows), not its full height.
+    const int act = t.rows > m0 ? min(XF, (t.rows - m0 + 16 * RG - 1) / (16 * RG)) : 0;
+    if (act == XF)
+        blocks(std::integral_constant<int, XF>());
+    else if (XF > 3 && act == 3)
+        blocks(std::integral_constant<int, std::min(XF, 3)>());
+    else if (act == 2)
+        blocks(std::integral_constant<int, 2>());
+    else if (act == 1)
         blocks(std::integral_constant<int, 1>());
     else
         blocks(std::integral_constant<int, 0>());
@@ -386,33 +397,37 @@ __global__ __launch_bounds__(512, 1) void fp8_tile_kernel(Fp8Args a)
 
     if constexpr (MODE == F8_GATEUP) {
         uint8_t *ht = smem;                                              // [BM][128]
-        float *mx = reinterpret_cast<float *>(smem + (size_t)BM * 128);   // [2][BM]
+        float *mx = reinterpret_cast<float *>(smem + (size_t)BM * 128);   // [CG][BM]
         __syncthreads();   // the ring is read by all
-        const bool in = n0 + wn * 64 < a.N;   // I is a multiple of 64: a wave is in or out
+        const bool in = n0 + wn * (WH * 16) < a.N;   // I is a multiple of 64: a wave is in or out
 #pragma unroll
-        for (int m = 0; m < MF; ++m) {
+        for (int m = 0; m < XF; ++m) {
             float top = 0.0f;
 #pragma unroll
-            for (int f = 0; f < 4; ++f)
+            for (int f = 0; f < WH; ++f)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float h = in ? swiglu_fast(acc[m][f][i], acc[m][4 + f][i]) : 0.0f;
+                    const float h = in ? swiglu_fast(acc[m][f][i], acc[m][WH + f][i]) : 0.0f;
                     acc[m][f][i] = h;
                     top = fmaxf(top, fabsf(h));
                 }
             top = fmaxf(top, __shfl_xor(top, 16, 64));
             top = fmaxf(top, __shfl_xor(top, 32, 64));
             if (q == 0)
-                mx[wn * BM + m * 64 + m0 + col] = top;
+                mx[wn * BM + m * 16 * RG + m0 + col] = top;
         }
         __syncthreads();
 #pragma unroll
-        for (int m = 0; m < MF; ++m) {
-            const int r = m * 64 + m0 + col;
-            const float sc = fp8_scale(fmaxf(mx[r], mx[BM + r]), true), inv = fp8_inv_pow2(sc);
+        for (int m = 0; m < XF; ++m) {
+            const int r = m * 16 * RG + m0 + col;
+            float top = mx[r];
 #pragma unroll
-            for (int f = 0; f < 4; ++f)
-                *reinterpret_cast<int *>(ht + r * 128 + wn * 64 + f * 16 + q * 4) =
+            for (int i = 1; i < CG; ++i)
+                top = fmaxf(top, mx[i * BM + r]);
+            const float sc = fp8_scale(top, true), inv = fp8_inv_pow2(sc);
+#pragma unroll
+            for (int f = 0; f < WH; ++f)
+                *reinterpret_cast<int *>(ht + r * 128 + wn * (WH * 16) + f * 16 + q * 4) =
                     fp8_pack4(acc[m][f][0] * inv, acc[m][f][1] * inv, acc[m][f][2] * inv,
                               acc[m][f][3] * inv);
             if (wn == 0 && q == 0 && r < t.rows)
@@ -438,21 +453,21 @@ __global__ __launch_bounds__(512, 1) void fp8_tile_kernel(Fp8Args a)
         const bool vec = (a.ldo * es) % 16 == 0 && ((uintptr_t)a.out & 15) == 0;
 #pragma unroll
         for (int h = 0; h < PASS; ++h) {
-            constexpr int MH = MF / PASS;
+            constexpr int MH = XF / PASS;
             __syncthreads();   // the ring, or the first half, is read by all
 #pragma unroll
             for (int mm = 0; mm < MH; ++mm) {
                 const int m = h * MH + mm;
-                const int r = mm * 64 + m0 + col;
+                const int r = mm * 16 * RG + m0 + col;
 #pragma unroll
-                for (int f = 0; f < 8; ++f)
-                    store4(smem + r * LR, dt, wn * 128 + f * 16 + q * 4, acc[m][f], 4, true);
+                for (int f = 0; f < WF; ++f)
+                    store4(smem + r * LR, dt, wn * (WF * 16) + f * 16 + q * 4, acc[m][f], 4, true);
             }
             __syncthreads();
             constexpr int np = 256 / gp;   // pieces of a row
-            for (int i = tid; i < 64 * MH * np; i += NTH) {
+            for (int i = tid; i < 16 * RG * MH * np; i += NTH) {
                 const int lr2 = i / np, c = (i % np) * gp;
-                const int r = h * 64 * MH + lr2;
+                const int r = h * 16 * RG * MH + lr2;
                 const int n = n0 + c;
                 if (r >= t.rows || n >= a.N)
                     continue;
