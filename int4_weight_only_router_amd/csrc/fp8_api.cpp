@@ -325,19 +325,27 @@ int moe_expert_ffn_w8a8_plan(int T, int H, int I, int E, int k, int regime, int 
         return rc;
     if (regime != MOE_REGIME_AUTO && regime != MOE_REGIME_DECODE && regime != MOE_REGIME_BATCHED)
         return set_error(MOE_EINVAL, "%s: bad regime %d", fn, regime);
-    // decode up to 64 routed rows (measured, us decode / batched: 64 experts,
-    // top-8, 1 token 15 / 32, 4: 32 / 36, 8: 48 / 64, 12: 73 / 75, 16: 92 / 78;
-    // 512 experts, top-10, 4: 21 / 31, 8: 32 / 32, 16: 54 / 37; 60 experts,
-    // top-4, 8: 41 / 60, 16: 77 / 74; 8 experts, top-2, 16: 19 / 31)
+    // decode up to 64 routed rows, and up to 192 of short tokens, where its one
+    // launch less counts more than quantising a token in every workgroup
+    // (measured, us decode / batched: H = 2048, 64 experts, top-8, 1 token 15 /
+    // 32, 4: 32 / 36, 8: 48 / 64, 12: 73 / 75, 16: 92 / 78; 60 experts, top-4,
+    // 8: 41 / 60, 16: 77 / 74; 8 experts, top-2, 16: 19 / 31; H = 1024, 96 rows
+    // over 82 experts of I = 384: 28 / 29, 192 over 59 of 768: 39 / 36; H = 512,
+    // 192 over 16 of 256: 12 / 15, 480 over 24 of 64: 20 / 18; H = 256, 192 over
+    // 97 of 512: 20 / 22, 320 over 12 of 768: 21 / 17)
     const bool fits = T <= FP8_DECODE_MAX_T &&
-                      T * ((std::max(H, I) + 127) / 128) <= FP8_DECODE_BLOCKS;
+                      std::min(T, FP8_DECODE_ROWS) * ((std::max(H, I) + 127) / 128) <=
+                          FP8_DECODE_BLOCKS;
+    const int64_t n = (int64_t)T * k;
+    const bool few = n <= 64 || (n <= 192 && n * ((H + 127) / 128) <= 1024);
     const int r = regime != MOE_REGIME_AUTO ? regime
-                  : fits && T * k <= 64     ? MOE_REGIME_DECODE
+                  : fits && few             ? MOE_REGIME_DECODE
                                             : MOE_REGIME_BATCHED;
     if (r == MOE_REGIME_DECODE && !fits)
         return set_error(MOE_EUNSUPPORTED,
-                         "%s: the decode regime takes T <= %d and T * ceil(max(H, I) / 128) <= %d "
-                         "(T=%d H=%d I=%d)", fn, FP8_DECODE_MAX_T, FP8_DECODE_BLOCKS, T, H, I);
+                         "%s: the decode regime takes T <= %d and min(T, %d) * ceil(max(H, I) / "
+                         "128) <= %d (T=%d H=%d I=%d)", fn, FP8_DECODE_MAX_T, FP8_DECODE_ROWS,
+                         FP8_DECODE_BLOCKS, T, H, I);
     if (resolved_regime)
         *resolved_regime = r;
     if (ws_bytes)

@@ -26,6 +26,8 @@
 // Decode experts quantise their rows in the workgroup (gate/up: the fp16
 // tokens; down: the fp32 h the first launch left in the workspace), hidden
 // behind the weight loads: no launch of its own.
+#include <algorithm>
+
 #include "k_fp8_frag.h"
 
 namespace moe {
@@ -80,8 +82,8 @@ constexpr int f8_rows_stage()
 
 // MODE F8_DENSE: grid (32-column tiles, 16*MT-row tiles).  F8_GATEUP /
 // F8_DOWN: grid (tiles of 16 intermediate / 32 output columns, sorted rows);
-// the workgroup at an expert's first row serves its T rows (an expert has at
-// most one row per token), the others leave at once.  Nothing is predicated
+// the workgroups at an expert's first row and every 16th (every T-th) after it
+// serve the rows up to the next, the others leave at once.  Nothing is predicated
 // between a matrix instruction and the use of its result: rows past the end
 // repeat the last one (their columns are not stored), blocks past the end
 // repeat the last one with a weight scale of zero.
@@ -97,6 +99,7 @@ __global__ __launch_bounds__(256) void fp8_rows_kernel(Fp8Args a)
     const int K = a.K, nkb = (K + 127) / 128;
 
     int row0 = blockIdx.y * 16 * MT, rows = min(16 * MT, a.M - row0);
+    const int held = min(a.T, FP8_DECODE_ROWS);   // decode: rows of a workgroup
     const uint8_t *w0 = a.w, *w1 = a.w;
     const float *s0 = a.ws, *s1 = a.ws;
     if constexpr (MODE != F8_DENSE) {
@@ -117,11 +120,10 @@ __global__ __launch_bounds__(256) void fp8_rows_kernel(Fp8Args a)
         }
         if (e >= a.E)
             return;   // behind the last routed row
-        // T rows to a workgroup (all of them, unless a token chose an expert twice)
-        if ((p - first) % a.T)
+        if ((p - first) % held)
             return;
         row0 = p;
-        rows = min(a.T, end - p);
+        rows = min(held, end - p);
         const uint8_t *blob = static_cast<const uint8_t *>(a.blobs[e]);
         if (!blob)
             return;
@@ -177,8 +179,8 @@ __global__ __launch_bounds__(256) void fp8_rows_kernel(Fp8Args a)
         for (int m = 0; m < MT; ++m)
             acc[f][m] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
 
-    uint8_t *xl = smem + 4 * STAGE;                                        // decode: [T][nkb*128]
-    float *sl = reinterpret_cast<float *>(xl + (size_t)a.T * nkb * 128);   // [T][nkb]
+    uint8_t *xl = smem + 4 * STAGE;                                        // decode: [held][nkb*128]
+    float *sl = reinterpret_cast<float *>(xl + (size_t)held * nkb * 128);   // [held][nkb]
     if constexpr (MODE != F8_DENSE) {
         // quantise this expert's rows while the weights arrive
         const int g = threadIdx.x >> 4, c = threadIdx.x & 15;
@@ -319,7 +321,9 @@ int launch_fp8_rows_dense(const Fp8Args &a, hipStream_t s)
 int launch_fp8_decode(Fp8Args a, const void *x_f16, float *h, int H, int I, const int64_t off[6],
                       void *y, hipStream_t s)
 {
-    auto lds = [&](int K) { return (size_t)a.T * ((K + 127) / 128) * (128 + 4); };
+    auto lds = [&](int K) {
+        return (size_t)std::min(a.T, FP8_DECODE_ROWS) * ((K + 127) / 128) * (128 + 4);
+    };
     a.src = x_f16;
     a.out = h;
     a.N = I;

@@ -127,8 +127,9 @@ struct LdsLimit {
 };
 
 enum { F8_DENSE = 0, F8_GATEUP = 1, F8_DOWN = 2 };
-constexpr int FP8_DECODE_MAX_T = 16;   // routed experts: decode kernels up to this many tokens
-constexpr int FP8_DECODE_BLOCKS = 600;   // and 128-blocks of quantised rows in LDS (132 bytes each)
+constexpr int FP8_DECODE_MAX_T = 128;   // routed experts: decode kernels up to this many tokens,
+constexpr int FP8_DECODE_ROWS = 16;     // of an expert in a workgroup,
+constexpr int FP8_DECODE_BLOCKS = 600;  // whose quantised rows are as many 128-blocks (132 bytes) in LDS
 
 // One row tile of the routed experts: its expert's blob, first sorted row and
 // rows.  Entry 0 of a table holds the number of tiles in `rows`.

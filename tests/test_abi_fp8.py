@@ -110,7 +110,7 @@ def test_product_no_rows():
     ((1, 8256, 1024, 64, 8), EUNSUP), ((1, 2048, 1024, 2048, 8), EUNSUP),
     ((1, 2048, 1024, 64, 17), EUNSUP), ((1, 2048, 1024, 64, 8, M.MOE_REGIME_SMALL), EINVAL),
     ((1, 2048, 1024, 64, 8, M.MOE_REGIME_AUTO | M.MOE_Y_TOKEN_ORDER), EINVAL),
-    ((17, 2048, 1024, 64, 8, M.MOE_REGIME_DECODE), EUNSUP),
+    ((129, 2048, 1024, 64, 8, M.MOE_REGIME_DECODE), EUNSUP),
     ((10, 64, 8192, 64, 8, M.MOE_REGIME_DECODE), EUNSUP)])
 def test_plan_refusals(args, code):
     assert _code(M.moe_expert_ffn_w8a8_plan, *args) == code
@@ -121,7 +121,12 @@ def test_plan_and_layout():
     assert M.moe_expert_ffn_w8a8_plan(8, 2048, 1024, 64, 8)[0] == M.MOE_REGIME_DECODE
     assert M.moe_expert_ffn_w8a8_plan(9, 2048, 1024, 64, 8)[0] == M.MOE_REGIME_BATCHED
     assert M.moe_expert_ffn_w8a8_plan(16, 2048, 1024, 8, 2)[0] == M.MOE_REGIME_DECODE
-    assert M.moe_expert_ffn_w8a8_plan(17, 2048, 1024, 8, 1)[0] == M.MOE_REGIME_BATCHED
+    assert M.moe_expert_ffn_w8a8_plan(64, 2048, 1024, 8, 1)[0] == M.MOE_REGIME_DECODE
+    assert M.moe_expert_ffn_w8a8_plan(65, 2048, 1024, 8, 1)[0] == M.MOE_REGIME_BATCHED
+    assert M.moe_expert_ffn_w8a8_plan(96, 640, 1024, 8, 2)[0] == M.MOE_REGIME_DECODE
+    assert M.moe_expert_ffn_w8a8_plan(97, 256, 1024, 8, 2)[0] == M.MOE_REGIME_BATCHED
+    assert M.moe_expert_ffn_w8a8_plan(86, 768, 1024, 8, 2)[0] == M.MOE_REGIME_BATCHED
+    assert M.moe_expert_ffn_w8a8_plan(129, 256, 1024, 8, 1)[0] == M.MOE_REGIME_BATCHED
     assert M.moe_expert_ffn_w8a8_plan(9, 64, 8192, 8, 2)[0] == M.MOE_REGIME_DECODE
     assert M.moe_expert_ffn_w8a8_plan(10, 64, 8192, 8, 2)[0] == M.MOE_REGIME_BATCHED
     r, n = M.moe_expert_ffn_w8a8_plan(4096, 2048, 1024, 64, 8)

@@ -269,8 +269,11 @@ FFN = [   # T, H, I, E, k, regime
     (1, 256, 512, 8, 2, 0), (1, 2048, 1024, 16, 8, 0), (4, 256, 192, 8, 2, 0),
     (3, 320, 64, 5, 3, 0), (1, 64, 64, 1, 1, 0), (4, 256, 192, 8, 2, M.MOE_REGIME_BATCHED),
     (5, 256, 192, 8, 2, 0), (16, 320, 64, 5, 3, M.MOE_REGIME_DECODE), (16, 320, 64, 5, 3, 0),
-    (11, 2048, 1408, 6, 2, 0), (1, 8192, 64, 2, 1, 0), (9, 64, 8192, 2, 2, 0), (10, 64, 8192, 2, 2, 0), (40, 512, 320, 8, 4, 0),
-    (100, 256, 192, 4, 2, 0), (300, 512, 448, 3, 1, 0), (70, 2048, 512, 70, 4, 0)]
+    (11, 2048, 1408, 6, 2, 0), (1, 8192, 64, 2, 1, 0), (9, 64, 8192, 2, 2, 0),
+    (10, 64, 8192, 2, 2, 0), (40, 512, 320, 8, 4, 0),
+    (17, 320, 64, 5, 3, M.MOE_REGIME_BATCHED), (40, 512, 320, 8, 4, M.MOE_REGIME_BATCHED),
+    (128, 256, 192, 8, 1, M.MOE_REGIME_DECODE), (100, 2048, 512, 3, 1, M.MOE_REGIME_DECODE),
+    (33, 4096, 128, 2, 2, M.MOE_REGIME_DECODE), (100, 256, 192, 4, 2, 0), (300, 512, 448, 3, 1, 0), (70, 2048, 512, 70, 4, 0)]
 
 
 @pytest.mark.parametrize("T,H,I,E,k,regime", FFN)
@@ -285,7 +288,7 @@ def test_experts(T, H, I, E, k, regime):
     _check_ffn(y, x, perm, offsets, vals, k)
 
 
-@pytest.mark.parametrize("T", [2, 4, 16, 30])
+@pytest.mark.parametrize("T", [2, 4, 16, 30, 60])
 def test_experts_uneven(T):
     """Every token with the same expert twice, ids that route nowhere (rows
     behind the last sorted row stay as they were), and an absent expert."""
@@ -320,7 +323,7 @@ def test_experts_short_tiles():
     _check_ffn(y, x, perm, offsets, vals, k)
 
 
-@pytest.mark.parametrize("T", [3, 40])
+@pytest.mark.parametrize("T", [3, 40, 120])
 def test_experts_non_finite_tokens(T):
     """A token with a NaN or an infinity has rows without a finite value; every
     other row keeps its bits."""
@@ -345,13 +348,13 @@ def test_experts_no_rows():
     say("experts no rows")
     H, I, E, k = 256, 128, 6, 2
     dev, vals, table = _blobs(np.random.default_rng(0), E, H, I)
-    for T in (2, 20):
+    for T in (2, 20, 120):
         x = torch.ones((T, H), dtype=torch.float16, device=DEV)
         perm, offsets = _grouping(np.full((T, k), -1), E)
         assert bool((_ffn(x, perm, offsets, table, T, H, I, E, k) == -7.0).all())
 
 
-@pytest.mark.parametrize("T", [1, 48])
+@pytest.mark.parametrize("T", [1, 48, 150])
 def test_experts_on_another_stream_and_captured(T):
     """A side stream gives the same bits; a captured call follows its buffers
     over replays, with eager calls on another workspace between them."""
