@@ -90,13 +90,14 @@ static Fp8Ws fp8_ws(int T, int H, int I, int E, int k, bool decode)
 // Kernel of a dense product: 64*mf x 256 tiles, or 0 for the kernel of few rows
 // (32 x 32 tiles).  The least of the times that were measured for one round of
 // tiles over the 256 compute units at K = 2048 (every form grows alike with K),
-// in us: 64-, 128-, 192- and 256-row tiles 13.5, 21, 27, 31, and 26, 37, 46,
-// 54 with fp32 outputs (the fp16 form); the kernel of few rows 2.5 and 9.8 for
-// every 1000 workgroups.  Against each form on 17 shapes from 64 x 5632 to
-// 4096 x 11264 the choice is the fastest or within 10% of it.
+// in us: 64-, 128-, 192- and 256-row tiles 14.5, 20.5, 24.5, 29.5, and 24, 33.5,
+// 43, 52.5 with fp32 outputs (the fp16 form); the kernel of few rows 2.5 and 9.8
+// for every 1000 workgroups.  Against each form on 28 products from 64 x 5632 to
+// 4096 x 11264 (K 512 to 5632, both forms) the choice is the fastest or within
+// 3% of it.
 static int dense_tile(int M, int N, bool f32)
 {
-    static const double round_us[2][4] = {{13.5, 21, 27, 31}, {26, 37, 46, 54}};
+    static const double round_us[2][4] = {{14.5, 20.5, 24.5, 29.5}, {24, 33.5, 43, 52.5}};
     const int64_t few = (int64_t)((M + 31) / 32) * ((N + 31) / 32);
     double best = 2.5 + 9.8e-3 * (double)few;
     int mf = 0;
