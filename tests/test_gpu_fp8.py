@@ -188,6 +188,16 @@ def test_product_strides(m, n, k, ldx, ldw, ldo, dtype):
     _product(m, n, k, dtype, ldx, ldw, ldo)
 
 
+@pytest.mark.parametrize("m,n,k,dtype,ldx,ldw,ldo", [
+    (20, 40, 144, "f32", 1 << 27, 1 << 27, (1 << 27) + 1),
+    (1500, 1500, 144, "f16", 1 << 21, 1 << 21, 1 << 21)])
+def test_product_far_rows(m, n, k, dtype, ldx, ldw, ldo):
+    """Rows whose offsets pass 32 bits, in both kernels."""
+    say("product far rows %dx%dx%d" % (m, n, k))
+    _product(m, n, k, dtype, ldx, ldw, ldo)
+    torch.cuda.empty_cache()
+
+
 def test_product_repeats_its_bits():
     say("product repeats")
     r = np.random.default_rng(1)
