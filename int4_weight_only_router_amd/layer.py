@@ -42,13 +42,19 @@ def load_experts_fp8(weights, H, I, device="cuda", stream=None):
 
     weights: iterable of (wg [I,H], wu [I,H], wd [H,I]) float32 arrays (numpy
     or torch).  Returns a uint8 device tensor [n, blob_bytes] in the layout of
-    moe_fp8_blob_layout, which the kernels read as it is."""
-    weights = list(weights)
+    moe_fp8_blob_layout, which the kernels read as it is.  ValueError for an
+    expert that is not three matrices of these shapes."""
+    shapes = ((I, H), (I, H), (H, I))
+    weights = [tuple(w) for w in weights]
+    for e, w in enumerate(weights):   # the quantiser sees addresses, not shapes
+        got = tuple(tuple(torch.as_tensor(m).shape) for m in w)
+        if got != shapes:
+            raise ValueError("expert %d: matrices of shapes %s, expected %s" % (e, got, shapes))
     off, total = A.moe_fp8_blob_layout(H, I)
     blobs = torch.zeros((len(weights), total), dtype=torch.uint8, device=device)
     for e, w in enumerate(weights):
         base = blobs[e].data_ptr()
-        for j, (m, (rows, cols)) in enumerate(zip(w, ((I, H), (I, H), (H, I)))):
+        for j, (m, (rows, cols)) in enumerate(zip(w, shapes)):
             m = torch.as_tensor(m).to(device=device, dtype=torch.float32).contiguous()
             if stream is not None:   # the copy was made on torch's current stream
                 torch.cuda.synchronize()
