@@ -43,7 +43,10 @@ def load_experts_fp8(weights, H, I, device="cuda", stream=None):
     weights: iterable of (wg [I,H], wu [I,H], wd [H,I]) float32 arrays (numpy
     or torch).  Returns a uint8 device tensor [n, blob_bytes] in the layout of
     moe_fp8_blob_layout, which the kernels read as it is.  ValueError for an
-    expert that is not three matrices of these shapes."""
+    expert that is not three matrices of these shapes.  The copies are made on
+    the device's current stream; with a stream of its own (an object or an
+    address) the quantisation waits for them there, and the current stream for
+    it, without the host."""
     shapes = ((I, H), (I, H), (H, I))
     weights = [tuple(w) for w in weights]
     for e, w in enumerate(weights):   # the quantiser sees addresses, not shapes
@@ -52,17 +55,26 @@ def load_experts_fp8(weights, H, I, device="cuda", stream=None):
             raise ValueError("expert %d: matrices of shapes %s, expected %s" % (e, got, shapes))
     off, total = A.moe_fp8_blob_layout(H, I)
     blobs = torch.zeros((len(weights), total), dtype=torch.uint8, device=device)
-    for e, w in enumerate(weights):
-        base = blobs[e].data_ptr()
-        for j, (m, (rows, cols)) in enumerate(zip(w, shapes)):
-            m = torch.as_tensor(m).to(device=device, dtype=torch.float32).contiguous()
-            if stream is not None:   # the copy was made on torch's current stream
-                torch.cuda.synchronize()
-            A.moe_quantize_fp8(m, A.MOE_DTYPE_F32, cols, rows, cols, 128, 0, base + off[j], cols,
-                               base + off[3 + j], stream)
-            if stream is not None:   # and its memory is free for the next one there
-                torch.cuda.synchronize()
+    with torch.cuda.device(blobs.device):   # the library launches on the current device
+        here = torch.cuda.current_stream()
+        there = here if stream is None else _stream_object(stream)
+        for e, w in enumerate(weights):
+            base = blobs[e].data_ptr()
+            for j, (m, (rows, cols)) in enumerate(zip(w, shapes)):
+                m = torch.as_tensor(m).to(device=blobs.device, dtype=torch.float32).contiguous()
+                there.wait_stream(here)
+                A.moe_quantize_fp8(m, A.MOE_DTYPE_F32, cols, rows, cols, 128, 0, base + off[j],
+                                   cols, base + off[3 + j], there)
+                here.wait_stream(there)   # m's memory goes to later work of this stream
     return blobs
+
+
+def _stream_object(stream):
+    """A torch stream of the current device for a stream given as such or as
+    an address (0: the default stream)."""
+    if not isinstance(stream, int):
+        return stream
+    return torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
 
 
 @dataclass
