@@ -292,6 +292,7 @@ class MoELayer:
         """This layer's combine into `out` plus the next layer's logit partials
         of `out` into `parts` (fp32, moe_logit_partials_bytes()), which
         nxt.experts_routed then routes from."""
+        nxt._check_partials()
         out = b.out if out is None else out
         inv = None if b.regime & A.MOE_Y_TOKEN_ORDER else b.inv_perm
         gate = self.shared_gate
@@ -308,15 +309,22 @@ class MoELayer:
         return (b.T == 1 and self.E <= 64 and b.regime & 0xFF == A.MOE_REGIME_DECODE and
                 not self.fp8 and self.routing is None)
 
+    def _check_partials(self):
+        if self.fp8 or self.routing is not None:
+            raise ValueError("routing from logit partials is for W4A16 experts and softmax top-k")
+
     def logit_partials(self, x, parts, stream=None):
         """This layer's logit partials of an input row in hand (the first
         layer of a stack) into `parts`, for experts_routed."""
+        self._check_partials()
         A.moe_logit_partials(x, self.router, 1, self.H, self.E, parts, stream)
 
     def experts_routed(self, x, b: LayerBuffers, parts, stream=None, shared=True):
         """Routing from the logit partials of the previous layer's combine and
         the routed experts in one launch (moe_expert_ffn_w4a16_routed): fills
-        b's routing arrays and y as route_permute + experts would."""
+        b's routing arrays and y as route_permute + experts would.  ValueError
+        for a layer with FP8 experts or score routing."""
+        self._check_partials()
         A.moe_expert_ffn_w4a16_routed(x, parts, self.bias, self.E, self.k, self.flags,
                                       b.topk_idx, b.topk_w, b.counts, b.offsets, b.perm,
                                       b.inv_perm, self.table, b.T, self.H, self.I, self.g,
