@@ -615,7 +615,9 @@ int moe_fp8_blob_layout(int H, int I, int64_t offsets[6], int64_t *total_bytes);
  * Rows behind offsets[E] are left as they were.  Regimes: DECODE (T <= 128 and
  * min(T, 16) * ceil(max(H, I) / 128) <= 600, else MOE_EUNSUPPORTED: two
  * launches over the weights' stream, activations quantised inside them) and
- * BATCHED (T * ceil(H / 128) up to 2^28 - 32); AUTO takes DECODE where it can
+ * BATCHED (T * ceil(H / 128) up to 2^28 - 32, and at most 2^23 - 8 tiles a
+ * launch, rounded up: (T k / rows + min(E, T k)) * max(I / 128, H / 256) with
+ * tiles of 64 to 192 rows; MOE_EUNSUPPORTED beyond, also by the plan); AUTO takes DECODE where it can
  * up to T * k = 64, and up to 192 while T * k * ceil(H / 128) <= 1024.  The sums of DECODE and of BATCHED's gate and up have fp32
  * accuracy; BATCHED's down is a 16-bit output as above.  H and I multiples of
  * 64, at most 8192; E <= 1024; k <= 16 (MOE_EUNSUPPORTED).  x, y and ws 16-byte

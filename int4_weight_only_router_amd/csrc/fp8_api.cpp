@@ -26,6 +26,7 @@ int launch_fp8_decode(Fp8Args, const void *, float *, int, int, const int64_t *,
                       hipStream_t);
 int fp8_pick_rows(int64_t rows, int E, int I);
 int64_t fp8_tile_bound(int64_t rows, int E, int bm);
+int64_t fp8_most_tiles(int64_t rows, int H, int I, int E);
 int launch_fp8_experts(Fp8Args, int, uint8_t *, float *, int, int, const int64_t *, void *,
                        hipStream_t);
 
@@ -347,6 +348,12 @@ int moe_expert_ffn_w8a8_plan(int T, int H, int I, int E, int k, int regime, int 
                          "%s: the decode regime takes T <= %d and min(T, %d) * ceil(max(H, I) / "
                          "128) <= %d (T=%d H=%d I=%d)", fn, FP8_DECODE_MAX_T, FP8_DECODE_ROWS,
                          FP8_DECODE_BLOCKS, T, H, I);
+    // what the batched launches hold; here, so that nothing is launched beyond it
+    if (r == MOE_REGIME_BATCHED && ((int64_t)T * ((H + 127) / 128) > FP8_MOST_TOKEN_BLOCKS ||
+                                    fp8_most_tiles(n, H, I, E) > FP8_MOST_TILES))
+        return set_error(MOE_EUNSUPPORTED,
+                         "%s: more than %d token blocks or %d tiles (T=%d H=%d I=%d E=%d k=%d)", fn,
+                         FP8_MOST_TOKEN_BLOCKS, FP8_MOST_TILES, T, H, I, E, k);
     if (resolved_regime)
         *resolved_regime = r;
     if (ws_bytes)

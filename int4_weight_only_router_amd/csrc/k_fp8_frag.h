@@ -130,6 +130,10 @@ enum { F8_DENSE = 0, F8_GATEUP = 1, F8_DOWN = 2 };
 constexpr int FP8_DECODE_MAX_T = 128;   // routed experts: decode kernels up to this many tokens,
 constexpr int FP8_DECODE_ROWS = 16;     // of an expert in a workgroup,
 constexpr int FP8_DECODE_BLOCKS = 600;  // whose quantised rows are as many 128-blocks (132 bytes) in LDS
+// A launch has fewer than 2^32 threads: tiles of 512 threads (in whole groups of
+// the 8 XCDs), 128-blocks of tokens of 16 threads (and one workgroup more).
+constexpr int FP8_MOST_TILES = (1 << 23) - 8;
+constexpr int FP8_MOST_TOKEN_BLOCKS = (1 << 28) - 32;
 
 // One row tile of the routed experts: its expert's blob, first sorted row and
 // rows.  Entry 0 of a table holds the number of tiles in `rows`.

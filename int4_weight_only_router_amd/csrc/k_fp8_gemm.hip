@@ -501,10 +501,10 @@ __global__ __launch_bounds__(512, 1) void fp8_tile_kernel(Fp8Args a)
 
 static int f8_grid(int64_t items, unsigned *grid)
 {
-    const int64_t g = (items + F8_NXCD - 1) / F8_NXCD * F8_NXCD;
-    if (g >= (1LL << 32) / 512)   // a launch has fewer than 2^32 threads
-        return set_error(MOE_EUNSUPPORTED, "FP8 product: 2^23 or more tiles");
-    *grid = (unsigned)g;
+    if (items > FP8_MOST_TILES)
+        return set_error(MOE_EUNSUPPORTED, "FP8 product: %lld tiles, at most %d",
+                         (long long)items, FP8_MOST_TILES);
+    *grid = (unsigned)((items + F8_NXCD - 1) / F8_NXCD * F8_NXCD);
     return MOE_OK;
 }
 
@@ -574,6 +574,13 @@ int fp8_pick_rows(int64_t rows, int E, int I)
 int64_t fp8_tile_bound(int64_t rows, int E, int bm)
 {
     return (rows + bm - 1) / bm + std::min<int64_t>(E, rows);
+}
+
+// Workgroups of the larger of the routed experts' two launches.
+int64_t fp8_most_tiles(int64_t rows, int H, int I, int E)
+{
+    return fp8_tile_bound(rows, E, fp8_pick_rows(rows, E, I)) *
+           std::max((I + 127) / 128, (H + 255) / 256);
 }
 
 // Routed experts over the tile table: gate/up into hq/hs, then down into y.

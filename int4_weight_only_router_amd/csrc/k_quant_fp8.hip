@@ -266,9 +266,10 @@ int launch_fp8_tokens(const void *x, int64_t rows, int cols, uint8_t *q, float *
                       const int32_t *offsets, const void *const *blobs, int E, int bm,
                       Fp8TileRec *tiles, hipStream_t s)
 {
-    const int64_t grid = (rows * ((cols + 127) / 128) + 15) / 16 + 1;
-    if (grid >= 1LL << 24)   // a launch has fewer than 2^32 threads
-        return set_error(MOE_EUNSUPPORTED, "FP8 experts: T * ceil(H / 128) above 2^28 - 32");
+    const int64_t blocks = rows * ((cols + 127) / 128), grid = (blocks + 15) / 16 + 1;
+    if (blocks > FP8_MOST_TOKEN_BLOCKS)
+        return set_error(MOE_EUNSUPPORTED, "FP8 experts: %lld token blocks, at most %d",
+                         (long long)blocks, FP8_MOST_TOKEN_BLOCKS);
     hipLaunchKernelGGL(fp8_tokens_kernel, dim3((unsigned)grid), dim3(256), 0, s,
                        static_cast<const f16 *>(x), rows, cols, q, scales, offsets, blobs, E, bm,
                        tiles);
