@@ -593,7 +593,8 @@ int moe_gemm_fp8(const void *xq, int64_t ldx, const float *x_scales, const void 
  * up_q[I][H], down_q[H][I] (e4m3, row-major) then gate_s, up_s
  * [ceil(I/128)][ceil(H/128)] and down_s[ceil(H/128)][ceil(I/128)] (fp32, one
  * per 128 x 128 block) -- moe_quantize_fp8 with block_rows = 128 writes such
- * sections.  The kernels read this layout as it is.  Host-only.
+ * sections.  The kernels read this layout as it is.  Host-only.  H and I up to
+ * 2^30 (MOE_EUNSUPPORTED).
  */
 int moe_fp8_blob_layout(int H, int I, int64_t offsets[6], int64_t *total_bytes);
 

@@ -313,6 +313,8 @@ int moe_fp8_blob_layout(int H, int I, int64_t offsets[6], int64_t *total_bytes)
     clear_error();
     if (!offsets || !total_bytes || H <= 0 || I <= 0)
         return set_error(MOE_EINVAL, "moe_fp8_blob_layout: bad arguments (H=%d I=%d)", H, I);
+    if (H > 1 << 30 || I > 1 << 30)   // three H x I sections fit 63 bits
+        return set_error(MOE_EUNSUPPORTED, "moe_fp8_blob_layout: H=%d I=%d above 2^30", H, I);
     fp8_blob(H, I, offsets, total_bytes);
     return MOE_OK;
 }

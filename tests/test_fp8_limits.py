@@ -32,3 +32,11 @@ def test_experts_at_the_limits():
     _unsupported(M.moe_expert_ffn_w8a8_plan, T + 12, 64, 8192, 16, 16)
     assert M.moe_expert_ffn_w8a8_plan((1 << 28) - 32, 64, 64, 8, 1)[0] == M.MOE_REGIME_BATCHED
     _unsupported(M.moe_expert_ffn_w8a8_plan, (1 << 28) - 31, 64, 64, 8, 1)
+
+
+def test_blob_layout_beyond_64_bits():
+    off, total = M.moe_fp8_blob_layout(1 << 30, 1 << 30)
+    assert off[:4] == [0, 1 << 60, 2 << 60, 3 << 60]
+    assert off[4] - off[3] == 4 << 46 and total == off[5] + (4 << 46)
+    for H, I in (((1 << 30) + 1, 64), (64, (1 << 31) - 1), ((1 << 31) - 1, (1 << 31) - 1)):
+        _unsupported(M.moe_fp8_blob_layout, H, I)
