@@ -496,7 +496,8 @@ int moe_expert_ffn_w4a16_routed(const void *x_f16, const float *logit_partials,
  * moe_route_select.
  *   x_f16 device fp16 [T][H], w_router_f16 device fp16 [E][H] (16-byte
  *   aligned), logit_bias device fp32 [E] or NULL; logits device fp32 [T][E].
- * H in {256, 512, 1024, 2048}, E <= 1024 (MOE_EUNSUPPORTED).  T = 0: no-op.
+ * H in {256, 512, 1024, 2048}, E <= 1024, T <= 2^27 - 8 (MOE_EUNSUPPORTED).
+ * T = 0: no-op.
  */
 int moe_router_logits(const void *x_f16, const void *w_router_f16, const float *logit_bias, int T,
                       int H, int E, float *logits, hipStream_t stream);

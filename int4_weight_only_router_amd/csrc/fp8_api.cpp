@@ -168,6 +168,8 @@ int moe_router_logits(const void *x_f16, const void *w_router_f16, const float *
     if (!h_supported(H) || E > 1024)
         return set_error(MOE_EUNSUPPORTED, "%s: H in {256, 512, 1024, 2048} and E <= 1024 required "
                          "(H=%d E=%d)", fn, H, E);
+    if (T > (1 << 27) - 8)   // 256 threads for 8 tokens, and a launch has fewer than 2^32
+        return set_error(MOE_EUNSUPPORTED, "%s: T=%d above 2^27 - 8", fn, T);
     if (T == 0)
         return MOE_OK;
     if (!x_f16 || !w_router_f16 || !logits)

@@ -40,3 +40,8 @@ def test_blob_layout_beyond_64_bits():
     assert off[4] - off[3] == 4 << 46 and total == off[5] + (4 << 46)
     for H, I in (((1 << 30) + 1, 64), (64, (1 << 31) - 1), ((1 << 31) - 1, (1 << 31) - 1)):
         _unsupported(M.moe_fp8_blob_layout, H, I)
+
+
+@pytest.mark.parametrize("T", [(1 << 27) - 7, (1 << 31) - 1])
+def test_logits_beyond_a_launch(T):
+    _unsupported(M.moe_router_logits, P, P, None, T, 256, 64, P, stream=0)
