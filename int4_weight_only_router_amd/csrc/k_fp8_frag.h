@@ -12,8 +12,6 @@
 // holds four consecutive output columns of one token.
 #pragma once
 
-#include <atomic>
-
 #include "moe_common.h"
 
 namespace moe {
@@ -108,23 +106,6 @@ __device__ __forceinline__ float row16_max(float a)
 #undef MOE_ROW_MAX
     return a;
 }
-
-// Raises a kernel's dynamic LDS limit once on each device that launches it.
-struct LdsLimit {
-    std::atomic<uint64_t> done{0};
-    int raise(const void *kernel, int bytes)
-    {
-        int dev = 0;
-        MOE_HIP_TRY(hipGetDevice(&dev));
-        const uint64_t bit = 1ull << (dev & 63);
-        if (!(done.load(std::memory_order_relaxed) & bit)) {
-            MOE_HIP_TRY(hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize,
-                                            bytes));
-            done.fetch_or(bit, std::memory_order_relaxed);
-        }
-        return MOE_OK;
-    }
-};
 
 enum { F8_DENSE = 0, F8_GATEUP = 1, F8_DOWN = 2 };
 constexpr int FP8_DECODE_MAX_T = 128;   // routed experts: decode kernels up to this many tokens,

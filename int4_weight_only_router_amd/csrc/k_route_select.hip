@@ -675,15 +675,6 @@ static int for_width(int E, F &&f)
     return f(std::integral_constant<int, 16>());
 }
 
-// Raises a kernel's LDS limit for group keys (idempotent).
-static int raise_lds(const void *kernel, size_t group_bytes)
-{
-    if (group_bytes)
-        MOE_HIP_TRY(hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize,
-                                        (int)RSC_KEY_BYTES));
-    return MOE_OK;
-}
-
 // The grouping's outputs (counts NULL: selection alone); hist: the chunked form.
 struct SelSort {
     int32_t *counts, *offsets, *perm, *inv_perm;
@@ -703,8 +694,11 @@ static int launch_select_t(const SelArgs &a, const SelSort &how, hipStream_t st)
             return MOE_OK;
         }
         if (how.counts && how.hist) {
-            if (const int rc = raise_lds((const void *)route_select_count_kernel<NV, LT>, g))
-                return rc;
+            static LdsLimit limit;
+            if (g)   // group keys
+                if (const int rc = limit.raise((const void *)route_select_count_kernel<NV, LT>,
+                                               (int)RSC_KEY_BYTES))
+                    return rc;
             const int chunks = (a.T + RSC_TOK - 1) / RSC_TOK;
             hipLaunchKernelGGL((route_select_count_kernel<NV, LT>), dim3(chunks),
                                dim3(RSC_WAVES * 64), g * RSC_WAVES, st, a, how.hist);
@@ -717,8 +711,11 @@ static int launch_select_t(const SelArgs &a, const SelSort &how, hipStream_t st)
             return MOE_OK;
         }
         if (how.counts) {
-            if (const int rc = raise_lds((const void *)route_select_sort_kernel<NV, LT>, g))
-                return rc;
+            static LdsLimit limit;
+            if (g)   // group keys
+                if (const int rc = limit.raise((const void *)route_select_sort_kernel<NV, LT>,
+                                               (int)RSC_KEY_BYTES))
+                    return rc;
             hipLaunchKernelGGL((route_select_sort_kernel<NV, LT>), dim3(1), dim3(a.T * 64),
                                g * a.T, st, a, how.counts, how.offsets, how.perm, how.inv_perm);
             MOE_LAUNCH_CHECK("route_select_sort_kernel");

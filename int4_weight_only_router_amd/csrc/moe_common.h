@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 #include <hip/hip_fp16.h>
 
+#include <atomic>
 #include <cstdarg>
 #include <cstdint>
 #include <cstdio>
@@ -82,6 +83,23 @@ void clear_error();
             return ::moe::set_error(MOE_EHIP, "launch of %s failed: %s (%d)",     \
                                     what, hipGetErrorString(_e), (int)_e);       \
     } while (0)
+
+// Raises a kernel's dynamic LDS limit once on each device that launches it.
+struct LdsLimit {
+    std::atomic<uint64_t> done{0};
+    int raise(const void *kernel, int bytes)
+    {
+        int dev = 0;
+        MOE_HIP_TRY(hipGetDevice(&dev));
+        const uint64_t bit = 1ull << (dev & 63);
+        if (!(done.load(std::memory_order_relaxed) & bit)) {
+            MOE_HIP_TRY(hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize,
+                                            bytes));
+            done.fetch_or(bit, std::memory_order_relaxed);
+        }
+        return MOE_OK;
+    }
+};
 
 inline int64_t al256(int64_t x) { return (x + 255) & ~int64_t(255); }
 
