@@ -88,14 +88,20 @@ __device__ __forceinline__ double key_choice(uint64_t k)
     return __builtin_bit_cast(double, b);
 }
 
-// exp(x) for x <= 709 (0 below -745): x = n ln 2 + r, |r| <= ln 2 / 2, Taylor
-// to r^13 (next term 4e-18).
+// exp(x) for x <= 709 (0 below -745): x = n ln 2 + r, |r| about ln 2 / 2 at
+// most, Taylor to r^13 (next term 4e-18).  The reduction is Cody and Waite's
+// (Software Manual for the Elementary Functions, 1980), ln 2 in two parts; with
+// fma the first may be ln 2 rounded to fp64 itself, LN2 = 0x1.62e42fefa39efp-1:
+// it is a multiple of 2^-53, x one of 2^-53 (|x| >= 1/2) or of 2^-54 (|x| >= 1/4,
+// then |n| <= 1, and below that n = 0), so x - n LN2, smaller than 1/2, fits 53
+// bits and is exact.  LN2_LO = ln 2 - LN2, rounded.
 __device__ __forceinline__ double exp_f64(double x)
 {
+    constexpr double LN2 = 0x1.62e42fefa39efp-1, LN2_LO = 0x1.abc9e3b39803fp-56;
     x = fmax(x, -746.0);
-    const double n = __builtin_rint(x * 1.4426950408889634074);
-    double r = __builtin_fma(n, -6.93147180369123816490e-01, x);
-    r = __builtin_fma(n, -1.90821492927058770002e-10, r);
+    const double n = __builtin_rint(x * (1.0 / LN2));
+    double r = __builtin_fma(n, -LN2, x);
+    r = __builtin_fma(n, -LN2_LO, r);
     double p = 1.0 / 6227020800.0;
     p = __builtin_fma(p, r, 1.0 / 479001600.0);
     p = __builtin_fma(p, r, 1.0 / 39916800.0);
