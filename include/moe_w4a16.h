@@ -68,6 +68,9 @@ enum { MOE_RENORM = 1u };                       /* moe_route flag */
 enum { MOE_GROUP_TOP2 = 2u };                   /* moe_route_select flag */
 enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
 enum { MOE_SCALE_POW2 = 1u };                   /* moe_quantize_fp8 flag */
+/* OR'd into out_dtype of moe_gemm_fp8 and into the regime of
+ * moe_expert_ffn_w8a8(_plan): every sum has fp32 accuracy, whatever the sizes. */
+enum { MOE_ACC_F32 = 0x800 };
 enum { MOE_REGIME_AUTO = 0, MOE_REGIME_DECODE = 1, MOE_REGIME_BATCHED = 2, MOE_REGIME_SMALL = 3 };
 /* OR'd into the regime of moe_expert_ffn_plan / moe_expert_ffn_w4a16: y rows
  * in token order (row t*k + j) instead of sorted order; see below. */
@@ -576,7 +579,11 @@ int moe_quantize_fp8(const void *x, int dtype, int64_t ldx, int64_t rows, int co
  * accuracy of fp32 sums.  16-bit outputs of many rows take the FP8 matrix
  * instruction, which adds runs of eight neighbouring products and drops there
  * what lies 13 bits below the run's largest (1.4e-5 relative on random data,
- * below the output's own rounding; at worst 7 * 2^-13 of the sum of |products|).
+ * below the output's own rounding; at worst 7 * 2^-13 of the sum of |products|,
+ * which exceeds that rounding where products cancel).  With MOE_ACC_F32 OR'd
+ * into out_dtype 16-bit outputs have the accuracy of fp32 sums at every size,
+ * so that a row's does not depend on how many rows come with it, at half the
+ * instruction's rate.
  *   xq  device e4m3 [M], ldx bytes apart;  x_scales device fp32 [M][ceil(K/128)]
  *   wq  device e4m3 [N], ldw bytes apart;  w_scales [ceil(N/128)][ceil(K/128)]
  *   out device [M] rows of N values (F16, BF16 or F32), ldo elements apart
@@ -621,7 +628,8 @@ int moe_fp8_blob_layout(int H, int I, int64_t offsets[6], int64_t *total_bytes);
  * launch, rounded up: (T k / rows + min(E, T k)) * max(I / 128, H / 256) with
  * tiles of 64 to 192 rows; MOE_EUNSUPPORTED beyond, also by the plan); AUTO takes DECODE where it can
  * up to T * k = 64, and up to 192 while T * k * ceil(H / 128) <= 1024.  The sums of DECODE and of BATCHED's gate and up have fp32
- * accuracy; BATCHED's down is a 16-bit output as above.  H and I multiples of
+ * accuracy; BATCHED's down is a 16-bit output as above, and MOE_ACC_F32 OR'd into
+ * the regime (the resolved one keeps it) gives its sums fp32 accuracy too.  H and I multiples of
  * 64, at most 8192; E <= 1024; k <= 16 (MOE_EUNSUPPORTED).  x, y and ws 16-byte
  * aligned (MOE_EINVAL).  T = 0: no-op.
  */

@@ -11,7 +11,7 @@ __all__ = [
     "MOE_ECAPACITY", "MOE_ESTATE", "MOE_RENORM", "MOE_REGIME_AUTO", "MOE_REGIME_DECODE",
     "MOE_REGIME_BATCHED", "MOE_REGIME_SMALL", "MOE_Y_TOKEN_ORDER", "MOE_Y_PARTIAL_ORDER",
     "MOE_DTYPE_F16", "MOE_DTYPE_F32", "MOE_DTYPE_F32_PM", "MOE_DTYPE_BF16",
-    "MOE_GROUP_TOP2", "MOE_SCORE_SOFTMAX", "MOE_SCORE_SIGMOID", "MOE_SCALE_POW2", "MOE_FMT_SYM", "MOE_FMT_ZP", "MOE_FMT_FP8", "MOE_W4_ZERO_POINT", "EXPORTS",
+    "MOE_GROUP_TOP2", "MOE_SCORE_SOFTMAX", "MOE_SCORE_SIGMOID", "MOE_SCALE_POW2", "MOE_ACC_F32", "MOE_FMT_SYM", "MOE_FMT_ZP", "MOE_FMT_FP8", "MOE_W4_ZERO_POINT", "EXPORTS",
     "moe_blob_layout_fmt", "moe_quantize_experts_fmt", "moe_prepack_experts_fmt",
     "moe_unpack_experts_fmt", "moe_prepack_expert_host", "moe_unpack_expert_host",
     "moe_last_error", "moe_workspace_clear", "moe_blob_layout", "moe_quantize_experts",
@@ -44,6 +44,7 @@ MOE_DTYPE_F16, MOE_DTYPE_F32, MOE_DTYPE_F32_PM, MOE_DTYPE_BF16 = 0, 1, 2, 3
 MOE_GROUP_TOP2 = 2          # moe_route_select flag: a group counts by its two best experts
 MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 MOE_SCALE_POW2 = 1          # moe_quantize_fp8 flag: power-of-two scales
+MOE_ACC_F32 = 0x800         # OR'd into moe_gemm_fp8's out_dtype and a w8a8 regime: fp32 sums
 MOE_FMT_SYM, MOE_FMT_ZP = 0, 1   # expert blob formats (zero point per group)
 MOE_FMT_FP8 = 2                  # e4m3 blobs (moe_fp8_blob_layout); no argument of the _fmt calls
 MOE_W4_ZERO_POINT = 0x200        # OR'd into a regime: the blobs are MOE_FMT_ZP

@@ -21,14 +21,14 @@ int launch_quant_fp8(const void *, int, int64_t, int64_t, int, int, bool, void *
 int launch_fp8_tokens(const void *, int64_t, int, uint8_t *, float *, const int32_t *,
                       const void *const *, int, int, Fp8TileRec *, hipStream_t);
 int launch_fp8_rows_dense(const Fp8Args &, hipStream_t);
-int launch_fp8_tile_dense(const Fp8Args &, int mf, hipStream_t);
+int launch_fp8_tile_dense(const Fp8Args &, int mf, bool acc32, hipStream_t);
 int launch_fp8_decode(Fp8Args, const void *, float *, int, int, const int64_t *, void *,
                       hipStream_t);
 int fp8_pick_rows(int64_t rows, int E, int I);
 int64_t fp8_tile_bound(int64_t rows, int E, int bm);
 int64_t fp8_most_tiles(int64_t rows, int H, int I, int E);
 int launch_fp8_experts(Fp8Args, int, uint8_t *, float *, int, int, const int64_t *, void *,
-                       hipStream_t);
+                       bool acc32, hipStream_t);
 
 static int check_types(const char *fn, int dtype)
 {
@@ -92,11 +92,11 @@ static Fp8Ws fp8_ws(int T, int H, int I, int E, int k, bool decode)
 // (32 x 32 tiles).  The least of the times that were measured for one round of
 // tiles over the 256 compute units at K = 2048 (every form grows alike with K),
 // in us: 64-, 128-, 192- and 256-row tiles 14.5, 20.5, 24.5, 29.5, and 24, 33.5,
-// 43, 52.5 with fp32 outputs (the fp16 form); the kernel of few rows 2.5 and 9.8
+// 43, 52.5 in the fp16 form (fp32 outputs or sums); the kernel of few rows 2.5 and 9.8
 // for every 1000 workgroups.  Against each form on 28 products from 64 x 5632 to
 // 4096 x 11264 (K 512 to 5632, both forms) the choice is the fastest or within
 // 3% of it.
-static int dense_tile(int M, int N, bool f32)
+static int dense_tile(int M, int N, bool f16_form)
 {
     static const double round_us[2][4] = {{14.5, 20.5, 24.5, 29.5}, {24, 33.5, 43, 52.5}};
     const int64_t few = (int64_t)((M + 31) / 32) * ((N + 31) / 32);
@@ -104,7 +104,7 @@ static int dense_tile(int M, int N, bool f32)
     int mf = 0;
     for (int i = 1; i <= 4; ++i) {
         const int64_t tiles = (int64_t)((M + 64 * i - 1) / (64 * i)) * ((N + 255) / 256);
-        const double t = 3 + (double)((tiles + 255) / 256) * (round_us[f32][i - 1] - 3);
+        const double t = 3 + (double)((tiles + 255) / 256) * (round_us[f16_form][i - 1] - 3);
         if (M > 32 && t < best) {
             best = t;
             mf = i;
@@ -266,6 +266,8 @@ int moe_gemm_fp8(const void *xq, int64_t ldx, const float *x_scales, const void 
     MOE_API_RANGE();
     clear_error();
     const char *fn = "moe_gemm_fp8";
+    const bool acc32 = (out_dtype & MOE_ACC_F32) != 0;
+    out_dtype &= ~MOE_ACC_F32;
     int rc = check_types(fn, out_dtype);
     if (rc)
         return rc;
@@ -299,11 +301,11 @@ int moe_gemm_fp8(const void *xq, int64_t ldx, const float *x_scales, const void 
     a.out = out;
     a.ldo = ldo;
     a.odt = out_dtype;
-    const int mf = dense_tile(M, N, out_dtype == MOE_DTYPE_F32);
+    const int mf = dense_tile(M, N, acc32 || out_dtype == MOE_DTYPE_F32);
     // (the tile kernel's offsets inside 256 weight rows are 32 bits wide)
     const bool few_rows = (M + 31) / 32 <= 65535 && N <= 1 << 28;   // its grid's limits
     if (ldw < (int64_t)1 << 22 && (mf || !few_rows))
-        return launch_fp8_tile_dense(a, mf ? mf : 4, stream);
+        return launch_fp8_tile_dense(a, mf ? mf : 4, acc32, stream);
     if (!few_rows)
         return set_error(MOE_EUNSUPPORTED, "%s: M=%d N=%d with ldw=%lld", fn, M, N,
                          (long long)ldw);
@@ -329,6 +331,8 @@ int moe_expert_ffn_w8a8_plan(int T, int H, int I, int E, int k, int regime, int 
     const int rc = check_fp8_shape(fn, T, H, I, E, k);
     if (rc)
         return rc;
+    const int acc32 = regime & MOE_ACC_F32;
+    regime &= ~MOE_ACC_F32;
     if (regime != MOE_REGIME_AUTO && regime != MOE_REGIME_DECODE && regime != MOE_REGIME_BATCHED)
         return set_error(MOE_EINVAL, "%s: bad regime %d", fn, regime);
     // decode up to 64 routed rows, and up to 192 of short tokens, where its one
@@ -359,7 +363,7 @@ int moe_expert_ffn_w8a8_plan(int T, int H, int I, int E, int k, int regime, int 
                          "%s: more than %d token blocks or %d tiles (T=%d H=%d I=%d E=%d k=%d)", fn,
                          FP8_MOST_TOKEN_BLOCKS, FP8_MOST_TILES, T, H, I, E, k);
     if (resolved_regime)
-        *resolved_regime = r;
+        *resolved_regime = r | acc32;
     if (ws_bytes)
         *ws_bytes = (size_t)fp8_ws(T, H, I, E, k, r == MOE_REGIME_DECODE).total;
     return MOE_OK;
@@ -382,7 +386,7 @@ int moe_expert_ffn_w8a8(const void *x_f16, const int32_t *perm, const int32_t *o
         return set_error(MOE_EINVAL, "%s: x, y and the workspace must be 16-byte aligned", fn);
     if (!ws || ws_bytes < need)
         return set_error(MOE_ENOMEM, "%s: workspace %zu < %zu bytes", fn, ws_bytes, need);
-    const bool decode = r == MOE_REGIME_DECODE;
+    const bool decode = (r & ~MOE_ACC_F32) == MOE_REGIME_DECODE;
     const Fp8Ws w = fp8_ws(T, H, I, E, k, decode);
     uint8_t *base = static_cast<uint8_t *>(ws);
     int64_t off[6], total = 0;
@@ -409,7 +413,7 @@ int moe_expert_ffn_w8a8(const void *x_f16, const int32_t *perm, const int32_t *o
     a.xs = xs;
     a.tiles = tiles;
     return launch_fp8_experts(a, bm, base + w.hq, reinterpret_cast<float *>(base + w.hs), H, I, off,
-                              y_f16, stream);
+                              y_f16, (r & MOE_ACC_F32) != 0, stream);
 }
 
 }  // extern "C"

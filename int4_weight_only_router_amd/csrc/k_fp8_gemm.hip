@@ -14,11 +14,12 @@
 //    eight products and drops there what lies 13 bits or more below the
 //    largest (measured: 1 + 2^-14 in one run gives 1, in two runs 1 + 2^-14;
 //    the smaller v_mfma_f32_16x16x32_fp8_fp8 gives the same bits), 1.4e-5
-//    relative on random data.  Used where the output is rounded to 16 bits
-//    anyway.
+//    relative on random data, but as much as the result where products cancel.
+//    Used where the output is rounded to 16 bits and the caller has not asked
+//    for fp32 sums (MOE_ACC_F32).
 //  - EX: both operands as fp16 (exactly) on v_mfma_f32_16x16x32_f16, half the
-//    rate, errors of fp32 sums.  Used for fp32 outputs, and for gate/up, whose
-//    result is quantised again: an error of 1e-5 there sends 1 element of 2000
+//    rate, errors of fp32 sums.  Used for fp32 outputs, with MOE_ACC_F32, and
+//    for gate/up, whose result is quantised again: an error of 1e-5 there sends 1 element of 2000
 //    to a neighbouring code (measured: the experts' error against 64 bits goes
 //    from 3e-4 to 1.1e-3).
 //
@@ -157,7 +158,8 @@ constexpr int f8_lds(int nkb)
     return f8_stages<MF>() * f8_stage_bytes<MF>() + 2 * F8_SCW * 64 * MF * 4 + 2 * nkb * 4;
 }
 
-template <int MODE, int MF, bool EX>
+// ES: bytes of an output element (gate/up: not used).
+template <int MODE, int MF, bool EX, int ES>
 __global__ __launch_bounds__(512, 1) void fp8_tile_kernel(Fp8Args a)
 {
     constexpr int NTH = 512;
@@ -455,11 +457,10 @@ __global__ __launch_bounds__(512, 1) void fp8_tile_kernel(Fp8Args a)
         // columns of a row: stored from there, 16 rows by 32 bytes at a time,
         // the 4096 x 11264 product spent a quarter of its time on them)
         const int dt = MODE == F8_DOWN ? MOE_DTYPE_F16 : a.odt;
-        constexpr int es = EX ? 4 : 2;               // EX is the fp32 output
-        constexpr int LR = 256 * es + 16;            // LDS row, off the banks' period
-        constexpr int PASS = EX && MF > 2 ? (MF == 4 ? 2 : 3) : 1;   // parts of the row fragments that fit
-        constexpr int gp = 16 / es;                  // columns of a 16-byte piece
-        const bool vec = (a.ldo * es) % 16 == 0 && ((uintptr_t)a.out & 15) == 0;
+        constexpr int LR = 256 * ES + 16;            // LDS row, off the banks' period
+        constexpr int PASS = ES == 4 && MF > 2 ? (MF == 4 ? 2 : 3) : 1;   // parts of the row fragments that fit
+        constexpr int gp = 16 / ES;                  // columns of a 16-byte piece
+        const bool vec = (a.ldo * ES) % 16 == 0 && ((uintptr_t)a.out & 15) == 0;
 #pragma unroll
         for (int h = 0; h < PASS; ++h) {
             constexpr int MH = XF / PASS;
@@ -480,13 +481,13 @@ __global__ __launch_bounds__(512, 1) void fp8_tile_kernel(Fp8Args a)
                 const int n = n0 + c;
                 if (r >= t.rows || n >= a.N)
                     continue;
-                uint8_t *to = static_cast<uint8_t *>(a.out) + ((t.row0 + r) * a.ldo + n) * es;
-                const uint8_t *from = smem + lr2 * LR + c * es;
+                uint8_t *to = static_cast<uint8_t *>(a.out) + ((t.row0 + r) * a.ldo + n) * ES;
+                const uint8_t *from = smem + lr2 * LR + c * ES;
                 if (vec && n + gp <= a.N) {
                     *reinterpret_cast<int4_t *>(to) = *reinterpret_cast<const int4_t *>(from);
                 } else {
                     for (int j = 0; j < gp && n + j < a.N; ++j) {
-                        if constexpr (EX)
+                        if constexpr (ES == 4)
                             reinterpret_cast<uint32_t *>(to)[j] =
                                 reinterpret_cast<const uint32_t *>(from)[j];
                         else
@@ -508,17 +509,17 @@ static int f8_grid(int64_t items, unsigned *grid)
     return MOE_OK;
 }
 
-template <int MODE, int MF, bool EX>
+template <int MODE, int MF, bool EX, int ES>
 static int launch_tile(const Fp8Args &a, int64_t items, hipStream_t s)
 {
     static LdsLimit limit;
     unsigned grid;
     int rc = f8_grid(items, &grid);
     if (!rc)
-        rc = limit.raise((const void *)fp8_tile_kernel<MODE, MF, EX>, 160 * 1024);
+        rc = limit.raise((const void *)fp8_tile_kernel<MODE, MF, EX, ES>, 160 * 1024);
     if (rc)
         return rc;
-    hipLaunchKernelGGL((fp8_tile_kernel<MODE, MF, EX>), dim3(grid), dim3(512),
+    hipLaunchKernelGGL((fp8_tile_kernel<MODE, MF, EX, ES>), dim3(grid), dim3(512),
                        f8_lds<MF>((a.K + 127) / 128), s, a);
     MOE_LAUNCH_CHECK("fp8_tile_kernel");
     return MOE_OK;
@@ -528,28 +529,29 @@ template <int MODE, bool EX>
 static int launch_tile_mf(const Fp8Args &a, int mf, int64_t items, hipStream_t s)
 {
     switch (mf) {
-    case 1: return launch_tile<MODE, 1, EX>(a, items, s);
-    case 2: return launch_tile<MODE, 2, EX>(a, items, s);
-    default: return launch_tile<MODE, 3, EX>(a, items, s);
+    case 1: return launch_tile<MODE, 1, EX, 2>(a, items, s);
+    case 2: return launch_tile<MODE, 2, EX, 2>(a, items, s);
+    default: return launch_tile<MODE, 3, EX, 2>(a, items, s);
     }
 }
 
 template <int MF>
-static int launch_tile_dense(const Fp8Args &a, hipStream_t s)
+static int launch_tile_dense(const Fp8Args &a, bool acc32, hipStream_t s)
 {
     const int64_t items = (int64_t)((a.M + 64 * MF - 1) / (64 * MF)) * ((a.N + 255) / 256);
     if (a.odt == MOE_DTYPE_F32)
-        return launch_tile<F8_DENSE, MF, true>(a, items, s);
-    return launch_tile<F8_DENSE, MF, false>(a, items, s);
+        return launch_tile<F8_DENSE, MF, true, 4>(a, items, s);
+    return acc32 ? launch_tile<F8_DENSE, MF, true, 2>(a, items, s)
+                 : launch_tile<F8_DENSE, MF, false, 2>(a, items, s);
 }
 
-int launch_fp8_tile_dense(const Fp8Args &a, int mf, hipStream_t s)
+int launch_fp8_tile_dense(const Fp8Args &a, int mf, bool acc32, hipStream_t s)
 {
     switch (mf) {
-    case 1: return launch_tile_dense<1>(a, s);
-    case 2: return launch_tile_dense<2>(a, s);
-    case 3: return launch_tile_dense<3>(a, s);
-    default: return launch_tile_dense<4>(a, s);
+    case 1: return launch_tile_dense<1>(a, acc32, s);
+    case 2: return launch_tile_dense<2>(a, acc32, s);
+    case 3: return launch_tile_dense<3>(a, acc32, s);
+    default: return launch_tile_dense<4>(a, acc32, s);
     }
 }
 
@@ -585,7 +587,7 @@ int64_t fp8_most_tiles(int64_t rows, int H, int I, int E)
 
 // Routed experts over the tile table: gate/up into hq/hs, then down into y.
 int launch_fp8_experts(Fp8Args a, int bm, uint8_t *hq, float *hs, int H, int I,
-                       const int64_t off[6], void *y, hipStream_t s)
+                       const int64_t off[6], void *y, bool acc32, hipStream_t s)
 {
     const int64_t bound = fp8_tile_bound((int64_t)a.T * a.k, a.E, bm);
     a.ldx = H;
@@ -611,7 +613,8 @@ int launch_fp8_experts(Fp8Args a, int bm, uint8_t *hq, float *hs, int H, int I,
     a.off_w0 = off[2];
     a.off_s0 = off[5];
     items = bound * ((H + 255) / 256);
-    return launch_tile_mf<F8_DOWN, false>(a, bm / 64, items, s);
+    return acc32 ? launch_tile_mf<F8_DOWN, true>(a, bm / 64, items, s)
+                 : launch_tile_mf<F8_DOWN, false>(a, bm / 64, items, s);
 }
 
 }  // namespace moe

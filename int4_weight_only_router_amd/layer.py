@@ -148,7 +148,8 @@ class MoELayer:
 
     def buffers(self, T, regime=A.MOE_REGIME_AUTO, partial_order=True) -> LayerBuffers:
         """partial_order: decode partials in partial-major column order, which
-        the fused combine + next route reads in whole lines."""
+        the fused combine + next route reads in whole lines.  FP8 layers:
+        regime may carry MOE_ACC_F32 (fp32 sums in every product)."""
         d = self.device
         if self.fp8:
             r, ffn_ws = A.moe_expert_ffn_w8a8_plan(T, self.H, self.I, self.E, self.k, regime)

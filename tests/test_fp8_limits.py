@@ -45,3 +45,18 @@ def test_blob_layout_beyond_64_bits():
 @pytest.mark.parametrize("T", [(1 << 27) - 7, (1 << 31) - 1])
 def test_logits_beyond_a_launch(T):
     _unsupported(M.moe_router_logits, P, P, None, T, 256, 64, P, stream=0)
+
+
+def test_fp32_sums_flag():
+    """The plan keeps the flag in what it resolves, and asks for the same workspace."""
+    for T, regime in ((1, M.MOE_REGIME_AUTO), (1, M.MOE_REGIME_BATCHED), (500, M.MOE_REGIME_AUTO)):
+        r, n = M.moe_expert_ffn_w8a8_plan(T, 256, 128, 8, 2, regime)
+        assert M.moe_expert_ffn_w8a8_plan(T, 256, 128, 8, 2, regime | M.MOE_ACC_F32) == \
+            (r | M.MOE_ACC_F32, n)
+    for call in (lambda: M.moe_expert_ffn_w8a8_plan(1, 256, 128, 8, 2, M.MOE_REGIME_SMALL | M.MOE_ACC_F32),
+                 lambda: M.moe_gemm_fp8(P, 256, P, P, 256, P, 4, 64, 256, P, 2 | M.MOE_ACC_F32, 64,
+                                        stream=0),
+                 lambda: M.moe_expert_ffn_plan(1, 256, 128, 8, 2, 64, M.MOE_ACC_F32)):
+        with pytest.raises(M.MoEError) as ei:
+            call()
+        assert ei.value.code == M.MOE_EINVAL
