@@ -10,18 +10,23 @@
 // 128-long block of K each.  A wave has one block in flight, in a stage of its
 // own in LDS filled by direct-to-LDS loads of 8 lanes per 128-byte row block
 // (loaded straight into the matrix instruction's layout, consecutive lanes are
-// consecutive rows, and the L1 serves 16 bytes a cycle instead of 64), and six
-// workgroups share a compute unit: many small stages beat few deep ones (64
-// experts, 4 tokens: 31.5 us with one stage per wave, 35 with two, 50 with
-// four, at a floor of 30.5; one token 14.7, 15.4, 16.8).  No barrier is needed until the waves' sums meet
-// in LDS, in wave order, so that results do not depend on timing.  The tokens
-// are the matrix core's second operand, 16 to a fragment; its idle columns
-// cost nothing here.  The fp16 form of a block's sum (fp32 accuracy).
+// consecutive rows, and the L1 serves 16 bytes a cycle instead of 64).  Several
+// workgroups share a compute unit, as many as its LDS (stages, decode rows, 8 KB
+// of sums, 16 for 32 rows) and registers hold: gate/up at H = 2048 five with one
+// token, four with four, two with sixteen; down at I = 1024 six with one, five
+// with four; dense four (16 rows) or three (32).  So many small stages beat few
+// deep ones (64 experts, 4 tokens: 31.5 us with one stage per wave, 35 with two,
+// 50 with four, at a floor of 30.5; one token 14.7, 15.4, 16.8).  No barrier is
+// needed until the waves' sums meet in LDS, in wave order, so that results do not
+// depend on timing.  The tokens are the matrix core's second operand, 16 to a
+// fragment; its idle columns cost nothing here.  The fp16 form of a block's sum
+// (fp32 accuracy).
 //
-// Measured: 1 x 5632 x 2048 4.9 us (11.5 MB, of which the loads alone need
-// 2.2), 333 x 1408 x 2000 with fp32 outputs 6.9 us; experts of 2048 x 1024,
-// top-8 of 64: one token 14.3 us for 50 MB (3.5 TB/s), four 32 us for 157 MB
-// (4.9 TB/s of the 5.15 that a large copy reaches).
+// Measured: 1 x 5632 x 2048 5.1 us a call, 4.1 on the card (11.5 MB, whose loads
+// alone need 2.2: a wave's four blocks of K come one after the other), 333 x 1408
+// x 2000 with fp32 outputs 6.9 us; experts of 2048 x 1024, top-8 of 64: one token
+// 14.3 us for 50 MB (3.5 TB/s), four 32.5 us for 176 MB in 28 experts (part of it
+// from the last-level cache in back-to-back calls), eight 47.5 for 258 in 41.
 //
 // Decode experts quantise their rows in the workgroup (gate/up: the fp16
 // tokens; down: the fp32 h the first launch left in the workspace), hidden
@@ -84,7 +89,8 @@ constexpr int f8_rows_stage()
 // F8_DOWN: grid (tiles of 16 intermediate / 32 output columns, sorted rows);
 // the workgroups at an expert's first row and every 16th (every T-th) after it
 // serve the rows up to the next, the others leave at once.  Nothing is predicated
-// between a matrix instruction and the use of its result: rows past the end
+// between a matrix instruction and the use of its result (on the path that jumps
+// over predicated loads the compiler leaves out wait states): rows past the end
 // repeat the last one (their columns are not stored), blocks past the end
 // repeat the last one with a weight scale of zero.
 template <int MODE, int MT>

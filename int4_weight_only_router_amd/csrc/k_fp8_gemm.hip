@@ -34,12 +34,17 @@
 // fragments; each sum enters its accumulator by one fma two sums later.  The
 // fma's run in the shadow of the matrix pipe.
 //
-// Measured (2048 columns of K): 4096 x 11264 with fp16 outputs 104 us (1.8
-// PFLOP/s), with fp32 outputs 175 (1.08); experts of 2048 x 1024, top-8 of 64,
-// 4096 tokens: gate/up about 265 us, down 118.  At 1.9 GHz, the clock that
-// power leaves, gate/up needs 274 k cycles a SIMD of matrix and 266 k of other
-// vector instructions (half of them conversions) of its 636 k; moving the loads,
-// the priorities or the conversions about changes the time by less than 2%.
+// Measured (2048 columns of K): 4096 x 11264 with fp16 outputs 105 us (1.8
+// PFLOP/s), with fp32 sums (MOE_ACC_F32) 172, with fp32 outputs 175 (1.08);
+// experts of 2048 x 1024, top-8 of 64, 4096 tokens: gate/up 279 us, down 110
+// (kernels in a run of 60 passes; 340 and 122 in the first ones after a pause),
+// the call 390, with fp32 sums in down 434.
+// Bounded by instruction issue and by what one workgroup a compute unit exposes:
+// of gate/up's 607 k cycles a SIMD the matrix pipe is busy 266 k, other vector
+// instructions (half of them conversions) take 271 k, and waves wait 31% of
+// theirs; of the product's 228 k 90 k and 78 k, waiting 34%; of down's 257 k 67 k
+// and 65 k, waiting 49%.  Moving the loads, the priorities or the conversions
+// about changes the time by less than 2%.
 //
 // gate/up: the 256 weight rows are 128 gate rows and the same 128 up rows (a
 // wave holds as many of each), so a workgroup forms 128 columns of h, exactly

@@ -33,10 +33,12 @@
 // own start in every expert's run) and places its elements: no order depends on
 // timing.
 //
-// Measured: 1 x 64 2.7 us; 777 x 60 top-4 in 6 groups 6.8 + 4.2; 4096 x 512
-// top-10 in 8 groups 13.2 + 6.8 (8.4 MB of logits are 1.6 us of that).  Bound by
-// the vector instructions of the selecting waves (1070 a token, a third of them
-// fp64; 66% of the time at 4096 x 512) and by the two launches.
+// Measured: 1 x 64 2.8 us; 777 x 60 top-4 in 6 groups 6.8 + 4.3; 4096 x 512
+// top-10 in 8 groups 13.4 + 6.7 (8.4 MB of logits are 1.6 us of that).  Of the 49 k
+// cycles of the last's selection a SIMD issues vector instructions in 17 k (1070
+// a token, a third of them fp64), and waves wait 54% of theirs: steps through
+// LDS and across lanes that depend on each other.  Placement reads every chunk's
+// counts in every workgroup (33 MB from the L2) and scatters with one wave.
 #include "k_sort_common.h"
 
 namespace moe {

@@ -122,7 +122,9 @@ class LayerBuffers:
 class MoELayer:
     """One MoE layer resident on the device: W4A16 experts (fmt MOE_FMT_SYM or
     MOE_FMT_ZP) or FP8 experts (MOE_FMT_FP8: blobs of load_experts_fp8, `group`
-    unused), routed by softmax top-k or, with `routing`, by scores and groups."""
+    unused), routed by softmax top-k or, with `routing`, by scores and groups.
+    Both routers take H in {256, 512, 1024, 2048}, also where the FP8 experts
+    would take more."""
 
     def __init__(self, H, I, E, k, group, router, table, bias=None, shared=None,
                  renorm=False, device="cuda", shared_gate=None, overlap_shared=False,
