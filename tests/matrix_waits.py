@@ -10,8 +10,7 @@ instruction may take the result as its whole accumulator input without waiting;
 as an operand, or a part of it as accumulator, it needs the same P + 4."""
 import re
 
-# 16 x 16 x 32 and 32 x 32 x 16 of 16-bit values, 16 x 16 x 128 of 8-bit ones:
-# 1024 multiply-adds a pass
+# 2048 multiply-adds a pass of 16-bit values, 4096 of 8-bit ones
 PASSES = {"v_mfma_f32_16x16x32_f16": 4, "v_mfma_f32_32x32x16_f16": 8,
           "v_mfma_f32_16x16x128_f8f6f4": 8, "v_mfma_scale_f32_16x16x128_f8f6f4": 8}
 _LINE = re.compile(r"^\s+(\S.*?)\s*// ([0-9A-F]+):(.*)$")
