@@ -35,7 +35,7 @@ def _short(text):
     return W.shortages(code)
 
 
-def test_checker_sees_the_taken_branch():
+def test_walk_takes_the_branch():
     assert _short(BRANCH % "") == [(0, 8, 3, 8)]
     # enough behind the join, or no branch
     assert _short(BRANCH.replace("102C", "1030") % "\ts_nop 4 // 00000000102C:\n") == []
@@ -44,7 +44,7 @@ def test_checker_sees_the_taken_branch():
     assert _short(straight.replace("s_nop 7", "s_nop 0")) == [(0, 7, 6, 8)]
 
 
-def test_checker_on_matrix_chains():
+def test_walk_of_matrix_chains():
     """The accumulator passes on at once; an operand, part of an accumulator, a
     store or an overwriting instruction has to wait."""
     chain = """
