@@ -68,6 +68,13 @@ enum { MOE_RENORM = 1u };                       /* moe_route flag */
 enum { MOE_GROUP_TOP2 = 2u };                   /* moe_route_select flag */
 enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
 enum { MOE_SCALE_POW2 = 1u };                   /* moe_quantize_fp8 flag */
+enum { MOE_NORM_RMS = 0, MOE_NORM_LAYER = 1 };
+/* moe_block_norm flags: the block's output is normed too; weights count as 1 + w */
+enum { MOE_NORM_POST = 1u, MOE_NORM_UNIT_OFFSET = 2u };
+/* activations of moe_linear_f16; GELU by the error function, GELU_TANH by its
+ * tanh form */
+enum { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_SILU = 2, MOE_ACT_GELU = 3,
+       MOE_ACT_GELU_TANH = 4 };
 /* OR'd into out_dtype of moe_gemm_fp8 and into the regime of
  * moe_expert_ffn_w8a8(_plan): every sum has fp32 accuracy, whatever the sizes. */
 enum { MOE_ACC_F32 = 0x800 };
@@ -83,7 +90,8 @@ enum { MOE_Y_TOKEN_ORDER = 0x100 };
  * partial j reads whole lines.  Needs C <= 64 or C a multiple of 64. */
 enum { MOE_Y_PARTIAL_ORDER = 0x400 };
 /* y dtypes: fp16, fp32 (decode slices), fp32 in partial-major column order;
- * bf16 where a call names it (moe_route_select, moe_quantize_fp8, moe_gemm_fp8). */
+ * bf16 where a call names it (moe_route_select, moe_quantize_fp8, moe_gemm_fp8,
+ * moe_block_norm, moe_balance_loss). */
 enum { MOE_DTYPE_F16 = 0, MOE_DTYPE_F32 = 1, MOE_DTYPE_F32_PM = 2, MOE_DTYPE_BF16 = 3 };
 /* Expert blob formats: symmetric codes, or codes with a zero point per group
  * (lucashiago.com.br explainer, step 1: each block carries a scale and a zero
@@ -638,6 +646,152 @@ int moe_expert_ffn_w8a8_plan(int T, int H, int I, int E, int k, int regime, int 
 int moe_expert_ffn_w8a8(const void *x_f16, const int32_t *perm, const int32_t *offsets,
                         const void *const *d_expert_blobs, int T, int H, int I, int E, int k,
                         int regime, void *y_f16, void *ws, size_t ws_bytes, hipStream_t stream);
+
+/* -------------------------------------------- around the block: norms */
+/*
+ * The end of one block and the start of the next, for each of T rows of H:
+ *   u = post(y) with MOE_NORM_POST, else y
+ *   r = residual + scale * gate * u          (out, rounded once)
+ *   n = pre(r), of the unrounded r           (n, rounded once)
+ * with the norms of `kind`, over the H columns,
+ *   RMS:   x / sqrt(mean(x^2) + eps) * w + b
+ *   LAYER: (x - mean(x)) / sqrt(mean((x - mean(x))^2) + eps) * w + b
+ * in fp32; with MOE_NORM_UNIT_OFFSET 1 + w stands for w.
+ *   y, residual  device [T] rows of `dtype` (F16, BF16 or F32), ldy and ldr
+ *                elements apart, element-aligned (fastest 16-byte aligned);
+ *                either may be NULL (zeros), not both; gate and post norm need y
+ *   gate         device [H] of dtype for all tokens (ldg = 0), or [T] rows ldg
+ *                apart; NULL: ones
+ *   post_w, post_b, pre_w, pre_b  device [H] of w_dtype (dtype or F32), each may
+ *                be NULL (w: ones, whatever the flags; b: zeros); post ones need
+ *                MOE_NORM_POST, pre ones need n
+ *   out, n       device [T] rows of dtype, ldo and ldn apart; either may be NULL,
+ *                not both.  They may be y, residual or gate rows themselves (the
+ *                same address and stride); no other overlap.
+ * Squares are summed in fp32: rows with values beyond 2^60 overflow there.  A row
+ * that holds a NaN or an infinity affects no other row.  H <= 8192
+ * (MOE_EUNSUPPORTED).  T = 0: no-op.  No workspace.
+ */
+int moe_block_norm(const void *y, int64_t ldy, const void *residual, int64_t ldr, const void *gate,
+                   int64_t ldg, float scale, const void *post_w, const void *post_b,
+                   const void *pre_w, const void *pre_b, int dtype, int w_dtype, int kind,
+                   unsigned flags, float eps, int T, int H, void *out, int64_t ldo, void *n,
+                   int64_t ldn, hipStream_t stream);
+
+/*
+ * Gradients of moe_block_norm from those of out and n (dout, dn: either may be
+ * NULL, not both; without dn there is no pre norm) and the forward call's inputs.
+ * A gradient of rows is laid out as the rows: dy as y (ldy), dresidual as
+ * residual (ldr), dgate as gate (ldg); dout and dn lie ldo and ldn apart.
+ *   dy, dresidual  device rows of dtype, or NULL
+ *   dgate          ldg = 0: device fp32 [H], the sum over the tokens; else rows of
+ *                  dtype; or NULL
+ *   dpost_w, dpost_b, dpre_w, dpre_b  device fp32 [H], sums over the tokens, or
+ *                  NULL; their order of addition depends on T and H only
+ * Everything is formed in fp32 and rounded once.  dy and dresidual may be dout or
+ * dn rows themselves (same address and stride), or y, residual, gate.
+ *   ws  device scratch of moe_block_norm_backward_workspace_bytes(T, H) bytes
+ *       where a sum over the tokens is asked for, 16-byte aligned, no
+ *       initialisation; calls that share it must not overlap
+ * T = 0: the sums are set to zero.
+ */
+size_t moe_block_norm_backward_workspace_bytes(int T, int H);
+int moe_block_norm_backward(const void *dout, int64_t ldo, const void *dn, int64_t ldn,
+                            const void *y, int64_t ldy, const void *residual, int64_t ldr,
+                            const void *gate, int64_t ldg, float scale, const void *post_w,
+                            const void *post_b, const void *pre_w, int dtype, int w_dtype, int kind,
+                            unsigned flags, float eps, int T, int H, void *dy, void *dresidual,
+                            void *dgate, float *dpost_w, float *dpost_b, float *dpre_w,
+                            float *dpre_b, void *ws, size_t ws_bytes, hipStream_t stream);
+
+/* ------------------------------------------ around the block: products */
+/*
+ * fp16 product with its epilogue:
+ *   z = x w^T + bias,   out = residual + act(z)
+ * summed in fp32; bias, activation and residual are applied before the one
+ * rounding to out_dtype.
+ *   x_f16     device fp16 [M] rows of K values, ldx apart; 16-byte aligned
+ *   w_f16     device fp16 [N] rows of K values, ldw apart; 16-byte aligned
+ *   bias      device fp32 [N] or NULL;  act: MOE_ACT_*
+ *   residual  device [M] rows of N values of out_dtype, ldr apart, or NULL; may be
+ *             out itself
+ *   out       device [M] rows of N values of out_dtype (F16 or F32), ldo apart
+ *   z_f16     device fp16 [M] rows of N values, ldz apart, or NULL: z rounded, as
+ *             moe_linear_f16_backward takes it
+ *   ws        device scratch of moe_linear_f16_workspace_bytes(M, N, K) bytes (may
+ *             be 0), 16-byte aligned, no initialisation; calls that share it must
+ *             not overlap
+ * The order of the fp32 additions depends on M, N and K only.  K, ldx and ldw
+ * multiples of 8 (MOE_EUNSUPPORTED).  M = 0: no-op.
+ */
+size_t moe_linear_f16_workspace_bytes(int M, int N, int K);
+int moe_linear_f16(const void *x_f16, int64_t ldx, const void *w_f16, int64_t ldw,
+                   const float *bias, int act, const void *residual, int64_t ldr, int M, int N,
+                   int K, void *out, int out_dtype, int64_t ldo, void *z_f16, int64_t ldz, void *ws,
+                   size_t ws_bytes, hipStream_t stream);
+
+/*
+ * Gradients of that product from dy, the gradient of out (which is also the
+ * residual's):
+ *   dz = dy * act'(z),   dx = dz w,   dw = dz^T x,   dbias = sum over rows of dz
+ *   dy_f16  device fp16 [M] rows of N values, lddy apart
+ *   z_f16   as the forward call wrote it; not read with MOE_ACT_NONE
+ *   x_f16, w_f16  as in the forward call (x is read for dw only, w for dx only)
+ *   dx      device [M] rows of K values of out_dtype, lddx apart, or NULL
+ *   dw      device [N] rows of K values of out_dtype, lddw apart, or NULL
+ *   dbias   device fp32 [N] or NULL, from the unrounded dz
+ *   ws      device scratch of moe_linear_f16_backward_workspace_bytes(M, N, K)
+ *           bytes, as above
+ * dz is rounded to fp16 for the products (exact with MOE_ACT_NONE), so out_dtype
+ * F32 is for MOE_ACT_NONE only (MOE_EUNSUPPORTED).  Gradients that would leave
+ * fp16's range belong scaled by the caller.  M = 0: dw and dbias are set to zero.
+ */
+size_t moe_linear_f16_backward_workspace_bytes(int M, int N, int K);
+int moe_linear_f16_backward(const void *dy_f16, int64_t lddy, const void *z_f16, int64_t ldz,
+                            int act, const void *x_f16, int64_t ldx, const void *w_f16, int64_t ldw,
+                            int M, int N, int K, void *dx, int64_t lddx, void *dw, int64_t lddw,
+                            int out_dtype, float *dbias, void *ws, size_t ws_bytes,
+                            hipStream_t stream);
+
+/* ------------------------------------------------- balance of the router */
+/*
+ * Per-expert counts, mean probabilities, balance loss and z loss of router logits,
+ * and the logits' gradient.  Over the n tokens that token_mask does not mask, with
+ * p the token's scores (MOE_SCORE_*) divided by their sum:
+ *   counts[e] = choices of e in topk_idx,   f_e = counts[e] / sum of counts
+ *   mean_prob[e] = 1/n sum_t p[t][e]
+ *   losses[0] = coef * E * sum_e f_e mean_prob[e]
+ *   losses[1] = z_coef / n * sum_t logsumexp(l_t)^2
+ *   dlogits = *d_loss * d(losses[0] + losses[1]) / dlogits, the counts constant;
+ *             zero for masked tokens
+ * A logit of -inf or NaN masks its expert (p = 0, gradient 0), +inf counts as the
+ * largest finite value, a token masked throughout has p = 0 and no z loss.
+ *   logits      device [T] rows of E values of logits_dtype (F32, F16, BF16), ld
+ *               apart, element-aligned
+ *   topk_idx    device int32 [T][k], from moe_route or moe_route_select (an index
+ *               outside [0, E) does not count), or NULL: counts is an input, such
+ *               as moe_route_select_permute's
+ *   token_mask  device uint8 [T], zero: masked; or NULL
+ *   counts      device int32 [E];  mean_prob device fp32 [E] or NULL
+ *   losses      device fp32 [2] or NULL
+ *   d_loss      device fp32 [1] or NULL (one): the losses' gradient, such as a
+ *               loss scale
+ *   dlogits     device [T] rows of E values of dlogits_dtype, ldd apart, or NULL;
+ *               must not overlap logits
+ *   ws          device scratch of moe_balance_loss_workspace_bytes(T, E) bytes (may
+ *               be 0), 16-byte aligned, no initialisation; calls that share it must
+ *               not overlap
+ * Counts are exact, sums fp32 in an order that depends on T and E only.
+ * Errors: MOE_EINVAL for bad sizes, types, coefficients that are not finite, null
+ * or misaligned pointers; MOE_EUNSUPPORTED for E > 1024 or T*k >= 2^31; MOE_ENOMEM.
+ * T = 0, or every token masked: everything is zero.
+ */
+size_t moe_balance_loss_workspace_bytes(int T, int E);
+int moe_balance_loss(const void *logits, int logits_dtype, int64_t ld, const int32_t *topk_idx,
+                     const uint8_t *token_mask, int T, int E, int k, int score, float coef,
+                     float z_coef, int32_t *counts, float *mean_prob, float *losses,
+                     const float *d_loss, void *dlogits, int dlogits_dtype, int64_t ldd, void *ws,
+                     size_t ws_bytes, hipStream_t stream);
 
 /* ------------------------------------------------- expert slot pool */
 /*

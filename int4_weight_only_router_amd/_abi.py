@@ -12,6 +12,8 @@ __all__ = [
     "MOE_REGIME_BATCHED", "MOE_REGIME_SMALL", "MOE_Y_TOKEN_ORDER", "MOE_Y_PARTIAL_ORDER",
     "MOE_DTYPE_F16", "MOE_DTYPE_F32", "MOE_DTYPE_F32_PM", "MOE_DTYPE_BF16",
     "MOE_GROUP_TOP2", "MOE_SCORE_SOFTMAX", "MOE_SCORE_SIGMOID", "MOE_SCALE_POW2", "MOE_ACC_F32", "MOE_FMT_SYM", "MOE_FMT_ZP", "MOE_FMT_FP8", "MOE_W4_ZERO_POINT", "EXPORTS",
+    "MOE_NORM_RMS", "MOE_NORM_LAYER", "MOE_NORM_POST", "MOE_NORM_UNIT_OFFSET", "MOE_ACT_NONE",
+    "MOE_ACT_RELU", "MOE_ACT_SILU", "MOE_ACT_GELU", "MOE_ACT_GELU_TANH",
     "moe_blob_layout_fmt", "moe_quantize_experts_fmt", "moe_prepack_experts_fmt",
     "moe_unpack_experts_fmt", "moe_prepack_expert_host", "moe_unpack_expert_host",
     "moe_last_error", "moe_workspace_clear", "moe_blob_layout", "moe_quantize_experts",
@@ -27,6 +29,10 @@ __all__ = [
     "moe_router_logits", "moe_route_select", "moe_route_select_workspace_bytes",
     "moe_route_select_permute", "moe_quantize_fp8", "moe_gemm_fp8", "moe_fp8_blob_layout",
     "moe_expert_ffn_w8a8_plan", "moe_expert_ffn_w8a8",
+    "moe_block_norm", "moe_block_norm_backward_workspace_bytes", "moe_block_norm_backward",
+    "moe_linear_f16_workspace_bytes", "moe_linear_f16",
+    "moe_linear_f16_backward_workspace_bytes", "moe_linear_f16_backward",
+    "moe_balance_loss_workspace_bytes", "moe_balance_loss",
     "PoolConfig",
     "PoolStats", "PoolLayerArgs",
     "moe_pool_create", "moe_pool_prepare", "moe_pool_layer_forward", "moe_pool_pin",
@@ -45,6 +51,9 @@ MOE_GROUP_TOP2 = 2          # moe_route_select flag: a group counts by its two b
 MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 MOE_SCALE_POW2 = 1          # moe_quantize_fp8 flag: power-of-two scales
 MOE_ACC_F32 = 0x800         # OR'd into moe_gemm_fp8's out_dtype and a w8a8 regime: fp32 sums
+MOE_NORM_RMS, MOE_NORM_LAYER = 0, 1
+MOE_NORM_POST, MOE_NORM_UNIT_OFFSET = 1, 2   # moe_block_norm flags
+MOE_ACT_NONE, MOE_ACT_RELU, MOE_ACT_SILU, MOE_ACT_GELU, MOE_ACT_GELU_TANH = 0, 1, 2, 3, 4
 MOE_FMT_SYM, MOE_FMT_ZP = 0, 1   # expert blob formats (zero point per group)
 MOE_FMT_FP8 = 2                  # e4m3 blobs (moe_fp8_blob_layout); no argument of the _fmt calls
 MOE_W4_ZERO_POINT = 0x200        # OR'd into a regime: the blobs are MOE_FMT_ZP
@@ -65,6 +74,10 @@ EXPORTS = [
     "moe_router_logits", "moe_route_select", "moe_route_select_workspace_bytes",
     "moe_route_select_permute", "moe_quantize_fp8", "moe_gemm_fp8", "moe_fp8_blob_layout",
     "moe_expert_ffn_w8a8_plan", "moe_expert_ffn_w8a8",
+    "moe_block_norm", "moe_block_norm_backward_workspace_bytes", "moe_block_norm_backward",
+    "moe_linear_f16_workspace_bytes", "moe_linear_f16",
+    "moe_linear_f16_backward_workspace_bytes", "moe_linear_f16_backward",
+    "moe_balance_loss_workspace_bytes", "moe_balance_loss",
     "moe_pool_create",
     "moe_pool_prepare",
     "moe_pool_layer_forward", "moe_pool_pin",
@@ -166,6 +179,21 @@ def _declare(L):
         "moe_expert_ffn_w8a8_plan": (i32, [i32, i32, i32, i32, i32, i32, vp, vp]),
         "moe_expert_ffn_w8a8": (i32, [vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, vp, vp, sz,
                                       vp]),
+        "moe_block_norm": (i32, [vp, i64, vp, i64, vp, i64, C.c_float, vp, vp, vp, vp, i32, i32,
+                                 i32, C.c_uint, C.c_float, i32, i32, vp, i64, vp, i64, vp]),
+        "moe_block_norm_backward_workspace_bytes": (sz, [i32, i32]),
+        "moe_block_norm_backward": (i32, [vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, C.c_float,
+                                          vp, vp, vp, i32, i32, i32, C.c_uint, C.c_float, i32,
+                                          i32, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
+        "moe_linear_f16_workspace_bytes": (sz, [i32, i32, i32]),
+        "moe_linear_f16": (i32, [vp, i64, vp, i64, vp, i32, vp, i64, i32, i32, i32, vp, i32, i64,
+                                 vp, i64, vp, sz, vp]),
+        "moe_linear_f16_backward_workspace_bytes": (sz, [i32, i32, i32]),
+        "moe_linear_f16_backward": (i32, [vp, i64, vp, i64, i32, vp, i64, vp, i64, i32, i32, i32,
+                                          vp, i64, vp, i64, i32, vp, vp, sz, vp]),
+        "moe_balance_loss_workspace_bytes": (sz, [i32, i32]),
+        "moe_balance_loss": (i32, [vp, i32, i64, vp, vp, i32, i32, i32, i32, C.c_float, C.c_float,
+                                   vp, vp, vp, vp, vp, i32, i64, vp, sz, vp]),
         "moe_pool_create": (i32, [C.POINTER(PoolConfig), vp, C.POINTER(vp)]),
         "moe_pool_prepare": (i32, [vp, i32, vp, i32, vp, C.POINTER(vp), C.POINTER(PoolStats)]),
         "moe_pool_layer_forward": (i32, [vp, i32, C.POINTER(PoolLayerArgs), vp,
@@ -489,6 +517,63 @@ def moe_expert_ffn_w8a8(x, perm, offsets, d_expert_blobs, T, H, I, E, k, regime,
                         ws_bytes=0, stream=None):
     return _check(lib().moe_expert_ffn_w8a8(_p(x), _p(perm), _p(offsets), _p(d_expert_blobs), T, H,
                                             I, E, k, regime, _p(y), _p(ws), ws_bytes, _s(stream)))
+
+
+def moe_block_norm(y, ldy, residual, ldr, gate, ldg, scale, post_w, post_b, pre_w, pre_b, dtype,
+                   w_dtype, kind, flags, eps, T, H, out, ldo, n, ldn, stream=None):
+    return _check(lib().moe_block_norm(
+        _p(y), ldy, _p(residual), ldr, _p(gate), ldg, scale, _p(post_w), _p(post_b), _p(pre_w),
+        _p(pre_b), dtype, w_dtype, kind, flags, eps, T, H, _p(out), ldo, _p(n), ldn, _s(stream)))
+
+
+def moe_block_norm_backward_workspace_bytes(T, H):
+    return lib().moe_block_norm_backward_workspace_bytes(T, H)
+
+
+def moe_block_norm_backward(dout, ldo, dn, ldn, y, ldy, residual, ldr, gate, ldg, scale, post_w,
+                            post_b, pre_w, dtype, w_dtype, kind, flags, eps, T, H, dy, dresidual,
+                            dgate, dpost_w, dpost_b, dpre_w, dpre_b, ws=None, ws_bytes=0,
+                            stream=None):
+    return _check(lib().moe_block_norm_backward(
+        _p(dout), ldo, _p(dn), ldn, _p(y), ldy, _p(residual), ldr, _p(gate), ldg, scale,
+        _p(post_w), _p(post_b), _p(pre_w), dtype, w_dtype, kind, flags, eps, T, H, _p(dy),
+        _p(dresidual), _p(dgate), _p(dpost_w), _p(dpost_b), _p(dpre_w), _p(dpre_b), _p(ws),
+        ws_bytes, _s(stream)))
+
+
+def moe_linear_f16_workspace_bytes(M, N, K):
+    return lib().moe_linear_f16_workspace_bytes(M, N, K)
+
+
+def moe_linear_f16(x, ldx, w, ldw, bias, act, residual, ldr, M, N, K, out, out_dtype, ldo, z=None,
+                   ldz=0, ws=None, ws_bytes=0, stream=None):
+    return _check(lib().moe_linear_f16(
+        _p(x), ldx, _p(w), ldw, _p(bias), act, _p(residual), ldr, M, N, K, _p(out), out_dtype, ldo,
+        _p(z), ldz, _p(ws), ws_bytes, _s(stream)))
+
+
+def moe_linear_f16_backward_workspace_bytes(M, N, K):
+    return lib().moe_linear_f16_backward_workspace_bytes(M, N, K)
+
+
+def moe_linear_f16_backward(dy, lddy, z, ldz, act, x, ldx, w, ldw, M, N, K, dx, lddx, dw, lddw,
+                            out_dtype, dbias=None, ws=None, ws_bytes=0, stream=None):
+    return _check(lib().moe_linear_f16_backward(
+        _p(dy), lddy, _p(z), ldz, act, _p(x), ldx, _p(w), ldw, M, N, K, _p(dx), lddx, _p(dw), lddw,
+        out_dtype, _p(dbias), _p(ws), ws_bytes, _s(stream)))
+
+
+def moe_balance_loss_workspace_bytes(T, E):
+    return lib().moe_balance_loss_workspace_bytes(T, E)
+
+
+def moe_balance_loss(logits, logits_dtype, ld, topk_idx, token_mask, T, E, k, score, coef, z_coef,
+                     counts, mean_prob, losses, d_loss=None, dlogits=None,
+                     dlogits_dtype=MOE_DTYPE_F32, ldd=0, ws=None, ws_bytes=0, stream=None):
+    return _check(lib().moe_balance_loss(
+        _p(logits), logits_dtype, ld, _p(topk_idx), _p(token_mask), T, E, k, score, coef, z_coef,
+        _p(counts), _p(mean_prob), _p(losses), _p(d_loss), _p(dlogits), dlogits_dtype, ldd, _p(ws),
+        ws_bytes, _s(stream)))
 
 
 def moe_pool_create(cfg: PoolConfig, pinned_src_ptrs):

@@ -1,0 +1,101 @@
+// k_block.h -- what the kernels around a routed block share: loads and stores of
+// eight columns in any activation type, and the norms' arguments.
+#pragma once
+
+#include "moe_common.h"
+
+namespace moe {
+
+typedef __bf16 bf16;
+typedef __bf16 bf168_t __attribute__((ext_vector_type(8)));
+
+template <typename T>
+struct Vec8;
+template <>
+struct Vec8<f16> { typedef half8_t type; };
+template <>
+struct Vec8<bf16> { typedef bf168_t type; };
+
+// Columns c .. c + 7 of a row; zeros from column `cols` on.  vec: rows are
+// 16-byte aligned.
+template <typename T>
+__device__ __forceinline__ void load8(const T *row, int c, int cols, bool vec, float (&v)[8])
+{
+    if (vec && c + 8 <= cols) {
+        if constexpr (sizeof(T) == 4) {
+            const float4_t a = *reinterpret_cast<const float4_t *>(row + c);
+            const float4_t b = *reinterpret_cast<const float4_t *>(row + c + 4);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[i] = a[i];
+                v[4 + i] = b[i];
+            }
+        } else {
+            const typename Vec8<T>::type a =
+                *reinterpret_cast<const typename Vec8<T>::type *>(row + c);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v[i] = (float)a[i];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] = c + i < cols ? (float)row[c + i] : 0.0f;
+    }
+}
+
+// The same columns, rounded once; those from `cols` on are left as they were.
+template <typename T>
+__device__ __forceinline__ void store8(T *row, int c, int cols, bool vec, const float (&v)[8])
+{
+    if (vec && c + 8 <= cols) {
+        if constexpr (sizeof(T) == 4) {
+            *reinterpret_cast<float4_t *>(row + c) = float4_t{v[0], v[1], v[2], v[3]};
+            *reinterpret_cast<float4_t *>(row + c + 4) = float4_t{v[4], v[5], v[6], v[7]};
+        } else {
+            typename Vec8<T>::type a;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                a[i] = (T)v[i];
+            *reinterpret_cast<typename Vec8<T>::type *>(row + c) = a;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (c + i < cols)
+                row[c + i] = (T)v[i];
+    }
+}
+
+// Rows of T x H; vec_*: whether a tensor's rows are 16-byte aligned.
+struct NormArgs {
+    const void *y, *residual, *gate, *post_w, *post_b, *pre_w, *pre_b;
+    void *out, *n;
+    int64_t ldy, ldr, ldg, ldo, ldn;   // ldg 0: one gate row for all
+    float scale, eps;
+    int T, H;
+    bool layer, post, offset;
+    bool vec_y, vec_r, vec_g, vec_o, vec_n, vec_w;
+    bool vec_dy, vec_dr, vec_dg;
+};
+
+// Gradients, laid out as what they are gradients of; `sums`: fp32 [H] over the
+// tokens (a shared gate's, the post norm's weight and bias, the pre norm's).
+struct NormGrads {
+    const void *dout, *dn;
+    void *dy, *dresidual, *dgate;
+    float *sums[5];
+    float *parts;
+    int nsums;
+};
+
+struct NormSums {
+    float *p[5];
+    int n;
+};
+
+int launch_block_norm(const NormArgs &, int dtype, int w_dtype, hipStream_t);
+size_t block_norm_backward_ws(int T, int H);
+int launch_block_norm_backward(const NormArgs &, NormGrads, int dtype, int w_dtype, hipStream_t);
+
+}  // namespace moe
