@@ -242,7 +242,7 @@ int moe_block_norm_backward(const void *dout, int64_t ldo, const void *dn, int64
 
 size_t moe_linear_f16_workspace_bytes(int M, int N, int K)
 {
-    return M <= 0 || N <= 0 || K <= 0 ? 0 : linear_ws(M, N, K);
+    return M <= 0 || N <= 0 || K <= 0 || !linear_fits(M, N, K) ? 0 : linear_ws(M, N, K);
 }
 
 int moe_linear_f16(const void *x_f16, int64_t ldx, const void *w_f16, int64_t ldw,
@@ -261,6 +261,11 @@ int moe_linear_f16(const void *x_f16, int64_t ldx, const void *w_f16, int64_t ld
     if (K % 8 || ldx % 8 || ldw % 8)
         return set_error(MOE_EUNSUPPORTED,
                          "%s: K, ldx and ldw must be multiples of 8 (K=%d ldx=%lld ldw=%lld)", fn, K,
+                         (long long)ldx, (long long)ldw);
+    if (ldx > LIN_MOST_LD || ldw > LIN_MOST_LD || (M > 0 && !linear_fits(M, N, K)))
+        return set_error(MOE_EUNSUPPORTED,
+                         "%s: rows of at most %d elements and %lld tiles (M=%d N=%d ldx=%lld "
+                         "ldw=%lld)", fn, LIN_MOST_LD, (long long)LIN_MOST_ITEMS, M, N,
                          (long long)ldx, (long long)ldw);
     if (M == 0)
         return MOE_OK;
@@ -298,7 +303,9 @@ int moe_linear_f16(const void *x_f16, int64_t ldx, const void *w_f16, int64_t ld
 
 size_t moe_linear_f16_backward_workspace_bytes(int M, int N, int K)
 {
-    return M <= 0 || N <= 0 || K <= 0 ? 0 : linear_backward_ws(M, N, K);
+    if (M <= 0 || N <= 0 || K <= 0 || !linear_fits(M, K, N) || !linear_fits(N, K, M))
+        return 0;
+    return linear_backward_ws(M, N, K);
 }
 
 int moe_linear_f16_backward(const void *dy_f16, int64_t lddy, const void *z_f16, int64_t ldz,
@@ -319,6 +326,12 @@ int moe_linear_f16_backward(const void *dy_f16, int64_t lddy, const void *z_f16,
     if (K % 8 || (dw && ldx % 8) || (dx && ldw % 8))
         return set_error(MOE_EUNSUPPORTED,
                          "%s: K, ldx and ldw must be multiples of 8 (K=%d ldx=%lld ldw=%lld)", fn, K,
+                         (long long)ldx, (long long)ldw);
+    if ((dw && ldx > LIN_MOST_LD) || (dx && ldw > LIN_MOST_LD) || N > LIN_MOST_LD ||
+        (M > 0 && ((dx && !linear_fits(M, K, N)) || (dw && !linear_fits(N, K, M)))))
+        return set_error(MOE_EUNSUPPORTED,
+                         "%s: rows of at most %d elements and %lld tiles (M=%d N=%d K=%d ldx=%lld "
+                         "ldw=%lld)", fn, LIN_MOST_LD, (long long)LIN_MOST_ITEMS, M, N, K,
                          (long long)ldx, (long long)ldw);
     if (act != MOE_ACT_NONE && out_dtype == MOE_DTYPE_F32)
         return set_error(MOE_EUNSUPPORTED,

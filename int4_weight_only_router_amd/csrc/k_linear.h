@@ -22,20 +22,44 @@ struct LinArgs {
     int64_t ldo;
     f16 *z;
     int64_t ldz;
+    // tiles: k dealt out over `splits` workgroups, kblocks blocks of 64 each, whose
+    // results lie split_stride elements apart
+    int splits, kblocks;
+    int64_t split_stride;
 };
 
-// Activations and their derivatives in fp32.
+// How a product is computed: the form of its tiles, and k in `splits` parts whose
+// sums a second launch joins.
+struct LinPlan {
+    int form, splits;
+    int64_t items;   // workgroups
+};
+constexpr int64_t LIN_MOST_ITEMS = (1 << 22) - 8;   // a launch has fewer than 2^32 threads
+constexpr int LIN_MOST_LD = 1 << 22;                // offsets inside a tile are 32 bits wide
+LinPlan linear_plan(int M, int N, int K);
+int launch_linear_tile(LinArgs, const LinPlan &, void *ws, hipStream_t);
+
+// 1 / (1 + exp(-x)) by the hardware's exp2 and reciprocal (an ulp each).
+__device__ __forceinline__ float logistic(float x)
+{
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.4426950408889634f * x));
+}
+
+// Activations and their derivatives in fp32.  The tanh form of GELU by (1 + tanh u) / 2
+// = logistic(2 u), with 2 u = GELU_A z (1 + GELU_B z^2).
+constexpr float GELU_A = 1.5957691216057308f, GELU_B = 0.044715f;
+
 __device__ __forceinline__ float act_value(float z, int act)
 {
     switch (act) {
     case MOE_ACT_RELU:
-        return z > 0.0f ? z : z != z ? z : 0.0f;
+        return z < 0.0f ? 0.0f : z;   // (NaN stays)
     case MOE_ACT_SILU:
-        return z / (1.0f + expf(-z));
+        return z * logistic(z);
     case MOE_ACT_GELU:
         return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
     case MOE_ACT_GELU_TANH:
-        return 0.5f * z * (1.0f + tanhf(0.79788456080286536f * (z + 0.044715f * z * z * z)));
+        return z * logistic(GELU_A * __builtin_fmaf(GELU_B * z * z, z, z));
     default:
         return z;
     }
@@ -47,16 +71,15 @@ __device__ __forceinline__ float act_grad(float z, int act)
     case MOE_ACT_RELU:
         return z > 0.0f ? 1.0f : 0.0f;
     case MOE_ACT_SILU: {
-        const float s = 1.0f / (1.0f + expf(-z));
+        const float s = logistic(z);
         return s * (1.0f + z * (1.0f - s));
     }
     case MOE_ACT_GELU:
         return 0.5f * (1.0f + erff(z * 0.70710678118654752f)) +
                z * 0.39894228040143268f * expf(-0.5f * z * z);
     case MOE_ACT_GELU_TANH: {
-        const float t = tanhf(0.79788456080286536f * (z + 0.044715f * z * z * z));
-        return 0.5f * (1.0f + t) +
-               0.5f * z * (1.0f - t * t) * 0.79788456080286536f * (1.0f + 0.134145f * z * z);
+        const float s = logistic(GELU_A * __builtin_fmaf(GELU_B * z * z, z, z));
+        return s * (1.0f + z * (1.0f - s) * GELU_A * __builtin_fmaf(3.0f * GELU_B * z, z, 1.0f));
     }
     default:
         return 1.0f;
@@ -65,6 +88,7 @@ __device__ __forceinline__ float act_grad(float z, int act)
 
 size_t linear_ws(int M, int N, int K);
 size_t linear_backward_ws(int M, int N, int K);
+bool linear_fits(int M, int N, int K);            // whether a launch holds the product's tiles
 int launch_linear(const LinArgs &, void *ws, hipStream_t);
 struct LinGrads {
     const f16 *dy, *z, *x, *w;

@@ -1,5 +1,6 @@
-// k_linear.hip -- fp16 matrix products with bias, activation and residual in
-// their epilogue, and their gradients:
+// k_linear.hip -- fp16 matrix products with bias, activation and residual in their
+// epilogue, and their gradients: choice of the tiles (k_linear_tile.hip), dz and the
+// bias gradient.
 //
 //   z = x w^T + bias,  out = residual + act(z)
 //   dz = dy act'(z),   dx = dz w,   dw = dz^T x,   dbias = sum_m dz
@@ -9,99 +10,125 @@
 
 namespace moe {
 
-__device__ __forceinline__ float out_value(const void *p, int dt, int64_t at)
-{
-    return dt == MOE_DTYPE_F32 ? static_cast<const float *>(p)[at]
-                               : (float)static_cast<const f16 *>(p)[at];
-}
+// The forms of a tile: rows, columns, groups that share its k, workgroups a compute
+// unit; and what they were measured to take, in us (fp16, K = 512 and 2048, 256
+// compute units all busy): `start` for a launch, `one` for a block of 64 k of a
+// workgroup (of its group, where groups share k), `two` for one of each of two
+// workgroups on a compute unit.
+//
+// With them the form and the parts of k that take the least time are chosen.  On 90
+// products from 1 x 1024 x 256 to 8192 x 8192 x 8192 the choice was the fastest form
+// or within 8% of it (at K = 2048, chosen / next best: 1 x 5632 16-row tiles 7.4 us,
+// 32-row 7.6; 333 x 1408 32-row 8.2, 64-row 9.4; 256 x 5632 64-row 13.7, 128-row
+// 17.3; 2048 x 2048 128-row of eight waves 20.8, of four 26.8; 4096 x 2048 the other
+// way round, 35.7 and 39.8; 4096 x 5632 192-row 83, 256-row 95; 4096 x 11264 256-row
+// 154, 192-row 163).
+struct LinForm {
+    int bm, bn, kg, per_cu;
+    double start, one, two;
+};
+static const LinForm FORMS[] = {
+    {16, 32, 8, 1, 3.0, 0.70, 0}, {32, 64, 2, 1, 3.0, 0.33, 0},  {64, 64, 2, 1, 2.6, 0.48, 0},
+    {64, 64, 1, 2, 1.7, 0.33, 0.46}, {128, 128, 1, 1, 3.8, 0.53, 0}, {128, 128, 1, 2, 2.9, 0.75, 1.02},
+    {192, 256, 1, 1, 4.4, 1.21, 0}, {256, 256, 1, 1, 5.5, 1.45, 0}};
 
-__device__ __forceinline__ void epilogue1(const LinArgs &a, int m, int n, float v)
+LinPlan linear_plan(int M, int N, int K)
 {
-    if (m >= a.M || n >= a.N)
-        return;
-    if (a.bias)
-        v += a.bias[n];
-    if (a.z)
-        a.z[m * a.ldz + n] = (f16)v;
-    v = act_value(v, a.act);
-    if (a.residual)
-        v += out_value(a.residual, a.odt, m * a.ldr + n);
-    if (a.odt == MOE_DTYPE_F32)
-        static_cast<float *>(a.out)[m * a.ldo + n] = v;
-    else
-        static_cast<f16 *>(a.out)[m * a.ldo + n] = (f16)v;
-}
-
-// 64 x 64 tiles of four waves, K in steps of 32 through LDS.
-__global__ __launch_bounds__(256) void linear_kernel(LinArgs a)
-{
-    __shared__ __align__(16) f16 as[64][40], bs[64][40];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int m0 = blockIdx.y * 64, n0 = blockIdx.x * 64;
-    float4_t acc[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        acc[i] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int k0 = 0; k0 < a.K; k0 += 32) {
-        __syncthreads();
-        for (int i = threadIdx.x; i < 64 * 32; i += 256) {
-            const int ra = a.a_ks ? i & 63 : i >> 5, ka = a.a_ks ? i >> 6 : i & 31;
-            const bool in_a = m0 + ra < a.M && k0 + ka < a.K;
-            const int64_t at_a = a.a_ks ? (k0 + ka) * a.lda + m0 + ra : (m0 + ra) * a.lda + k0 + ka;
-            as[ra][ka] = in_a ? a.a[at_a] : (f16)0.0f;
-            const int rb = a.b_ks ? i & 63 : i >> 5, kb = a.b_ks ? i >> 6 : i & 31;
-            const bool in_b = n0 + rb < a.N && k0 + kb < a.K;
-            const int64_t at_b = a.b_ks ? (k0 + kb) * a.ldb + n0 + rb : (n0 + rb) * a.ldb + k0 + kb;
-            bs[rb][kb] = in_b ? a.b[at_b] : (f16)0.0f;
-        }
-        __syncthreads();
-        const int r = lane & 15, q = (lane >> 4) * 8;
-        const half8_t x = *reinterpret_cast<const half8_t *>(&as[wave * 16 + r][q]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const half8_t w = *reinterpret_cast<const half8_t *>(&bs[i * 16 + r][q]);
-            acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w, x, acc[i], 0, 0, 0);
+    LinPlan best{};
+    double least = 1e300;
+    const int nkb = (K + 63) / 64;
+    for (int f = 0; f < 8; ++f) {
+        const LinForm &o = FORMS[f];
+        if (f == 0 && M > 16)
+            continue;
+        const int64_t tiles = (int64_t)(((int64_t)M + o.bm - 1) / o.bm) * (((int64_t)N + o.bn - 1) / o.bn);
+        for (int s = 1; s <= 8; s *= 2) {
+            const int each = (nkb + s - 1) / s;
+            if (s > 1 && (tiles * s > 256 || (nkb + each - 1) / each != s))
+                break;   // no more parts than compute units, none empty
+            const double n = (double)((tiles * s + 255) / 256);   // workgroups of a compute unit
+            const double blocks = (each + o.kg - 1) / o.kg;
+            const double pairs = o.per_cu == 2 ? (double)((int64_t)n / 2) : 0;
+            double t = o.start + blocks * (pairs * o.two + (n - 2 * pairs) * o.one);
+            if (s > 1)   // a launch more, and the parts' sums written and read
+                t += 4.5 + (2.0 * s + 1) * 4.0 * M * N / 3e6;
+            if (t < least) {
+                least = t;
+                best = LinPlan{f, s, tiles * s};
+            }
         }
     }
-    // a lane holds four consecutive columns of one row
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            epilogue1(a, m0 + wave * 16 + (lane & 15), n0 + i * 16 + (lane >> 4) * 4 + j, acc[i][j]);
+    return best;
 }
 
-size_t linear_ws(int, int, int) { return 0; }
-
-int launch_linear(const LinArgs &a, void *, hipStream_t s)
+bool linear_fits(int M, int N, int K)
 {
-    hipLaunchKernelGGL(linear_kernel, dim3((a.N + 63) / 64, (a.M + 63) / 64), dim3(256), 0, s, a);
-    MOE_LAUNCH_CHECK("linear_kernel");
-    return MOE_OK;
+    return M <= 1 << 30 && N <= 1 << 30 && linear_plan(M, N, K).items <= LIN_MOST_ITEMS;
 }
 
-// dz = dy act'(z) in fp16 (rows of ldd, zeros behind column N) and its column
-// sums over 64 rows, from the unrounded values.
-constexpr int DZ_ROWS = 64;
+static size_t plan_ws(const LinPlan &p, int M, int N)
+{
+    return p.splits == 1 ? 0 : (size_t)p.splits * M * ((N + 7) / 8 * 8) * sizeof(float);
+}
+
+size_t linear_ws(int M, int N, int K) { return plan_ws(linear_plan(M, N, K), M, N); }
+
+int launch_linear(const LinArgs &a, void *ws, hipStream_t s)
+{
+    return launch_linear_tile(a, linear_plan(a.M, a.N, a.K), ws, s);
+}
+
+// ------------------------------------------------------------------ gradients
+
+// dz = dy act'(z) in fp16 (rows of ldd, zeros up to the next multiple of 8 behind
+// column N), where dz is not null, and its column sums over DZ_ROWS rows, from the
+// unrounded values, where parts is not null.  32 threads a row, eight columns each.
+constexpr int DZ_ROWS = 64, DZ_COLS = 256;
 __global__ __launch_bounds__(256) void linear_dz_kernel(LinGrads g, f16 *dz, int64_t ldd,
-                                                        float *parts)
+                                                        float *parts, bool vec_y, bool vec_z)
 {
-    const int n = blockIdx.x * 256 + threadIdx.x;
-    const int64_t m0 = (int64_t)blockIdx.y * DZ_ROWS, m1 = min(m0 + DZ_ROWS, (int64_t)g.M);
-    if (n >= ldd)
-        return;
-    float s = 0.0f;
-    for (int64_t m = m0; m < m1; ++m) {
-        float v = n < g.N ? (float)g.dy[m * g.lddy + n] : 0.0f;
-        if (g.act != MOE_ACT_NONE && n < g.N)
-            v *= act_grad((float)g.z[m * g.ldz + n], g.act);
-        dz[m * ldd + n] = (f16)v;
-        s += v;
+    __shared__ float sums[8][DZ_COLS];
+    const int n = blockIdx.x * DZ_COLS + (threadIdx.x & 31) * 8;
+    const int64_t m0 = (int64_t)blockIdx.y * DZ_ROWS;
+    const int cols = g.N - n;
+    float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+    for (int i = threadIdx.x >> 5; i < DZ_ROWS; i += 8) {
+        const int64_t m = m0 + i;
+        if (m >= g.M || cols <= 0)
+            break;
+        float v[8];
+        load8<f16>(g.dy + m * g.lddy + n, 0, cols, vec_y, v);
+        if (g.act != MOE_ACT_NONE) {
+            float z[8];
+            load8<f16>(g.z + m * g.ldz + n, 0, cols, vec_z, z);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[j] = j < cols ? v[j] * act_grad(z[j], g.act) : 0.0f;
+        }
+        if (dz)
+            store8<f16>(dz + m * ldd + n, 0, 8, true, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            s[j] += v[j];
     }
-    if (parts && n < g.N)
-        parts[(int64_t)blockIdx.y * g.N + n] = s;
+    if (!parts)
+        return;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        sums[threadIdx.x >> 5][(threadIdx.x & 31) * 8 + j] = s[j];
+    __syncthreads();
+    const int c = blockIdx.x * DZ_COLS + threadIdx.x;
+    if (c < g.N) {
+        float v = sums[0][threadIdx.x];
+#pragma unroll
+        for (int i = 1; i < 8; ++i)
+            v += sums[i][threadIdx.x];
+        parts[(int64_t)blockIdx.y * g.N + c] = v;
+    }
 }
 
+// Column sums of the partial sums [G][N]: 16 at a time, joined in a fixed order.
 __global__ __launch_bounds__(1024) void linear_dbias_kernel(const float *parts, int G, int N,
                                                             float *out)
 {
@@ -121,59 +148,109 @@ __global__ __launch_bounds__(1024) void linear_dbias_kernel(const float *parts, 
     }
 }
 
+// Zeros into rows of `cols` elements, ld apart.
+template <typename T>
+__global__ __launch_bounds__(256) void zero_rows_kernel(T *p, int64_t ld, int64_t rows, int cols)
+{
+    for (int64_t i = blockIdx.x * 256LL + threadIdx.x; i < rows * cols; i += gridDim.x * 256LL)
+        p[i / cols * ld + i % cols] = (T)0.0f;
+}
+
 static int64_t dz_ld(int N) { return ((int64_t)N + 7) / 8 * 8; }
 
-size_t linear_backward_ws(int M, int N, int)
+// Workspace: dz, the column sums, and what the products need.
+struct GradWs {
+    int64_t parts, products, total;
+};
+static GradWs grad_ws(int M, int N, int K)
 {
-    return (size_t)al256((int64_t)M * dz_ld(N) * 2) +
-           (size_t)((M + DZ_ROWS - 1) / DZ_ROWS) * N * 4;
+    GradWs w;
+    w.parts = al256((int64_t)M * dz_ld(N) * 2);
+    w.products = w.parts + al256((int64_t)((M + DZ_ROWS - 1) / DZ_ROWS) * N * 4);
+    w.total = w.products + (int64_t)std::max(linear_ws(M, K, N), linear_ws(N, K, M));
+    return w;
 }
+
+size_t linear_backward_ws(int M, int N, int K) { return (size_t)grad_ws(M, N, K).total; }
 
 int launch_linear_backward(const LinGrads &g, void *ws, hipStream_t s)
 {
-    const int64_t ldd = dz_ld(g.N);
-    f16 *dz = static_cast<f16 *>(ws);
-    float *parts = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) +
-                                             al256((int64_t)g.M * ldd * 2));
-    const int G = (g.M + DZ_ROWS - 1) / DZ_ROWS;
-    if (g.M > 0) {
-        hipLaunchKernelGGL(linear_dz_kernel, dim3((unsigned)((ldd + 255) / 256), G), dim3(256), 0, s,
-                           g, dz, ldd, g.dbias ? parts : nullptr);
-        MOE_LAUNCH_CHECK("linear_dz_kernel");
+    if (g.M == 0) {
+        if (g.dbias) {
+            hipLaunchKernelGGL(linear_dbias_kernel, dim3((g.N + 63) / 64), dim3(1024), 0, s, nullptr,
+                               0, g.N, g.dbias);
+            MOE_LAUNCH_CHECK("linear_dbias_kernel");
+        }
+        if (g.dw) {
+            const unsigned grid =
+                (unsigned)std::min<int64_t>(((int64_t)g.N * g.K + 255) / 256, 4096);
+            if (g.odt == MOE_DTYPE_F32)
+                hipLaunchKernelGGL(zero_rows_kernel<float>, dim3(grid), dim3(256), 0, s,
+                                   static_cast<float *>(g.dw), g.lddw, (int64_t)g.N, g.K);
+            else
+                hipLaunchKernelGGL(zero_rows_kernel<f16>, dim3(grid), dim3(256), 0, s,
+                                   static_cast<f16 *>(g.dw), g.lddw, (int64_t)g.N, g.K);
+            MOE_LAUNCH_CHECK("zero_rows_kernel");
+        }
+        return MOE_OK;
     }
-    if (g.dbias) {
-        hipLaunchKernelGGL(linear_dbias_kernel, dim3((g.N + 63) / 64), dim3(1024), 0, s, parts, G,
-                           g.N, g.dbias);
-        MOE_LAUNCH_CHECK("linear_dbias_kernel");
+    const GradWs w = grad_ws(g.M, g.N, g.K);
+    uint8_t *base = static_cast<uint8_t *>(ws);
+    float *parts = reinterpret_cast<float *>(base + w.parts);
+    // dy itself is dz where nothing changes it and its rows end on whole pieces
+    const bool own = g.act != MOE_ACT_NONE || g.N % 8 || g.lddy % 8 || (uintptr_t)g.dy % 16 ||
+                     g.lddy > LIN_MOST_LD;
+    const f16 *dz = own ? static_cast<const f16 *>(ws) : g.dy;
+    const int64_t ldd = own ? dz_ld(g.N) : g.lddy;
+    if ((own && (g.dx || g.dw)) || g.dbias) {
+        const int G = (g.M + DZ_ROWS - 1) / DZ_ROWS;
+        auto rows16 = [](const void *p, int64_t ld) { return (uintptr_t)p % 16 == 0 && ld % 8 == 0; };
+        for (int g0 = 0; g0 < G; g0 += 65535) {   // (rows of a grid)
+            LinGrads part = g;
+            const int64_t m0 = (int64_t)g0 * DZ_ROWS;
+            const int n = std::min(G - g0, 65535);
+            part.dy += m0 * g.lddy;
+            part.z += g.act != MOE_ACT_NONE ? m0 * g.ldz : 0;
+            part.M = (int)std::min<int64_t>(g.M - m0, (int64_t)n * DZ_ROWS);
+            f16 *to = own && (g.dx || g.dw) ? static_cast<f16 *>(ws) + m0 * ldd : nullptr;
+            hipLaunchKernelGGL(linear_dz_kernel, dim3((g.N + DZ_COLS - 1) / DZ_COLS, n), dim3(256), 0,
+                               s, part, to, ldd, g.dbias ? parts + (int64_t)g0 * g.N : nullptr,
+                               rows16(g.dy, g.lddy), rows16(g.z, g.ldz));
+            MOE_LAUNCH_CHECK("linear_dz_kernel");
+        }
+        if (g.dbias) {
+            hipLaunchKernelGGL(linear_dbias_kernel, dim3((g.N + 63) / 64), dim3(1024), 0, s, parts, G,
+                               g.N, g.dbias);
+            MOE_LAUNCH_CHECK("linear_dbias_kernel");
+        }
     }
     LinArgs a{};
     a.act = MOE_ACT_NONE;
     a.odt = g.odt;
     a.a = dz;
     a.lda = ldd;
-    if (g.dx && g.M > 0) {
+    a.b_ks = true;
+    a.N = g.K;
+    if (g.dx) {
         a.b = g.w;
         a.ldb = g.ldw;
-        a.b_ks = true;
         a.M = g.M;
-        a.N = g.K;
         a.K = g.N;
         a.out = g.dx;
         a.ldo = g.lddx;
-        const int rc = launch_linear(a, nullptr, s);
+        const int rc = launch_linear(a, base + w.products, s);
         if (rc)
             return rc;
     }
     if (g.dw) {
-        a.a_ks = a.b_ks = true;
+        a.a_ks = true;
         a.b = g.x;
         a.ldb = g.ldx;
         a.M = g.N;
-        a.N = g.K;
         a.K = g.M;
         a.out = g.dw;
         a.ldo = g.lddw;
-        return launch_linear(a, nullptr, s);
+        return launch_linear(a, base + w.products, s);
     }
     return MOE_OK;
 }
