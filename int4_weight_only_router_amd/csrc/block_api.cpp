@@ -60,17 +60,18 @@ static int check_rows(const char *fn, const char *what, const void *p, int64_t l
     return MOE_OK;
 }
 
-static void norm_alignment(NormArgs &a, int dtype, int w_dtype)
+// Whether the rows (of a gradient: those of what it is of) and weights can all be read
+// and written 16 bytes at a time.
+static bool norm_vec(const NormArgs &a, const NormGrads &d, int dtype)
 {
     const size_t s = type_size(dtype);
-    a.vec_y = rows16(a.y, a.ldy, s);
-    a.vec_r = rows16(a.residual, a.ldr, s);
-    a.vec_g = rows16(a.gate, a.ldg, s);
-    a.vec_o = rows16(a.out, a.ldo, s);
-    a.vec_n = rows16(a.n, a.ldn, s);
-    (void)w_dtype;
-    a.vec_w = (((uintptr_t)a.post_w | (uintptr_t)a.post_b | (uintptr_t)a.pre_w |
-                (uintptr_t)a.pre_b) & 15u) == 0;
+    const uintptr_t weights = (uintptr_t)a.post_w | (uintptr_t)a.post_b | (uintptr_t)a.pre_w |
+                              (uintptr_t)a.pre_b;
+    auto rows = [&](const void *p, int64_t ld) { return !p || rows16(p, ld, s); };
+    return a.H % 8 == 0 && weights % 16 == 0 && rows(a.y, a.ldy) && rows(d.dy, a.ldy) &&
+           rows(a.residual, a.ldr) && rows(d.dresidual, a.ldr) && rows(a.gate, a.ldg) &&
+           (!a.ldg || rows(d.dgate, a.ldg)) && rows(a.out, a.ldo) && rows(d.dout, a.ldo) &&
+           rows(a.n, a.ldn) && rows(d.dn, a.ldn);
 }
 
 static bool known_act(int act) { return act >= MOE_ACT_NONE && act <= MOE_ACT_GELU_TANH; }
@@ -120,6 +121,7 @@ int moe_block_norm(const void *y, int64_t ldy, const void *residual, int64_t ldr
     a.eps = eps;
     a.T = T;
     a.H = H;
+    a.w32 = w_dtype == MOE_DTYPE_F32;
     a.layer = kind == MOE_NORM_LAYER;
     a.post = (flags & MOE_NORM_POST) != 0;
     a.offset = (flags & MOE_NORM_UNIT_OFFSET) != 0;
@@ -138,8 +140,8 @@ int moe_block_norm(const void *y, int64_t ldy, const void *residual, int64_t ldr
         (rc = check_rows(fn, "out", out, ldo, H, dtype)) ||
         (rc = check_rows(fn, "n", n, ldn, H, dtype)))
         return rc;
-    norm_alignment(a, dtype, w_dtype);
-    return launch_block_norm(a, dtype, w_dtype, stream);
+    a.vec = norm_vec(a, NormGrads{}, dtype);
+    return launch_block_norm(a, dtype, stream);
 }
 
 size_t moe_block_norm_backward_workspace_bytes(int T, int H)
@@ -176,6 +178,7 @@ int moe_block_norm_backward(const void *dout, int64_t ldo, const void *dn, int64
     a.eps = eps;
     a.T = T;
     a.H = H;
+    a.w32 = w_dtype == MOE_DTYPE_F32;
     a.layer = kind == MOE_NORM_LAYER;
     a.post = (flags & MOE_NORM_POST) != 0;
     a.offset = (flags & MOE_NORM_UNIT_OFFSET) != 0;
@@ -230,14 +233,8 @@ int moe_block_norm_backward(const void *dout, int64_t ldo, const void *dn, int64
         }
     }
     d.parts = static_cast<float *>(ws);
-    a.out = const_cast<void *>(dout);
-    a.n = const_cast<void *>(dn);
-    norm_alignment(a, dtype, w_dtype);
-    const size_t s = type_size(dtype);
-    a.vec_dy = rows16(dy, ldy, s);
-    a.vec_dr = rows16(dresidual, ldr, s);
-    a.vec_dg = rows16(dgate, ldg, s);
-    return launch_block_norm_backward(a, d, dtype, w_dtype, stream);
+    a.vec = norm_vec(a, d, dtype);
+    return launch_block_norm_backward(a, d, dtype, stream);
 }
 
 size_t moe_linear_f16_workspace_bytes(int M, int N, int K)

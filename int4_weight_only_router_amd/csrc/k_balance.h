@@ -22,8 +22,8 @@ struct BalanceArgs {
     int64_t ldd;
     int gtype;
     // workspace
-    int count_groups;
-    int *part_counts, *part_n;
+    int count_groups;         // workgroups that count, 0: every one for itself
+    int *n, *part_counts, *part_n;
     float *part_p;
 };
 

@@ -11,17 +11,25 @@
 // The counts are needed before any gradient, the logits only once: a wave takes a
 // row, holds it in registers and writes its gradient at once.
 //
-// A sigmoid score's ratio is formed as a_e / sum a with a_e = exp(min(l_e, 0) - m)
-// / (1 + exp(-|l_e|)) and m the row's largest min(l, 0), so that it does not
-// underflow where every logit is far below zero.
+// A sigmoid score's ratio is formed as a_e / sum a with a_e = exp(min(l_e, 0) - m) /
+// (1 + exp(-|l_e|)) and m the row's largest min(l, 0) where that is far below zero,
+// so that it does not underflow where every logit is.
+//
+// Launches: up to 64 tokens one workgroup does it all; else the rows (a wave each, 16
+// waves a workgroup, sums of p over them to the workspace) and the joining of their
+// sums, and before them the counts where every workgroup counting all choices for
+// itself would take longer.  Bound by the launches and their dependent steps.
 #include <algorithm>
 
 #include "k_balance.h"
 
 namespace moe {
 
-constexpr int BL_THREADS = 256, BL_WAVES = BL_THREADS / 64;
-constexpr int BL_ONE_THREADS = 1024;
+constexpr int BL_THREADS = 1024, BL_WAVES = BL_THREADS / 64;
+// Waves of a workgroup of rows: half as many where a lane holds 16 experts (registers).
+template <int NE>
+constexpr int bl_waves() { return NE > 8 ? 8 : 16; }
+constexpr float BL_FAR = -60.0f;   // exp(-60) and its sums are far inside fp32's range
 
 template <typename T>
 __device__ __forceinline__ float logit_value(T v)
@@ -29,6 +37,17 @@ __device__ __forceinline__ float logit_value(T v)
     const float f = (float)v;
     // NaN counts as masked, +inf as the largest finite value (as in the selection)
     return f == f ? fminf(f, 3.402823466e+38f) : -__builtin_inff();
+}
+
+// exp(x) for x <= 0 by the hardware's exp2 (an ulp), with the rounding of x log2(e)
+// made good: 0 far below fp32's range and for -inf.
+__device__ __forceinline__ float exp_neg(float x)
+{
+    constexpr float L2E = 1.4426950408889634f, L2E_LO = 1.9259629911266175e-8f;
+    const float t = fmaxf(x, -200.0f) * L2E;
+    const float r = __builtin_fmaf(fmaxf(x, -200.0f), L2E, -t) + fmaxf(x, -200.0f) * L2E_LO;
+    const float e = __builtin_amdgcn_exp2f(t);
+    return __builtin_fmaf(e * r, 0.69314718055994531f, e);
 }
 
 __device__ __forceinline__ float wave_max(float v)
@@ -41,24 +60,27 @@ __device__ __forceinline__ float wave_max(float v)
 
 // Choices and unmasked tokens of the tokens t0 <= t < t1 into hist (LDS [E]) and
 // the return value (this thread's share).
-__device__ __forceinline__ int count_tokens(const BalanceArgs &a, int64_t t0, int64_t t1, int *hist,
-                                            int threads)
+template <int THREADS>
+__device__ __forceinline__ int count_tokens(const BalanceArgs &a, int64_t t0, int64_t t1, int *hist)
 {
     int n = 0;
-    for (int64_t t = t0 + threadIdx.x; t < t1; t += threads)
+    for (int64_t t = t0 + threadIdx.x; t < t1; t += THREADS)
         n += !a.mask || a.mask[t];
-    if (a.idx)
-        for (int64_t i = t0 * a.k + threadIdx.x; i < t1 * a.k; i += threads)
-            if (!a.mask || a.mask[i / a.k]) {
-                const int e = a.idx[i];
-                if ((unsigned)e < (unsigned)a.E)
-                    atomicAdd(&hist[e], 1);
-            }
+    if (a.idx) {
+        const int64_t i1 = t1 * a.k;
+#pragma unroll 4
+        for (int64_t i = t0 * a.k + threadIdx.x; i < i1; i += THREADS) {
+            const int e = a.idx[i];
+            if ((unsigned)e < (unsigned)a.E && (!a.mask || a.mask[i / a.k]))
+                atomicAdd(&hist[e], 1);
+        }
+    }
     return n;
 }
 
 // Sum over the workgroup (every thread gets it); s: one int a wave.
-__device__ __forceinline__ int block_sum(int v, int *s, int waves)
+template <int WAVES>
+__device__ __forceinline__ int block_sum(int v, int *s)
 {
 #pragma unroll
     for (int o = 32; o; o >>= 1)
@@ -67,92 +89,101 @@ __device__ __forceinline__ int block_sum(int v, int *s, int waves)
         s[threadIdx.x >> 6] = v;
     __syncthreads();
     v = 0;
-    for (int i = 0; i < waves; ++i)
+#pragma unroll
+    for (int i = 0; i < WAVES; ++i)
         v += s[i];
-    __syncthreads();
     return v;
 }
 
-// One row: its p into p[], its share of the balance loss and lse^2 added up, its
-// gradient written.  Lane l holds experts l, l + 64, ...
+// A row's logits in registers: lane l holds experts l, l + 64, ... (-inf past E and
+// for a masked token).
 template <typename LT, int NE>
-__device__ __forceinline__ void balance_row(const BalanceArgs &a, int64_t t, const float (&d)[NE],
-                                            float per_n, float up, float (&psum)[NE], float &loss,
-                                            float &zsum)
+__device__ __forceinline__ void load_row(const BalanceArgs &a, int64_t t, bool on, float (&l)[NE])
 {
-    const int lane = threadIdx.x & 63;
-    const bool on = !a.mask || a.mask[t];
-    if (!on && !a.dlogits)
-        return;
     const LT *row = static_cast<const LT *>(a.logits) + t * a.ld;
-    float l[NE], p[NE], top = -__builtin_inff();
 #pragma unroll
     for (int i = 0; i < NE; ++i) {
-        const int e = lane + 64 * i;
+        const int e = (threadIdx.x & 63) + 64 * i;
         l[i] = on && e < a.E ? logit_value<LT>(row[e]) : -__builtin_inff();
-        top = fmaxf(top, l[i]);
     }
+}
+
+// The row: its p added to psum[], its share of the balance loss and lse^2 added up,
+// its gradient written.
+template <int NE>
+__device__ __forceinline__ void balance_row(const BalanceArgs &a, int64_t t, bool on,
+                                            const float (&l)[NE], const float (&d)[NE], float per_n,
+                                            float up, float (&psum)[NE], float &loss, float &zsum)
+{
+    const int lane = threadIdx.x & 63;
+    float top = l[0];
+#pragma unroll
+    for (int i = 1; i < NE; ++i)
+        top = fmaxf(top, l[i]);
     top = wave_max(top);
     const bool some = top > -__builtin_inff();   // not masked throughout
     const bool sig = a.score == MOE_SCORE_SIGMOID;
-    const float zc = a.zcoef * per_n;
-    float lse = 0.0f, inv_soft = 0.0f;
+    float soft[NE], p[NE], lse = 0.0f;
     if (some && (!sig || a.zcoef != 0.0f)) {
         float s = 0.0f;
 #pragma unroll
         for (int i = 0; i < NE; ++i) {
-            p[i] = expf(l[i] - top);
-            s += p[i];
+            soft[i] = exp_neg(l[i] - top);
+            s += soft[i];
         }
         s = wave_sum_f32(s);
-        lse = top + logf(s);
-        inv_soft = 1.0f / s;
+        lse = top + __logf(s);
+        const float inv = 1.0f / s;
+#pragma unroll
+        for (int i = 0; i < NE; ++i)
+            soft[i] *= inv;
+    } else {
+#pragma unroll
+        for (int i = 0; i < NE; ++i)
+            soft[i] = 0.0f;
     }
-    float dot = 0.0f, share = 0.0f;
-    float part[NE];   // p (softmax: without its 1/s factor until below)
+    float rest[NE];   // sigmoid scores: 1 - s
     if (sig) {
-        const float m = fminf(top, 0.0f);
         float s = 0.0f;
+        const bool far = top < BL_FAR;
 #pragma unroll
         for (int i = 0; i < NE; ++i) {
-            part[i] = some ? expf(fminf(l[i], 0.0f) - m) / (1.0f + expf(-fabsf(l[i]))) : 0.0f;
-            s += part[i];
+            const float x = exp_neg(-fabsf(l[i])), q = __builtin_amdgcn_rcpf(1.0f + x);
+            rest[i] = (l[i] > 0.0f ? x : 1.0f) * q;
+            p[i] = some ? (l[i] > 0.0f ? 1.0f : far ? exp_neg(l[i] - top) : x) * q : 0.0f;
+            s += p[i];
         }
         s = wave_sum_f32(s);
         const float inv = some ? 1.0f / s : 0.0f;
 #pragma unroll
         for (int i = 0; i < NE; ++i)
-            part[i] *= inv;
+            p[i] *= inv;
     } else {
 #pragma unroll
         for (int i = 0; i < NE; ++i)
-            part[i] = some ? p[i] * inv_soft : 0.0f;
+            p[i] = soft[i];
     }
+    float dot = 0.0f, share = 0.0f;
 #pragma unroll
     for (int i = 0; i < NE; ++i) {
-        psum[i] += part[i];
-        dot = __builtin_fmaf(part[i], d[i], dot);
-        share += part[i];
+        psum[i] += p[i];
+        dot = __builtin_fmaf(p[i], d[i], dot);
+        share += p[i];
     }
     dot = wave_sum_f32(dot);
     loss += dot + wave_sum_f32(share);   // sum p (d + 1)
-    if (a.zcoef != 0.0f)
-        zsum = __builtin_fmaf(lse, lse, zsum);
+    zsum = __builtin_fmaf(lse, lse, zsum);
     if (!a.dlogits)
         return;
-    const float cb = up * a.coef * per_n, cz = up * zc * 2.0f * lse * inv_soft;
+    const float cb = up * a.coef * per_n, cz = a.zcoef != 0.0f ? up * a.zcoef * per_n * 2.0f * lse : 0.0f;
 #pragma unroll
     for (int i = 0; i < NE; ++i) {
         const int e = lane + 64 * i;
-        float g = cb * part[i] * (d[i] - dot);
-        if (sig) {   // 1 - sigmoid(l)
-            const float x = expf(-fabsf(l[i]));
-            g *= (l[i] > 0.0f ? x : 1.0f) / (1.0f + x);
-        }
-        if (a.zcoef != 0.0f && some)
-            g = __builtin_fmaf(cz, p[i], g);
+        float g = cb * p[i] * (d[i] - dot);
+        if (sig)
+            g *= rest[i];
+        g = some ? __builtin_fmaf(cz, soft[i], g) : 0.0f;
         if (e < a.E) {
-            g = on ? g : 0.0f;
             const int64_t at = t * a.ldd + e;
             if (a.gtype == MOE_DTYPE_F32)
                 static_cast<float *>(a.dlogits)[at] = g;
@@ -166,195 +197,185 @@ __device__ __forceinline__ void balance_row(const BalanceArgs &a, int64_t t, con
 
 // d_e of this lane's experts from whole counts.
 template <int NE>
-__device__ __forceinline__ void deviations(const int *hist, int64_t total, int E, float (&d)[NE])
+__device__ __forceinline__ void deviations(const int *hist, int E, float (&d)[NE])
 {
     const int lane = threadIdx.x & 63;
+    int64_t total = 0;   // every wave for itself
+#pragma unroll
+    for (int i = 0; i < NE; ++i)
+        total += lane + 64 * i < E ? hist[lane + 64 * i] : 0;
+#pragma unroll
+    for (int o = 32; o; o >>= 1)
+        total += __shfl_xor(total, o, 64);
+    const double inv = 1.0 / (double)(total > 0 ? total : 1);
 #pragma unroll
     for (int i = 0; i < NE; ++i) {
         const int e = lane + 64 * i;
-        d[i] = e < E ? (float)((double)(hist[e] * (int64_t)E - total) /
-                               (double)(total > 0 ? total : 1))
-                     : 0.0f;
+        d[i] = e < E ? (float)((double)(hist[e] * (int64_t)E - total) * inv) : 0.0f;
     }
-}
-
-__device__ __forceinline__ int64_t total_choices(const int *hist, int E)
-{
-    int64_t s = 0;   // every wave for itself
-    for (int e = threadIdx.x & 63; e < E; e += 64)
-        s += hist[e];
-#pragma unroll
-    for (int o = 32; o; o >>= 1)
-        s += __shfl_xor(s, o, 64);
-    return s;
 }
 
 // Partial counts of the tokens dealt out over the workgroups: [G][E] and the
 // unmasked tokens [G].
-__global__ __launch_bounds__(BL_ONE_THREADS) void balance_count_kernel(BalanceArgs a)
+__global__ __launch_bounds__(BL_THREADS) void balance_count_kernel(BalanceArgs a)
 {
     __shared__ int hist[BL_MAX_E];
-    __shared__ int s[BL_ONE_THREADS / 64];
-    for (int e = threadIdx.x; e < a.E; e += BL_ONE_THREADS)
+    __shared__ int s[BL_WAVES];
+    for (int e = threadIdx.x; e < a.E; e += BL_THREADS)
         hist[e] = 0;
     __syncthreads();
     const int64_t each = ((int64_t)a.T + gridDim.x - 1) / gridDim.x;
     const int64_t t0 = blockIdx.x * each;
-    const int n = block_sum(count_tokens(a, t0, min(t0 + each, (int64_t)a.T), hist, BL_ONE_THREADS),
-                            s, BL_ONE_THREADS / 64);
-    for (int e = threadIdx.x; e < a.E; e += BL_ONE_THREADS)
+    const int n = block_sum<BL_WAVES>(
+        count_tokens<BL_THREADS>(a, t0, min(t0 + each, (int64_t)a.T), hist), s);
+    for (int e = threadIdx.x; e < a.E; e += BL_THREADS)
         a.part_counts[(int64_t)blockIdx.x * a.E + e] = hist[e];
     if (threadIdx.x == 0)
         a.part_n[blockIdx.x] = n;
 }
 
-// Rows: partial sums of p [G][E], of the balance loss and of lse^2 [G][2].
-template <typename LT, int NE>
-__global__ __launch_bounds__(BL_THREADS) void balance_rows_kernel(BalanceArgs a)
+// Rows.  ONE: of one workgroup, which writes the outputs; else its sums of p, of the
+// balance loss and of lse^2 to the workspace [G][E + 2], and workgroup 0 the counts
+// and the number of unmasked tokens.
+template <typename LT, int NE, bool ONE>
+__global__ __launch_bounds__(64 * bl_waves<NE>()) void balance_rows_kernel(BalanceArgs a)
 {
+    constexpr int WAVES = bl_waves<NE>(), THREADS = 64 * WAVES, HALF = WAVES / 2;
     __shared__ int hist[64 * NE];
-    __shared__ float cols[BL_WAVES][64 * NE + 2];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    for (int e = threadIdx.x; e < a.E; e += BL_THREADS) {
-        int c = 0;
-        if (a.idx)
-            for (int g = 0; g < a.count_groups; ++g)
-                c += a.part_counts[(int64_t)g * a.E + e];
-        else
-            c = a.counts[e];
-        hist[e] = c;
-    }
+    __shared__ int s[WAVES];
+    __shared__ float cols[HALF][64 * NE + 2];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    int64_t t = (int64_t)blockIdx.x * WAVES + wave;
+    // the first row's logits are on their way while the choices are counted
+    auto counted = [&](int64_t t) {   // (the same for the whole wave)
+        return !a.mask || __builtin_amdgcn_readfirstlane(a.mask[t]);
+    };
+    bool on = t < a.T && counted(t);
+    float l[NE];
+    load_row<LT, NE>(a, t < a.T ? t : 0, on, l);
+    const float up = a.dlogits && a.d_loss ? *a.d_loss : 1.0f;
     int64_t n = a.T;
-    if (a.mask) {
-        n = 0;
-        for (int g = 0; g < a.count_groups; ++g)
-            n += a.part_n[g];
+    const bool self = ONE || !a.count_groups;   // counts for itself
+    if (self) {
+        for (int e = threadIdx.x; e < 64 * NE; e += THREADS)
+            hist[e] = a.idx || e >= a.E ? 0 : a.counts[e];
+        __syncthreads();
+        if (a.idx || a.mask)
+            n = block_sum<WAVES>(count_tokens<THREADS>(a, 0, a.T, hist), s);
+    } else {
+        for (int e = threadIdx.x; e < 64 * NE; e += THREADS) {
+            int c = 0;
+            if (e < a.E && !a.idx) {
+                c = a.counts[e];
+            } else if (e < a.E) {
+#pragma unroll 16
+                for (int g = 0; g < a.count_groups; ++g)
+                    c += a.part_counts[(int64_t)g * a.E + e];
+            }
+            hist[e] = c;
+        }
+        if (a.mask)
+            n = block_sum<WAVES>(threadIdx.x < a.count_groups ? a.part_n[threadIdx.x] : 0, s);
     }
     __syncthreads();
     float d[NE], psum[NE], loss = 0.0f, zsum = 0.0f;
-    deviations<NE>(hist, total_choices(hist, a.E), a.E, d);
+    deviations<NE>(hist, a.E, d);
 #pragma unroll
     for (int i = 0; i < NE; ++i)
         psum[i] = 0.0f;
     const float per_n = n > 0 ? 1.0f / (float)n : 0.0f;
-    const float up = a.dlogits && a.d_loss ? *a.d_loss : 1.0f;
-    for (int64_t t = (int64_t)blockIdx.x * BL_WAVES + wave; t < a.T;
-         t += (int64_t)gridDim.x * BL_WAVES)
-        balance_row<LT, NE>(a, t, d, per_n, up, psum, loss, zsum);
+    const int64_t step = (int64_t)gridDim.x * WAVES;
+    while (t < a.T) {
+        if (on || a.dlogits)
+            balance_row<NE>(a, t, on, l, d, per_n, up, psum, loss, zsum);
+        t += step;
+        if (t < a.T) {
+            on = counted(t);
+            load_row<LT, NE>(a, t, on, l);
+        }
+    }
+    // the waves' sums: the upper half's onto the lower half's, then those
+    if (wave >= HALF) {
 #pragma unroll
-    for (int i = 0; i < NE; ++i)
-        cols[wave][lane + 64 * i] = psum[i];
-    if (lane == 0) {
-        cols[wave][64 * NE] = loss;
-        cols[wave][64 * NE + 1] = zsum;
+        for (int i = 0; i < NE; ++i)
+            cols[wave - HALF][lane + 64 * i] = psum[i];
+        if (lane == 0) {
+            cols[wave - HALF][64 * NE] = loss;
+            cols[wave - HALF][64 * NE + 1] = zsum;
+        }
     }
     __syncthreads();
-    float *to = a.part_p + (int64_t)blockIdx.x * (a.E + 2);
-    for (int e = threadIdx.x; e < a.E + 2; e += BL_THREADS) {
-        const int at = e < a.E ? e : 64 * NE + e - a.E;
-        to[e] = (cols[0][at] + cols[1][at]) + (cols[2][at] + cols[3][at]);
+    if (wave < HALF) {
+#pragma unroll
+        for (int i = 0; i < NE; ++i)
+            cols[wave][lane + 64 * i] += psum[i];
+        if (lane == 0) {
+            cols[wave][64 * NE] += loss;
+            cols[wave][64 * NE + 1] += zsum;
+        }
     }
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.E + 2; e += THREADS) {
+        const int at = e < a.E ? e : 64 * NE + e - a.E;
+        float v = cols[0][at];
+#pragma unroll
+        for (int w = 1; w < HALF; ++w)
+            v += cols[w][at];
+        if (!ONE) {
+            a.part_p[(int64_t)blockIdx.x * (a.E + 2) + e] = v;
+        } else if (e >= a.E) {
+            if (a.losses)
+                a.losses[e - a.E] = e > a.E && a.zcoef == 0.0f ? 0.0f
+                                    : (e == a.E ? a.coef : a.zcoef) * (v * per_n);
+        } else if (a.mean_prob) {
+            a.mean_prob[e] = v * per_n;
+        }
+        if (blockIdx.x == 0 && e < a.E && a.idx)
+            a.counts[e] = hist[e];
+    }
+    if (!ONE && blockIdx.x == 0 && threadIdx.x == 0)
+        *a.n = (int)n;
 }
 
 // The outputs from the partial sums: 64 experts a workgroup, 16 partial sums at a
-// time; workgroup 0 also the losses.
-__global__ __launch_bounds__(BL_ONE_THREADS) void balance_join_kernel(BalanceArgs a, int G)
+// time; the last workgroup the losses.
+__global__ __launch_bounds__(BL_THREADS) void balance_join_kernel(BalanceArgs a, int G)
 {
     __shared__ float s[16][64];
-    __shared__ int si[16][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int e = blockIdx.x * 64 + lane;
-    int64_t n = a.T;
-    if (a.mask) {
-        n = 0;
-        for (int g = 0; g < a.count_groups; ++g)
-            n += a.part_n[g];
+    const int n = *a.n;
+    const double per_n = n > 0 ? 1.0 / n : 0.0;
+    const int64_t ld = a.E + 2;
+    if (blockIdx.x == gridDim.x - 1) {
+        if (wave > 1 || !a.losses)
+            return;
+        double v = 0.0;
+#pragma unroll 4
+        for (int g = lane; g < G; g += 64)
+            v += a.part_p[g * ld + a.E + wave];
+#pragma unroll
+        for (int o = 32; o; o >>= 1)
+            v += __shfl_xor(v, o, 64);
+        if (lane == 0)
+            a.losses[wave] = wave && a.zcoef == 0.0f ? 0.0f
+                             : (float)((wave ? a.zcoef : a.coef) * v * per_n);
+        return;
     }
-    const double per_n = n > 0 ? 1.0 / (double)n : 0.0;
     float v = 0.0f;
-    int c = 0;
     if (e < a.E) {
+#pragma unroll 16
         for (int g = wave; g < G; g += 16)
-            v += a.part_p[(int64_t)g * (a.E + 2) + e];
-        if (a.idx)
-            for (int g = wave; g < a.count_groups; g += 16)
-                c += a.part_counts[(int64_t)g * a.E + e];
+            v += a.part_p[g * ld + e];
     }
     s[wave][lane] = v;
-    si[wave][lane] = c;
     __syncthreads();
     if (wave == 0 && e < a.E) {
-        for (int i = 1; i < 16; ++i) {
+#pragma unroll
+        for (int i = 1; i < 16; ++i)
             v += s[i][lane];
-            c += si[i][lane];
-        }
         if (a.mean_prob)
             a.mean_prob[e] = (float)(v * per_n);
-        if (a.idx)
-            a.counts[e] = c;
-    }
-    if (blockIdx.x == 0 && wave == 1 && a.losses) {
-        double b = 0.0, z = 0.0;
-        for (int g = lane; g < G; g += 64) {
-            b += a.part_p[(int64_t)g * (a.E + 2) + a.E];
-            z += a.part_p[(int64_t)g * (a.E + 2) + a.E + 1];
-        }
-#pragma unroll
-        for (int o = 32; o; o >>= 1) {
-            b += __shfl_xor(b, o, 64);
-            z += __shfl_xor(z, o, 64);
-        }
-        if (lane == 0) {
-            a.losses[0] = (float)(a.coef * b * per_n);
-            a.losses[1] = a.zcoef != 0.0f ? (float)(a.zcoef * z * per_n) : 0.0f;
-        }
-    }
-}
-
-// Few tokens: all of it in one workgroup.
-template <typename LT, int NE>
-__global__ __launch_bounds__(BL_ONE_THREADS) void balance_one_kernel(BalanceArgs a)
-{
-    constexpr int WAVES = BL_ONE_THREADS / 64;
-    __shared__ int hist[64 * NE];
-    __shared__ int s[WAVES];
-    __shared__ float cols[WAVES][64 * NE + 2];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    for (int e = threadIdx.x; e < a.E; e += BL_ONE_THREADS)
-        hist[e] = a.idx ? 0 : a.counts[e];
-    __syncthreads();
-    const int n = block_sum(count_tokens(a, 0, a.T, hist, BL_ONE_THREADS), s, WAVES);
-    float d[NE], psum[NE], loss = 0.0f, zsum = 0.0f;
-    deviations<NE>(hist, total_choices(hist, a.E), a.E, d);
-#pragma unroll
-    for (int i = 0; i < NE; ++i)
-        psum[i] = 0.0f;
-    const float per_n = n > 0 ? 1.0f / (float)n : 0.0f;
-    const float up = a.dlogits && a.d_loss ? *a.d_loss : 1.0f;
-    for (int t = wave; t < a.T; t += WAVES)
-        balance_row<LT, NE>(a, t, d, per_n, up, psum, loss, zsum);
-#pragma unroll
-    for (int i = 0; i < NE; ++i)
-        cols[wave][lane + 64 * i] = psum[i];
-    if (lane == 0) {
-        cols[wave][64 * NE] = loss;
-        cols[wave][64 * NE + 1] = zsum;
-    }
-    __syncthreads();
-    for (int e = threadIdx.x; e < a.E + 2; e += BL_ONE_THREADS) {
-        const int at = e < a.E ? e : 64 * NE + e - a.E;
-        float v = 0.0f;
-        for (int w = 0; w < WAVES; ++w)
-            v += cols[w][at];
-        v *= per_n;
-        if (e < a.E) {
-            if (a.mean_prob)
-                a.mean_prob[e] = v;
-            if (a.idx)
-                a.counts[e] = hist[e];
-        } else if (a.losses) {
-            a.losses[e - a.E] = e == a.E ? a.coef * v : a.zcoef != 0.0f ? a.zcoef * v : 0.0f;
-        }
     }
 }
 
@@ -370,37 +391,51 @@ __global__ void balance_none_kernel(BalanceArgs a)
         a.losses[threadIdx.x] = 0.0f;
 }
 
-constexpr int BL_ONE_ROWS = 64;   // rows up to which one workgroup does it all
-constexpr int BL_COUNT_GROUPS = 16, BL_GROUPS = 512;
+constexpr int BL_ONE_ROWS = 64;   // tokens up to which one workgroup does it all
+// Choices up to which every workgroup counts all of them for itself (eight a thread:
+// 1 us, against 2 to 3 of another launch), else in up to 16 workgroups of a launch.
+constexpr int BL_SELF = 8192;
+constexpr int BL_COUNT_GROUPS = 16, BL_GROUPS = 256;
 
-static int count_groups(int T) { return std::min((T + 255) / 256, BL_COUNT_GROUPS); }
-static int row_groups(int T) { return std::min((T + BL_WAVES - 1) / BL_WAVES, BL_GROUPS); }
+// 0: counted by every workgroup.  (Given counts count as few: k = 1.)
+static int count_groups(int T, int k)
+{
+    return (int64_t)T * k <= BL_SELF ? 0 : std::min((int)(((int64_t)T + 255) / 256), BL_COUNT_GROUPS);
+}
+static int row_groups(int T, int E)
+{
+    const int waves = E > 512 ? bl_waves<16>() : bl_waves<8>();
+    return (int)std::min<int64_t>(((int64_t)T + waves - 1) / waves, BL_GROUPS);
+}
 
 size_t balance_ws(int T, int E)
 {
     if (T <= BL_ONE_ROWS)
         return 0;
-    return (size_t)al256((int64_t)count_groups(T) * (E + 1) * 4) +
-           (size_t)row_groups(T) * (E + 2) * 4;
+    return (size_t)al256((int64_t)BL_COUNT_GROUPS * (E + 1) * 4 + 4) +
+           (size_t)row_groups(T, E) * (E + 2) * 4;
 }
 
 template <typename LT, int NE>
 static int launch_ne(const BalanceArgs &a, hipStream_t s)
 {
     if (a.T <= BL_ONE_ROWS) {
-        hipLaunchKernelGGL((balance_one_kernel<LT, NE>), dim3(1), dim3(BL_ONE_THREADS), 0, s, a);
-        MOE_LAUNCH_CHECK("balance_one_kernel");
+        hipLaunchKernelGGL((balance_rows_kernel<LT, NE, true>), dim3(1), dim3(64 * bl_waves<NE>()), 0, s, a);
+        MOE_LAUNCH_CHECK("balance_rows_kernel");
         return MOE_OK;
     }
-    if (a.idx || a.mask) {
-        hipLaunchKernelGGL(balance_count_kernel, dim3(a.count_groups), dim3(BL_ONE_THREADS), 0, s, a);
+    if (a.count_groups) {
+        hipLaunchKernelGGL(balance_count_kernel, dim3(a.count_groups), dim3(BL_THREADS), 0, s, a);
         MOE_LAUNCH_CHECK("balance_count_kernel");
     }
-    const int G = row_groups(a.T);
-    hipLaunchKernelGGL((balance_rows_kernel<LT, NE>), dim3(G), dim3(BL_THREADS), 0, s, a);
+    const int G = row_groups(a.T, a.E);
+    hipLaunchKernelGGL((balance_rows_kernel<LT, NE, false>), dim3(G), dim3(64 * bl_waves<NE>()), 0, s, a);
     MOE_LAUNCH_CHECK("balance_rows_kernel");
-    hipLaunchKernelGGL(balance_join_kernel, dim3((a.E + 63) / 64), dim3(BL_ONE_THREADS), 0, s, a, G);
-    MOE_LAUNCH_CHECK("balance_join_kernel");
+    if (a.mean_prob || a.losses) {
+        hipLaunchKernelGGL(balance_join_kernel, dim3((a.E + 63) / 64 + 1), dim3(BL_THREADS), 0, s, a,
+                           G);
+        MOE_LAUNCH_CHECK("balance_join_kernel");
+    }
     return MOE_OK;
 }
 
@@ -421,11 +456,13 @@ int launch_balance(BalanceArgs a, int dtype, void *ws, hipStream_t s)
         MOE_LAUNCH_CHECK("balance_none_kernel");
         return MOE_OK;
     }
-    a.count_groups = count_groups(a.T);
+    // without choices to count and tokens to leave out there is nothing to count
+    a.count_groups = a.idx ? count_groups(a.T, a.k) : a.mask ? count_groups(a.T, 1) : 0;
     uint8_t *base = static_cast<uint8_t *>(ws);
-    a.part_counts = reinterpret_cast<int *>(base);
-    a.part_n = a.part_counts + (int64_t)a.count_groups * a.E;
-    a.part_p = reinterpret_cast<float *>(base + al256((int64_t)a.count_groups * (a.E + 1) * 4));
+    a.n = reinterpret_cast<int *>(base);
+    a.part_counts = a.n + 1;
+    a.part_n = a.part_counts + (int64_t)BL_COUNT_GROUPS * a.E;
+    a.part_p = reinterpret_cast<float *>(base + al256((int64_t)BL_COUNT_GROUPS * (a.E + 1) * 4 + 4));
     if (dtype == MOE_DTYPE_F32)
         return launch_type<float>(a, s);
     return dtype == MOE_DTYPE_F16 ? launch_type<f16>(a, s) : launch_type<__bf16>(a, s);

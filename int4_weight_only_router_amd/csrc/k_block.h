@@ -67,16 +67,14 @@ __device__ __forceinline__ void store8(T *row, int c, int cols, bool vec, const 
     }
 }
 
-// Rows of T x H; vec_*: whether a tensor's rows are 16-byte aligned.
+// Rows of T x H.  vec: H a multiple of 8 and every tensor's rows 16-byte aligned.
 struct NormArgs {
     const void *y, *residual, *gate, *post_w, *post_b, *pre_w, *pre_b;
     void *out, *n;
     int64_t ldy, ldr, ldg, ldo, ldn;   // ldg 0: one gate row for all
     float scale, eps;
     int T, H;
-    bool layer, post, offset;
-    bool vec_y, vec_r, vec_g, vec_o, vec_n, vec_w;
-    bool vec_dy, vec_dr, vec_dg;
+    bool layer, post, offset, w32, vec;
 };
 
 // Gradients, laid out as what they are gradients of; `sums`: fp32 [H] over the
@@ -94,8 +92,8 @@ struct NormSums {
     int n;
 };
 
-int launch_block_norm(const NormArgs &, int dtype, int w_dtype, hipStream_t);
+int launch_block_norm(const NormArgs &, int dtype, hipStream_t);
 size_t block_norm_backward_ws(int T, int H);
-int launch_block_norm_backward(const NormArgs &, NormGrads, int dtype, int w_dtype, hipStream_t);
+int launch_block_norm_backward(const NormArgs &, NormGrads, int dtype, hipStream_t);
 
 }  // namespace moe

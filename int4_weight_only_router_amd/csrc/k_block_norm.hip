@@ -13,6 +13,52 @@
 
 namespace moe {
 
+// The columns of a row among its threads.  VEC: chunk i of a thread is eight
+// columns in a row (16 bytes of fp16).  Otherwise (odd sizes, strides or addresses)
+// eight columns `span` apart, so that a wave's loads are contiguous all the same.
+template <bool VEC>
+struct Cols {
+    int t, span, H;   // thread of the row, threads of a row, columns
+    __device__ __forceinline__ int col(int i, int j) const
+    {
+        return VEC ? (i * span + t) * 8 + j : (i * 8 + j) * span + t;
+    }
+    __device__ __forceinline__ bool in(int i, int j) const { return col(i, VEC ? 0 : j) < H; }
+    template <typename T>
+    __device__ __forceinline__ void load(const T *row, int i, float (&v)[8]) const
+    {
+        if constexpr (VEC) {
+            load8<T>(row, col(i, 0), in(i, 0) ? H : 0, true, v);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[j] = in(i, j) ? (float)row[col(i, j)] : 0.0f;
+        }
+    }
+    template <typename T>
+    __device__ __forceinline__ void store(T *row, int i, const float (&v)[8]) const
+    {
+        if constexpr (VEC) {
+            if (in(i, 0))
+                store8<T>(row, col(i, 0), H, true, v);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (in(i, j))
+                    row[col(i, j)] = (T)v[j];
+        }
+    }
+    // weights: fp32 or of the rows' type
+    template <typename T>
+    __device__ __forceinline__ void weights(const void *w, bool w32, int i, float (&v)[8]) const
+    {
+        if (sizeof(T) == 4 || w32)
+            load<float>(static_cast<const float *>(w), i, v);
+        else
+            load<T>(static_cast<const T *>(w), i, v);
+    }
+};
+
 // Sum over the row's threads: its wave, or all four waves of the workgroup.
 // `part` alternates between two halves, so one barrier per sum suffices: a half
 // is written again only behind the barrier of the sum in between.
@@ -33,11 +79,10 @@ __device__ __forceinline__ float row_sum(float v, float *part, int &half)
 }
 
 // v normalised in place (columns past H hold zeros and stay so).
-template <int W, int NC>
-__device__ __forceinline__ void normalise(float (&v)[NC][8], int c0, const NormArgs &a, float *part,
-                                          int &half)
+template <int W, int NC, bool VEC>
+__device__ __forceinline__ void normalise(float (&v)[NC][8], const Cols<VEC> &c, const NormArgs &a,
+                                          float *part, int &half)
 {
-    constexpr int STEP = W * 512;
     if (a.layer) {
         float s = 0.0f;
 #pragma unroll
@@ -50,7 +95,7 @@ __device__ __forceinline__ void normalise(float (&v)[NC][8], int c0, const NormA
         for (int i = 0; i < NC; ++i)
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                v[i][j] = c0 + i * STEP + j < a.H ? v[i][j] - mean : 0.0f;
+                v[i][j] = c.in(i, j) ? v[i][j] - mean : 0.0f;
     }
     float s = 0.0f;
 #pragma unroll
@@ -67,24 +112,22 @@ __device__ __forceinline__ void normalise(float (&v)[NC][8], int c0, const NormA
 }
 
 // v * weight + bias; either may be absent.
-template <typename WT, int NC, int STEP>
-__device__ __forceinline__ void affine(float (&v)[NC][8], int c0, const NormArgs &a, const void *w,
-                                       const void *b)
+template <typename XT, int NC, bool VEC>
+__device__ __forceinline__ void affine(float (&v)[NC][8], const Cols<VEC> &c, const NormArgs &a,
+                                       const void *w, const void *b)
 {
     const float one = a.offset ? 1.0f : 0.0f;
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-        const int c = c0 + i * STEP;
+        float t[8];
         if (w) {
-            float t[8];
-            load8<WT>(static_cast<const WT *>(w), c, a.H, a.vec_w, t);
+            c.template weights<XT>(w, a.w32, i, t);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 v[i][j] *= t[j] + one;
         }
         if (b) {
-            float t[8];
-            load8<WT>(static_cast<const WT *>(b), c, a.H, a.vec_w, t);
+            c.template weights<XT>(b, a.w32, i, t);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 v[i][j] += t[j];
@@ -94,70 +137,71 @@ __device__ __forceinline__ void affine(float (&v)[NC][8], int c0, const NormArgs
 
 // W waves a row of up to 512 W NC columns: a wave a row (no barrier, all its
 // loads in flight together) up to 2048 columns, above that the workgroup.
-template <typename XT, typename WT, int W, int NC>
+template <typename XT, bool VEC, int W, int NC>
 __global__ __launch_bounds__(256) void block_norm_kernel(NormArgs a)
 {
     __shared__ float part[2 * W];
-    constexpr int ROWS = 4 / W, STEP = W * 512;
-    const int c0 = (W == 1 ? (int)(threadIdx.x & 63) : (int)threadIdx.x) * 8;
+    constexpr int ROWS = 4 / W;
+    const Cols<VEC> c = {W == 1 ? (int)(threadIdx.x & 63) : (int)threadIdx.x, 64 * W, a.H};
     int half = 0;
-    for (int64_t t = (int64_t)blockIdx.x * ROWS + (W == 1 ? threadIdx.x >> 6 : 0); t < a.T;
-         t += (int64_t)gridDim.x * ROWS) {
+    const int64_t t = (int64_t)blockIdx.x * ROWS + (W == 1 ? threadIdx.x >> 6 : 0);
+    if (t < a.T) {   // (the whole row's threads)
         float r[NC][8], u[NC][8];
-        if (a.residual) {
 #pragma unroll
-            for (int i = 0; i < NC; ++i)
-                load8<XT>(static_cast<const XT *>(a.residual) + t * a.ldr, c0 + i * STEP, a.H,
-                          a.vec_r, r[i]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < NC; ++i)
+        for (int i = 0; i < NC; ++i) {
+            if (a.residual) {
+                c.load(static_cast<const XT *>(a.residual) + t * a.ldr, i, r[i]);
+            } else {
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
                     r[i][j] = 0.0f;
+            }
         }
         if (a.y) {
 #pragma unroll
             for (int i = 0; i < NC; ++i)
-                load8<XT>(static_cast<const XT *>(a.y) + t * a.ldy, c0 + i * STEP, a.H, a.vec_y,
-                          u[i]);
+                c.load(static_cast<const XT *>(a.y) + t * a.ldy, i, u[i]);
             if (a.post) {
-                normalise<W, NC>(u, c0, a, part, half);
-                affine<WT, NC, STEP>(u, c0, a, a.post_w, a.post_b);
+                normalise<W, NC>(u, c, a, part, half);
+                affine<XT>(u, c, a, a.post_w, a.post_b);
             }
 #pragma unroll
             for (int i = 0; i < NC; ++i) {
-                float g[8];
-                if (a.gate)
-                    load8<XT>(static_cast<const XT *>(a.gate) + t * a.ldg, c0 + i * STEP, a.H,
-                              a.vec_g, g);
+                if (a.gate) {
+                    float g[8];
+                    c.load(static_cast<const XT *>(a.gate) + t * a.ldg, i, g);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        u[i][j] *= g[j];
+                }
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    r[i][j] = __builtin_fmaf(a.scale, a.gate ? g[j] * u[i][j] : u[i][j], r[i][j]);
+                    r[i][j] = __builtin_fmaf(a.scale, u[i][j], r[i][j]);
             }
         }
         if (a.out) {
 #pragma unroll
             for (int i = 0; i < NC; ++i)
-                store8<XT>(static_cast<XT *>(a.out) + t * a.ldo, c0 + i * STEP, a.H, a.vec_o, r[i]);
+                c.store(static_cast<XT *>(a.out) + t * a.ldo, i, r[i]);
         }
         if (a.n) {
-            normalise<W, NC>(r, c0, a, part, half);
-            affine<WT, NC, STEP>(r, c0, a, a.pre_w, a.pre_b);
+            normalise<W, NC>(r, c, a, part, half);
+            affine<XT>(r, c, a, a.pre_w, a.pre_b);
 #pragma unroll
             for (int i = 0; i < NC; ++i)
-                store8<XT>(static_cast<XT *>(a.n) + t * a.ldn, c0 + i * STEP, a.H, a.vec_n, r[i]);
+                c.store(static_cast<XT *>(a.n) + t * a.ldn, i, r[i]);
         }
     }
 }
 
-template <typename XT, typename WT>
+template <typename XT, bool VEC>
 static int launch_norm_t(const NormArgs &a, hipStream_t s)
 {
-    const int64_t rows = a.H <= 2048 ? 4 : 1;   // of a workgroup
-    const int64_t grid = std::min<int64_t>((a.T + rows - 1) / rows, 1 << 20);   // the rest in its loop
-#define MOE_N(W, NC)                                                                            \
-    hipLaunchKernelGGL((block_norm_kernel<XT, WT, W, NC>), dim3((unsigned)grid), dim3(256), 0, s, a)
+    const int rows = a.H <= 2048 ? 4 : 1;   // of a workgroup
+    const int64_t grid = ((int64_t)a.T + rows - 1) / rows;
+#define MOE_N(W, NC)                                                                             \
+    hipLaunchKernelGGL((block_norm_kernel<XT, VEC, W, NC>), dim3((unsigned)grid), dim3(256), 0, s, \
+                       a)
     if (a.H <= 512) MOE_N(1, 1);
     else if (a.H <= 1024) MOE_N(1, 2);
     else if (a.H <= 2048) MOE_N(1, 4);
@@ -169,18 +213,32 @@ static int launch_norm_t(const NormArgs &a, hipStream_t s)
 }
 
 template <typename XT>
-static int launch_norm_x(const NormArgs &a, bool w32, hipStream_t s)
+static int launch_norm_x(NormArgs a, hipStream_t s)
 {
-    return w32 ? launch_norm_t<XT, float>(a, s) : launch_norm_t<XT, XT>(a, s);
+    // a launch has fewer than 2^32 threads: rows beyond that take another
+    const int64_t most = (1 << 23), s1 = sizeof(XT);
+    auto on = [&](const void *p, int64_t ld) {
+        return p ? static_cast<const char *>(p) + most * ld * s1 : nullptr;
+    };
+    for (int64_t left = a.T; left > 0; left -= most) {
+        a.T = (int)std::min(left, most);
+        const int rc = a.vec ? launch_norm_t<XT, true>(a, s) : launch_norm_t<XT, false>(a, s);
+        if (rc)
+            return rc;
+        a.y = on(a.y, a.ldy);
+        a.residual = on(a.residual, a.ldr);
+        a.gate = on(a.gate, a.ldg);
+        a.out = const_cast<char *>(on(a.out, a.ldo));
+        a.n = const_cast<char *>(on(a.n, a.ldn));
+    }
+    return MOE_OK;
 }
 
-int launch_block_norm(const NormArgs &a, int dtype, int w_dtype, hipStream_t s)
+int launch_block_norm(const NormArgs &a, int dtype, hipStream_t s)
 {
-    const bool w32 = w_dtype == MOE_DTYPE_F32;
     if (dtype == MOE_DTYPE_F32)
-        return launch_norm_t<float, float>(a, s);
-    return dtype == MOE_DTYPE_F16 ? launch_norm_x<f16>(a, w32, s)
-                                  : launch_norm_x<bf16>(a, w32, s);
+        return launch_norm_x<float>(a, s);
+    return dtype == MOE_DTYPE_F16 ? launch_norm_x<f16>(a, s) : launch_norm_x<bf16>(a, s);
 }
 
 // ------------------------------------------------------------------ gradients
@@ -223,8 +281,9 @@ __device__ __forceinline__ void group_sum2(float &a, float &b, int W, float2 *pa
 
 // v to its normalised values; returns the reciprocal root (0 for a turn past the
 // last row, whose zeros must stay zeros also where eps is 0).
-__device__ __forceinline__ float normalise_group(float (&v)[8], int c, bool live, const NormArgs &a,
-                                                 int W, float2 *part, int &half)
+template <bool VEC>
+__device__ __forceinline__ float normalise_group(float (&v)[8], const Cols<VEC> &c, bool live,
+                                                 const NormArgs &a, int W, float2 *part, int &half)
 {
     float s = 0.0f, q = 0.0f;
     if (a.layer) {
@@ -235,7 +294,7 @@ __device__ __forceinline__ float normalise_group(float (&v)[8], int c, bool live
         const float mean = s / (float)a.H;
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            v[j] = c + j < a.H ? v[j] - mean : 0.0f;
+            v[j] = c.in(0, j) ? v[j] - mean : 0.0f;
     }
     s = q = 0.0f;
 #pragma unroll
@@ -266,17 +325,16 @@ __device__ __forceinline__ void norm_input_grad(float (&g)[8], const float (&m)[
         g[j] = rho * (g[j] - mean - m[j] * along);
 }
 
-template <typename XT, typename WT>
+template <typename XT, bool VEC>
 __global__ __launch_bounds__(NB_THREADS) void block_norm_backward_kernel(NormArgs a, NormGrads d,
                                                                          int W)
 {
     __shared__ float2 part[2 * (NB_THREADS / 64)];
     __shared__ float cols[NB_THREADS * 8];
-    const int wave = threadIdx.x >> 6;
     const int groups = NB_THREADS / 64 / W;   // rows at a time
-    const int grp = wave / W;
-    const int c = ((wave - grp * W) * 64 + (threadIdx.x & 63)) * 8;
+    const int grp = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) / W;
     const int H = a.H;
+    Cols<VEC> c = {(int)threadIdx.x - grp * W * 64, 64 * W, H};
     const float one = a.offset ? 1.0f : 0.0f;
     int half = 0;
     float sum[NB_SUMS][8];
@@ -288,38 +346,48 @@ __global__ __launch_bounds__(NB_THREADS) void block_norm_backward_kernel(NormArg
     // every group takes as many turns (its sums meet at barriers); one past the
     // last row works on zeros and stores nothing
     for (int64_t t0 = (int64_t)blockIdx.x * groups; t0 < a.T; t0 += (int64_t)gridDim.x * groups) {
-        const int64_t t = t0 + grp;
-        const int cols_in = t < a.T ? H : 0;   // columns that this thread may touch
-        const int64_t row = t < a.T ? t : 0;
+        // (the weights are read again every turn, out of the caches: kept, they would
+        // take the registers of the sums)
+        asm volatile("" : "+s"(a.post_w), "+s"(a.post_b), "+s"(a.pre_w));
+        const bool live = t0 + grp < a.T;
+        const int64_t t = live ? t0 + grp : 0;
+        c.H = live ? H : 0;   // columns that this turn may touch
         float u[8], r[8], gate[8], pm[8], dr[8], g[8];
         float post_rho = 0.0f;
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             u[j] = r[j] = pm[j] = dr[j] = 0.0f;
         if (a.residual)
-            load8<XT>(static_cast<const XT *>(a.residual) + row * a.ldr, c, cols_in, a.vec_r, r);
+            c.load(static_cast<const XT *>(a.residual) + t * a.ldr, 0, r);
+        if (a.y)
+            c.load(static_cast<const XT *>(a.y) + t * a.ldy, 0, u);
         if (d.dout)
-            load8<XT>(static_cast<const XT *>(d.dout) + row * a.ldo, c, cols_in, a.vec_o, dr);
+            c.load(static_cast<const XT *>(d.dout) + t * a.ldo, 0, dr);
         if (d.dn)
-            load8<XT>(static_cast<const XT *>(d.dn) + row * a.ldn, c, cols_in, a.vec_n, g);
+            c.load(static_cast<const XT *>(d.dn) + t * a.ldn, 0, g);
         if (a.y) {
-            load8<XT>(static_cast<const XT *>(a.y) + row * a.ldy, c, cols_in, a.vec_y, u);
             if (a.gate)
-                load8<XT>(static_cast<const XT *>(a.gate) + row * a.ldg, c, cols_in, a.vec_g, gate);
+                c.load(static_cast<const XT *>(a.gate) + t * a.ldg, 0, gate);
             if (a.post) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
                     pm[j] = u[j];
-                post_rho = normalise_group(pm, c, t < a.T, a, W, part, half);
-                float w[8], b[8];
-                if (a.post_w)
-                    load8<WT>(static_cast<const WT *>(a.post_w), c, H, a.vec_w, w);
-                if (a.post_b)
-                    load8<WT>(static_cast<const WT *>(a.post_b), c, H, a.vec_w, b);
+                post_rho = normalise_group(pm, c, live, a, W, part, half);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    u[j] = a.post_w ? pm[j] * (w[j] + one) : pm[j];
-                    u[j] = a.post_b && c + j < cols_in ? u[j] + b[j] : u[j];
+                for (int j = 0; j < 8; ++j)
+                    u[j] = pm[j];
+                float w[8];
+                if (a.post_w) {
+                    c.template weights<XT>(a.post_w, a.w32, 0, w);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        u[j] *= w[j] + one;
+                }
+                if (a.post_b) {
+                    c.template weights<XT>(a.post_b, a.w32, 0, w);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        u[j] += w[j];
                 }
             }
 #pragma unroll
@@ -327,15 +395,18 @@ __global__ __launch_bounds__(NB_THREADS) void block_norm_backward_kernel(NormArg
                 r[j] = __builtin_fmaf(a.scale, a.gate ? gate[j] * u[j] : u[j], r[j]);
         }
         if (d.dn) {
-            const float rho = normalise_group(r, c, t < a.T, a, W, part, half);   // r: normalised from here
-            float w[8];
-            if (a.pre_w)
-                load8<WT>(static_cast<const WT *>(a.pre_w), c, H, a.vec_w, w);
+            const float rho = normalise_group(r, c, live, a, W, part, half);   // r: normalised from here
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 sum[NB_PRE_W][j] = __builtin_fmaf(g[j], r[j], sum[NB_PRE_W][j]);
                 sum[NB_PRE_B][j] += g[j];
-                g[j] = a.pre_w ? g[j] * (w[j] + one) : g[j];
+            }
+            if (a.pre_w) {
+                float w[8];
+                c.template weights<XT>(a.pre_w, a.w32, 0, w);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    g[j] *= w[j] + one;
             }
             norm_input_grad(g, r, rho, a, W, part, half);
 #pragma unroll
@@ -343,35 +414,38 @@ __global__ __launch_bounds__(NB_THREADS) void block_norm_backward_kernel(NormArg
                 dr[j] += g[j];
         }
         if (d.dresidual)
-            store8<XT>(static_cast<XT *>(d.dresidual) + row * a.ldr, c, cols_in, a.vec_dr, dr);
+            c.store(static_cast<XT *>(d.dresidual) + t * a.ldr, 0, dr);
         if (a.y) {
-            float dg[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                dr[j] = c + j < cols_in ? a.scale * dr[j] : 0.0f;   // of gate * u
-                dg[j] = dr[j] * u[j];
-                sum[NB_GATE][j] += dg[j];
-                dr[j] = a.gate ? dr[j] * gate[j] : dr[j];   // of u
+                dr[j] = c.in(0, j) ? a.scale * dr[j] : 0.0f;   // of gate * u
+                u[j] *= dr[j];                                 // the gate's
+                sum[NB_GATE][j] += u[j];
+                dr[j] = a.gate ? dr[j] * gate[j] : dr[j];      // of u
             }
             if (d.dgate && a.ldg)
-                store8<XT>(static_cast<XT *>(d.dgate) + row * a.ldg, c, cols_in, a.vec_dg, dg);
+                c.store(static_cast<XT *>(d.dgate) + t * a.ldg, 0, u);
             if (a.post) {
-                float w[8];
-                if (a.post_w)
-                    load8<WT>(static_cast<const WT *>(a.post_w), c, H, a.vec_w, w);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     sum[NB_POST_W][j] = __builtin_fmaf(dr[j], pm[j], sum[NB_POST_W][j]);
                     sum[NB_POST_B][j] += dr[j];
-                    dr[j] = a.post_w ? dr[j] * (w[j] + one) : dr[j];
+                }
+                if (a.post_w) {
+                    float w[8];
+                    c.template weights<XT>(a.post_w, a.w32, 0, w);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        dr[j] *= w[j] + one;
                 }
                 norm_input_grad(dr, pm, post_rho, a, W, part, half);
             }
             if (d.dy)
-                store8<XT>(static_cast<XT *>(d.dy) + row * a.ldy, c, cols_in, a.vec_dy, dr);
+                c.store(static_cast<XT *>(d.dy) + t * a.ldy, 0, dr);
         }
     }
     // the groups' sums, in the order of the groups
+    c.H = H;
     float *to = d.parts + (int64_t)blockIdx.x * d.nsums * H;
 #pragma unroll
     for (int k = 0; k < NB_SUMS; ++k) {
@@ -390,7 +464,7 @@ __global__ __launch_bounds__(NB_THREADS) void block_norm_backward_kernel(NormArg
                         sum[k][j] += cols[j * NB_THREADS + i * W * 64 + threadIdx.x];
         }
         if (grp == 0)
-            store8<float>(to, c, H, H % 4 == 0, sum[k]);
+            c.store(to, 0, sum[k]);
         to += H;
     }
 }
@@ -405,12 +479,15 @@ __global__ __launch_bounds__(1024) void norm_sums_kernel(const float *__restrict
     const int col = blockIdx.x * 64 + lane;
     const int64_t n = to.n;
     float v = 0.0f;
-    if (col < H)
+    if (col < H) {
+#pragma unroll 8
         for (int g = wave; g < G; g += 16)
             v += parts[(g * n + blockIdx.y) * H + col];
+    }
     s[wave][lane] = v;
     __syncthreads();
     if (wave == 0 && col < H) {
+#pragma unroll
         for (int i = 1; i < 16; ++i)
             v += s[i][lane];
         to.p[blockIdx.y][col] = v;
@@ -437,8 +514,18 @@ size_t block_norm_backward_ws(int T, int H)
     return (size_t)norm_backward_grid(T, H) * NB_SUMS * H * sizeof(float);
 }
 
-int launch_block_norm_backward(const NormArgs &a, NormGrads d, int dtype, int w_dtype,
-                               hipStream_t s)
+template <typename XT>
+static void launch_backward_x(const NormArgs &a, const NormGrads &d, int G, int W, hipStream_t s)
+{
+    if (a.vec)
+        hipLaunchKernelGGL((block_norm_backward_kernel<XT, true>), dim3((unsigned)G),
+                           dim3(NB_THREADS), 0, s, a, d, W);
+    else
+        hipLaunchKernelGGL((block_norm_backward_kernel<XT, false>), dim3((unsigned)G),
+                           dim3(NB_THREADS), 0, s, a, d, W);
+}
+
+int launch_block_norm_backward(const NormArgs &a, NormGrads d, int dtype, hipStream_t s)
 {
     const int W = norm_waves(a.H), G = norm_backward_grid(a.T, a.H);
     NormSums to{};
@@ -447,16 +534,12 @@ int launch_block_norm_backward(const NormArgs &a, NormGrads d, int dtype, int w_
             to.p[to.n++] = d.sums[k];
     d.nsums = to.n;
     if (a.T > 0) {
-#define MOE_NB(XT, WT)                                                                           \
-    hipLaunchKernelGGL((block_norm_backward_kernel<XT, WT>), dim3((unsigned)G), dim3(NB_THREADS), 0, \
-                       s, a, d, W)
-        const bool w32 = w_dtype == MOE_DTYPE_F32;
-        if (dtype == MOE_DTYPE_F32) MOE_NB(float, float);
-        else if (dtype == MOE_DTYPE_F16 && w32) MOE_NB(f16, float);
-        else if (dtype == MOE_DTYPE_F16) MOE_NB(f16, f16);
-        else if (w32) MOE_NB(bf16, float);
-        else MOE_NB(bf16, bf16);
-#undef MOE_NB
+        if (dtype == MOE_DTYPE_F32)
+            launch_backward_x<float>(a, d, G, W, s);
+        else if (dtype == MOE_DTYPE_F16)
+            launch_backward_x<f16>(a, d, G, W, s);
+        else
+            launch_backward_x<bf16>(a, d, G, W, s);
         MOE_LAUNCH_CHECK("block_norm_backward_kernel");
     }
     if (to.n) {   // without tokens: zeros

@@ -11,10 +11,10 @@
 namespace moe {
 
 // The forms of a tile: rows, columns, groups that share its k, workgroups a compute
-// unit; and what they were measured to take, in us (fp16, K = 512 and 2048, 256
-// compute units all busy): `start` for a launch, `one` for a block of 64 k of a
-// workgroup (of its group, where groups share k), `two` for one of each of two
-// workgroups on a compute unit.
+// unit; and what they were measured to take, in us (fp16, K = 256, 512 and 2048, 256
+// compute units busy with one to eight workgroups each): a workgroup `end` for its
+// first loads and its results and `one` for a block of 64 k (of its group, where
+// groups share k); two workgroups on a compute unit together `two` for a block of each.
 //
 // With them the form and the parts of k that take the least time are chosen.  On 90
 // products from 1 x 1024 x 256 to 8192 x 8192 x 8192 the choice was the fastest form
@@ -25,12 +25,12 @@ namespace moe {
 // 154, 192-row 163).
 struct LinForm {
     int bm, bn, kg, per_cu;
-    double start, one, two;
+    double end, one, two;
 };
 static const LinForm FORMS[] = {
-    {16, 32, 8, 1, 3.0, 0.70, 0}, {32, 64, 2, 1, 3.0, 0.33, 0},  {64, 64, 2, 1, 2.6, 0.48, 0},
-    {64, 64, 1, 2, 1.7, 0.33, 0.46}, {128, 128, 1, 1, 3.8, 0.53, 0}, {128, 128, 1, 2, 2.9, 0.75, 1.02},
-    {192, 256, 1, 1, 4.4, 1.21, 0}, {256, 256, 1, 1, 5.5, 1.45, 0}};
+    {16, 32, 8, 1, 3.0, 0.80, 0},     {32, 64, 2, 1, 2.2, 0.30, 0},  {64, 64, 2, 1, 2.2, 0.44, 0},
+    {64, 64, 1, 2, 0.9, 0.33, 0.33},  {128, 128, 1, 1, 3.5, 0.50, 0}, {128, 128, 1, 2, 1.8, 0.72, 0.90},
+    {192, 256, 1, 1, 6.0, 1.13, 0},   {256, 256, 1, 1, 5.0, 1.45, 0}};
 
 LinPlan linear_plan(int M, int N, int K)
 {
@@ -41,15 +41,15 @@ LinPlan linear_plan(int M, int N, int K)
         const LinForm &o = FORMS[f];
         if (f == 0 && M > 16)
             continue;
-        const int64_t tiles = (int64_t)(((int64_t)M + o.bm - 1) / o.bm) * (((int64_t)N + o.bn - 1) / o.bn);
+        const int64_t tiles = ((int64_t)M + o.bm - 1) / o.bm * (((int64_t)N + o.bn - 1) / o.bn);
         for (int s = 1; s <= 8; s *= 2) {
             const int each = (nkb + s - 1) / s;
             if (s > 1 && (tiles * s > 256 || (nkb + each - 1) / each != s))
                 break;   // no more parts than compute units, none empty
-            const double n = (double)((tiles * s + 255) / 256);   // workgroups of a compute unit
+            const int64_t n = (tiles * s + 255) / 256;   // workgroups of a compute unit
+            const int64_t pairs = o.per_cu == 2 ? n / 2 : 0;
             const double blocks = (each + o.kg - 1) / o.kg;
-            const double pairs = o.per_cu == 2 ? (double)((int64_t)n / 2) : 0;
-            double t = o.start + blocks * (pairs * o.two + (n - 2 * pairs) * o.one);
+            double t = 1.0 + n * o.end + blocks * (pairs * o.two + (n - 2 * pairs) * o.one);
             if (s > 1)   // a launch more, and the parts' sums written and read
                 t += 4.5 + (2.0 * s + 1) * 4.0 * M * N / 3e6;
             if (t < least) {
