@@ -21,7 +21,8 @@ POOL_HOST_LIB = os.path.join(PKG, "libmoe_pool_host.so")
 HIP_SOURCES = ["moe_api.cpp", "k_route.hip", "k_permute.hip", "k_ffn_decode.hip", "k_shared_gemv.hip",
                "k_ffn_grouped.hip", "k_ffn_small.hip", "k_combine.hip", "k_combine_route.hip", "k_quant.hip", "pool_hip.cpp",
                "prepack_host.cpp", "fp8_api.cpp", "k_route_select.hip", "k_quant_fp8.hip", "k_fp8_decode.hip",
-               "k_fp8_gemm.hip", "block_api.cpp", "k_block_norm.hip", "k_linear.hip", "k_linear_tile.hip", "k_balance.hip"]
+               "k_fp8_gemm.hip", "block_api.cpp", "k_block_norm.hip", "k_linear.hip", "k_linear_tile.hip", "k_linear_rows.hip",
+               "k_balance.hip"]
 HEADERS = ["moe_common.h", "k_w4_frag.h", "k_decode_frag.h", "k_sort_common.h", "k_combine_tile.h",
            "k_fp8_frag.h", "k_block.h", "k_linear.h", "k_balance.h", "pool_core.h", "trace.h"]
 

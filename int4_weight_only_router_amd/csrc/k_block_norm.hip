@@ -13,9 +13,73 @@
 
 namespace moe {
 
+// One value of a row of H, zero past its end (`at` in bytes), by buffer instructions:
+// their range check does without a branch, and without a lane mask, for every value.
+template <typename T>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t row_rsrc(const T *row, int H)
+{
+    constexpr int RAW = 0x00020000;   // 32-bit data, no swizzle
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<T *>(row), 0, H * (int)sizeof(T), RAW);
+}
+template <typename T>
+__device__ __forceinline__ float row_load(__amdgpu_buffer_rsrc_t r, int at)
+{
+    if constexpr (sizeof(T) == 4)
+        return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(r, at, 0, 0));
+    else
+        return (float)__builtin_bit_cast(
+            T, (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, at, 0, 0));
+}
+template <typename T>
+__device__ __forceinline__ void row_store(__amdgpu_buffer_rsrc_t r, int at, float v)
+{
+    if constexpr (sizeof(T) == 4)
+        __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), r, at, 0, 0);
+    else
+        __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, (T)v), r, at, 0, 0);
+}
+
+// Eight values in a row of H (a multiple of 8), 16 bytes at a time.
+template <typename T>
+__device__ __forceinline__ void row_load8(__amdgpu_buffer_rsrc_t r, int at, float (&v)[8])
+{
+    if constexpr (sizeof(T) == 4) {
+        const float4_t a = __builtin_bit_cast(float4_t, __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0));
+        const float4_t b =
+            __builtin_bit_cast(float4_t, __builtin_amdgcn_raw_buffer_load_b128(r, at + 16, 0, 0));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[j] = a[j];
+            v[4 + j] = b[j];
+        }
+    } else {
+        typedef typename Vec8<T>::type V;
+        const V a = __builtin_bit_cast(V, __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0));
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            v[j] = (float)a[j];
+    }
+}
+template <typename T>
+__device__ __forceinline__ void row_store8(__amdgpu_buffer_rsrc_t r, int at, const float (&v)[8])
+{
+    if constexpr (sizeof(T) == 4) {
+        const float4_t a = {v[0], v[1], v[2], v[3]}, b = {v[4], v[5], v[6], v[7]};
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(uint4_t, a), r, at, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(uint4_t, b), r, at + 16, 0, 0);
+    } else {
+        typename Vec8<T>::type a;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            a[j] = (T)v[j];
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(uint4_t, a), r, at, 0, 0);
+    }
+}
+
 // The columns of a row among its threads.  VEC: chunk i of a thread is eight
 // columns in a row (16 bytes of fp16).  Otherwise (odd sizes, strides or addresses)
 // eight columns `span` apart, so that a wave's loads are contiguous all the same.
+// Rows are the same for a whole wave.
 template <bool VEC>
 struct Cols {
     int t, span, H;   // thread of the row, threads of a row, columns
@@ -23,29 +87,39 @@ struct Cols {
     {
         return VEC ? (i * span + t) * 8 + j : (i * 8 + j) * span + t;
     }
-    __device__ __forceinline__ bool in(int i, int j) const { return col(i, VEC ? 0 : j) < H; }
+    // (The column is formed anew at each use: kept, the places and masks of a thread's
+    // columns take the registers of its values.)
+    __device__ __forceinline__ int fresh(int i, int j) const
+    {
+        int k = t;
+        asm volatile("" : "+v"(k));
+        return VEC ? (i * span + k) * 8 + j : (i * 8 + j) * span + k;
+    }
+    __device__ __forceinline__ bool in(int i, int j) const { return fresh(i, VEC ? 0 : j) < H; }
     template <typename T>
     __device__ __forceinline__ void load(const T *row, int i, float (&v)[8]) const
     {
         if constexpr (VEC) {
-            load8<T>(row, col(i, 0), in(i, 0) ? H : 0, true, v);
+            row_load8<T>(row_rsrc(row, H), col(i, 0) * (int)sizeof(T), v);
         } else {
+            const __amdgpu_buffer_rsrc_t r = row_rsrc(row, H);
+            const int k = fresh(i, 0);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                v[j] = in(i, j) ? (float)row[col(i, j)] : 0.0f;
+                v[j] = row_load<T>(r, (k + j * span) * (int)sizeof(T));
         }
     }
     template <typename T>
     __device__ __forceinline__ void store(T *row, int i, const float (&v)[8]) const
     {
         if constexpr (VEC) {
-            if (in(i, 0))
-                store8<T>(row, col(i, 0), H, true, v);
+            row_store8<T>(row_rsrc(row, H), col(i, 0) * (int)sizeof(T), v);
         } else {
+            const __amdgpu_buffer_rsrc_t r = row_rsrc(row, H);
+            const int k = fresh(i, 0);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                if (in(i, j))
-                    row[col(i, j)] = (T)v[j];
+                row_store<T>(r, (k + j * span) * (int)sizeof(T), v[j]);
         }
     }
     // weights: fp32 or of the rows' type
@@ -136,7 +210,8 @@ __device__ __forceinline__ void affine(float (&v)[NC][8], const Cols<VEC> &c, co
 }
 
 // W waves a row of up to 512 W NC columns: a wave a row (no barrier, all its
-// loads in flight together) up to 2048 columns, above that the workgroup.
+// loads in flight together) up to 2048 columns, above that, and for few rows, the
+// workgroup.
 template <typename XT, bool VEC, int W, int NC>
 __global__ __launch_bounds__(256) void block_norm_kernel(NormArgs a)
 {
@@ -144,7 +219,8 @@ __global__ __launch_bounds__(256) void block_norm_kernel(NormArgs a)
     constexpr int ROWS = 4 / W;
     const Cols<VEC> c = {W == 1 ? (int)(threadIdx.x & 63) : (int)threadIdx.x, 64 * W, a.H};
     int half = 0;
-    const int64_t t = (int64_t)blockIdx.x * ROWS + (W == 1 ? threadIdx.x >> 6 : 0);
+    const int64_t t = (int64_t)blockIdx.x * ROWS +
+                      (W == 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0);
     if (t < a.T) {   // (the whole row's threads)
         float r[NC][8], u[NC][8];
 #pragma unroll
@@ -197,14 +273,17 @@ __global__ __launch_bounds__(256) void block_norm_kernel(NormArgs a)
 template <typename XT, bool VEC>
 static int launch_norm_t(const NormArgs &a, hipStream_t s)
 {
-    const int rows = a.H <= 2048 ? 4 : 1;   // of a workgroup
+    // a wave a row where rows alone give every SIMD (1024) one
+    const bool wave = a.H <= 512 || (a.H <= 2048 && a.T >= 1024);
+    const int rows = wave ? 4 : 1;   // of a workgroup
     const int64_t grid = ((int64_t)a.T + rows - 1) / rows;
 #define MOE_N(W, NC)                                                                             \
     hipLaunchKernelGGL((block_norm_kernel<XT, VEC, W, NC>), dim3((unsigned)grid), dim3(256), 0, s, \
                        a)
-    if (a.H <= 512) MOE_N(1, 1);
-    else if (a.H <= 1024) MOE_N(1, 2);
-    else if (a.H <= 2048) MOE_N(1, 4);
+    if (wave && a.H <= 512) MOE_N(1, 1);
+    else if (wave && a.H <= 1024) MOE_N(1, 2);
+    else if (wave) MOE_N(1, 4);
+    else if (a.H <= 2048) MOE_N(4, 1);
     else if (a.H <= 4096) MOE_N(4, 2);
     else MOE_N(4, 4);
 #undef MOE_N
@@ -252,97 +331,135 @@ int launch_block_norm(const NormArgs &a, int dtype, hipStream_t s)
 // groups of a workgroup meet in LDS at the end, the workgroups' sums in a second
 // launch, both in a fixed order.
 
-constexpr int NB_THREADS = 1024;
+constexpr int NB_THREADS = 512, NB_WAVES = NB_THREADS / 64;
 enum { NB_GATE = 0, NB_POST_W, NB_POST_B, NB_PRE_W, NB_PRE_B, NB_SUMS };
 
-// Sums of two values over a row's W waves (groups of W waves in a row).
-__device__ __forceinline__ void group_sum2(float &a, float &b, int W, float2 *part, int &half)
+// Sums over a row's W waves (groups of W waves in a row) of a and, with `two`, of b.
+__device__ __forceinline__ void group_sum(float &a, float &b, bool two, int W, float2 *part,
+                                          int &half)
 {
     a = wave_sum_f32(a);
-    b = wave_sum_f32(b);
+    if (two)
+        b = wave_sum_f32(b);
     if (W == 1)
         return;
     const int wave = threadIdx.x >> 6;
-    float2 *p = part + half * (NB_THREADS / 64);
+    float2 *p = part + half * NB_WAVES;
     half ^= 1;
     if ((threadIdx.x & 63) == 0)
         p[wave] = float2{a, b};
     __syncthreads();
     const int w0 = wave & ~(W - 1);
-    float sa = 0.0f, sb = 0.0f;
-    for (int i = 0; i < W; ++i) {
-        const float2 v = p[w0 + i];
-        sa += v.x;
-        sb += v.y;
+    float2 v = p[w0];
+    for (int i = 1; i < W; ++i) {
+        v.x += p[w0 + i].x;
+        v.y += p[w0 + i].y;
     }
-    a = sa;
-    b = sb;
+    a = v.x;
+    b = v.y;
 }
 
 // v to its normalised values; returns the reciprocal root (0 for a turn past the
 // last row, whose zeros must stay zeros also where eps is 0).
-template <bool VEC>
-__device__ __forceinline__ float normalise_group(float (&v)[8], const Cols<VEC> &c, bool live,
+template <int NC, bool VEC>
+__device__ __forceinline__ float normalise_group(float (&v)[NC][8], const Cols<VEC> &c, bool live,
                                                  const NormArgs &a, int W, float2 *part, int &half)
 {
-    float s = 0.0f, q = 0.0f;
+    float s = 0.0f, none = 0.0f;
     if (a.layer) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            s += v[j];
-        group_sum2(s, q, W, part, half);
+        for (int i = 0; i < NC; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                s += v[i][j];
+        group_sum(s, none, false, W, part, half);
         const float mean = s / (float)a.H;
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            v[j] = c.in(0, j) ? v[j] - mean : 0.0f;
-    }
-    s = q = 0.0f;
+        for (int i = 0; i < NC; ++i)
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-        s = __builtin_fmaf(v[j], v[j], s);
-    group_sum2(s, q, W, part, half);
+            for (int j = 0; j < 8; ++j)
+                v[i][j] = c.in(i, j) ? v[i][j] - mean : 0.0f;
+        s = 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < NC; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            s = __builtin_fmaf(v[i][j], v[i][j], s);
+    group_sum(s, none, false, W, part, half);
     const float rho = live ? 1.0f / sqrtf(s / (float)a.H + a.eps) : 0.0f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-        v[j] *= rho;
+    for (int i = 0; i < NC; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            v[i][j] *= rho;
     return rho;
 }
 
 // g = dn * w to the gradient of the normed row; m its normalised values.
-__device__ __forceinline__ void norm_input_grad(float (&g)[8], const float (&m)[8], float rho,
-                                                const NormArgs &a, int W, float2 *part, int &half)
+template <int NC>
+__device__ __forceinline__ void norm_input_grad(float (&g)[NC][8], const float (&m)[NC][8],
+                                                float rho, const NormArgs &a, int W, float2 *part,
+                                                int &half)
 {
     float s = 0.0f, q = 0.0f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        s += g[j];
-        q = __builtin_fmaf(g[j], m[j], q);
-    }
-    group_sum2(s, q, W, part, half);
+    for (int i = 0; i < NC; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            q = __builtin_fmaf(g[i][j], m[i][j], q);
+            if (a.layer)
+                s += g[i][j];
+        }
+    group_sum(q, s, a.layer, W, part, half);
     const float mean = a.layer ? s / (float)a.H : 0.0f, along = q / (float)a.H;
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-        g[j] = rho * (g[j] - mean - m[j] * along);
+    for (int i = 0; i < NC; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            g[i][j] = rho * __builtin_fmaf(-m[i][j], along, g[i][j] - mean);
 }
 
-template <typename XT, bool VEC>
-__global__ __launch_bounds__(NB_THREADS) void block_norm_backward_kernel(NormArgs a, NormGrads d,
-                                                                         int W)
+// v *= w (+ one)
+template <typename XT, int NC, bool VEC>
+__device__ __forceinline__ void times_weight(float (&v)[NC][8], const Cols<VEC> &c,
+                                             const NormArgs &a, const void *w)
 {
-    __shared__ float2 part[2 * (NB_THREADS / 64)];
+    const float one = a.offset ? 1.0f : 0.0f;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+        float t[8];
+        c.template weights<XT>(w, a.w32, i, t);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            v[i][j] *= t[j] + one;
+    }
+}
+
+// NC: eights of columns of a thread (W waves hold 512 W NC).  The sums of the biases'
+// gradients are seldom asked for; they stand in LDS, each thread's in places of its
+// own, and leave the registers to the others.
+template <typename XT, bool VEC, int NC>
+__global__ __launch_bounds__(NB_THREADS, NC == 1 ? 4 : 2) void block_norm_backward_kernel(
+    NormArgs a, NormGrads d, int W)
+{
+    __shared__ float2 part[2 * NB_WAVES];
     __shared__ float cols[NB_THREADS * 8];
-    const int groups = NB_THREADS / 64 / W;   // rows at a time
+    __shared__ float bias[2][NC * 8][NB_THREADS];   // post, pre
+    const int groups = NB_WAVES / W;   // rows at a time
     const int grp = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) / W;
     const int H = a.H;
     Cols<VEC> c = {(int)threadIdx.x - grp * W * 64, 64 * W, H};
-    const float one = a.offset ? 1.0f : 0.0f;
     int half = 0;
-    float sum[NB_SUMS][8];
+    float sum[NB_SUMS][NC][8];
+    const bool post_b = d.sums[NB_POST_B], pre_b = d.sums[NB_PRE_B];
 #pragma unroll
-    for (int k = 0; k < NB_SUMS; ++k)
+    for (int i = 0; i < NC; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            sum[k][j] = 0.0f;
+        for (int j = 0; j < 8; ++j) {
+            sum[NB_GATE][i][j] = sum[NB_POST_W][i][j] = sum[NB_PRE_W][i][j] = 0.0f;
+            bias[0][i * 8 + j][threadIdx.x] = bias[1][i * 8 + j][threadIdx.x] = 0.0f;
+        }
     // every group takes as many turns (its sums meet at barriers); one past the
     // last row works on zeros and stores nothing
     for (int64_t t0 = (int64_t)blockIdx.x * groups; t0 < a.T; t0 += (int64_t)gridDim.x * groups) {
@@ -352,96 +469,108 @@ __global__ __launch_bounds__(NB_THREADS) void block_norm_backward_kernel(NormArg
         const bool live = t0 + grp < a.T;
         const int64_t t = live ? t0 + grp : 0;
         c.H = live ? H : 0;   // columns that this turn may touch
-        float u[8], r[8], gate[8], pm[8], dr[8], g[8];
+        float u[NC][8], r[NC][8], gate[NC][8], pm[NC][8], dr[NC][8], g[NC][8];
         float post_rho = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            u[j] = r[j] = pm[j] = dr[j] = 0.0f;
-        if (a.residual)
-            c.load(static_cast<const XT *>(a.residual) + t * a.ldr, 0, r);
-        if (a.y)
-            c.load(static_cast<const XT *>(a.y) + t * a.ldy, 0, u);
-        if (d.dout)
-            c.load(static_cast<const XT *>(d.dout) + t * a.ldo, 0, dr);
-        if (d.dn)
-            c.load(static_cast<const XT *>(d.dn) + t * a.ldn, 0, g);
-        if (a.y) {
-            if (a.gate)
-                c.load(static_cast<const XT *>(a.gate) + t * a.ldg, 0, gate);
-            if (a.post) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    pm[j] = u[j];
-                post_rho = normalise_group(pm, c, live, a, W, part, half);
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    u[j] = pm[j];
-                float w[8];
-                if (a.post_w) {
-                    c.template weights<XT>(a.post_w, a.w32, 0, w);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        u[j] *= w[j] + one;
-                }
-                if (a.post_b) {
-                    c.template weights<XT>(a.post_b, a.w32, 0, w);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        u[j] += w[j];
-                }
-            }
+        for (int i = 0; i < NC; ++i) {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                r[j] = __builtin_fmaf(a.scale, a.gate ? gate[j] * u[j] : u[j], r[j]);
+                u[i][j] = r[i][j] = dr[i][j] = g[i][j] = 0.0f;
+            if (a.y)
+                c.load(static_cast<const XT *>(a.y) + t * a.ldy, i, u[i]);
+            if (a.residual)
+                c.load(static_cast<const XT *>(a.residual) + t * a.ldr, i, r[i]);
+            if (d.dn)
+                c.load(static_cast<const XT *>(d.dn) + t * a.ldn, i, g[i]);
+            if (d.dout)
+                c.load(static_cast<const XT *>(d.dout) + t * a.ldo, i, dr[i]);
+            if (a.gate) {
+                c.load(static_cast<const XT *>(a.gate) + t * a.ldg, i, gate[i]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    gate[i][j] = 1.0f;
+            }
+        }
+        if (a.y) {
+            if (a.post) {
+                post_rho = normalise_group(u, c, live, a, W, part, half);
+#pragma unroll
+                for (int i = 0; i < NC; ++i)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        pm[i][j] = u[i][j];
+                if (a.post_w)
+                    times_weight<XT>(u, c, a, a.post_w);
+                if (a.post_b)
+#pragma unroll
+                    for (int i = 0; i < NC; ++i) {
+                        float w[8];
+                        c.template weights<XT>(a.post_b, a.w32, i, w);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            u[i][j] += w[j];
+                    }
+            }
+#pragma unroll
+            for (int i = 0; i < NC; ++i)
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    r[i][j] = __builtin_fmaf(a.scale, gate[i][j] * u[i][j], r[i][j]);
         }
         if (d.dn) {
             const float rho = normalise_group(r, c, live, a, W, part, half);   // r: normalised from here
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                sum[NB_PRE_W][j] = __builtin_fmaf(g[j], r[j], sum[NB_PRE_W][j]);
-                sum[NB_PRE_B][j] += g[j];
-            }
-            if (a.pre_w) {
-                float w[8];
-                c.template weights<XT>(a.pre_w, a.w32, 0, w);
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    g[j] *= w[j] + one;
-            }
-            norm_input_grad(g, r, rho, a, W, part, half);
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                dr[j] += g[j];
-        }
-        if (d.dresidual)
-            c.store(static_cast<XT *>(d.dresidual) + t * a.ldr, 0, dr);
-        if (a.y) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                dr[j] = c.in(0, j) ? a.scale * dr[j] : 0.0f;   // of gate * u
-                u[j] *= dr[j];                                 // the gate's
-                sum[NB_GATE][j] += u[j];
-                dr[j] = a.gate ? dr[j] * gate[j] : dr[j];      // of u
-            }
-            if (d.dgate && a.ldg)
-                c.store(static_cast<XT *>(d.dgate) + t * a.ldg, 0, u);
-            if (a.post) {
+            for (int i = 0; i < NC; ++i)
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    sum[NB_POST_W][j] = __builtin_fmaf(dr[j], pm[j], sum[NB_POST_W][j]);
-                    sum[NB_POST_B][j] += dr[j];
+                    sum[NB_PRE_W][i][j] = __builtin_fmaf(g[i][j], r[i][j], sum[NB_PRE_W][i][j]);
+                    if (pre_b)
+                        bias[1][i * 8 + j][threadIdx.x] += g[i][j];
                 }
-                if (a.post_w) {
-                    float w[8];
-                    c.template weights<XT>(a.post_w, a.w32, 0, w);
+            if (a.pre_w)
+                times_weight<XT>(g, c, a, a.pre_w);
+            norm_input_grad(g, r, rho, a, W, part, half);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        dr[j] *= w[j] + one;
+            for (int i = 0; i < NC; ++i)
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    dr[i][j] += g[i][j];
+        }
+        if (d.dresidual)
+#pragma unroll
+            for (int i = 0; i < NC; ++i)
+                c.store(static_cast<XT *>(d.dresidual) + t * a.ldr, i, dr[i]);
+        if (a.y) {
+#pragma unroll
+            for (int i = 0; i < NC; ++i) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    dr[i][j] = c.in(i, j) ? a.scale * dr[i][j] : 0.0f;   // of gate * u
+                    u[i][j] *= dr[i][j];                                 // the gate's
+                    sum[NB_GATE][i][j] += u[i][j];
+                    dr[i][j] *= gate[i][j];                              // of u
                 }
+                if (d.dgate && a.ldg)
+                    c.store(static_cast<XT *>(d.dgate) + t * a.ldg, i, u[i]);
+            }
+            if (a.post) {
+#pragma unroll
+                for (int i = 0; i < NC; ++i)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        sum[NB_POST_W][i][j] = __builtin_fmaf(dr[i][j], pm[i][j], sum[NB_POST_W][i][j]);
+                        if (post_b)
+                            bias[0][i * 8 + j][threadIdx.x] += dr[i][j];
+                    }
+                if (a.post_w)
+                    times_weight<XT>(dr, c, a, a.post_w);
                 norm_input_grad(dr, pm, post_rho, a, W, part, half);
             }
             if (d.dy)
-                c.store(static_cast<XT *>(d.dy) + t * a.ldy, 0, dr);
+#pragma unroll
+                for (int i = 0; i < NC; ++i)
+                    c.store(static_cast<XT *>(d.dy) + t * a.ldy, i, dr[i]);
         }
     }
     // the groups' sums, in the order of the groups
@@ -451,20 +580,27 @@ __global__ __launch_bounds__(NB_THREADS) void block_norm_backward_kernel(NormArg
     for (int k = 0; k < NB_SUMS; ++k) {
         if (!d.sums[k])
             continue;
-        if (groups > 1) {
-            __syncthreads();
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                cols[j * NB_THREADS + threadIdx.x] = sum[k][j];
-            __syncthreads();
+        for (int i = 0; i < NC; ++i) {
+            if (k == NB_POST_B || k == NB_PRE_B)
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    sum[k][i][j] = bias[k == NB_PRE_B][i * 8 + j][threadIdx.x];
+            if (groups > 1) {
+                __syncthreads();
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    cols[j * NB_THREADS + threadIdx.x] = sum[k][i][j];
+                __syncthreads();
+                if (grp == 0)
+                    for (int o = 1; o < groups; ++o)
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            sum[k][i][j] += cols[j * NB_THREADS + o * W * 64 + threadIdx.x];
+            }
             if (grp == 0)
-                for (int i = 1; i < groups; ++i)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        sum[k][j] += cols[j * NB_THREADS + i * W * 64 + threadIdx.x];
+                c.store(to, i, sum[k][i]);
         }
-        if (grp == 0)
-            c.store(to, 0, sum[k]);
         to += H;
     }
 }
@@ -494,19 +630,21 @@ __global__ __launch_bounds__(1024) void norm_sums_kernel(const float *__restrict
     }
 }
 
-// Waves a row: the fewest (a power of two) that hold H columns, eight a lane.
+// Waves a row: the fewest (a power of two, up to a workgroup's) that hold H columns,
+// eight a lane; rows of more than 4096 columns take 16 a lane.
 static int norm_waves(int H)
 {
     int w = 1;
-    while (w * 512 < H)
+    while (w * 512 < H && w < NB_WAVES)
         w *= 2;
     return w;
 }
 
+constexpr int NB_GRID = 512;   // two workgroups a compute unit
 static int norm_backward_grid(int T, int H)
 {
-    const int rows = NB_THREADS / 64 / norm_waves(H);
-    return (int)std::min<int64_t>(((int64_t)T + rows - 1) / rows, 256);
+    const int rows = NB_WAVES / norm_waves(H);
+    return (int)std::min<int64_t>(((int64_t)T + rows - 1) / rows, NB_GRID);
 }
 
 size_t block_norm_backward_ws(int T, int H)
@@ -514,15 +652,24 @@ size_t block_norm_backward_ws(int T, int H)
     return (size_t)norm_backward_grid(T, H) * NB_SUMS * H * sizeof(float);
 }
 
+template <typename XT, bool VEC>
+static void launch_backward_v(const NormArgs &a, const NormGrads &d, int G, int W, hipStream_t s)
+{
+    if (a.H <= 512 * NB_WAVES)
+        hipLaunchKernelGGL((block_norm_backward_kernel<XT, VEC, 1>), dim3((unsigned)G),
+                           dim3(NB_THREADS), 0, s, a, d, W);
+    else
+        hipLaunchKernelGGL((block_norm_backward_kernel<XT, VEC, 2>), dim3((unsigned)G),
+                           dim3(NB_THREADS), 0, s, a, d, W);
+}
+
 template <typename XT>
 static void launch_backward_x(const NormArgs &a, const NormGrads &d, int G, int W, hipStream_t s)
 {
     if (a.vec)
-        hipLaunchKernelGGL((block_norm_backward_kernel<XT, true>), dim3((unsigned)G),
-                           dim3(NB_THREADS), 0, s, a, d, W);
+        launch_backward_v<XT, true>(a, d, G, W, s);
     else
-        hipLaunchKernelGGL((block_norm_backward_kernel<XT, false>), dim3((unsigned)G),
-                           dim3(NB_THREADS), 0, s, a, d, W);
+        launch_backward_v<XT, false>(a, d, G, W, s);
 }
 
 int launch_block_norm_backward(const NormArgs &a, NormGrads d, int dtype, hipStream_t s)

@@ -71,10 +71,15 @@ static size_t plan_ws(const LinPlan &p, int M, int N)
     return p.splits == 1 ? 0 : (size_t)p.splits * M * ((N + 7) / 8 * 8) * sizeof(float);
 }
 
-size_t linear_ws(int M, int N, int K) { return plan_ws(linear_plan(M, N, K), M, N); }
+size_t linear_ws(int M, int N, int K)
+{
+    return M <= LIN_FEW_ROWS ? 0 : plan_ws(linear_plan(M, N, K), M, N);
+}
 
 int launch_linear(const LinArgs &a, void *ws, hipStream_t s)
 {
+    if (a.M <= LIN_FEW_ROWS && !a.a_ks && !a.b_ks)
+        return launch_linear_rows(a, s);
     return launch_linear_tile(a, linear_plan(a.M, a.N, a.K), ws, s);
 }
 
@@ -82,18 +87,19 @@ int launch_linear(const LinArgs &a, void *ws, hipStream_t s)
 
 // dz = dy act'(z) in fp16 (rows of ldd, zeros up to the next multiple of 8 behind
 // column N), where dz is not null, and its column sums over DZ_ROWS rows, from the
-// unrounded values, where parts is not null.  32 threads a row, eight columns each.
-constexpr int DZ_ROWS = 64, DZ_COLS = 256;
+// unrounded values, where parts is not null.  2^lt threads a row, eight columns each.
+constexpr int DZ_ROWS = 64;
 __global__ __launch_bounds__(256) void linear_dz_kernel(LinGrads g, f16 *dz, int64_t ldd,
-                                                        float *parts, bool vec_y, bool vec_z)
+                                                        float *parts, bool vec_y, bool vec_z, int lt)
 {
-    __shared__ float sums[8][DZ_COLS];
-    const int n = blockIdx.x * DZ_COLS + (threadIdx.x & 31) * 8;
+    __shared__ float sums[256 * 8];   // [row of threads][column]
+    const int c = (threadIdx.x & ((1 << lt) - 1)) * 8, rows = 256 >> lt;
+    const int n = (blockIdx.x << lt) * 8 + c;
     const int64_t m0 = (int64_t)blockIdx.y * DZ_ROWS;
     const int cols = g.N - n;
     float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 4
-    for (int i = threadIdx.x >> 5; i < DZ_ROWS; i += 8) {
+    for (int i = threadIdx.x >> lt; i < DZ_ROWS; i += rows) {
         const int64_t m = m0 + i;
         if (m >= g.M || cols <= 0)
             break;
@@ -114,17 +120,18 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(LinGrads g, f16 *dz, int
     }
     if (!parts)
         return;
+    const int width = 8 << lt;
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-        sums[threadIdx.x >> 5][(threadIdx.x & 31) * 8 + j] = s[j];
+        sums[(threadIdx.x >> lt) * width + c + j] = s[j];
     __syncthreads();
-    const int c = blockIdx.x * DZ_COLS + threadIdx.x;
-    if (c < g.N) {
-        float v = sums[0][threadIdx.x];
-#pragma unroll
-        for (int i = 1; i < 8; ++i)
-            v += sums[i][threadIdx.x];
-        parts[(int64_t)blockIdx.y * g.N + c] = v;
+    for (int i = threadIdx.x; i < width; i += 256) {
+        const int k = (blockIdx.x << lt) * 8 + i;
+        float v = sums[i];
+        for (int r = 1; r < rows; ++r)
+            v += sums[r * width + i];
+        if (k < g.N)
+            parts[(int64_t)blockIdx.y * g.N + k] = v;
     }
 }
 
@@ -167,7 +174,8 @@ static GradWs grad_ws(int M, int N, int K)
     GradWs w;
     w.parts = al256((int64_t)M * dz_ld(N) * 2);
     w.products = w.parts + al256((int64_t)((M + DZ_ROWS - 1) / DZ_ROWS) * N * 4);
-    w.total = w.products + (int64_t)std::max(linear_ws(M, K, N), linear_ws(N, K, M));
+    w.total = w.products + (int64_t)std::max(plan_ws(linear_plan(M, K, N), M, K),
+                                             plan_ws(linear_plan(N, K, M), N, K));
     return w;
 }
 
@@ -204,6 +212,9 @@ int launch_linear_backward(const LinGrads &g, void *ws, hipStream_t s)
     const int64_t ldd = own ? dz_ld(g.N) : g.lddy;
     if ((own && (g.dx || g.dw)) || g.dbias) {
         const int G = (g.M + DZ_ROWS - 1) / DZ_ROWS;
+        int lt = 0;   // threads of a row: up to 32
+        while (lt < 5 && (8 << lt) < g.N)
+            ++lt;
         auto rows16 = [](const void *p, int64_t ld) { return (uintptr_t)p % 16 == 0 && ld % 8 == 0; };
         for (int g0 = 0; g0 < G; g0 += 65535) {   // (rows of a grid)
             LinGrads part = g;
@@ -213,9 +224,9 @@ int launch_linear_backward(const LinGrads &g, void *ws, hipStream_t s)
             part.z += g.act != MOE_ACT_NONE ? m0 * g.ldz : 0;
             part.M = (int)std::min<int64_t>(g.M - m0, (int64_t)n * DZ_ROWS);
             f16 *to = own && (g.dx || g.dw) ? static_cast<f16 *>(ws) + m0 * ldd : nullptr;
-            hipLaunchKernelGGL(linear_dz_kernel, dim3((g.N + DZ_COLS - 1) / DZ_COLS, n), dim3(256), 0,
+            hipLaunchKernelGGL(linear_dz_kernel, dim3((g.N + (8 << lt) - 1) / (8 << lt), n), dim3(256), 0,
                                s, part, to, ldd, g.dbias ? parts + (int64_t)g0 * g.N : nullptr,
-                               rows16(g.dy, g.lddy), rows16(g.z, g.ldz));
+                               rows16(g.dy, g.lddy), rows16(g.z, g.ldz), lt);
             MOE_LAUNCH_CHECK("linear_dz_kernel");
         }
         if (g.dbias) {
