@@ -38,8 +38,8 @@ constexpr int64_t LIN_MOST_ITEMS = (1 << 22) - 8;   // a launch has fewer than 2
 constexpr int LIN_MOST_LD = 1 << 22;                // offsets inside a tile are 32 bits wide
 LinPlan linear_plan(int M, int N, int K);
 int launch_linear_tile(LinArgs, const LinPlan &, void *ws, hipStream_t);
-constexpr int LIN_FEW_ROWS = 16;
-int launch_linear_rows(const LinArgs &, hipStream_t);   // up to 16 rows, both operands along k
+constexpr int LIN_FEW_ROWS = 2;
+int launch_linear_rows(const LinArgs &, hipStream_t);   // so many rows, both operands along k
 
 // 1 / (1 + exp(-x)) by the hardware's exp2 and reciprocal (an ulp each).
 __device__ __forceinline__ float logistic(float x)

@@ -1,103 +1,112 @@
-// k_linear_rows.hip -- fp16 products of up to 16 rows (decode), out = residual +
+// k_linear_rows.hip -- fp16 products of one or two rows (decode), out = residual +
 // act(x w^T + bias): bound by the stream of the weights.
 //
-// A workgroup of eight waves forms 16 columns: each wave takes every eighth block of
-// 64 k and loads weights and tokens straight into the matrix instruction's layout, so
-// that everything it needs for four blocks is in flight at once and nothing waits at
-// a barrier before the waves' sums meet in LDS.  (Lanes then read 16 bytes of 16
-// different rows, which the L1 serves at a quarter of its rate: 34 GB/s a compute
-// unit, still more than its share of memory.  Staged through LDS by tiles of 16 x 32,
-// 8 groups of waves and three stages: 8.3 us for one row of 5632 x 2048 out of
-// memory; so 6.5.)
+// A wave takes a row of the weights and walks k with its 64 lanes side by side (1 KB
+// of the row an instruction, four in flight), each lane multiplying its eight k with
+// those of the tokens (v_dot2_f32_f16, fp32 sums); the lanes meet at the end.  No
+// LDS, no barrier.  Out of memory, in a captured run of calls: one row of 5632 x 2048
+// 6.0 us (3.8 TB/s), of 11264 x 2048 9.6 (4.8), two rows 6.7 and 10.8; for more rows
+// the tokens' loads and sums outweigh the stream (four 8.9, eight 11, sixteen 17),
+// and the 16-row tiles (8.4 for any of them) are faster.
 #include <algorithm>
+#include <type_traits>
 
 #include "k_linear.h"
 
 namespace moe {
 
-constexpr int LR_WAVES = 8, LR_UNROLL = 4;
-
-// Two steps of 32 k: block b of the lane's row, zeros behind K.
-struct LrPair {
-    half8_t v[2];
-};
-__device__ __forceinline__ LrPair lr_load(const f16 *row, int b, int K)
+template <typename T, int MT>
+__global__ __launch_bounds__(256) void linear_rows_kernel(LinArgs a)
 {
-    LrPair r;
+    constexpr int U = 4;   // chunks in flight
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    // (a wave past the last row repeats it and stores nothing: without a branch here
+    // the arguments arrive together)
+    const int n = min((int)blockIdx.x * 4 + wave, a.N - 1);
+    const f16 *w = a.b + n * a.ldb, *x[MT];
+    float acc[MT];
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-        const int k = b * 64 + s * 32 + ((threadIdx.x & 63) >> 4) * 8;
-        const half8_t v = ldg(reinterpret_cast<const half8_t *>(row + min(k, K - 8)));
-        r.v[s] = k < K ? v : half8_t{};
+    for (int m = 0; m < MT; ++m) {
+        x[m] = a.a + min(m, a.M - 1) * a.lda;
+        acc[m] = 0.0f;
     }
-    return r;
+    // U chunks of 512 k from k0 on; CUT: they may reach past K
+    auto chunks = [&](int k0, auto cut) {
+        constexpr bool CUT = decltype(cut)::value;
+        half8_t wv[U];
+        auto at = [&](int u) {
+            const int k = k0 + u * 512 + lane * 8;
+            return CUT ? min(k, a.K - 8) : k;
+        };
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            wv[u] = ldg(reinterpret_cast<const half8_t *>(w + at(u)));
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const bool in = !CUT || k0 + u * 512 + lane * 8 < a.K;
+            if (CUT)
+                wv[u] = in ? wv[u] : half8_t{};
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                half8_t xv = ldg(reinterpret_cast<const half8_t *>(x[m] + at(u)));
+                if (CUT)
+                    xv = in ? xv : half8_t{};
+#pragma unroll
+                for (int j = 0; j < 8; j += 2)
+                    acc[m] = dot2(half2_t{wv[u][j], wv[u][j + 1]}, half2_t{xv[j], xv[j + 1]},
+                                  acc[m]);
+            }
+        }
+    };
+    const bool stores = lane < a.M && (int)blockIdx.x * 4 + wave < a.N;
+    const float bias = a.bias ? a.bias[n] : 0.0f;
+    const float res = a.residual && stores
+                          ? (float)static_cast<const T *>(a.residual)[lane * a.ldr + n] : 0.0f;
+    int k0 = 0;
+    for (; k0 + U * 512 <= a.K; k0 += U * 512)
+        chunks(k0, std::false_type());
+    if (k0 < a.K)
+        chunks(k0, std::true_type());
+    float v = 0.0f;   // lane m: row m's
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+        const float s = wave_sum_f32(acc[m]);
+        v = lane == m ? s : v;
+    }
+    if (stores) {
+        v += bias;
+        if (a.z)
+            a.z[lane * a.ldz + n] = (f16)v;
+        static_cast<T *>(a.out)[lane * a.ldo + n] = (T)(act_value(v, a.act) + res);
+    }
 }
 
 template <typename T>
-__global__ __launch_bounds__(64 * LR_WAVES) void linear_rows_kernel(LinArgs a)
+static void launch_rows_t(LinArgs a, hipStream_t s)
 {
-    __shared__ float red[LR_WAVES][16][17];
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int col = lane & 15, q = lane >> 4;
-    const int nkb = (a.K + 63) / 64;
-    const f16 *x = a.a + min(col, a.M - 1) * a.lda;
-    for (int64_t n0 = (int64_t)blockIdx.x * 16; n0 < a.N; n0 += (int64_t)gridDim.x * 16) {
-        const f16 *w = a.b + min(n0 + col, (int64_t)a.N - 1) * a.ldb;
-        float4_t acc[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
-        int b = wave;
-        for (; b + (LR_UNROLL - 1) * LR_WAVES < nkb; b += LR_UNROLL * LR_WAVES) {
-            LrPair wv[LR_UNROLL], xv[LR_UNROLL];
-#pragma unroll
-            for (int u = 0; u < LR_UNROLL; ++u)
-                wv[u] = lr_load(w, b + u * LR_WAVES, a.K);
-#pragma unroll
-            for (int u = 0; u < LR_UNROLL; ++u)
-                xv[u] = lr_load(x, b + u * LR_WAVES, a.K);
-#pragma unroll
-            for (int u = 0; u < LR_UNROLL; ++u)
-#pragma unroll
-                for (int s = 0; s < 2; ++s)
-                    acc[s] = __builtin_amdgcn_mfma_f32_16x16x32_f16(wv[u].v[s], xv[u].v[s], acc[s],
-                                                                    0, 0, 0);
-        }
-        for (; b < nkb; b += LR_WAVES) {
-            const LrPair wv = lr_load(w, b, a.K), xv = lr_load(x, b, a.K);
-#pragma unroll
-            for (int s = 0; s < 2; ++s)
-                acc[s] = __builtin_amdgcn_mfma_f32_16x16x32_f16(wv.v[s], xv.v[s], acc[s], 0, 0, 0);
-        }
-        acc[0] += acc[1];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)   // a lane holds four columns of row `col`
-            red[wave][col][q * 4 + i] = acc[0][i];
-        __syncthreads();
-        const int m = threadIdx.x >> 4;
-        const int64_t n = n0 + (threadIdx.x & 15);
-        if (m < a.M && n < a.N) {   // the waves' sums in their order
-            float v = red[0][m][threadIdx.x & 15];
-#pragma unroll
-            for (int i = 1; i < LR_WAVES; ++i)
-                v += red[i][m][threadIdx.x & 15];
-            if (a.bias)
-                v += a.bias[n];
-            if (a.z)
-                a.z[m * a.ldz + n] = (f16)v;
-            v = act_value(v, a.act);
-            if (a.residual)
-                v += (float)static_cast<const T *>(a.residual)[m * a.ldr + n];
-            static_cast<T *>(a.out)[m * a.ldo + n] = (T)v;
-        }
-        __syncthreads();
+    // a launch has fewer than 2^32 threads: columns beyond that take another
+    const int most = 1 << 25;
+    for (int left = a.N; left > 0; left -= most) {
+        a.N = std::min(left, most);
+        const unsigned grid = (unsigned)((a.N + 3) / 4);
+        if (a.M == 1)
+            hipLaunchKernelGGL((linear_rows_kernel<T, 1>), dim3(grid), dim3(256), 0, s, a);
+        else
+            hipLaunchKernelGGL((linear_rows_kernel<T, 2>), dim3(grid), dim3(256), 0, s, a);
+        a.b += most * a.ldb;
+        a.bias = a.bias ? a.bias + most : nullptr;
+        a.z = a.z ? a.z + most : nullptr;
+        a.residual = a.residual ? static_cast<const T *>(a.residual) + most : nullptr;
+        a.out = static_cast<T *>(a.out) + most;
     }
 }
 
 int launch_linear_rows(const LinArgs &a, hipStream_t s)
 {
-    const unsigned grid = (unsigned)std::min<int64_t>(((int64_t)a.N + 15) / 16, 1 << 16);
     if (a.odt == MOE_DTYPE_F32)
-        hipLaunchKernelGGL(linear_rows_kernel<float>, dim3(grid), dim3(64 * LR_WAVES), 0, s, a);
+        launch_rows_t<float>(a, s);
     else
-        hipLaunchKernelGGL(linear_rows_kernel<f16>, dim3(grid), dim3(64 * LR_WAVES), 0, s, a);
+        launch_rows_t<f16>(a, s);
     MOE_LAUNCH_CHECK("linear_rows_kernel");
     return MOE_OK;
 }

@@ -90,6 +90,58 @@ class ScoreRouting:
     scale: float = 1.0
 
 
+@dataclass
+class BlockNorms:
+    """The norms, gate and residual scale around a layer's block (moe_block_norm):
+    h' = h + scale * gate * post(MoE(pre(h))).  Weights fp16 or fp32 [H] device (all
+    of one type), gate fp16 [H] device."""
+    pre_w: torch.Tensor | None = None
+    pre_b: torch.Tensor | None = None
+    post: bool = False                        # norm the block's output too
+    post_w: torch.Tensor | None = None
+    post_b: torch.Tensor | None = None
+    gate: torch.Tensor | None = None
+    scale: float = 1.0
+    kind: int = A.MOE_NORM_RMS
+    eps: float = 1e-5
+    unit_offset: bool = False                 # weights count as 1 + w
+
+    def __post_init__(self):
+        types = {w.dtype for w in (self.pre_w, self.pre_b, self.post_w, self.post_b)
+                 if w is not None}
+        if len(types) > 1 or types - {torch.float16, torch.float32}:
+            raise ValueError("norm weights must all be fp16 or all fp32")
+        self.w_dtype = A.MOE_DTYPE_F32 if torch.float32 in types else A.MOE_DTYPE_F16
+
+    @property
+    def form(self):
+        """What the norms of a stack have in common."""
+        return self.kind, self.eps, self.unit_offset
+
+
+def block_norm(y, h, end, start, out, n, stream=None):
+    """The end of one block and the start of the next on fp16 rows: out = h +
+    scale * gate * post(y) as `end` says (None: there is no block, y is None) and n =
+    pre(out) as `start` says (None: n is None).  One moe_block_norm call."""
+    norms = end if start is None else start
+    if end is not None and start is not None:
+        if end.form != start.form:
+            raise ValueError("the norms of a stack must have one kind, eps and unit_offset")
+        if end.w_dtype != start.w_dtype and (end.post_w is not None or end.post_b is not None):
+            raise ValueError("the norms of a stack must have weights of one type")
+    T, H = h.shape
+    flags = A.MOE_NORM_UNIT_OFFSET if norms.unit_offset else 0
+    gate = post_w = post_b = None
+    scale = 1.0
+    if end is not None:
+        gate, scale = end.gate, end.scale
+        if end.post:
+            post_w, post_b, flags = end.post_w, end.post_b, flags | A.MOE_NORM_POST
+    pre_w, pre_b = (None, None) if start is None else (start.pre_w, start.pre_b)
+    A.moe_block_norm(y, H, h, H, gate, 0, scale, post_w, post_b, pre_w, pre_b, A.MOE_DTYPE_F16,
+                     norms.w_dtype, norms.kind, flags, norms.eps, T, H, out, H, n, H, stream)
+
+
 def blob_table(blobs: torch.Tensor) -> torch.Tensor:
     """Device array of per-expert blob addresses for a [E, bytes] tensor."""
     E, nbytes = blobs.shape
@@ -117,18 +169,36 @@ class LayerBuffers:
     shared_ws: torch.Tensor | None
     out: torch.Tensor
     logits: torch.Tensor | None = None
+    router_ws: torch.Tensor | None = None
+    normed: torch.Tensor | None = None
+
+
+@dataclass
+class BalanceBuffers:
+    """What MoELayer.balance and router_backward write (MoELayer.balance_buffers)."""
+    logits: torch.Tensor       # fp32 [T, E]: the router's, where the routing keeps none
+    counts: torch.Tensor       # int32 [E]
+    mean_prob: torch.Tensor    # fp32 [E]
+    losses: torch.Tensor       # fp32 [2]: balance loss, z loss
+    dlogits: torch.Tensor      # fp16 [T, E]
+    d_router: torch.Tensor     # fp32 [E, H]
+    d_bias: torch.Tensor       # fp32 [E]
+    dx: torch.Tensor           # fp32 [T, H]
+    ws: torch.Tensor
 
 
 class MoELayer:
     """One MoE layer resident on the device: W4A16 experts (fmt MOE_FMT_SYM or
     MOE_FMT_ZP) or FP8 experts (MOE_FMT_FP8: blobs of load_experts_fp8, `group`
     unused), routed by softmax top-k or, with `routing`, by scores and groups.
-    Both routers take H in {256, 512, 1024, 2048}, also where the FP8 experts
-    would take more."""
+    The softmax router takes H in {256, 512, 1024, 2048}; with `routing` the
+    logits of other H come from moe_linear_f16 (any multiple of 8).  `norms`: the
+    norms around the block, which stack_forward applies."""
 
     def __init__(self, H, I, E, k, group, router, table, bias=None, shared=None,
                  renorm=False, device="cuda", shared_gate=None, overlap_shared=False,
-                 fmt=A.MOE_FMT_SYM, routing: ScoreRouting | None = None):
+                 fmt=A.MOE_FMT_SYM, routing: ScoreRouting | None = None,
+                 norms: BlockNorms | None = None):
         self.H, self.I, self.E, self.k, self.g = H, I, E, k, group
         self.fmt = fmt                  # blob format of the routed experts
         self.router = router            # fp16 [E, H] device
@@ -142,6 +212,7 @@ class MoELayer:
             raise ValueError("a shared-expert gate needs a shared expert")
         self.flags = A.MOE_RENORM if renorm else 0
         self.routing = routing
+        self.norms = norms
         self.device = device
 
     @property
@@ -173,10 +244,15 @@ class MoELayer:
         pws = max(A.moe_permute_workspace_bytes(T, self.k, self.E),
                   A.moe_route_permute_workspace_bytes(T, self.k, self.E),
                   A.moe_combine_route_permute_workspace_bytes(T, self.k, self.E))
-        logits = None
+        logits = router_ws = normed = None
         if self.routing is not None:
             pws = max(pws, A.moe_route_select_workspace_bytes(T, self.k, self.E))
             logits = torch.empty((T, self.E), dtype=torch.float32, device=d)
+            if not self.pinned_router:
+                n = A.moe_linear_f16_workspace_bytes(T, self.E, self.H)
+                router_ws = torch.empty(n, dtype=torch.uint8, device=d) if n else None
+        if self.norms is not None:
+            normed = torch.empty((T, self.H), dtype=torch.float16, device=d)
         n = T * self.k
         ytype = torch.float16 if ydt == A.MOE_DTYPE_F16 else torch.float32
         sh_out = sh_ws = None
@@ -200,15 +276,30 @@ class MoELayer:
             ffn_ws=torch.empty(ffn_ws, dtype=torch.uint8, device=d) if ffn_ws else None,
             shared_out=sh_out, shared_ws=sh_ws,
             out=torch.empty((T, self.H), dtype=torch.float16, device=d),
-            logits=logits,
+            logits=logits, router_ws=router_ws, normed=normed,
         )
+
+    @property
+    def pinned_router(self) -> bool:
+        """Whether the router's logits have the pinned summation order (moe_route's)."""
+        return self.H in (256, 512, 1024, 2048)
+
+    def router_logits(self, x, logits, ws=None, stream=None):
+        """The router's fp32 logits [T, E] of x."""
+        T = logits.shape[0]
+        if self.pinned_router:
+            A.moe_router_logits(x, self.router, self.bias, T, self.H, self.E, logits, stream)
+            return
+        A.moe_linear_f16(x, self.H, self.router, self.H, self.bias, A.MOE_ACT_NONE, None, 0, T,
+                         self.E, self.H, logits, A.MOE_DTYPE_F32, self.E, None, 0, ws,
+                         0 if ws is None else ws.numel(), stream)
 
     def route_permute(self, x, b: LayerBuffers, stream=None, fused=True):
         T = b.T
         nws = 0 if b.perm_ws is None else b.perm_ws.numel()
         if self.routing is not None:
             s = self.routing
-            A.moe_router_logits(x, self.router, self.bias, T, self.H, self.E, b.logits, stream)
+            self.router_logits(x, b.logits, b.router_ws, stream)
             A.moe_route_select_permute(
                 b.logits, A.MOE_DTYPE_F32, self.E, s.select_bias, T, self.E, self.k, s.score,
                 s.n_group, s.topk_group, self.flags | (A.MOE_GROUP_TOP2 if s.group_top2 else 0),
@@ -335,13 +426,49 @@ class MoELayer:
         if shared and self.shared is not None:
             self.shared_ffn(x, b, stream)
 
+    def balance_buffers(self, T) -> BalanceBuffers:
+        d = self.device
+        e = lambda *s, t=torch.float32: torch.empty(s, dtype=t, device=d)  # noqa: E731
+        n = max(A.moe_balance_loss_workspace_bytes(T, self.E),
+                A.moe_linear_f16_workspace_bytes(T, self.E, self.H),
+                A.moe_linear_f16_backward_workspace_bytes(T, self.E, self.H), 1)
+        return BalanceBuffers(
+            logits=e(T, self.E), counts=e(self.E, t=torch.int32), mean_prob=e(self.E), losses=e(2),
+            dlogits=e(T, self.E, t=torch.float16), d_router=e(self.E, self.H), d_bias=e(self.E),
+            dx=e(T, self.H), ws=e(n, t=torch.uint8))
+
+    def balance(self, x, b: LayerBuffers, g: BalanceBuffers, coef, z_coef=0.0, mask=None,
+                d_loss=None, stream=None):
+        """After route_permute of x into b: the routing's balance loss, z loss, counts
+        and mean probabilities over the tokens that `mask` (uint8 [T], zero: padding)
+        leaves, and the logits' gradient times d_loss (fp32 [1] device, such as a loss
+        scale: the gradient is fp16), into g.  Scores as the layer's router forms
+        them, without the selection's bias.  Returns g.losses."""
+        logits = b.logits
+        if logits is None:
+            logits = g.logits
+            self.router_logits(x, logits, g.ws, stream)
+        score = A.MOE_SCORE_SOFTMAX if self.routing is None else self.routing.score
+        A.moe_balance_loss(logits, A.MOE_DTYPE_F32, self.E, b.topk_idx, mask, b.T, self.E, self.k,
+                           score, coef, z_coef, g.counts, g.mean_prob, g.losses, d_loss,
+                           g.dlogits, A.MOE_DTYPE_F16, self.E, g.ws, g.ws.numel(), stream)
+        return g.losses
+
+    def router_backward(self, x, g: BalanceBuffers, stream=None):
+        """Gradients of the router's weights, of its bias and of x from g.dlogits (from
+        balance), into g.d_router, g.d_bias and g.dx: fp32, times balance's d_loss."""
+        A.moe_linear_f16_backward(g.dlogits, self.E, None, 0, A.MOE_ACT_NONE, x, self.H,
+                                  self.router, self.H, g.dlogits.shape[0], self.E, self.H, g.dx,
+                                  self.H, g.d_router, self.H, A.MOE_DTYPE_F32, g.d_bias, g.ws,
+                                  g.ws.numel(), stream)
+
     def pool_args(self, b: LayerBuffers, host_ids):
         """PoolLayerArgs for moe_pool_layer_forward with this layer's weights and
         b's buffers; x_f16 / residual_f16 / out_f16 are set per call."""
         if self.shared is not None:
             raise ValueError("pooled layers carry no shared expert")
-        if self.fp8 or self.routing is not None:
-            raise ValueError("pooled layers are W4A16 with the softmax router")
+        if self.fp8 or self.routing is not None or self.norms is not None:
+            raise ValueError("pooled layers are W4A16 with the softmax router, without norms")
         z = lambda t: 0 if t is None else t.data_ptr()
         a = A.PoolLayerArgs()
         a.w_router_f16, a.logit_bias = z(self.router), z(self.bias)
@@ -399,8 +526,15 @@ def stack_forward(layers, bufs, acts, stream=None, fuse=True, parts=None):
     buffer of moe_logit_partials_bytes()), a decode token's combine hands the
     next layer only its logit partials and that layer's expert launch routes
     from them (combine_partials_next + experts_routed), the first layer's
-    from moe_logit_partials of its input.  Every form gives the same bits."""
+    from moe_logit_partials of its input.  Every form gives the same bits.
+
+    Layers with `norms` (all of the stack or none; ValueError otherwise) compute
+    x_{l+1} = x_l + scale_l * gate_l * post_l(MoE_l(pre_l(x_l))): the end of a block
+    and the start of the next are one moe_block_norm call between a layer's combine
+    and the next layer's routing, which then are not fused."""
     L = len(layers)
+    if any(lay.norms is not None for lay in layers):
+        return _stack_normed(layers, bufs, acts, stream)
     # routed: this layer's routing is still to be formed from `parts`
     routed = fuse and parts is not None and layers[0].route_from_partials_ok(bufs[0])
     if routed:
@@ -428,4 +562,24 @@ def stack_forward(layers, bufs, acts, stream=None, fuse=True, parts=None):
                                        out=acts[l + 1], stream=stream, x=acts[l])
         else:
             lay.combine(bufs[l], residual=acts[l], out=acts[l + 1], stream=stream, x=acts[l])
+    return acts[L]
+
+
+def _stack_normed(layers, bufs, acts, stream):
+    if any(lay.norms is None for lay in layers):
+        raise ValueError("a stack's layers must all have norms, or none")
+    for a, b in zip(layers, layers[1:]):   # before anything is launched
+        if a.norms.form != b.norms.form or a.norms.w_dtype != b.norms.w_dtype:
+            raise ValueError("the norms of a stack must have one kind, eps, unit_offset and "
+                             "weights of one type")
+    L = len(layers)
+    block_norm(None, acts[0], None, layers[0].norms, None, bufs[0].normed, stream)
+    for l, lay in enumerate(layers):
+        b = bufs[l]
+        lay.route_permute(b.normed, b, stream)
+        lay.experts(b.normed, b, stream=stream)
+        lay.combine(b, stream=stream, x=b.normed)
+        last = l + 1 == L
+        block_norm(b.out, acts[l], lay.norms, None if last else layers[l + 1].norms, acts[l + 1],
+                   None if last else bufs[l + 1].normed, stream)
     return acts[L]

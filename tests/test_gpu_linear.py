@@ -128,6 +128,17 @@ def test_bad_values(act, m):
     assert (out[rest][:, 6] == (-60000.0 if act == "none" else 0.0)).all()
 
 
+@pytest.mark.parametrize("m,n,k", [(1, 64, 520), (2, 64, 512), (7, 64, 64), (70, 70, 64)])
+def test_subnormal_operands(m, n, k):
+    """fp16's subnormals count in full: 2^-20 times 2^10, k times."""
+    x = put(torch.full((m, k), 2.0 ** -20), 0)
+    w = put(torch.full((n, k), 1024.0), 0)
+    out = run(x, w, None, "none", None, m, n, k, "f32")
+    assert (out == k * 2.0 ** -10).all()
+    out = run(w, x, None, "none", None, n, m, k, "f32")
+    assert (out == k * 2.0 ** -10).all()
+
+
 def test_weights_past_the_end_are_not_read_into_results():
     """NaN all around the operands: rows, columns and padding that a tile covers but
     the product does not hold."""
