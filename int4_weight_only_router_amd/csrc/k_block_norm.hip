@@ -95,7 +95,10 @@ struct Cols {
         asm volatile("" : "+v"(k));
         return VEC ? (i * span + k) * 8 + j : (i * 8 + j) * span + k;
     }
-    __device__ __forceinline__ bool in(int i, int j) const { return fresh(i, VEC ? 0 : j) < H; }
+    __device__ __forceinline__ bool in(int i, int j) const
+    {
+        return (VEC ? col(i, 0) : fresh(i, j)) < H;
+    }
     template <typename T>
     __device__ __forceinline__ void load(const T *row, int i, float (&v)[8]) const
     {
@@ -331,11 +334,19 @@ int launch_block_norm(const NormArgs &a, int dtype, hipStream_t s)
 // groups of a workgroup meet in LDS at the end, the workgroups' sums in a second
 // launch, both in a fixed order.
 
+typedef float float2v_t __attribute__((ext_vector_type(2)));
 constexpr int NB_THREADS = 512, NB_WAVES = NB_THREADS / 64;
 enum { NB_GATE = 0, NB_POST_W, NB_POST_B, NB_PRE_W, NB_PRE_B, NB_SUMS };
 
+// LDS accesses while direct-to-LDS loads are in flight: without a restrict pointer the
+// compiler takes them to alias those loads and waits for them.
+template <typename T>
+__device__ __forceinline__ T lds_get(const T *__restrict__ p) { return *p; }
+template <typename T>
+__device__ __forceinline__ void lds_put(T *__restrict__ p, T v) { *p = v; }
+
 // Sums over a row's W waves (groups of W waves in a row) of a and, with `two`, of b.
-__device__ __forceinline__ void group_sum(float &a, float &b, bool two, int W, float2 *part,
+__device__ __forceinline__ void group_sum(float &a, float &b, bool two, int W, float2v_t *part,
                                           int &half)
 {
     a = wave_sum_f32(a);
@@ -344,26 +355,36 @@ __device__ __forceinline__ void group_sum(float &a, float &b, bool two, int W, f
     if (W == 1)
         return;
     const int wave = threadIdx.x >> 6;
-    float2 *p = part + half * NB_WAVES;
+    float2v_t *p = part + half * NB_WAVES;
     half ^= 1;
     if ((threadIdx.x & 63) == 0)
-        p[wave] = float2{a, b};
-    __syncthreads();
+        lds_put(p + wave, float2v_t{a, b});
+    lds_barrier();
     const int w0 = wave & ~(W - 1);
-    float2 v = p[w0];
+    float2v_t v = lds_get(p + w0);
     for (int i = 1; i < W; ++i) {
-        v.x += p[w0 + i].x;
-        v.y += p[w0 + i].y;
+        const float2v_t o = lds_get(p + w0 + i);
+        v.x += o.x;
+        v.y += o.y;
     }
     a = v.x;
     b = v.y;
+}
+
+// 1 / sqrt(v) by the hardware's reciprocal root (an ulp); values below its range are
+// scaled into it.
+__device__ __forceinline__ float recip_root(float v)
+{
+    const bool low = v < 0x1p-100f;
+    return __builtin_amdgcn_rsqf(low ? v * 0x1p100f : v) * (low ? 0x1p50f : 1.0f);
 }
 
 // v to its normalised values; returns the reciprocal root (0 for a turn past the
 // last row, whose zeros must stay zeros also where eps is 0).
 template <int NC, bool VEC>
 __device__ __forceinline__ float normalise_group(float (&v)[NC][8], const Cols<VEC> &c, bool live,
-                                                 const NormArgs &a, int W, float2 *part, int &half)
+                                                 const NormArgs &a, float per_h, int W,
+                                                 float2v_t *part, int &half)
 {
     float s = 0.0f, none = 0.0f;
     if (a.layer) {
@@ -373,7 +394,7 @@ __device__ __forceinline__ float normalise_group(float (&v)[NC][8], const Cols<V
             for (int j = 0; j < 8; ++j)
                 s += v[i][j];
         group_sum(s, none, false, W, part, half);
-        const float mean = s / (float)a.H;
+        const float mean = s * per_h;
 #pragma unroll
         for (int i = 0; i < NC; ++i)
 #pragma unroll
@@ -387,7 +408,7 @@ __device__ __forceinline__ float normalise_group(float (&v)[NC][8], const Cols<V
         for (int j = 0; j < 8; ++j)
             s = __builtin_fmaf(v[i][j], v[i][j], s);
     group_sum(s, none, false, W, part, half);
-    const float rho = live ? 1.0f / sqrtf(s / (float)a.H + a.eps) : 0.0f;
+    const float rho = live ? recip_root(__builtin_fmaf(s, per_h, a.eps)) : 0.0f;
 #pragma unroll
     for (int i = 0; i < NC; ++i)
 #pragma unroll
@@ -396,59 +417,99 @@ __device__ __forceinline__ float normalise_group(float (&v)[NC][8], const Cols<V
     return rho;
 }
 
-// g = dn * w to the gradient of the normed row; m its normalised values.
-template <int NC>
+// g = dn * w to the gradient of the normed row (zeros past its end); m its normalised
+// values.
+template <int NC, bool VEC>
 __device__ __forceinline__ void norm_input_grad(float (&g)[NC][8], const float (&m)[NC][8],
-                                                float rho, const NormArgs &a, int W, float2 *part,
-                                                int &half)
+                                                const Cols<VEC> &c, float rho, const NormArgs &a,
+                                                float per_h, int W, float2v_t *part, int &half)
 {
     float s = 0.0f, q = 0.0f;
 #pragma unroll
     for (int i = 0; i < NC; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < 8; ++j)
             q = __builtin_fmaf(g[i][j], m[i][j], q);
-            if (a.layer)
+    if (a.layer) {
+#pragma unroll
+        for (int i = 0; i < NC; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
                 s += g[i][j];
-        }
+    }
     group_sum(q, s, a.layer, W, part, half);
-    const float mean = a.layer ? s / (float)a.H : 0.0f, along = q / (float)a.H;
+    const float along = q * per_h * rho;
+    if (a.layer) {
+        const float mean = s * per_h;
+#pragma unroll
+        for (int i = 0; i < NC; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                g[i][j] = c.in(i, j) ? g[i][j] - mean : 0.0f;
+    }
 #pragma unroll
     for (int i = 0; i < NC; ++i)
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            g[i][j] = rho * __builtin_fmaf(-m[i][j], along, g[i][j] - mean);
+            g[i][j] = __builtin_fmaf(-m[i][j], along, rho * g[i][j]);
 }
 
-// v *= w (+ one)
-template <typename XT, int NC, bool VEC>
-__device__ __forceinline__ void times_weight(float (&v)[NC][8], const Cols<VEC> &c,
-                                             const NormArgs &a, const void *w)
+// v *= a weight; weight(i, t): its values in columns i
+template <int NC, typename F>
+__device__ __forceinline__ void times_weight(float (&v)[NC][8], F &&weight)
 {
-    const float one = a.offset ? 1.0f : 0.0f;
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
         float t[8];
-        c.template weights<XT>(w, a.w32, i, t);
+        weight(i, t);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            v[i][j] *= t[j] + one;
+            v[i][j] *= t[j];
     }
 }
 
+// Floats from one workgroup's sums to the next one's: a memory channel's run more than
+// they are, since H is often a multiple of all channels' and their reader's loads would
+// meet on one.
+__host__ __device__ constexpr int64_t nb_pitch(int n, int H) { return (int64_t)n * H + 64; }
+
+// LDS of a workgroup: the row sums' halves, the biases' sums (each thread's in places
+// of its own), and behind them, AHEAD, a piece a thread of every tensor's next row and
+// the weights; where those stood the groups meet at the end.
+constexpr int NB_PART = 2 * NB_WAVES * sizeof(float2v_t), NB_PIECES = NB_THREADS * 16;
+constexpr int NB_COLS = NB_THREADS * 8 * sizeof(float);
+static int norm_backward_lds(const NormArgs &a, const NormGrads &d, int W, bool ahead)
+{
+    const int nc = a.H > 512 * W ? 2 : 1;
+    const int biases = (d.sums[NB_POST_B] != nullptr) + (d.sums[NB_PRE_B] != nullptr);
+    const int rows = (a.y != nullptr) + (a.residual != nullptr) + (d.dn != nullptr) +
+                     (d.dout != nullptr) + (a.gate != nullptr);
+    const int weights = a.post + (a.post_b != nullptr) + 1;
+    const int next = ahead ? rows * NB_PIECES + weights * W * 512 * (int)sizeof(float) : 0;
+    return NB_PART + biases * nc * NB_COLS + std::max(next, NB_COLS);
+}
+
 // NC: eights of columns of a thread (W waves hold 512 W NC).  The sums of the biases'
-// gradients are seldom asked for; they stand in LDS, each thread's in places of its
-// own, and leave the registers to the others.
-template <typename XT, bool VEC, int NC>
+// gradients are seldom asked for; they stand in LDS and leave the registers to the
+// others.  AHEAD (16-bit rows): the next turn's rows travel to LDS while this turn is
+// computed, each thread's piece to its own place, so no barrier is needed for them;
+// the weights (ones for absent ones) stand in LDS too, as loads behind those would
+// wait for them.
+template <typename XT, bool VEC, int NC, bool AHEAD>
 __global__ __launch_bounds__(NB_THREADS, NC == 1 ? 4 : 2) void block_norm_backward_kernel(
     NormArgs a, NormGrads d, int W)
 {
-    __shared__ float2 part[2 * NB_WAVES];
-    __shared__ float cols[NB_THREADS * 8];
-    __shared__ float bias[2][NC * 8][NB_THREADS];   // post, pre
+    static_assert(!AHEAD || (VEC && NC == 1 && sizeof(XT) == 2), "a piece is 16 bytes");
+    extern __shared__ __align__(16) unsigned char nb_smem[];
+    float2v_t *part = reinterpret_cast<float2v_t *>(nb_smem);
+    typedef float Places[NB_THREADS];   // of one sum
+    Places *post_bias = reinterpret_cast<Places *>(nb_smem + NB_PART);
+    Places *pre_bias = post_bias + (d.sums[NB_POST_B] ? NC * 8 : 0);
+    float *cols = reinterpret_cast<float *>(pre_bias + (d.sums[NB_PRE_B] ? NC * 8 : 0));
     const int groups = NB_WAVES / W;   // rows at a time
     const int grp = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) / W;
     const int H = a.H;
+    const float per_h = 1.0f / (float)H;
     Cols<VEC> c = {(int)threadIdx.x - grp * W * 64, 64 * W, H};
     int half = 0;
     float sum[NB_SUMS][NC][8];
@@ -458,14 +519,89 @@ __global__ __launch_bounds__(NB_THREADS, NC == 1 ? 4 : 2) void block_norm_backwa
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             sum[NB_GATE][i][j] = sum[NB_POST_W][i][j] = sum[NB_PRE_W][i][j] = 0.0f;
-            bias[0][i * 8 + j][threadIdx.x] = bias[1][i * 8 + j][threadIdx.x] = 0.0f;
+            if (post_b)
+                post_bias[i * 8 + j][threadIdx.x] = 0.0f;
+            if (pre_b)
+                pre_bias[i * 8 + j][threadIdx.x] = 0.0f;
         }
+    // AHEAD: the pieces of y, residual, dn, dout and gate, then the weights
+    unsigned char *pieces = reinterpret_cast<unsigned char *>(cols);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    auto each_row = [&](int64_t t, auto &&f) {   // f(number of the tensor, its row)
+        auto row = [&](const void *p, int64_t ld) { return static_cast<const XT *>(p) + t * ld; };
+        int n = 0;
+        if (a.y)
+            f(n++, row(a.y, a.ldy));
+        if (a.residual)
+            f(n++, row(a.residual, a.ldr));
+        if (d.dn)
+            f(n++, row(d.dn, a.ldn));
+        if (d.dout)
+            f(n++, row(d.dout, a.ldo));
+        if (a.gate)
+            f(n++, row(a.gate, a.ldg));
+    };
+    auto send = [&](int64_t t0) {   // the rows of a turn on their way
+        const int at = c.t * 8 < H ? c.t * 8 : 0;
+        each_row(t0 + grp < a.T ? t0 + grp : 0, [&](int n, const XT *row) {
+            dma16(row + at, pieces + n * NB_PIECES + wave * 1024);
+        });
+        asm volatile("" ::: "memory");
+    };
+    const float *lds_w[3];   // post_w, post_b, pre_w
+    if constexpr (AHEAD) {
+        send((int64_t)blockIdx.x * groups);
+        int rows = 0;
+        each_row(0, [&](int, const XT *) { ++rows; });
+        float *to = reinterpret_cast<float *>(pieces + rows * NB_PIECES);
+        const void *from[3] = {a.post_w, a.post_b, a.pre_w};
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            lds_w[k] = to;
+            if (k == 1 ? !a.post_b : k == 0 && !a.post)
+                continue;
+            const float one = k != 1 && (a.offset || !from[k]) ? 1.0f : 0.0f;
+            for (int i = threadIdx.x; i < W * 512; i += NB_THREADS) {
+                float w = 0.0f;
+                if (from[k] && i < H)
+                    w = a.w32 ? static_cast<const float *>(from[k])[i]
+                              : (float)static_cast<const XT *>(from[k])[i];
+                to[i] = w + one;
+            }
+            to += W * 512;
+        }
+        wait_vm<0>();
+        __syncthreads();
+    }
+    auto weight = [&](int k, const void *w, int i, float (&v)[8]) {
+        if constexpr (AHEAD) {
+            const float4_t *p = reinterpret_cast<const float4_t *>(lds_w[k] + c.t * 8);
+            const float4_t lo = lds_get(p), hi = lds_get(p + 1);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                v[j] = lo[j];
+                v[4 + j] = hi[j];
+            }
+        } else {
+            c.template weights<XT>(w, a.w32, i, v);
+            const float one = a.offset && k != 1 ? 1.0f : 0.0f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[j] += one;
+        }
+    };
+    auto bump = [](float *p, float v) { lds_put(p, lds_get(p) + v); };
+    // stores of a turn, which stand behind the next turn's loads
+    const int stores = (d.dresidual != nullptr) +
+                       (a.y ? (d.dgate && a.ldg) + (d.dy != nullptr) : 0);
+    const int64_t turn = (int64_t)gridDim.x * groups;
     // every group takes as many turns (its sums meet at barriers); one past the
     // last row works on zeros and stores nothing
-    for (int64_t t0 = (int64_t)blockIdx.x * groups; t0 < a.T; t0 += (int64_t)gridDim.x * groups) {
+    for (int64_t t0 = (int64_t)blockIdx.x * groups; t0 < a.T; t0 += turn) {
         // (the weights are read again every turn, out of the caches: kept, they would
         // take the registers of the sums)
-        asm volatile("" : "+s"(a.post_w), "+s"(a.post_b), "+s"(a.pre_w));
+        if constexpr (!AHEAD)
+            asm volatile("" : "+s"(a.post_w), "+s"(a.post_b), "+s"(a.pre_w));
         const bool live = t0 + grp < a.T;
         const int64_t t = live ? t0 + grp : 0;
         c.H = live ? H : 0;   // columns that this turn may touch
@@ -476,37 +612,56 @@ __global__ __launch_bounds__(NB_THREADS, NC == 1 ? 4 : 2) void block_norm_backwa
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 u[i][j] = r[i][j] = dr[i][j] = g[i][j] = 0.0f;
-            if (a.y)
-                c.load(static_cast<const XT *>(a.y) + t * a.ldy, i, u[i]);
-            if (a.residual)
-                c.load(static_cast<const XT *>(a.residual) + t * a.ldr, i, r[i]);
-            if (d.dn)
-                c.load(static_cast<const XT *>(d.dn) + t * a.ldn, i, g[i]);
-            if (d.dout)
-                c.load(static_cast<const XT *>(d.dout) + t * a.ldo, i, dr[i]);
-            if (a.gate) {
-                c.load(static_cast<const XT *>(a.gate) + t * a.ldg, i, gate[i]);
-            } else {
+            if (!a.gate)
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
                     gate[i][j] = 1.0f;
-            }
+            auto load = [&](int n, const void *p, int64_t ld, float (&v)[8]) {
+                if constexpr (AHEAD) {
+                    typedef typename Vec8<XT>::type V;
+                    const uint4_t p = *reinterpret_cast<const uint4_t *>(
+                        pieces + n * NB_PIECES + threadIdx.x * 16);
+                    const V x = __builtin_bit_cast(V, p & (c.t * 8 < c.H ? ~0u : 0u));
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        v[j] = (float)x[j];
+                } else {
+                    c.load(static_cast<const XT *>(p) + t * ld, i, v);
+                }
+            };
+            int n = 0;
+            if (a.y)
+                load(n++, a.y, a.ldy, u[i]);
+            if (a.residual)
+                load(n++, a.residual, a.ldr, r[i]);
+            if (d.dn)
+                load(n++, d.dn, a.ldn, g[i]);
+            if (d.dout)
+                load(n++, d.dout, a.ldo, dr[i]);
+            if (a.gate)
+                load(n++, a.gate, a.ldg, gate[i]);
+        }
+        const bool more = t0 + turn < a.T;
+        if constexpr (AHEAD) {
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the pieces are read
+            if (more)
+                send(t0 + turn);
         }
         if (a.y) {
             if (a.post) {
-                post_rho = normalise_group(u, c, live, a, W, part, half);
+                post_rho = normalise_group(u, c, live, a, per_h, W, part, half);
 #pragma unroll
                 for (int i = 0; i < NC; ++i)
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
                         pm[i][j] = u[i][j];
-                if (a.post_w)
-                    times_weight<XT>(u, c, a, a.post_w);
+                if (AHEAD || a.post_w)
+                    times_weight(u, [&](int i, float (&v)[8]) { weight(0, a.post_w, i, v); });
                 if (a.post_b)
 #pragma unroll
                     for (int i = 0; i < NC; ++i) {
                         float w[8];
-                        c.template weights<XT>(a.post_b, a.w32, i, w);
+                        weight(1, a.post_b, i, w);
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
                             u[i][j] += w[j];
@@ -519,18 +674,18 @@ __global__ __launch_bounds__(NB_THREADS, NC == 1 ? 4 : 2) void block_norm_backwa
                     r[i][j] = __builtin_fmaf(a.scale, gate[i][j] * u[i][j], r[i][j]);
         }
         if (d.dn) {
-            const float rho = normalise_group(r, c, live, a, W, part, half);   // r: normalised from here
+            const float rho = normalise_group(r, c, live, a, per_h, W, part, half);   // r: normalised
 #pragma unroll
             for (int i = 0; i < NC; ++i)
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     sum[NB_PRE_W][i][j] = __builtin_fmaf(g[i][j], r[i][j], sum[NB_PRE_W][i][j]);
                     if (pre_b)
-                        bias[1][i * 8 + j][threadIdx.x] += g[i][j];
+                        bump(&pre_bias[i * 8 + j][threadIdx.x], g[i][j]);
                 }
-            if (a.pre_w)
-                times_weight<XT>(g, c, a, a.pre_w);
-            norm_input_grad(g, r, rho, a, W, part, half);
+            if (AHEAD || a.pre_w)
+                times_weight(g, [&](int i, float (&v)[8]) { weight(2, a.pre_w, i, v); });
+            norm_input_grad(g, r, c, rho, a, per_h, W, part, half);
 #pragma unroll
             for (int i = 0; i < NC; ++i)
 #pragma unroll
@@ -546,7 +701,7 @@ __global__ __launch_bounds__(NB_THREADS, NC == 1 ? 4 : 2) void block_norm_backwa
             for (int i = 0; i < NC; ++i) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    dr[i][j] = c.in(i, j) ? a.scale * dr[i][j] : 0.0f;   // of gate * u
+                    dr[i][j] *= a.scale;                                 // of gate * u
                     u[i][j] *= dr[i][j];                                 // the gate's
                     sum[NB_GATE][i][j] += u[i][j];
                     dr[i][j] *= gate[i][j];                              // of u
@@ -561,21 +716,33 @@ __global__ __launch_bounds__(NB_THREADS, NC == 1 ? 4 : 2) void block_norm_backwa
                     for (int j = 0; j < 8; ++j) {
                         sum[NB_POST_W][i][j] = __builtin_fmaf(dr[i][j], pm[i][j], sum[NB_POST_W][i][j]);
                         if (post_b)
-                            bias[0][i * 8 + j][threadIdx.x] += dr[i][j];
+                            bump(&post_bias[i * 8 + j][threadIdx.x], dr[i][j]);
                     }
-                if (a.post_w)
-                    times_weight<XT>(dr, c, a, a.post_w);
-                norm_input_grad(dr, pm, post_rho, a, W, part, half);
+                if (AHEAD || a.post_w)
+                    times_weight(dr, [&](int i, float (&v)[8]) { weight(0, a.post_w, i, v); });
+                norm_input_grad(dr, pm, c, post_rho, a, per_h, W, part, half);
             }
             if (d.dy)
 #pragma unroll
                 for (int i = 0; i < NC; ++i)
                     c.store(static_cast<XT *>(d.dy) + t * a.ldy, i, dr[i]);
         }
+        if (AHEAD && more) {   // the next rows are there, if not yet this turn's stores
+            if (stores == 3)
+                wait_vm<3>();
+            else if (stores == 2)
+                wait_vm<2>();
+            else if (stores == 1)
+                wait_vm<1>();
+            else
+                wait_vm<0>();
+        }
     }
+    if constexpr (AHEAD)
+        __syncthreads();   // the weights' places are the groups' from here
     // the groups' sums, in the order of the groups
     c.H = H;
-    float *to = d.parts + (int64_t)blockIdx.x * d.nsums * H;
+    float *to = d.parts + blockIdx.x * nb_pitch(d.nsums, H);
 #pragma unroll
     for (int k = 0; k < NB_SUMS; ++k) {
         if (!d.sums[k])
@@ -585,7 +752,7 @@ __global__ __launch_bounds__(NB_THREADS, NC == 1 ? 4 : 2) void block_norm_backwa
             if (k == NB_POST_B || k == NB_PRE_B)
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    sum[k][i][j] = bias[k == NB_PRE_B][i * 8 + j][threadIdx.x];
+                    sum[k][i][j] = (k == NB_PRE_B ? pre_bias : post_bias)[i * 8 + j][threadIdx.x];
             if (groups > 1) {
                 __syncthreads();
 #pragma unroll
@@ -613,12 +780,12 @@ __global__ __launch_bounds__(1024) void norm_sums_kernel(const float *__restrict
     __shared__ float s[16][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int col = blockIdx.x * 64 + lane;
-    const int64_t n = to.n;
+    const int64_t pitch = nb_pitch(to.n, H);
     float v = 0.0f;
     if (col < H) {
-#pragma unroll 8
+#pragma unroll 16
         for (int g = wave; g < G; g += 16)
-            v += parts[(g * n + blockIdx.y) * H + col];
+            v += parts[g * pitch + blockIdx.y * (int64_t)H + col];
     }
     s[wave][lane] = v;
     __syncthreads();
@@ -649,27 +816,34 @@ static int norm_backward_grid(int T, int H)
 
 size_t block_norm_backward_ws(int T, int H)
 {
-    return (size_t)norm_backward_grid(T, H) * NB_SUMS * H * sizeof(float);
+    return (size_t)(norm_backward_grid(T, H) * nb_pitch(NB_SUMS, H)) * sizeof(float);
 }
 
-template <typename XT, bool VEC>
-static void launch_backward_v(const NormArgs &a, const NormGrads &d, int G, int W, hipStream_t s)
+template <typename XT, bool VEC, int NC, bool AHEAD>
+static int launch_backward_t(const NormArgs &a, const NormGrads &d, int G, int W, hipStream_t s)
 {
-    if (a.H <= 512 * NB_WAVES)
-        hipLaunchKernelGGL((block_norm_backward_kernel<XT, VEC, 1>), dim3((unsigned)G),
-                           dim3(NB_THREADS), 0, s, a, d, W);
-    else
-        hipLaunchKernelGGL((block_norm_backward_kernel<XT, VEC, 2>), dim3((unsigned)G),
-                           dim3(NB_THREADS), 0, s, a, d, W);
+    static LdsLimit limit;
+    const int rc = limit.raise((const void *)block_norm_backward_kernel<XT, VEC, NC, AHEAD>,
+                               160 * 1024);
+    if (rc)
+        return rc;
+    hipLaunchKernelGGL((block_norm_backward_kernel<XT, VEC, NC, AHEAD>), dim3((unsigned)G),
+                       dim3(NB_THREADS), norm_backward_lds(a, d, W, AHEAD), s, a, d, W);
+    MOE_LAUNCH_CHECK("block_norm_backward_kernel");
+    return MOE_OK;
 }
 
 template <typename XT>
-static void launch_backward_x(const NormArgs &a, const NormGrads &d, int G, int W, hipStream_t s)
+static int launch_backward_x(const NormArgs &a, const NormGrads &d, int G, int W, hipStream_t s)
 {
-    if (a.vec)
-        launch_backward_v<XT, true>(a, d, G, W, s);
-    else
-        launch_backward_v<XT, false>(a, d, G, W, s);
+    if (a.H > 512 * NB_WAVES)
+        return a.vec ? launch_backward_t<XT, true, 2, false>(a, d, G, W, s)
+                     : launch_backward_t<XT, false, 2, false>(a, d, G, W, s);
+    if constexpr (sizeof(XT) == 2)   // ahead where LDS holds two workgroups all the same
+        if (a.vec && norm_backward_lds(a, d, W, true) <= 80 * 1024)
+            return launch_backward_t<XT, true, 1, true>(a, d, G, W, s);
+    return a.vec ? launch_backward_t<XT, true, 1, false>(a, d, G, W, s)
+                 : launch_backward_t<XT, false, 1, false>(a, d, G, W, s);
 }
 
 int launch_block_norm_backward(const NormArgs &a, NormGrads d, int dtype, hipStream_t s)
@@ -681,13 +855,11 @@ int launch_block_norm_backward(const NormArgs &a, NormGrads d, int dtype, hipStr
             to.p[to.n++] = d.sums[k];
     d.nsums = to.n;
     if (a.T > 0) {
-        if (dtype == MOE_DTYPE_F32)
-            launch_backward_x<float>(a, d, G, W, s);
-        else if (dtype == MOE_DTYPE_F16)
-            launch_backward_x<f16>(a, d, G, W, s);
-        else
-            launch_backward_x<bf16>(a, d, G, W, s);
-        MOE_LAUNCH_CHECK("block_norm_backward_kernel");
+        const int rc = dtype == MOE_DTYPE_F32   ? launch_backward_x<float>(a, d, G, W, s)
+                       : dtype == MOE_DTYPE_F16 ? launch_backward_x<f16>(a, d, G, W, s)
+                                                : launch_backward_x<bf16>(a, d, G, W, s);
+        if (rc)
+            return rc;
     }
     if (to.n) {   // without tokens: zeros
         hipLaunchKernelGGL(norm_sums_kernel, dim3((a.H + 63) / 64, to.n), dim3(1024), 0, s,
