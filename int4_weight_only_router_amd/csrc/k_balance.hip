@@ -29,6 +29,11 @@ constexpr int BL_THREADS = 1024, BL_WAVES = BL_THREADS / 64;
 // Waves of a workgroup of rows: half as many where a lane holds 16 experts (registers).
 template <int NE>
 constexpr int bl_waves() { return NE > 8 ? 8 : 16; }
+constexpr int BL_ONE_ROWS = 64;   // tokens up to which one workgroup does it all
+// Choices up to which every workgroup counts all of them for itself (eight a thread:
+// 1 us, against 2 to 3 of another launch), else in up to 16 workgroups of a launch.
+constexpr int BL_SELF = 8192;
+constexpr int BL_COUNT_GROUPS = 16, BL_GROUPS = 256;
 constexpr float BL_FAR = -60.0f;   // exp(-60) and its sums are far inside fp32's range
 
 template <typename T>
@@ -50,12 +55,23 @@ __device__ __forceinline__ float exp_neg(float x)
     return __builtin_fmaf(e * r, 0.69314718055994531f, e);
 }
 
+template <int CTRL>
+__device__ __forceinline__ float dpp_max_step(float v)
+{
+    return fmaxf(v, __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(
+                                                  0, __builtin_bit_cast(int, v), CTRL, 0xF, 0xF, false)));
+}
 __device__ __forceinline__ float wave_max(float v)
 {
-#pragma unroll
-    for (int o = 32; o; o >>= 1)
-        v = fmaxf(v, __shfl_xor(v, o, 64));
-    return v;
+    v = dpp_max_step<0xB1>(v);    // the steps of wave_sum_f32
+    v = dpp_max_step<0x4E>(v);
+    v = dpp_max_step<0x141>(v);
+    v = dpp_max_step<0x140>(v);
+    const int i = __builtin_bit_cast(int, v);
+    auto row = [&](int lane) {
+        return __builtin_bit_cast(float, __builtin_amdgcn_readlane(i, lane));
+    };
+    return fmaxf(fmaxf(row(0), row(16)), fmaxf(row(32), row(48)));
 }
 
 // Choices and unmasked tokens of the tokens t0 <= t < t1 into hist (LDS [E]) and
@@ -87,7 +103,7 @@ __device__ __forceinline__ int block_sum(int v, int *s)
         v += __shfl_xor(v, o, 64);
     if ((threadIdx.x & 63) == 0)
         s[threadIdx.x >> 6] = v;
-    __syncthreads();
+    lds_barrier();
     v = 0;
 #pragma unroll
     for (int i = 0; i < WAVES; ++i)
@@ -95,18 +111,31 @@ __device__ __forceinline__ int block_sum(int v, int *s)
     return v;
 }
 
-// A row's logits in registers: lane l holds experts l, l + 64, ... (-inf past E and
-// for a masked token).
+// A row's logits and its token's mask in registers, as they were loaded: lane l holds
+// experts l, l + 64, ...  (Nothing here waits for them.)
 template <typename LT, int NE>
-__device__ __forceinline__ void load_row(const BalanceArgs &a, int64_t t, bool on, float (&l)[NE])
-{
-    const LT *row = static_cast<const LT *>(a.logits) + t * a.ld;
+struct Row {
+    LT v[NE];
+    uint8_t mask;
+    __device__ __forceinline__ void load(const BalanceArgs &a, int64_t t)
+    {
+        const LT *row = static_cast<const LT *>(a.logits) + t * a.ld;
+        mask = a.mask ? a.mask[t] : 1;
 #pragma unroll
-    for (int i = 0; i < NE; ++i) {
-        const int e = (threadIdx.x & 63) + 64 * i;
-        l[i] = on && e < a.E ? logit_value<LT>(row[e]) : -__builtin_inff();
+        for (int i = 0; i < NE; ++i)
+            v[i] = row[min((int)(threadIdx.x & 63) + 64 * i, a.E - 1)];
     }
-}
+    // the logits (-inf past E and for a masked token), and whether the token counts
+    __device__ __forceinline__ bool values(const BalanceArgs &a, float (&l)[NE]) const
+    {
+        const bool on = __builtin_amdgcn_readfirstlane(mask);   // (the same for the whole wave)
+#pragma unroll
+        for (int i = 0; i < NE; ++i)
+            l[i] = on && (int)(threadIdx.x & 63) + 64 * i < a.E ? logit_value<LT>(v[i])
+                                                              : -__builtin_inff();
+        return on;
+    }
+};
 
 // The row: its p added to psum[], its share of the balance loss and lse^2 added up,
 // its gradient written.
@@ -163,15 +192,14 @@ __device__ __forceinline__ void balance_row(const BalanceArgs &a, int64_t t, boo
         for (int i = 0; i < NE; ++i)
             p[i] = soft[i];
     }
-    float dot = 0.0f, share = 0.0f;
+    float dot = 0.0f;
 #pragma unroll
     for (int i = 0; i < NE; ++i) {
         psum[i] += p[i];
         dot = __builtin_fmaf(p[i], d[i], dot);
-        share += p[i];
     }
     dot = wave_sum_f32(dot);
-    loss += dot + wave_sum_f32(share);   // sum p (d + 1)
+    loss += some ? dot + 1.0f : 0.0f;   // sum p (d + 1)
     zsum = __builtin_fmaf(lse, lse, zsum);
     if (!a.dlogits)
         return;
@@ -200,19 +228,31 @@ template <int NE>
 __device__ __forceinline__ void deviations(const int *hist, int E, float (&d)[NE])
 {
     const int lane = threadIdx.x & 63;
-    int64_t total = 0;   // every wave for itself
-#pragma unroll
-    for (int i = 0; i < NE; ++i)
-        total += lane + 64 * i < E ? hist[lane + 64 * i] : 0;
-#pragma unroll
-    for (int o = 32; o; o >>= 1)
-        total += __shfl_xor(total, o, 64);
-    const double inv = 1.0 / (double)(total > 0 ? total : 1);
+    int c[NE];
+    int64_t own = 0;
 #pragma unroll
     for (int i = 0; i < NE; ++i) {
-        const int e = lane + 64 * i;
-        d[i] = e < E ? (float)((double)(hist[e] * (int64_t)E - total) * inv) : 0.0f;
+        c[i] = hist[lane + 64 * i];   // (zeros past E)
+        own += c[i];
     }
+    // the total, every wave for itself: 16 bits and the rest are sums of whole numbers
+    // below 2^24, so exact in fp32
+    const int64_t total = (int64_t)wave_sum_f32((float)(own & 0xffff)) +
+                          ((int64_t)wave_sum_f32((float)(own >> 16)) << 16);
+    const float inv = 1.0f / (float)(total > 0 ? total : 1);
+    if (total * E < 1LL << 31) {
+#pragma unroll
+        for (int i = 0; i < NE; ++i)
+            d[i] = (float)(c[i] * E - (int)total) * inv;
+    } else {
+#pragma unroll
+        for (int i = 0; i < NE; ++i)
+            d[i] = (float)(c[i] * (int64_t)E - total) * inv;
+    }
+#pragma unroll
+    for (int i = 0; i < NE; ++i)
+        if (lane + 64 * i >= E)
+            d[i] = 0.0f;
 }
 
 // Partial counts of the tokens dealt out over the workgroups: [G][E] and the
@@ -246,38 +286,39 @@ __global__ __launch_bounds__(64 * bl_waves<NE>()) void balance_rows_kernel(Balan
     __shared__ float cols[HALF][64 * NE + 2];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     int64_t t = (int64_t)blockIdx.x * WAVES + wave;
-    // the first row's logits are on their way while the choices are counted
-    auto counted = [&](int64_t t) {   // (the same for the whole wave)
-        return !a.mask || __builtin_amdgcn_readfirstlane(a.mask[t]);
-    };
-    bool on = t < a.T && counted(t);
-    float l[NE];
-    load_row<LT, NE>(a, t < a.T ? t : 0, on, l);
+    // the first row is on its way while the choices are counted
+    Row<LT, NE> row;
+    row.load(a, t < a.T ? t : 0);
     const float up = a.dlogits && a.d_loss ? *a.d_loss : 1.0f;
     int64_t n = a.T;
     const bool self = ONE || !a.count_groups;   // counts for itself
     if (self) {
         for (int e = threadIdx.x; e < 64 * NE; e += THREADS)
             hist[e] = a.idx || e >= a.E ? 0 : a.counts[e];
-        __syncthreads();
+        lds_barrier();
         if (a.idx || a.mask)
             n = block_sum<WAVES>(count_tokens<THREADS>(a, 0, a.T, hist), s);
     } else {
+        const int mine = a.mask && threadIdx.x < a.count_groups ? a.part_n[threadIdx.x] : 0;
         for (int e = threadIdx.x; e < 64 * NE; e += THREADS) {
             int c = 0;
             if (e < a.E && !a.idx) {
                 c = a.counts[e];
             } else if (e < a.E) {
-#pragma unroll 16
-                for (int g = 0; g < a.count_groups; ++g)
-                    c += a.part_counts[(int64_t)g * a.E + e];
+                int part[BL_COUNT_GROUPS];   // (all on their way together)
+#pragma unroll
+                for (int g = 0; g < BL_COUNT_GROUPS; ++g)
+                    part[g] = a.part_counts[(int64_t)min(g, a.count_groups - 1) * a.E + e];
+#pragma unroll
+                for (int g = 0; g < BL_COUNT_GROUPS; ++g)
+                    c += g < a.count_groups ? part[g] : 0;
             }
             hist[e] = c;
         }
         if (a.mask)
-            n = block_sum<WAVES>(threadIdx.x < a.count_groups ? a.part_n[threadIdx.x] : 0, s);
+            n = block_sum<WAVES>(mine, s);
     }
-    __syncthreads();
+    lds_barrier();
     float d[NE], psum[NE], loss = 0.0f, zsum = 0.0f;
     deviations<NE>(hist, a.E, d);
 #pragma unroll
@@ -286,13 +327,14 @@ __global__ __launch_bounds__(64 * bl_waves<NE>()) void balance_rows_kernel(Balan
     const float per_n = n > 0 ? 1.0f / (float)n : 0.0f;
     const int64_t step = (int64_t)gridDim.x * WAVES;
     while (t < a.T) {
-        if (on || a.dlogits)
-            balance_row<NE>(a, t, on, l, d, per_n, up, psum, loss, zsum);
+        float l[NE];
+        const bool on = row.values(a, l);
+        const int64_t t0 = t;
         t += step;
-        if (t < a.T) {
-            on = counted(t);
-            load_row<LT, NE>(a, t, on, l);
-        }
+        if (t < a.T)
+            row.load(a, t);
+        if (on || a.dlogits)
+            balance_row<NE>(a, t0, on, l, d, per_n, up, psum, loss, zsum);
     }
     // the waves' sums: the upper half's onto the lower half's, then those
     if (wave >= HALF) {
@@ -304,7 +346,7 @@ __global__ __launch_bounds__(64 * bl_waves<NE>()) void balance_rows_kernel(Balan
             cols[wave - HALF][64 * NE + 1] = zsum;
         }
     }
-    __syncthreads();
+    lds_barrier();
     if (wave < HALF) {
 #pragma unroll
         for (int i = 0; i < NE; ++i)
@@ -314,7 +356,7 @@ __global__ __launch_bounds__(64 * bl_waves<NE>()) void balance_rows_kernel(Balan
             cols[wave][64 * NE + 1] += zsum;
         }
     }
-    __syncthreads();
+    lds_barrier();
     for (int e = threadIdx.x; e < a.E + 2; e += THREADS) {
         const int at = e < a.E ? e : 64 * NE + e - a.E;
         float v = cols[0][at];
@@ -390,12 +432,6 @@ __global__ void balance_none_kernel(BalanceArgs a)
     if (a.losses && threadIdx.x < 2)
         a.losses[threadIdx.x] = 0.0f;
 }
-
-constexpr int BL_ONE_ROWS = 64;   // tokens up to which one workgroup does it all
-// Choices up to which every workgroup counts all of them for itself (eight a thread:
-// 1 us, against 2 to 3 of another launch), else in up to 16 workgroups of a launch.
-constexpr int BL_SELF = 8192;
-constexpr int BL_COUNT_GROUPS = 16, BL_GROUPS = 256;
 
 // 0: counted by every workgroup.  (Given counts count as few: k = 1.)
 static int count_groups(int T, int k)
