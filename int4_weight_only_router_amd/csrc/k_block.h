@@ -16,52 +16,42 @@ struct Vec8<f16> { typedef half8_t type; };
 template <>
 struct Vec8<bf16> { typedef bf168_t type; };
 
-// Columns c .. c + 7 of a row; zeros from column `cols` on.  vec: rows are
+// C values in a row, up to 16 bytes an instruction.
+template <typename T, int C>
+struct alignas(C * sizeof(T) < 16 ? C * sizeof(T) : 16) Piece {
+    T v[C];
+};
+
+// Columns c .. c + C - 1 of a row; zeros from column `cols` on.  vec: rows are
 // 16-byte aligned.
-template <typename T>
-__device__ __forceinline__ void load8(const T *row, int c, int cols, bool vec, float (&v)[8])
+template <typename T, int C>
+__device__ __forceinline__ void load_piece(const T *row, int c, int cols, bool vec, float (&v)[C])
 {
-    if (vec && c + 8 <= cols) {
-        if constexpr (sizeof(T) == 4) {
-            const float4_t a = *reinterpret_cast<const float4_t *>(row + c);
-            const float4_t b = *reinterpret_cast<const float4_t *>(row + c + 4);
+    if (vec && c + C <= cols) {
+        const Piece<T, C> a = *reinterpret_cast<const Piece<T, C> *>(row + c);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                v[i] = a[i];
-                v[4 + i] = b[i];
-            }
-        } else {
-            const typename Vec8<T>::type a =
-                *reinterpret_cast<const typename Vec8<T>::type *>(row + c);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                v[i] = (float)a[i];
-        }
+        for (int i = 0; i < C; ++i)
+            v[i] = (float)a.v[i];
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < C; ++i)
             v[i] = c + i < cols ? (float)row[c + i] : 0.0f;
     }
 }
 
 // The same columns, rounded once; those from `cols` on are left as they were.
-template <typename T>
-__device__ __forceinline__ void store8(T *row, int c, int cols, bool vec, const float (&v)[8])
+template <typename T, int C>
+__device__ __forceinline__ void store_piece(T *row, int c, int cols, bool vec, const float (&v)[C])
 {
-    if (vec && c + 8 <= cols) {
-        if constexpr (sizeof(T) == 4) {
-            *reinterpret_cast<float4_t *>(row + c) = float4_t{v[0], v[1], v[2], v[3]};
-            *reinterpret_cast<float4_t *>(row + c + 4) = float4_t{v[4], v[5], v[6], v[7]};
-        } else {
-            typename Vec8<T>::type a;
+    if (vec && c + C <= cols) {
+        Piece<T, C> a;
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                a[i] = (T)v[i];
-            *reinterpret_cast<typename Vec8<T>::type *>(row + c) = a;
-        }
+        for (int i = 0; i < C; ++i)
+            a.v[i] = (T)v[i];
+        *reinterpret_cast<Piece<T, C> *>(row + c) = a;
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < C; ++i)
             if (c + i < cols)
                 row[c + i] = (T)v[i];
     }

@@ -86,34 +86,33 @@ int launch_linear(const LinArgs &a, void *ws, hipStream_t s)
 // ------------------------------------------------------------------ gradients
 
 // dz = dy act'(z) in fp16 (rows of ldd, zeros up to the next multiple of 8 behind
-// column N), where dz is not null, and its column sums over DZ_ROWS rows, from the
+// column N), where dz is not null, and its column sums over `tall` rows, from the
 // unrounded values, where parts is not null.  2^lt threads a row, eight columns each.
-constexpr int DZ_ROWS = 64;
 __global__ __launch_bounds__(256) void linear_dz_kernel(LinGrads g, f16 *dz, int64_t ldd,
-                                                        float *parts, bool vec_y, bool vec_z, int lt)
+                                                        float *parts, bool vec_y, bool vec_z, int lt, int tall)
 {
     __shared__ float sums[256 * 8];   // [row of threads][column]
     const int c = (threadIdx.x & ((1 << lt) - 1)) * 8, rows = 256 >> lt;
     const int n = (blockIdx.x << lt) * 8 + c;
-    const int64_t m0 = (int64_t)blockIdx.y * DZ_ROWS;
+    const int64_t m0 = (int64_t)blockIdx.y * tall;
     const int cols = g.N - n;
     float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 4
-    for (int i = threadIdx.x >> lt; i < DZ_ROWS; i += rows) {
+    for (int i = threadIdx.x >> lt; i < tall; i += rows) {
         const int64_t m = m0 + i;
         if (m >= g.M || cols <= 0)
             break;
         float v[8];
-        load8<f16>(g.dy + m * g.lddy + n, 0, cols, vec_y, v);
+        load_piece<f16, 8>(g.dy + m * g.lddy + n, 0, cols, vec_y, v);
         if (g.act != MOE_ACT_NONE) {
             float z[8];
-            load8<f16>(g.z + m * g.ldz + n, 0, cols, vec_z, z);
+            load_piece<f16, 8>(g.z + m * g.ldz + n, 0, cols, vec_z, z);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 v[j] = j < cols ? v[j] * act_grad(z[j], g.act) : 0.0f;
         }
         if (dz)
-            store8<f16>(dz + m * ldd + n, 0, 8, true, v);
+            store_piece<f16, 8>(dz + m * ldd + n, 0, 8, true, v);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             s[j] += v[j];
@@ -135,24 +134,10 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(LinGrads g, f16 *dz, int
     }
 }
 
-// Column sums of the partial sums [G][N]: 16 at a time, joined in a fixed order.
-__global__ __launch_bounds__(1024) void linear_dbias_kernel(const float *parts, int G, int N,
-                                                            float *out)
+__global__ __launch_bounds__(1024) void linear_dbias_kernel(LinColumns c)
 {
     __shared__ float s[16][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int n = blockIdx.x * 64 + lane;
-    float v = 0.0f;
-    if (n < N)
-        for (int g = wave; g < G; g += 16)
-            v += parts[(int64_t)g * N + n];
-    s[wave][lane] = v;
-    __syncthreads();
-    if (wave == 0 && n < N) {
-        for (int i = 1; i < 16; ++i)
-            v += s[i][lane];
-        out[n] = v;
-    }
+    column_sums<16>(c, blockIdx.x, s);
 }
 
 // Zeros into rows of `cols` elements, ld apart.
@@ -163,6 +148,14 @@ __global__ __launch_bounds__(256) void zero_rows_kernel(T *p, int64_t ld, int64_
         p[i / cols * ld + i % cols] = (T)0.0f;
 }
 
+// Rows of a workgroup of linear_dz_kernel: in up to 512 parts, whose sums one more
+// workgroup for 64 columns adds up.
+static int dz_rows(int M)
+{
+    const int64_t each = ((int64_t)M + 511) / 512;
+    return (int)(each < 64 ? 64 : each);
+}
+static int dz_groups(int M) { return (M + dz_rows(M) - 1) / dz_rows(M); }
 static int64_t dz_ld(int N) { return ((int64_t)N + 7) / 8 * 8; }
 
 // Workspace: dz, the column sums, and what the products need.
@@ -173,7 +166,7 @@ static GradWs grad_ws(int M, int N, int K)
 {
     GradWs w;
     w.parts = al256((int64_t)M * dz_ld(N) * 2);
-    w.products = w.parts + al256((int64_t)((M + DZ_ROWS - 1) / DZ_ROWS) * N * 4);
+    w.products = w.parts + al256((int64_t)dz_groups(M) * N * 4);
     w.total = w.products + (int64_t)std::max(plan_ws(linear_plan(M, K, N), M, K),
                                              plan_ws(linear_plan(N, K, M), N, K));
     return w;
@@ -185,8 +178,8 @@ int launch_linear_backward(const LinGrads &g, void *ws, hipStream_t s)
 {
     if (g.M == 0) {
         if (g.dbias) {
-            hipLaunchKernelGGL(linear_dbias_kernel, dim3((g.N + 63) / 64), dim3(1024), 0, s, nullptr,
-                               0, g.N, g.dbias);
+            hipLaunchKernelGGL(linear_dbias_kernel, dim3((g.N + 63) / 64), dim3(1024), 0, s,
+                               LinColumns{nullptr, 0, g.N, g.dbias});
             MOE_LAUNCH_CHECK("linear_dbias_kernel");
         }
         if (g.dw) {
@@ -210,28 +203,22 @@ int launch_linear_backward(const LinGrads &g, void *ws, hipStream_t s)
                      g.lddy > LIN_MOST_LD;
     const f16 *dz = own ? static_cast<const f16 *>(ws) : g.dy;
     const int64_t ldd = own ? dz_ld(g.N) : g.lddy;
+    const int G = dz_groups(g.M);
+    const LinColumns cols = {parts, G, g.N, g.dbias};
+    // the bias gradient's last step joins the launch that joins dw's parts, if there is one
+    const bool late = g.dw && linear_plan(g.N, g.K, g.M).splits > 1;
     if ((own && (g.dx || g.dw)) || g.dbias) {
-        const int G = (g.M + DZ_ROWS - 1) / DZ_ROWS;
         int lt = 0;   // threads of a row: up to 32
         while (lt < 5 && (8 << lt) < g.N)
             ++lt;
         auto rows16 = [](const void *p, int64_t ld) { return (uintptr_t)p % 16 == 0 && ld % 8 == 0; };
-        for (int g0 = 0; g0 < G; g0 += 65535) {   // (rows of a grid)
-            LinGrads part = g;
-            const int64_t m0 = (int64_t)g0 * DZ_ROWS;
-            const int n = std::min(G - g0, 65535);
-            part.dy += m0 * g.lddy;
-            part.z += g.act != MOE_ACT_NONE ? m0 * g.ldz : 0;
-            part.M = (int)std::min<int64_t>(g.M - m0, (int64_t)n * DZ_ROWS);
-            f16 *to = own && (g.dx || g.dw) ? static_cast<f16 *>(ws) + m0 * ldd : nullptr;
-            hipLaunchKernelGGL(linear_dz_kernel, dim3((g.N + (8 << lt) - 1) / (8 << lt), n), dim3(256), 0,
-                               s, part, to, ldd, g.dbias ? parts + (int64_t)g0 * g.N : nullptr,
-                               rows16(g.dy, g.lddy), rows16(g.z, g.ldz), lt);
-            MOE_LAUNCH_CHECK("linear_dz_kernel");
-        }
-        if (g.dbias) {
-            hipLaunchKernelGGL(linear_dbias_kernel, dim3((g.N + 63) / 64), dim3(1024), 0, s, parts, G,
-                               g.N, g.dbias);
+        hipLaunchKernelGGL(linear_dz_kernel, dim3((g.N + (8 << lt) - 1) / (8 << lt), G), dim3(256), 0,
+                           s, g, own && (g.dx || g.dw) ? static_cast<f16 *>(ws) : nullptr, ldd,
+                           g.dbias ? parts : nullptr, rows16(g.dy, g.lddy), rows16(g.z, g.ldz), lt,
+                           dz_rows(g.M));
+        MOE_LAUNCH_CHECK("linear_dz_kernel");
+        if (g.dbias && !late) {
+            hipLaunchKernelGGL(linear_dbias_kernel, dim3((g.N + 63) / 64), dim3(1024), 0, s, cols);
             MOE_LAUNCH_CHECK("linear_dbias_kernel");
         }
     }
@@ -261,6 +248,8 @@ int launch_linear_backward(const LinGrads &g, void *ws, hipStream_t s)
         a.K = g.M;
         a.out = g.dw;
         a.ldo = g.lddw;
+        if (g.dbias && late)
+            a.columns = cols;
         return launch_linear(a, base + w.products, s);
     }
     return MOE_OK;

@@ -181,33 +181,33 @@ __device__ __forceinline__ bool lt_item(const LinArgs &a, int MT, int NT, LtItem
 template <typename F>
 using LtAcc = float4_t[F::FM][F::FN];
 
-// Columns n .. n + 7 of row m with the whole epilogue (v: their sums).
-template <typename T>
-__device__ __forceinline__ void lt_finish(const LinArgs &a, T *out, int64_t m, int n, float (&v)[8],
+// Columns n .. n + C - 1 of row m with the whole epilogue (v: their sums).
+template <typename T, int C>
+__device__ __forceinline__ void lt_finish(const LinArgs &a, T *out, int64_t m, int n, float (&v)[C],
                                           bool vec)
 {
     const int cols = a.N - n;
     if (a.bias) {
-        float b[8];
-        load8<float>(a.bias + n, 0, cols, (uintptr_t)a.bias % 16 == 0, b);
+        float b[C];
+        load_piece<float, C>(a.bias + n, 0, cols, (uintptr_t)a.bias % 16 == 0, b);
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
+        for (int j = 0; j < C; ++j)
             v[j] += b[j];
     }
     if (a.z)
-        store8<f16>(a.z + m * a.ldz + n, 0, cols, vec, v);
+        store_piece<f16, C>(a.z + m * a.ldz + n, 0, cols, vec, v);
     if (a.act != MOE_ACT_NONE)
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
+        for (int j = 0; j < C; ++j)
             v[j] = act_value(v[j], a.act);
     if (a.residual) {
-        float r[8];
-        load8<T>(static_cast<const T *>(a.residual) + m * a.ldr + n, 0, cols, vec, r);
+        float r[C];
+        load_piece<T, C>(static_cast<const T *>(a.residual) + m * a.ldr + n, 0, cols, vec, r);
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
+        for (int j = 0; j < C; ++j)
             v[j] += r[j];
     }
-    store8<T>(out + m * a.ldo + n, 0, cols, vec, v);
+    store_piece<T, C>(out + m * a.ldo + n, 0, cols, vec, v);
 }
 
 // Whether every tensor of the epilogue can be read and written 16 bytes at a time.
@@ -221,17 +221,19 @@ __device__ __forceinline__ bool lt_vec(const LinArgs &a, const T *out)
            (!a.z || rows16(a.z, a.ldz, 2));
 }
 
-// The sums through LDS, where the groups' meet in their order, and out in whole lines.
+// The sums through LDS, where the groups' meet in their order, and out in whole lines,
+// C columns a thread: as many as keep the workgroup's threads at work.
 template <typename F, typename T>
 __device__ __forceinline__ void lt_epilogue(const LinArgs &a, LtAcc<F> &acc, const LtItem &it,
                                             int m0, int n0, int wm, int nw, unsigned char *smem)
 {
-    constexpr int NP = F::BN / 8, LROWS = F::BM / F::PASS, MH = F::FM / F::PASS;
+    constexpr int LROWS = F::BM / F::PASS, MH = F::FM / F::PASS;
+    constexpr int C = std::min(8, std::max(2, LROWS * F::BN / F::THREADS)), NP = F::BN / C;
     const int lane = threadIdx.x & 63, grp = threadIdx.x / F::NTH;
     T *out = static_cast<T *>(a.out) + it.split * a.split_stride;
     const bool vec = lt_vec<T>(a, out);
     auto at = [&](int g, int r, int c) {
-        return reinterpret_cast<float4_t *>(smem + (g * LROWS + r) * F::ROW + c * 4);
+        return reinterpret_cast<float *>(smem + (g * LROWS + r) * F::ROW + c * 4);
     };
 #pragma unroll
     for (int h = 0; h < F::PASS; ++h) {
@@ -240,22 +242,25 @@ __device__ __forceinline__ void lt_epilogue(const LinArgs &a, LtAcc<F> &acc, con
         for (int m = 0; m < MH; ++m)
 #pragma unroll
             for (int n = 0; n < F::FN; ++n)   // a lane holds four columns of a row
-                *at(grp, wm * F::HR + m * 16 + (lane & 15), nw + n * 16 + (lane >> 4) * 4) =
-                    acc[h * MH + m][n];
+                *reinterpret_cast<float4_t *>(at(grp, wm * F::HR + m * 16 + (lane & 15),
+                                                 nw + n * 16 + (lane >> 4) * 4)) = acc[h * MH + m][n];
         __syncthreads();
         for (int i = threadIdx.x; i < LROWS * NP; i += F::THREADS) {
-            const int r = i / NP, c = i % NP * 8;
+            const int r = i / NP, c = i % NP * C;
             const int64_t m = m0 + r / F::HR * (F::BM / F::WM) + h * F::HR + r % F::HR;
             if (m >= a.M || n0 + c >= a.N)
                 continue;
-            float4_t lo = *at(0, r, c), hi = *at(0, r, c + 4);
+            float v[C];
+            load_piece<float, C>(at(0, r, c), 0, C, true, v);
 #pragma unroll
             for (int g = 1; g < F::KG; ++g) {
-                lo += *at(g, r, c);
-                hi += *at(g, r, c + 4);
+                float o[C];
+                load_piece<float, C>(at(g, r, c), 0, C, true, o);
+#pragma unroll
+                for (int j = 0; j < C; ++j)
+                    v[j] += o[j];
             }
-            float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-            lt_finish<T>(a, out, m, n0 + c, v, vec);
+            lt_finish<T, C>(a, out, m, n0 + c, v, vec);
         }
     }
 }
@@ -304,6 +309,43 @@ __device__ __forceinline__ void lt_epilogue_f16(const LinArgs &a, LtAcc<F> &acc,
             for (int j = 0; j < 8; ++j)
                 if (j < cols)
                     to[j] = v[j];
+        }
+    }
+}
+
+// The same for fp32 results: straight from the registers, four columns of a row a lane,
+// so that a store of the wave fills 64 bytes of each of 16 rows.
+template <typename F>
+__device__ __forceinline__ void lt_epilogue_f32(const LinArgs &a, LtAcc<F> &acc, float *out, int m0,
+                                                int n0, int mw, int nw)
+{
+    const int lane = threadIdx.x & 63;
+    const bool vec = (uintptr_t)out % 16 == 0 && a.ldo % 4 == 0;
+#pragma unroll
+    for (int n = 0; n < F::FN; ++n) {
+        const int c = n0 + nw + n * 16 + (lane >> 4) * 4, cols = a.N - c;
+        if (cols <= 0)
+            continue;
+        float4_t b = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (a.bias)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                b[j] = a.bias[min(c + j, a.N - 1)];
+#pragma unroll
+        for (int m = 0; m < F::FM; ++m) {
+            const int64_t r = m0 + mw + m * 16 + (lane & 15);
+            if (r >= a.M)
+                continue;
+            float *to = out + r * a.ldo + c;
+            const float4_t v = acc[m][n] + b;
+            if (vec && cols >= 4) {
+                *reinterpret_cast<float4_t *>(to) = v;
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (j < cols)
+                        to[j] = v[j];
+            }
         }
     }
 }
@@ -485,8 +527,12 @@ __global__ __launch_bounds__(F::THREADS, 2) void linear_tile_kernel(LinArgs a)
             clear(kb + 1);
         }
     if constexpr (F::KG == 1)
-        if (a.odt == MOE_DTYPE_F16 && a.act == MOE_ACT_NONE && !a.residual && !a.z) {
-            lt_epilogue_f16<F>(a, acc, m0, n0, mw, nw, smem);
+        if (a.act == MOE_ACT_NONE && !a.residual && !a.z) {
+            if (a.odt == MOE_DTYPE_F16)
+                lt_epilogue_f16<F>(a, acc, m0, n0, mw, nw, smem);
+            else
+                lt_epilogue_f32<F>(a, acc, static_cast<float *>(a.out) + it.split * a.split_stride,
+                                   m0, n0, mw, nw);
             return;
         }
     if (a.odt == MOE_DTYPE_F32)
@@ -495,26 +541,33 @@ __global__ __launch_bounds__(F::THREADS, 2) void linear_tile_kernel(LinArgs a)
         lt_epilogue<F, f16>(a, acc, it, m0, n0, wave / F::WN, nw, smem);
 }
 
-// Sums of the splits' partial products, in their order, with the epilogue.
+// Sums of the splits' partial products, in their order, with the epilogue; behind the
+// `blocks` workgroups for them those of a.columns.
 template <typename T>
-__global__ __launch_bounds__(256) void linear_join_kernel(LinArgs a, const float *parts, int64_t ld)
+__global__ __launch_bounds__(256) void linear_join_kernel(LinArgs a, const float *parts, int64_t ld,
+                                                          int blocks)
 {
+    __shared__ float s[16][64];
+    if ((int)blockIdx.x >= blocks) {
+        column_sums<4>(a.columns, blockIdx.x - blocks, s);
+        return;
+    }
     const int64_t chunks = (a.N + 7) / 8, total = chunks * a.M;
     const bool vec = lt_vec<T>(a, static_cast<const T *>(a.out));
-    for (int64_t i = blockIdx.x * 256LL + threadIdx.x; i < total; i += gridDim.x * 256LL) {
+    for (int64_t i = blockIdx.x * 256LL + threadIdx.x; i < total; i += blocks * 256LL) {
         const int64_t m = i / chunks;
         const int n = (int)(i - m * chunks) * 8;
         const float *p = parts + m * ld + n;
         float v[8];
-        load8<float>(p, 0, 8, true, v);
+        load_piece<float, 8>(p, 0, 8, true, v);
         for (int s = 1; s < a.splits; ++s) {
             float w[8];
-            load8<float>(p + s * a.split_stride, 0, 8, true, w);
+            load_piece<float, 8>(p + s * a.split_stride, 0, 8, true, w);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 v[j] += w[j];
         }
-        lt_finish<T>(a, static_cast<T *>(a.out), m, n, v, vec);
+        lt_finish<T, 8>(a, static_cast<T *>(a.out), m, n, v, vec);
     }
 }
 
@@ -585,13 +638,14 @@ int launch_linear_tile(LinArgs a, const LinPlan &p, void *ws, hipStream_t s)
         return rc;
     a.split_stride = part.split_stride;
     const int64_t total = (int64_t)((a.N + 7) / 8) * a.M;
-    const unsigned grid = (unsigned)std::min<int64_t>((total + 255) / 256, 4096);
+    const int blocks = (int)std::min<int64_t>((total + 255) / 256, 4096);
+    const dim3 grid(blocks + (a.columns.out ? (a.columns.n + 63) / 64 : 0));
     if (a.odt == MOE_DTYPE_F32)
-        hipLaunchKernelGGL(linear_join_kernel<float>, dim3(grid), dim3(256), 0, s, a,
-                           static_cast<const float *>(ws), part.ldo);
+        hipLaunchKernelGGL(linear_join_kernel<float>, grid, dim3(256), 0, s, a,
+                           static_cast<const float *>(ws), part.ldo, blocks);
     else
-        hipLaunchKernelGGL(linear_join_kernel<f16>, dim3(grid), dim3(256), 0, s, a,
-                           static_cast<const float *>(ws), part.ldo);
+        hipLaunchKernelGGL(linear_join_kernel<f16>, grid, dim3(256), 0, s, a,
+                           static_cast<const float *>(ws), part.ldo, blocks);
     MOE_LAUNCH_CHECK("linear_join_kernel");
     return MOE_OK;
 }
