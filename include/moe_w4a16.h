@@ -721,8 +721,10 @@ int moe_block_norm_backward(const void *dout, int64_t ldo, const void *dn, int64
  *   ws        device scratch of moe_linear_f16_workspace_bytes(M, N, K) bytes (may
  *             be 0), 16-byte aligned, no initialisation; calls that share it must
  *             not overlap
- * The order of the fp32 additions depends on M, N and K only.  K, ldx and ldw
- * multiples of 8 (MOE_EUNSUPPORTED).  M = 0: no-op.
+ * The order of the fp32 additions depends on M, N and K only.  K, ldx and ldw are
+ * multiples of 8, rows lie at most 2^22 elements apart, M and N are at most 2^30 and
+ * small enough for a launch (tiles of 256 x 256: fewer than 2^22); else
+ * MOE_EUNSUPPORTED.  M = 0: no-op.
  */
 size_t moe_linear_f16_workspace_bytes(int M, int N, int K);
 int moe_linear_f16(const void *x_f16, int64_t ldx, const void *w_f16, int64_t ldw,
@@ -744,7 +746,9 @@ int moe_linear_f16(const void *x_f16, int64_t ldx, const void *w_f16, int64_t ld
  *           bytes, as above
  * dz is rounded to fp16 for the products (exact with MOE_ACT_NONE), so out_dtype
  * F32 is for MOE_ACT_NONE only (MOE_EUNSUPPORTED).  Gradients that would leave
- * fp16's range belong scaled by the caller.  M = 0: dw and dbias are set to zero.
+ * fp16's range belong scaled by the caller.  Limits as above, for the products of
+ * dx and dw, whichever is asked for, and N at most 2^22 (MOE_EUNSUPPORTED); lddy, ldz,
+ * lddx and lddw are free.  M = 0: dw and dbias are set to zero.
  */
 size_t moe_linear_f16_backward_workspace_bytes(int M, int N, int K);
 int moe_linear_f16_backward(const void *dy_f16, int64_t lddy, const void *z_f16, int64_t ldz,

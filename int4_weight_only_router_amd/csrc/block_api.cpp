@@ -325,7 +325,7 @@ int moe_linear_f16_backward(const void *dy_f16, int64_t lddy, const void *z_f16,
                          "%s: K, ldx and ldw must be multiples of 8 (K=%d ldx=%lld ldw=%lld)", fn, K,
                          (long long)ldx, (long long)ldw);
     if ((dw && ldx > LIN_MOST_LD) || (dx && ldw > LIN_MOST_LD) || N > LIN_MOST_LD ||
-        (M > 0 && ((dx && !linear_fits(M, K, N)) || (dw && !linear_fits(N, K, M)))))
+        (M > 0 && (!linear_fits(M, K, N) || !linear_fits(N, K, M))))
         return set_error(MOE_EUNSUPPORTED,
                          "%s: rows of at most %d elements and %lld tiles (M=%d N=%d K=%d ldx=%lld "
                          "ldw=%lld)", fn, LIN_MOST_LD, (long long)LIN_MOST_ITEMS, M, N, K,

@@ -36,7 +36,7 @@ LinPlan linear_plan(int M, int N, int K)
 {
     LinPlan best{};
     double least = 1e300;
-    const int nkb = (K + 63) / 64;
+    const int nkb = (int)(((int64_t)K + 63) / 64);
     for (int f = 0; f < 8; ++f) {
         const LinForm &o = FORMS[f];
         if (f == 0 && M > 16)

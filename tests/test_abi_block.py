@@ -118,6 +118,26 @@ def test_linear_backward_refusals(kw, code):
     assert _code(M.moe_linear_f16_backward, *_linear_backward(**kw), stream=0) == code
 
 
+@pytest.mark.parametrize("kw", [
+    dict(ldx=(1 << 22) + 8), dict(ldw=(1 << 22) + 8), dict(m=(1 << 30) + 1), dict(n=(1 << 30) + 1, ldo=1 << 31,
+                                                                              ldr=1 << 31, ldz=1 << 31),
+    dict(m=1 << 29, n=1 << 20, ldo=1 << 20, ldr=1 << 20, ldz=1 << 20)])
+def test_linear_limits(kw):
+    assert _code(M.moe_linear_f16, *_linear(**kw), stream=0) == EUNSUP
+
+
+@pytest.mark.parametrize("kw", [
+    dict(ldx=(1 << 22) + 8), dict(ldw=(1 << 22) + 8), dict(m=(1 << 30) + 1),
+    dict(m=(1 << 30) + 1, dx=None, dw=None), dict(m=(1 << 31) - 1, dx=None),
+    dict(n=(1 << 22) + 1, lddy=1 << 23, ldz=1 << 23),
+    dict(m=1 << 29, k=1 << 20, ldx=1 << 20, ldw=1 << 20, lddx=1 << 20, lddw=1 << 20, dx=None)])
+def test_linear_backward_limits(kw):
+    assert _code(M.moe_linear_f16_backward, *_linear_backward(**kw), stream=0) == EUNSUP
+    a = dict(dict(m=4, n=32, k=64), **kw)
+    if max(a.get("ldx", 0), a.get("ldw", 0), a["n"]) <= 1 << 22:   # (strides are not in the query)
+        assert M.moe_linear_f16_backward_workspace_bytes(a["m"], a["n"], a["k"]) == 0
+
+
 def _balance(l=P, dt=F32, ld=64, idx=P, mask=P, T=100, E=64, k=8, score=0, c=0.1, z=0.1, counts=P,
              mean=P, losses=P, up=P, dl=P, gt=F32, ldd=64, ws=P, ws_bytes=1 << 30):
     return (l, dt, ld, idx, mask, T, E, k, score, c, z, counts, mean, losses, up, dl, gt, ldd, ws,
