@@ -112,6 +112,31 @@ def test_against_definition(T, E, k, masked, zcoef, dtype, gtype, pad, score):
     assert all(torch.equal(a, b) for a, b in zip(given, got))
 
 
+@pytest.mark.parametrize("T,E,k,score", [(5000, 100, 4, "softmax"), (2500, 1000, 3, "sigmoid")])
+def test_more_rows_than_waves(T, E, k, score):
+    say("balance %dx%d %s" % (T, E, score))
+    l, idx, mask = draw(T, E, k, 0.3, 1.1, "f16", pad=1)
+    up = torch.tensor([64.0], device=DEV)
+    got = call(l.to(DEV), idx.to(DEV), mask.to(DEV), k, score, 0.01, 0.01, up, "f16", pad=2, E=E)
+    torch.cuda.synchronize()
+    check(got, l, idx, mask, E, k, score, 0.01, 0.01, 64.0, "f16")
+
+
+def test_given_counts_of_any_size():
+    """Counts beyond what T tokens choose, such as those of many steps together."""
+    l, idx, _ = draw(70, 60, 2)
+    c = torch.randint(0, 1 << 30, (60,), generator=torch.Generator().manual_seed(2)).int()
+    got = call(l.to(DEV), None, None, 2, "softmax", 0.5, 0.0, counts=c.to(DEV))
+    f = c.double() / c.double().sum()
+    p = torch.softmax(l.double(), 1)
+    want = 0.5 * 60 * float((f * p.mean(0)).sum())
+    assert abs(float(got[2][0]) - want) <= 4 * STEPS * U * want
+    d = 60 * f - 1.0
+    grad = 0.5 / 70 * p * (d - (p * d).sum(1, keepdim=True))
+    size = 0.5 / 70 * p * (d.abs() + (p * d).abs().sum(1, keepdim=True))
+    assert ((got[3].cpu().double() - grad).abs() <= 2 * (STEPS + 16) * U * size).all()
+
+
 @pytest.mark.parametrize("score", list(SCORES))
 @pytest.mark.parametrize("T", [9, 130])
 def test_masked_experts_and_far_logits(T, score):

@@ -372,6 +372,62 @@ def test_backward_in_place():
         assert torch.equal(a, w)
 
 
+# more rows than the workgroups' first turn takes: later turns' rows travel while the
+# turn before is computed
+TURNS = [case(T=3100, H=2048, bias=False, pad=8, gate="column"),
+         case(T=2100, H=2000, bias=False, pad=0, gate="token", dtype="bf16", w_dtype="f32"),
+         case(T=8300, H=264, bias=False, pad=8, gate="none", offset=True),
+         case(T=1100, H=4096, bias=False, pad=0, post=False, gate="none", kind="layer"),
+         case(T=2100, H=1024, bias=True, pad=0, gate="none", kind="layer", residual=False)]
+
+
+@pytest.mark.parametrize("c", TURNS, ids=name)
+def test_backward_turns(c):
+    say("block norm backward, turns: " + name(c))
+    d, v = inputs(c)
+    (dout, dn), (vo, vn) = grads_in(c, d)
+    out = gradient_buffers(c, d)
+    backward(c, d, dout, dn, out)
+    torch.cuda.synchronize()
+    want, size = reference(c, v, vo, vn), sizes(c, v, vo, vn)
+    for n, got in zip(NAMES, out):
+        if got is None:
+            continue
+        w, summed = want[n], got.dim() == 1
+        rest = None if summed else got[:, c["H"]:]
+        got = got if summed else got[:, :c["H"]]
+        check(got.reshape(w.shape), w, size[n].reshape(w.shape),
+              SUM_STEPS if summed else BACKWARD_STEPS,
+              torch.float32 if summed else R.TYPES[c["dtype"]][0], n)
+        assert rest is None or (rest == -3.0).all()
+    # any number of stores behind the loads, and over the rows that came in: the same bits
+    for keep in ([], [0], [1], [2], [0, 1], [0, 2], [1, 2]):
+        some = [torch.full_like(t, -3.0) if t is not None and (i in keep or i > 2) else None
+                for i, t in enumerate(out)]
+        backward(c, d, dout, dn, some)
+        for a, b in zip(some, out):
+            assert a is None or torch.equal(a, b)
+    rows_in = [dn, dout][:2 if out[1] is not None else 1]
+    over = rows_in + [None] * (7 - len(rows_in))
+    backward(c, d, dout, dn, over)
+    for a, b in zip(rows_in, out):
+        assert torch.equal(a[:, :c["H"]], b[:, :c["H"]])
+
+
+def test_backward_bad_rows_stay_alone():
+    c = case(T=2100, H=2048, bias=False, pad=0, gate="token")
+    d, _ = inputs(c)
+    (dout, dn), _ = grads_in(c, d)
+    good = [0, 1, 3, 1023, 1024, 1025, 2047, 2048, 2049, 2099]
+    bad = [2, 1022, 1026, 2050]
+    out, again = gradient_buffers(c, d), gradient_buffers(c, d)
+    backward(c, d, dout, dn, out)
+    d["y"][bad, 5], dn[bad, 9] = float("nan"), float("inf")
+    backward(c, d, dout, dn, again)
+    for a, b in zip(out[:3], again[:3]):
+        assert torch.equal(a[good], b[good]) and not torch.isfinite(b[bad]).all()
+
+
 def test_backward_no_rows():
     c = case(T=0, H=72)
     out = [None, None, torch.full((72,), 5.0, device=DEV)] + \

@@ -167,9 +167,31 @@ def backward(dy, z, act, x, w, m, n, k, dtype, dx, dw, db, stream=None, ws=None)
     return ws
 
 
+@pytest.mark.parametrize("dtype", ["f16", "f32"])
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("m,n,k", [(70, 131, 72), (1000, 1003, 264), (2050, 2054, 136),
+                                   (4100, 5009, 72), (4100, 8200, 64)])
+def test_sums_and_bias_only(m, n, k, bias, dtype):
+    """Nothing but the sums and a bias leaves: of every tile's form."""
+    say("linear sums %dx%dx%d %s" % (m, n, k, dtype))
+    g = torch.Generator().manual_seed(m + n)
+    x, w = put(rand(g, m, k), 0), put(0.05 * rand(g, n, k), 8)
+    b = rand(g, n).to(DEV) if bias else None
+    out = run(x, w, b, "none", None, m, n, k, dtype, pad=n % 4)
+    xv, wv = f64(x, k), f64(w, k)
+    want, size = xv @ wv.t(), xv.abs() @ wv.abs().t()
+    if bias:
+        want, size = want + b.cpu().double(), size + b.cpu().double().abs()
+    dt = R.TYPES[dtype][0]
+    e = sum_bound(k) * size
+    check(out[:, :n], want, e + R.half_step(dt) * (want.abs() + e) + R.tiny(dt), l2_bound(dtype, k), "out")
+    assert (out[:, n:] == -3.0).all()
+
+
 BACKWARD = [(1, 64, 64), (2, 1, 8), (3, 17, 24), (16, 1408, 2048), (33, 300, 520), (64, 60, 2048),
             (65, 1000, 8), (130, 257, 1032), (255, 256, 264), (333, 1408, 2000), (777, 60, 2048),
-            (1000, 1000, 1000), (1025, 520, 264), (4096, 64, 2048), (4099, 3, 256)]
+            (1000, 1000, 1000), (1025, 520, 264), (4096, 64, 2048), (4099, 3, 256),
+            (33000, 24, 64), (70001, 7, 8)]
 
 
 @pytest.mark.parametrize("dtype,act", [("f16", "silu"), ("f32", "none"), ("f16", "none")])
