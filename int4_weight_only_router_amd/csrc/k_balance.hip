@@ -36,12 +36,10 @@ constexpr int BL_SELF = 8192;
 constexpr int BL_COUNT_GROUPS = 16, BL_GROUPS = 256;
 constexpr float BL_FAR = -60.0f;   // exp(-60) and its sums are far inside fp32's range
 
-template <typename T>
-__device__ __forceinline__ float logit_value(T v)
+// NaN counts as masked, +inf as the largest finite value (as in the selection)
+__device__ __forceinline__ float logit_value(float f)
 {
-    const float f = (float)v;
-    // NaN counts as masked, +inf as the largest finite value (as in the selection)
-    return f == f ? fminf(f, 3.402823466e+38f) : -__builtin_inff();
+    return fminf(fmaxf(f, -__builtin_inff()), 3.402823466e+38f);
 }
 
 // exp(x) for x <= 0 by the hardware's exp2 (an ulp), with the rounding of x log2(e)
@@ -80,8 +78,9 @@ template <int THREADS>
 __device__ __forceinline__ int count_tokens(const BalanceArgs &a, int64_t t0, int64_t t1, int *hist)
 {
     int n = 0;
-    for (int64_t t = t0 + threadIdx.x; t < t1; t += THREADS)
-        n += !a.mask || a.mask[t];
+    if (a.mask)
+        for (int64_t t = t0 + threadIdx.x; t < t1; t += THREADS)
+            n += a.mask[t] != 0;
     if (a.idx) {
         const int64_t i1 = t1 * a.k;
 #pragma unroll 4
@@ -94,21 +93,27 @@ __device__ __forceinline__ int count_tokens(const BalanceArgs &a, int64_t t0, in
     return n;
 }
 
-// Sum over the workgroup (every thread gets it); s: one int a wave.
-template <int WAVES>
-__device__ __forceinline__ int block_sum(int v, int *s)
+__device__ __forceinline__ int wave_sum_int(int v)
 {
 #pragma unroll
     for (int o = 32; o; o >>= 1)
         v += __shfl_xor(v, o, 64);
-    if ((threadIdx.x & 63) == 0)
-        s[threadIdx.x >> 6] = v;
-    lds_barrier();
-    v = 0;
-#pragma unroll
-    for (int i = 0; i < WAVES; ++i)
-        v += s[i];
     return v;
+}
+// (16 bits and the rest are sums of whole numbers below 2^24, so exact in fp32)
+__device__ __forceinline__ int64_t wave_sum_counts(int64_t v)
+{
+    return (int64_t)wave_sum_f32((float)(v & 0xffff)) +
+           ((int64_t)wave_sum_f32((float)(v >> 16)) << 16);
+}
+
+// A row of E values by buffer instructions, whose range check does without masks: zeros
+// are read past its end, and nothing is written there.
+template <typename T>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t row_rsrc(const T *row, int E)
+{
+    constexpr int RAW = 0x00020000;   // 32-bit data, no swizzle
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<T *>(row), 0, E * (int)sizeof(T), RAW);
 }
 
 // A row's logits and its token's mask in registers, as they were loaded: lane l holds
@@ -119,23 +124,44 @@ struct Row {
     uint8_t mask;
     __device__ __forceinline__ void load(const BalanceArgs &a, int64_t t)
     {
-        const LT *row = static_cast<const LT *>(a.logits) + t * a.ld;
+        const __amdgpu_buffer_rsrc_t r = row_rsrc(static_cast<const LT *>(a.logits) + t * a.ld, a.E);
         mask = a.mask ? a.mask[t] : 1;
 #pragma unroll
-        for (int i = 0; i < NE; ++i)
-            v[i] = row[min((int)(threadIdx.x & 63) + 64 * i, a.E - 1)];
+        for (int i = 0; i < NE; ++i) {
+            const int at = ((int)(threadIdx.x & 63) + 64 * i) * (int)sizeof(LT);
+            if constexpr (sizeof(LT) == 4)
+                v[i] = __builtin_bit_cast(LT, __builtin_amdgcn_raw_buffer_load_b32(r, at, 0, 0));
+            else
+                v[i] = __builtin_bit_cast(
+                    LT, (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, at, 0, 0));
+        }
     }
     // the logits (-inf past E and for a masked token), and whether the token counts
     __device__ __forceinline__ bool values(const BalanceArgs &a, float (&l)[NE]) const
     {
         const bool on = __builtin_amdgcn_readfirstlane(mask);   // (the same for the whole wave)
+        const int E = on ? a.E : 0;
 #pragma unroll
         for (int i = 0; i < NE; ++i)
-            l[i] = on && (int)(threadIdx.x & 63) + 64 * i < a.E ? logit_value<LT>(v[i])
-                                                              : -__builtin_inff();
+            l[i] = (int)(threadIdx.x & 63) + 64 * i < E ? logit_value((float)v[i])
+                                                      : -__builtin_inff();
         return on;
     }
 };
+
+template <int NE, typename T>
+__device__ __forceinline__ void store_row(const BalanceArgs &a, int64_t t, const float (&g)[NE])
+{
+    const __amdgpu_buffer_rsrc_t r = row_rsrc(static_cast<T *>(a.dlogits) + t * a.ldd, a.E);
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {
+        const int at = ((int)(threadIdx.x & 63) + 64 * i) * (int)sizeof(T);
+        if constexpr (sizeof(T) == 4)
+            __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, g[i]), r, at, 0, 0);
+        else
+            __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, (T)g[i]), r, at, 0, 0);
+    }
+}
 
 // The row: its p added to psum[], its share of the balance loss and lse^2 added up,
 // its gradient written.
@@ -144,7 +170,6 @@ __device__ __forceinline__ void balance_row(const BalanceArgs &a, int64_t t, boo
                                             const float (&l)[NE], const float (&d)[NE], float per_n,
                                             float up, float (&psum)[NE], float &loss, float &zsum)
 {
-    const int lane = threadIdx.x & 63;
     float top = l[0];
 #pragma unroll
     for (int i = 1; i < NE; ++i)
@@ -174,14 +199,21 @@ __device__ __forceinline__ void balance_row(const BalanceArgs &a, int64_t t, boo
     float rest[NE];   // sigmoid scores: 1 - s
     if (sig) {
         float s = 0.0f;
-        const bool far = top < BL_FAR;
 #pragma unroll
         for (int i = 0; i < NE; ++i) {
             const float x = exp_neg(-fabsf(l[i])), q = __builtin_amdgcn_rcpf(1.0f + x);
-            rest[i] = (l[i] > 0.0f ? x : 1.0f) * q;
-            p[i] = some ? (l[i] > 0.0f ? 1.0f : far ? exp_neg(l[i] - top) : x) * q : 0.0f;
-            s += p[i];
+            const bool up = l[i] > 0.0f;
+            rest[i] = up ? x * q : q;
+            p[i] = up ? q : x * q;
         }
+        if (top < BL_FAR) {   // (all of them far below zero: rest is one)
+#pragma unroll
+            for (int i = 0; i < NE; ++i)
+                p[i] = some ? exp_neg(l[i] - top) : 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < NE; ++i)
+            s += p[i];
         s = wave_sum_f32(s);
         const float inv = some ? 1.0f / s : 0.0f;
 #pragma unroll
@@ -204,55 +236,31 @@ __device__ __forceinline__ void balance_row(const BalanceArgs &a, int64_t t, boo
     if (!a.dlogits)
         return;
     const float cb = up * a.coef * per_n, cz = a.zcoef != 0.0f ? up * a.zcoef * per_n * 2.0f * lse : 0.0f;
-#pragma unroll
-    for (int i = 0; i < NE; ++i) {
-        const int e = lane + 64 * i;
-        float g = cb * p[i] * (d[i] - dot);
-        if (sig)
-            g *= rest[i];
-        g = some ? __builtin_fmaf(cz, soft[i], g) : 0.0f;
-        if (e < a.E) {
-            const int64_t at = t * a.ldd + e;
-            if (a.gtype == MOE_DTYPE_F32)
-                static_cast<float *>(a.dlogits)[at] = g;
-            else if (a.gtype == MOE_DTYPE_F16)
-                static_cast<f16 *>(a.dlogits)[at] = (f16)g;
-            else
-                static_cast<__bf16 *>(a.dlogits)[at] = (__bf16)g;
-        }
-    }
-}
-
-// d_e of this lane's experts from whole counts.
-template <int NE>
-__device__ __forceinline__ void deviations(const int *hist, int E, float (&d)[NE])
-{
-    const int lane = threadIdx.x & 63;
-    int c[NE];
-    int64_t own = 0;
-#pragma unroll
-    for (int i = 0; i < NE; ++i) {
-        c[i] = hist[lane + 64 * i];   // (zeros past E)
-        own += c[i];
-    }
-    // the total, every wave for itself: 16 bits and the rest are sums of whole numbers
-    // below 2^24, so exact in fp32
-    const int64_t total = (int64_t)wave_sum_f32((float)(own & 0xffff)) +
-                          ((int64_t)wave_sum_f32((float)(own >> 16)) << 16);
-    const float inv = 1.0f / (float)(total > 0 ? total : 1);
-    if (total * E < 1LL << 31) {
-#pragma unroll
-        for (int i = 0; i < NE; ++i)
-            d[i] = (float)(c[i] * E - (int)total) * inv;
-    } else {
-#pragma unroll
-        for (int i = 0; i < NE; ++i)
-            d[i] = (float)(c[i] * (int64_t)E - total) * inv;
-    }
+    float g[NE];
 #pragma unroll
     for (int i = 0; i < NE; ++i)
-        if (lane + 64 * i >= E)
-            d[i] = 0.0f;
+        g[i] = cb * p[i] * (d[i] - dot);
+    if (sig)
+#pragma unroll
+        for (int i = 0; i < NE; ++i)
+            g[i] *= rest[i];
+    // (zeros without a score, also where up is not finite)
+#pragma unroll
+    for (int i = 0; i < NE; ++i)
+        g[i] = some ? __builtin_fmaf(cz, soft[i], g[i]) : 0.0f;
+    if (a.gtype == MOE_DTYPE_F32)
+        store_row<NE, float>(a, t, g);
+    else if (a.gtype == MOE_DTYPE_F16)
+        store_row<NE, f16>(a, t, g);
+    else
+        store_row<NE, __bf16>(a, t, g);
+}
+
+// d_e = E f_e - 1 from whole counts.
+__device__ __forceinline__ float deviation(int c, int E, int64_t total, float inv)
+{
+    const bool low = total < 1 << 23 && total * E < 1LL << 31;   // (full-rate products)
+    return (low ? (float)(__mul24(c, E) - (int)total) : (float)(c * (int64_t)E - total)) * inv;
 }
 
 // Partial counts of the tokens dealt out over the workgroups: [G][E] and the
@@ -266,12 +274,19 @@ __global__ __launch_bounds__(BL_THREADS) void balance_count_kernel(BalanceArgs a
     __syncthreads();
     const int64_t each = ((int64_t)a.T + gridDim.x - 1) / gridDim.x;
     const int64_t t0 = blockIdx.x * each;
-    const int n = block_sum<BL_WAVES>(
-        count_tokens<BL_THREADS>(a, t0, min(t0 + each, (int64_t)a.T), hist), s);
+    const int own = wave_sum_int(count_tokens<BL_THREADS>(a, t0, min(t0 + each, (int64_t)a.T), hist));
+    if ((threadIdx.x & 63) == 0)
+        s[threadIdx.x >> 6] = own;
+    __syncthreads();
     for (int e = threadIdx.x; e < a.E; e += BL_THREADS)
         a.part_counts[(int64_t)blockIdx.x * a.E + e] = hist[e];
-    if (threadIdx.x == 0)
+    if (threadIdx.x == 0) {
+        int n = 0;
+#pragma unroll
+        for (int i = 0; i < BL_WAVES; ++i)
+            n += s[i];
         a.part_n[blockIdx.x] = n;
+    }
 }
 
 // Rows.  ONE: of one workgroup, which writes the outputs; else its sums of p, of the
@@ -281,8 +296,11 @@ template <typename LT, int NE, bool ONE>
 __global__ __launch_bounds__(64 * bl_waves<NE>()) void balance_rows_kernel(BalanceArgs a)
 {
     constexpr int WAVES = bl_waves<NE>(), THREADS = 64 * WAVES, HALF = WAVES / 2;
+    constexpr int PER = (64 * NE + THREADS - 1) / THREADS;   // experts of a thread
     __shared__ int hist[64 * NE];
-    __shared__ int s[WAVES];
+    __shared__ float dev[64 * NE];
+    __shared__ int64_t totals[WAVES];
+    __shared__ int tokens[WAVES];
     __shared__ float cols[HALF][64 * NE + 2];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     int64_t t = (int64_t)blockIdx.x * WAVES + wave;
@@ -290,40 +308,76 @@ __global__ __launch_bounds__(64 * bl_waves<NE>()) void balance_rows_kernel(Balan
     Row<LT, NE> row;
     row.load(a, t < a.T ? t : 0);
     const float up = a.dlogits && a.d_loss ? *a.d_loss : 1.0f;
-    int64_t n = a.T;
     const bool self = ONE || !a.count_groups;   // counts for itself
+    int c[PER], own_n = 0;
     if (self) {
-        for (int e = threadIdx.x; e < 64 * NE; e += THREADS)
-            hist[e] = a.idx || e >= a.E ? 0 : a.counts[e];
-        lds_barrier();
+        if (a.idx) {
+            for (int e = threadIdx.x; e < 64 * NE; e += THREADS)
+                hist[e] = 0;
+            lds_barrier();
+        }
         if (a.idx || a.mask)
-            n = block_sum<WAVES>(count_tokens<THREADS>(a, 0, a.T, hist), s);
-    } else {
-        const int mine = a.mask && threadIdx.x < a.count_groups ? a.part_n[threadIdx.x] : 0;
-        for (int e = threadIdx.x; e < 64 * NE; e += THREADS) {
-            int c = 0;
-            if (e < a.E && !a.idx) {
-                c = a.counts[e];
-            } else if (e < a.E) {
+            own_n = count_tokens<THREADS>(a, 0, a.T, hist);
+        if (a.idx)
+            lds_barrier();
+    } else if (a.mask && threadIdx.x < a.count_groups) {
+        own_n = a.part_n[threadIdx.x];
+    }
+    int64_t own = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int e = threadIdx.x + i * THREADS;
+        c[i] = 0;
+        if (e < a.E) {
+            if (!a.idx) {
+                c[i] = a.counts[e];
+            } else if (self) {
+                c[i] = hist[e];
+            } else {
                 int part[BL_COUNT_GROUPS];   // (all on their way together)
 #pragma unroll
                 for (int g = 0; g < BL_COUNT_GROUPS; ++g)
                     part[g] = a.part_counts[(int64_t)min(g, a.count_groups - 1) * a.E + e];
 #pragma unroll
                 for (int g = 0; g < BL_COUNT_GROUPS; ++g)
-                    c += g < a.count_groups ? part[g] : 0;
+                    c[i] += g < a.count_groups ? part[g] : 0;
             }
-            hist[e] = c;
         }
-        if (a.mask)
-            n = block_sum<WAVES>(mine, s);
+        own += c[i];
+    }
+    own = wave_sum_counts(own);
+    if (a.mask)
+        own_n = wave_sum_int(own_n);
+    if (lane == 0) {
+        totals[wave] = own;
+        tokens[wave] = own_n;
+    }
+    lds_barrier();
+    int64_t total = 0;
+    int n = a.mask ? 0 : a.T;
+#pragma unroll
+    for (int i = 0; i < WAVES; ++i)
+        total += totals[i];
+    if (a.mask)
+#pragma unroll
+        for (int i = 0; i < WAVES; ++i)
+            n += tokens[i];
+    const float inv = 1.0f / (float)(total > 0 ? total : 1);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int e = threadIdx.x + i * THREADS;
+        if (e < 64 * NE)
+            dev[e] = e < a.E ? deviation(c[i], a.E, total, inv) : 0.0f;
+        if (blockIdx.x == 0 && e < a.E && a.idx)
+            a.counts[e] = c[i];
     }
     lds_barrier();
     float d[NE], psum[NE], loss = 0.0f, zsum = 0.0f;
-    deviations<NE>(hist, a.E, d);
 #pragma unroll
-    for (int i = 0; i < NE; ++i)
+    for (int i = 0; i < NE; ++i) {
+        d[i] = dev[lane + 64 * i];
         psum[i] = 0.0f;
+    }
     const float per_n = n > 0 ? 1.0f / (float)n : 0.0f;
     const int64_t step = (int64_t)gridDim.x * WAVES;
     while (t < a.T) {
@@ -372,11 +426,9 @@ __global__ __launch_bounds__(64 * bl_waves<NE>()) void balance_rows_kernel(Balan
         } else if (a.mean_prob) {
             a.mean_prob[e] = v * per_n;
         }
-        if (blockIdx.x == 0 && e < a.E && a.idx)
-            a.counts[e] = hist[e];
     }
     if (!ONE && blockIdx.x == 0 && threadIdx.x == 0)
-        *a.n = (int)n;
+        *a.n = n;
 }
 
 // The outputs from the partial sums: 64 experts a workgroup, 16 partial sums at a
