@@ -239,7 +239,7 @@ int moe_block_norm_backward(const void *dout, int64_t ldo, const void *dn, int64
 
 size_t moe_linear_f16_workspace_bytes(int M, int N, int K)
 {
-    return M <= 0 || N <= 0 || K <= 0 || !linear_fits(M, N, K) ? 0 : linear_ws(M, N, K);
+    return M <= 0 || N <= 0 || K <= 0 || !linear_fits(M, N, K, false) ? 0 : linear_ws(M, N, K);
 }
 
 int moe_linear_f16(const void *x_f16, int64_t ldx, const void *w_f16, int64_t ldw,
@@ -259,7 +259,7 @@ int moe_linear_f16(const void *x_f16, int64_t ldx, const void *w_f16, int64_t ld
         return set_error(MOE_EUNSUPPORTED,
                          "%s: K, ldx and ldw must be multiples of 8 (K=%d ldx=%lld ldw=%lld)", fn, K,
                          (long long)ldx, (long long)ldw);
-    if (ldx > LIN_MOST_LD || ldw > LIN_MOST_LD || (M > 0 && !linear_fits(M, N, K)))
+    if (ldx > LIN_MOST_LD || ldw > LIN_MOST_LD || (M > 0 && !linear_fits(M, N, K, false)))
         return set_error(MOE_EUNSUPPORTED,
                          "%s: rows of at most %d elements and %lld tiles (M=%d N=%d ldx=%lld "
                          "ldw=%lld)", fn, LIN_MOST_LD, (long long)LIN_MOST_ITEMS, M, N,
@@ -300,7 +300,7 @@ int moe_linear_f16(const void *x_f16, int64_t ldx, const void *w_f16, int64_t ld
 
 size_t moe_linear_f16_backward_workspace_bytes(int M, int N, int K)
 {
-    if (M <= 0 || N <= 0 || K <= 0 || !linear_fits(M, K, N) || !linear_fits(N, K, M))
+    if (M <= 0 || N <= 0 || K <= 0 || !linear_fits(M, K, N, true) || !linear_fits(N, K, M, true))
         return 0;
     return linear_backward_ws(M, N, K);
 }
@@ -325,7 +325,7 @@ int moe_linear_f16_backward(const void *dy_f16, int64_t lddy, const void *z_f16,
                          "%s: K, ldx and ldw must be multiples of 8 (K=%d ldx=%lld ldw=%lld)", fn, K,
                          (long long)ldx, (long long)ldw);
     if ((dw && ldx > LIN_MOST_LD) || (dx && ldw > LIN_MOST_LD) || N > LIN_MOST_LD ||
-        (M > 0 && (!linear_fits(M, K, N) || !linear_fits(N, K, M))))
+        (M > 0 && (!linear_fits(M, K, N, true) || !linear_fits(N, K, M, true))))
         return set_error(MOE_EUNSUPPORTED,
                          "%s: rows of at most %d elements and %lld tiles (M=%d N=%d K=%d ldx=%lld "
                          "ldw=%lld)", fn, LIN_MOST_LD, (long long)LIN_MOST_ITEMS, M, N, K,

@@ -75,7 +75,7 @@ struct LinPlan {
 };
 constexpr int64_t LIN_MOST_ITEMS = (1 << 22) - 8;   // a launch has fewer than 2^32 threads
 constexpr int LIN_MOST_LD = 1 << 22;                // offsets inside a tile are 32 bits wide
-LinPlan linear_plan(int M, int N, int K);
+LinPlan linear_plan(int M, int N, int K, bool across);   // across: an operand's rows do
 int launch_linear_tile(LinArgs, const LinPlan &, void *ws, hipStream_t);
 constexpr int LIN_FEW_ROWS = 2;
 int launch_linear_rows(const LinArgs &, hipStream_t);   // so many rows, both operands along k
@@ -156,7 +156,8 @@ __device__ __forceinline__ float act_grad(float z, int act)
 
 size_t linear_ws(int M, int N, int K);
 size_t linear_backward_ws(int M, int N, int K);
-bool linear_fits(int M, int N, int K);   // whether a launch holds the product's tiles
+// whether a launch holds the product's tiles
+bool linear_fits(int M, int N, int K, bool across);
 int launch_linear(const LinArgs &, void *ws, hipStream_t);
 struct LinGrads {
     const f16 *dy, *z, *x, *w;

@@ -11,36 +11,38 @@
 namespace moe {
 
 // The forms of a tile: rows, columns, groups that share its k, workgroups a compute
-// unit; and what they were measured to take, in us (fp16, K = 256, 512 and 2048, 256
+// unit; and what they were measured to take, in us (fp16, K from 256 to 5632, 256
 // compute units busy with one to eight workgroups each): a workgroup `end` for its
 // first loads and its results and `one` for a block of 64 k (of its group, where
 // groups share k); two workgroups on a compute unit together `two` for a block of each.
+// The smallest form reads 32 and 64 bytes at a time of an operand whose rows run across
+// k, and takes `across` for a block then.
 //
 // With them the form and the parts of k that take the least time are chosen.  On 90
 // products from 1 x 1024 x 256 to 8192 x 8192 x 8192 the choice was the fastest form
-// or within 8% of it (at K = 2048, chosen / next best: 1 x 5632 16-row tiles 7.4 us,
-// 32-row 7.6; 333 x 1408 32-row 8.2, 64-row 9.4; 256 x 5632 64-row 13.7, 128-row
+// or within 8% of it (at K = 2048, chosen / next best: 16 x 5632 16-row tiles 7.4 us,
+// 32-row 7.6; 333 x 1408 32-row 8.2, 64-row 9.0; 256 x 5632 64-row 13.7, 128-row
 // 17.3; 2048 x 2048 128-row of eight waves 20.8, of four 26.8; 4096 x 2048 the other
-// way round, 35.7 and 39.8; 4096 x 5632 192-row 83, 256-row 95; 4096 x 11264 256-row
-// 154, 192-row 163).
+// way round, 35.7 and 39.8; 4096 x 5632 192-row 86, 256-row 95; 4096 x 11264 256-row
+// 154, 192-row 163; at K = 5632 64 x 2048 16-row 9.7, 32-row in four parts 11.1).
 struct LinForm {
     int bm, bn, kg, per_cu;
-    double end, one, two;
+    double end, one, two, across;
 };
 static const LinForm FORMS[] = {
-    {16, 32, 8, 1, 3.0, 0.80, 0},     {32, 64, 2, 1, 2.2, 0.30, 0},  {64, 64, 2, 1, 2.2, 0.44, 0},
-    {64, 64, 1, 2, 0.9, 0.33, 0.33},  {128, 128, 1, 1, 3.5, 0.50, 0}, {128, 128, 1, 2, 1.8, 0.72, 0.90},
-    {192, 256, 1, 1, 6.0, 1.13, 0},   {256, 256, 1, 1, 5.0, 1.45, 0}};
+    {16, 32, 8, 1, 3.0, 0.50, 0, 0.80},      {32, 64, 2, 1, 2.2, 0.30, 0, 0.30},
+    {64, 64, 2, 1, 2.2, 0.44, 0, 0.44},      {64, 64, 1, 2, 0.9, 0.33, 0.33, 0.33},
+    {128, 128, 1, 1, 3.5, 0.50, 0, 0.50},    {128, 128, 1, 2, 1.8, 0.72, 0.90, 0.72},
+    {192, 256, 1, 1, 6.0, 1.13, 0, 1.13},    {256, 256, 1, 1, 5.0, 1.45, 0, 1.45}};
 
-LinPlan linear_plan(int M, int N, int K)
+LinPlan linear_plan(int M, int N, int K, bool across)
 {
     LinPlan best{};
     double least = 1e300;
     const int nkb = (int)(((int64_t)K + 63) / 64);
     for (int f = 0; f < 8; ++f) {
         const LinForm &o = FORMS[f];
-        if (f == 0 && M > 16)
-            continue;
+        const double one = across ? o.across : o.one;
         const int64_t tiles = ((int64_t)M + o.bm - 1) / o.bm * (((int64_t)N + o.bn - 1) / o.bn);
         for (int s = 1; s <= 8; s *= 2) {
             const int each = (nkb + s - 1) / s;
@@ -49,7 +51,7 @@ LinPlan linear_plan(int M, int N, int K)
             const int64_t n = (tiles * s + 255) / 256;   // workgroups of a compute unit
             const int64_t pairs = o.per_cu == 2 ? n / 2 : 0;
             const double blocks = (each + o.kg - 1) / o.kg;
-            double t = 1.0 + n * o.end + blocks * (pairs * o.two + (n - 2 * pairs) * o.one);
+            double t = 1.0 + n * o.end + blocks * (pairs * o.two + (n - 2 * pairs) * one);
             if (s > 1)   // a launch more, and the parts' sums written and read
                 t += 4.5 + (2.0 * s + 1) * 4.0 * M * N / 3e6;
             if (t < least) {
@@ -61,9 +63,9 @@ LinPlan linear_plan(int M, int N, int K)
     return best;
 }
 
-bool linear_fits(int M, int N, int K)
+bool linear_fits(int M, int N, int K, bool across)
 {
-    return M <= 1 << 30 && N <= 1 << 30 && linear_plan(M, N, K).items <= LIN_MOST_ITEMS;
+    return M <= 1 << 30 && N <= 1 << 30 && linear_plan(M, N, K, across).items <= LIN_MOST_ITEMS;
 }
 
 static size_t plan_ws(const LinPlan &p, int M, int N)
@@ -73,14 +75,14 @@ static size_t plan_ws(const LinPlan &p, int M, int N)
 
 size_t linear_ws(int M, int N, int K)
 {
-    return M <= LIN_FEW_ROWS ? 0 : plan_ws(linear_plan(M, N, K), M, N);
+    return M <= LIN_FEW_ROWS ? 0 : plan_ws(linear_plan(M, N, K, false), M, N);
 }
 
 int launch_linear(const LinArgs &a, void *ws, hipStream_t s)
 {
     if (a.M <= LIN_FEW_ROWS && !a.a_ks && !a.b_ks)
         return launch_linear_rows(a, s);
-    return launch_linear_tile(a, linear_plan(a.M, a.N, a.K), ws, s);
+    return launch_linear_tile(a, linear_plan(a.M, a.N, a.K, a.a_ks || a.b_ks), ws, s);
 }
 
 // ------------------------------------------------------------------ gradients
@@ -167,8 +169,8 @@ static GradWs grad_ws(int M, int N, int K)
     GradWs w;
     w.parts = al256((int64_t)M * dz_ld(N) * 2);
     w.products = w.parts + al256((int64_t)dz_groups(M) * N * 4);
-    w.total = w.products + (int64_t)std::max(plan_ws(linear_plan(M, K, N), M, K),
-                                             plan_ws(linear_plan(N, K, M), N, K));
+    w.total = w.products + (int64_t)std::max(plan_ws(linear_plan(M, K, N, true), M, K),
+                                             plan_ws(linear_plan(N, K, M, true), N, K));
     return w;
 }
 
@@ -206,7 +208,7 @@ int launch_linear_backward(const LinGrads &g, void *ws, hipStream_t s)
     const int G = dz_groups(g.M);
     const LinColumns cols = {parts, G, g.N, g.dbias};
     // the bias gradient's last step joins the launch that joins dw's parts, if there is one
-    const bool late = g.dw && linear_plan(g.N, g.K, g.M).splits > 1;
+    const bool late = g.dw && linear_plan(g.N, g.K, g.M, true).splits > 1;
     if ((own && (g.dx || g.dw)) || g.dbias) {
         int lt = 0;   // threads of a row: up to 32
         while (lt < 5 && (8 << lt) < g.N)
