@@ -744,8 +744,9 @@ int moe_linear_f16(const void *x_f16, int64_t ldx, const void *w_f16, int64_t ld
  *   dbias   device fp32 [N] or NULL, from the unrounded dz
  *   ws      device scratch of moe_linear_f16_backward_workspace_bytes(M, N, K)
  *           bytes, as above
- * dz is rounded to fp16 for the products (exact with MOE_ACT_NONE), so out_dtype
- * F32 is for MOE_ACT_NONE only (MOE_EUNSUPPORTED).  Gradients that would leave
+ * dz is rounded to fp16 for the products (exact with MOE_ACT_NONE and RELU; where dz,
+ * dx or dw have few values, it enters as the sum of two fp16), so out_dtype F32 is for
+ * MOE_ACT_NONE only (MOE_EUNSUPPORTED).  Gradients that would leave
  * fp16's range belong scaled by the caller.  Limits as above, for the products of
  * dx and dw, whichever is asked for, and N at most 2^22 (MOE_EUNSUPPORTED); lddy, ldz,
  * lddx and lddw are free.  M = 0: dw and dbias are set to zero.

@@ -239,7 +239,10 @@ int moe_block_norm_backward(const void *dout, int64_t ldo, const void *dn, int64
 
 size_t moe_linear_f16_workspace_bytes(int M, int N, int K)
 {
-    return M <= 0 || N <= 0 || K <= 0 || !linear_fits(M, N, K, false) ? 0 : linear_ws(M, N, K);
+    if (M <= 0 || N <= 0 || K <= 0)
+        return 0;
+    const LinPlan p = linear_forward_plan(M, N, K);
+    return p.items > LIN_MOST_ITEMS ? 0 : linear_ws(p, M, N);
 }
 
 int moe_linear_f16(const void *x_f16, int64_t ldx, const void *w_f16, int64_t ldw,
@@ -259,7 +262,9 @@ int moe_linear_f16(const void *x_f16, int64_t ldx, const void *w_f16, int64_t ld
         return set_error(MOE_EUNSUPPORTED,
                          "%s: K, ldx and ldw must be multiples of 8 (K=%d ldx=%lld ldw=%lld)", fn, K,
                          (long long)ldx, (long long)ldw);
-    if (ldx > LIN_MOST_LD || ldw > LIN_MOST_LD || (M > 0 && !linear_fits(M, N, K, false)))
+    const bool far = ldx > LIN_MOST_LD || ldw > LIN_MOST_LD;
+    const LinPlan plan = far || M == 0 ? LinPlan{} : linear_forward_plan(M, N, K);
+    if (far || plan.items > LIN_MOST_ITEMS)
         return set_error(MOE_EUNSUPPORTED,
                          "%s: rows of at most %d elements and %lld tiles (M=%d N=%d ldx=%lld "
                          "ldw=%lld)", fn, LIN_MOST_LD, (long long)LIN_MOST_ITEMS, M, N,
@@ -273,7 +278,7 @@ int moe_linear_f16(const void *x_f16, int64_t ldx, const void *w_f16, int64_t ld
     if ((uintptr_t)bias % 4 || (uintptr_t)z_f16 % 2 ||
         ((uintptr_t)out | (uintptr_t)residual) % type_size(out_dtype))
         return set_error(MOE_EINVAL, "%s: misaligned bias, residual, out or z", fn);
-    const size_t need = linear_ws(M, N, K);
+    const size_t need = linear_ws(plan, M, N);
     if (need && (!ws || ws_bytes < need))
         return set_error(MOE_ENOMEM, "%s: workspace %zu < %zu bytes", fn, ws_bytes, need);
     if (need && (uintptr_t)ws % 16)
@@ -295,14 +300,15 @@ int moe_linear_f16(const void *x_f16, int64_t ldx, const void *w_f16, int64_t ld
     a.ldo = ldo;
     a.z = static_cast<f16 *>(z_f16);
     a.ldz = ldz;
-    return launch_linear(a, ws, stream);
+    return launch_linear(a, plan, ws, stream);
 }
 
 size_t moe_linear_f16_backward_workspace_bytes(int M, int N, int K)
 {
-    if (M <= 0 || N <= 0 || K <= 0 || !linear_fits(M, K, N, true) || !linear_fits(N, K, M, true))
+    if (M <= 0 || N <= 0 || K <= 0)
         return 0;
-    return linear_backward_ws(M, N, K);
+    const LinGradPlan p = linear_grad_plan(M, N, K);
+    return p.fits ? (size_t)p.total : 0;
 }
 
 int moe_linear_f16_backward(const void *dy_f16, int64_t lddy, const void *z_f16, int64_t ldz,
@@ -324,8 +330,9 @@ int moe_linear_f16_backward(const void *dy_f16, int64_t lddy, const void *z_f16,
         return set_error(MOE_EUNSUPPORTED,
                          "%s: K, ldx and ldw must be multiples of 8 (K=%d ldx=%lld ldw=%lld)", fn, K,
                          (long long)ldx, (long long)ldw);
-    if ((dw && ldx > LIN_MOST_LD) || (dx && ldw > LIN_MOST_LD) || N > LIN_MOST_LD ||
-        (M > 0 && (!linear_fits(M, K, N, true) || !linear_fits(N, K, M, true))))
+    const bool far = (dw && ldx > LIN_MOST_LD) || (dx && ldw > LIN_MOST_LD) || N > LIN_MOST_LD;
+    const LinGradPlan plan = far || M == 0 ? LinGradPlan{} : linear_grad_plan(M, N, K);
+    if (far || (M > 0 && !plan.fits))
         return set_error(MOE_EUNSUPPORTED,
                          "%s: rows of at most %d elements and %lld tiles (M=%d N=%d K=%d ldx=%lld "
                          "ldw=%lld)", fn, LIN_MOST_LD, (long long)LIN_MOST_ITEMS, M, N, K,
@@ -342,7 +349,7 @@ int moe_linear_f16_backward(const void *dy_f16, int64_t lddy, const void *z_f16,
     if ((uintptr_t)dy_f16 % 2 || (act != MOE_ACT_NONE && (uintptr_t)z_f16 % 2) ||
         (uintptr_t)dbias % 4 || ((uintptr_t)dx | (uintptr_t)dw) % type_size(out_dtype))
         return set_error(MOE_EINVAL, "%s: misaligned dy, z or gradients", fn);
-    const size_t need = moe_linear_f16_backward_workspace_bytes(M, N, K);
+    const size_t need = (size_t)plan.total;
     if (need && (!ws || ws_bytes < need))
         return set_error(MOE_ENOMEM, "%s: workspace %zu < %zu bytes", fn, ws_bytes, need);
     if (need && (uintptr_t)ws % 16)
@@ -366,7 +373,7 @@ int moe_linear_f16_backward(const void *dy_f16, int64_t lddy, const void *z_f16,
     g.lddw = lddw;
     g.odt = out_dtype;
     g.dbias = dbias;
-    return launch_linear_backward(g, ws, stream);
+    return launch_linear_backward(g, plan, ws, stream);
 }
 
 size_t moe_balance_loss_workspace_bytes(int T, int E)

@@ -50,6 +50,7 @@ struct LinArgs {
     const f16 *a, *b;
     int64_t lda, ldb;
     bool a_ks, b_ks;
+    int wrap;   // b_ks: k from here on starts over in b (0: nowhere)
     int M, N, K;
     const float *bias;
     int act;
@@ -75,7 +76,10 @@ struct LinPlan {
 };
 constexpr int64_t LIN_MOST_ITEMS = (1 << 22) - 8;   // a launch has fewer than 2^32 threads
 constexpr int LIN_MOST_LD = 1 << 22;                // offsets inside a tile are 32 bits wide
-LinPlan linear_plan(int M, int N, int K, bool across);   // across: an operand's rows do
+// across: operands whose rows run across k (b, then a too); small: by one of the first
+// LIN_SMALL forms
+constexpr int LIN_SMALL = 4;
+LinPlan linear_plan(int M, int N, int K, int across, bool small = false);
 int launch_linear_tile(LinArgs, const LinPlan &, void *ws, hipStream_t);
 constexpr int LIN_FEW_ROWS = 2;
 int launch_linear_rows(const LinArgs &, hipStream_t);   // so many rows, both operands along k
@@ -154,11 +158,18 @@ __device__ __forceinline__ float act_grad(float z, int act)
     }
 }
 
-size_t linear_ws(int M, int N, int K);
-size_t linear_backward_ws(int M, int N, int K);
-// whether a launch holds the product's tiles
-bool linear_fits(int M, int N, int K, bool across);
-int launch_linear(const LinArgs &, void *ws, hipStream_t);
+// One call's plan (items of LIN_MOST_ITEMS + 1 and more: no launch holds them).
+LinPlan linear_forward_plan(int M, int N, int K);
+size_t linear_ws(const LinPlan &, int M, int N);
+int launch_linear(const LinArgs &, const LinPlan &, void *ws, hipStream_t);
+struct LinGradPlan {
+    LinPlan dx, dw;
+    bool fits;
+    bool two;   // dz as the sum of two fp16 where an activation changes it
+    LinPlan dx2, dw2;
+    int64_t col, parts, products, total;   // workspace (dz, or its form for dx, stands first)
+};
+LinGradPlan linear_grad_plan(int M, int N, int K);
 struct LinGrads {
     const f16 *dy, *z, *x, *w;
     int64_t lddy, ldz, ldx, ldw;
@@ -168,6 +179,6 @@ struct LinGrads {
     int odt;
     float *dbias;
 };
-int launch_linear_backward(const LinGrads &, void *ws, hipStream_t);
+int launch_linear_backward(const LinGrads &, const LinGradPlan &, void *ws, hipStream_t);
 
 }  // namespace moe

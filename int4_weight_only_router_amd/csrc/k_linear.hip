@@ -16,7 +16,7 @@ namespace moe {
 // first loads and its results and `one` for a block of 64 k (of its group, where
 // groups share k); two workgroups on a compute unit together `two` for a block of each.
 // The smallest form reads 32 and 64 bytes at a time of an operand whose rows run across
-// k, and takes `across` for a block then.
+// k, and takes across[0] for a block where b is such, across[1] where both are.
 //
 // With them the form and the parts of k that take the least time are chosen.  On 90
 // products from 1 x 1024 x 256 to 8192 x 8192 x 8192 the choice was the fastest form
@@ -27,22 +27,22 @@ namespace moe {
 // 154, 192-row 163; at K = 5632 64 x 2048 16-row 9.7, 32-row in four parts 11.1).
 struct LinForm {
     int bm, bn, kg, per_cu;
-    double end, one, two, across;
+    double end, one, two, across[2];
 };
 static const LinForm FORMS[] = {
-    {16, 32, 8, 1, 3.0, 0.50, 0, 0.80},      {32, 64, 2, 1, 2.2, 0.30, 0, 0.30},
-    {64, 64, 2, 1, 2.2, 0.44, 0, 0.44},      {64, 64, 1, 2, 0.9, 0.33, 0.33, 0.33},
-    {128, 128, 1, 1, 3.5, 0.50, 0, 0.50},    {128, 128, 1, 2, 1.8, 0.72, 0.90, 0.72},
-    {192, 256, 1, 1, 6.0, 1.13, 0, 1.13},    {256, 256, 1, 1, 5.0, 1.45, 0, 1.45}};
+    {16, 32, 8, 1, 3.0, 0.50, 0, {0.80, 1.30}},   {32, 64, 2, 1, 2.2, 0.30, 0, {0.30, 0.30}},
+    {64, 64, 2, 1, 2.2, 0.44, 0, {0.44, 0.44}},   {64, 64, 1, 2, 0.9, 0.33, 0.33, {0.33, 0.33}},
+    {128, 128, 1, 1, 3.5, 0.50, 0, {0.50, 0.50}}, {128, 128, 1, 2, 1.8, 0.72, 0.90, {0.72, 0.72}},
+    {192, 256, 1, 1, 6.0, 1.13, 0, {1.13, 1.13}}, {256, 256, 1, 1, 5.0, 1.45, 0, {1.45, 1.45}}};
 
-LinPlan linear_plan(int M, int N, int K, bool across)
+LinPlan linear_plan(int M, int N, int K, int across, bool small)
 {
     LinPlan best{};
     double least = 1e300;
     const int nkb = (int)(((int64_t)K + 63) / 64);
-    for (int f = 0; f < 8; ++f) {
+    for (int f = 0; f < (small ? LIN_SMALL : 8); ++f) {
         const LinForm &o = FORMS[f];
-        const double one = across ? o.across : o.one;
+        const double one = across ? o.across[across - 1] : o.one;
         const int64_t tiles = ((int64_t)M + o.bm - 1) / o.bm * (((int64_t)N + o.bn - 1) / o.bn);
         for (int s = 1; s <= 8; s *= 2) {
             const int each = (nkb + s - 1) / s;
@@ -63,35 +63,60 @@ LinPlan linear_plan(int M, int N, int K, bool across)
     return best;
 }
 
-bool linear_fits(int M, int N, int K, bool across)
-{
-    return M <= 1 << 30 && N <= 1 << 30 && linear_plan(M, N, K, across).items <= LIN_MOST_ITEMS;
-}
-
 static size_t plan_ws(const LinPlan &p, int M, int N)
 {
     return p.splits == 1 ? 0 : (size_t)p.splits * M * ((N + 7) / 8 * 8) * sizeof(float);
 }
 
-size_t linear_ws(int M, int N, int K)
+LinPlan linear_forward_plan(int M, int N, int K)
 {
-    return M <= LIN_FEW_ROWS ? 0 : plan_ws(linear_plan(M, N, K, false), M, N);
+    if (M > 1 << 30 || N > 1 << 30)
+        return LinPlan{0, 1, LIN_MOST_ITEMS + 1};
+    return M <= LIN_FEW_ROWS ? LinPlan{0, 1, 1} : linear_plan(M, N, K, 0);
 }
 
-int launch_linear(const LinArgs &a, void *ws, hipStream_t s)
+size_t linear_ws(const LinPlan &p, int M, int N) { return plan_ws(p, M, N); }
+
+int launch_linear(const LinArgs &a, const LinPlan &p, void *ws, hipStream_t s)
 {
     if (a.M <= LIN_FEW_ROWS && !a.a_ks && !a.b_ks)
         return launch_linear_rows(a, s);
-    return launch_linear_tile(a, linear_plan(a.M, a.N, a.K, a.a_ks || a.b_ks), ws, s);
+    return launch_linear_tile(a, p, ws, s);
 }
 
 // ------------------------------------------------------------------ gradients
+
+// dz as the sum of two fp16, where it, dx or dw have few values: its rounding to one
+// adds as much to the errors of dx and dw as their own, and among few values by chance
+// much more (1 x 5632 x 2048: 1.48 of their rounding's, with two 1.00).  The products take
+// twice the k (4 x 1408 x 2048: 19.5 us against 14.1).
+constexpr int64_t DZ_FEW = 1 << 13, DZ_FEW_OUT = 1 << 11, DZ_FEW_MOST = 1 << 20;
+// Both have dz's sign and neither is zero (but for values that fp16 hardly holds), so
+// that an infinity in x or w meets no zero and no other sign: hi is the last fp16 before
+// dz, lo the rest of up to a step.
+__device__ __forceinline__ void split_f16(float v, float &hi, float &lo)
+{
+    f16 h = (f16)v;
+    if (fabsf((float)h) >= fabsf(v) && fabsf((float)h) > 0x1p-23f && fabsf((float)h) <= 65504.0f)
+        h = __builtin_bit_cast(f16, (uint16_t)(__builtin_bit_cast(uint16_t, h) - 1));
+    hi = (float)h;
+    lo = (float)(f16)(v - hi);
+    if (lo == 0.0f && fabsf(hi) >= 0x1p-23f)
+        lo = copysignf(0x1p-24f, v);
+    if (fabsf(hi) > 65504.0f)
+        lo = hi;
+}
+struct DzTwo {      // null: one fp16 each
+    f16 *row, *col;  // [M][dz, rest] for dx and [dz, rest][M] for dw
+    int64_t ld_row, ld_col;
+};
 
 // dz = dy act'(z) in fp16 (rows of ldd, zeros up to the next multiple of 8 behind
 // column N), where dz is not null, and its column sums over `tall` rows, from the
 // unrounded values, where parts is not null.  2^lt threads a row, eight columns each.
 __global__ __launch_bounds__(256) void linear_dz_kernel(LinGrads g, f16 *dz, int64_t ldd,
-                                                        float *parts, bool vec_y, bool vec_z, int lt, int tall)
+                                                        float *parts, bool vec_y, bool vec_z, int lt, int tall,
+                                                        DzTwo two)
 {
     __shared__ float sums[256 * 8];   // [row of threads][column]
     const int c = (threadIdx.x & ((1 << lt) - 1)) * 8, rows = 256 >> lt;
@@ -115,6 +140,20 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(LinGrads g, f16 *dz, int
         }
         if (dz)
             store_piece<f16, 8>(dz + m * ldd + n, 0, 8, true, v);
+        if (two.row) {
+            float hi[8], lo[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                split_f16(v[j], hi[j], lo[j]);
+            const bool vec = g.N % 8 == 0;
+            store_piece<f16, 8>(two.row + m * two.ld_row + n, 0, cols, vec, hi);
+            store_piece<f16, 8>(two.row + m * two.ld_row + g.N + n, 0, cols, vec, lo);
+            store_piece<f16, 8>(two.col + m * two.ld_col + n, 0, 8, true, hi);
+            store_piece<f16, 8>(two.col + (g.M + m) * two.ld_col + n, 0, 8, true, lo);
+            if (n + 8 >= g.N)   // zeros up to the next multiple of 8
+                for (int64_t k = 2 * (int64_t)g.N; k < two.ld_row; ++k)
+                    two.row[m * two.ld_row + k] = (f16)0.0f;
+        }
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             s[j] += v[j];
@@ -160,23 +199,31 @@ static int dz_rows(int M)
 static int dz_groups(int M) { return (M + dz_rows(M) - 1) / dz_rows(M); }
 static int64_t dz_ld(int N) { return ((int64_t)N + 7) / 8 * 8; }
 
-// Workspace: dz, the column sums, and what the products need.
-struct GradWs {
-    int64_t parts, products, total;
-};
-static GradWs grad_ws(int M, int N, int K)
+LinGradPlan linear_grad_plan(int M, int N, int K)
 {
-    GradWs w;
-    w.parts = al256((int64_t)M * dz_ld(N) * 2);
-    w.products = w.parts + al256((int64_t)dz_groups(M) * N * 4);
-    w.total = w.products + (int64_t)std::max(plan_ws(linear_plan(M, K, N, true), M, K),
-                                             plan_ws(linear_plan(N, K, M, true), N, K));
-    return w;
+    LinGradPlan p{};
+    if (M > 1 << 30 || K > 1 << 30 || N > LIN_MOST_LD)
+        return p;
+    p.dx = linear_plan(M, K, N, 1);
+    p.dw = linear_plan(N, K, M, 2);
+    p.fits = p.dx.items <= LIN_MOST_ITEMS && p.dw.items <= LIN_MOST_ITEMS;
+    const int64_t values = (int64_t)M * N, out = (int64_t)std::min(M, N) * K;
+    if (values <= DZ_FEW || (out <= DZ_FEW_OUT && values <= DZ_FEW_MOST)) {
+        p.dx2 = linear_plan(M, K, 2 * N, 1, true);
+        p.dw2 = linear_plan(N, K, 2 * M, 2, true);
+        p.two = p.dx2.items <= LIN_MOST_ITEMS && p.dw2.items <= LIN_MOST_ITEMS;
+    }
+    size_t most = std::max(plan_ws(p.dx, M, K), plan_ws(p.dw, N, K));
+    if (p.two)
+        most = std::max({most, plan_ws(p.dx2, M, K), plan_ws(p.dw2, N, K)});
+    p.col = al256((int64_t)M * dz_ld(p.two ? 2 * N : N) * 2);
+    p.parts = p.col + (p.two ? al256(2 * (int64_t)M * dz_ld(N) * 2) : 0);
+    p.products = p.parts + al256((int64_t)dz_groups(M) * N * 4);
+    p.total = p.products + (int64_t)most;
+    return p;
 }
 
-size_t linear_backward_ws(int M, int N, int K) { return (size_t)grad_ws(M, N, K).total; }
-
-int launch_linear_backward(const LinGrads &g, void *ws, hipStream_t s)
+int launch_linear_backward(const LinGrads &g, const LinGradPlan &w, void *ws, hipStream_t s)
 {
     if (g.M == 0) {
         if (g.dbias) {
@@ -197,27 +244,31 @@ int launch_linear_backward(const LinGrads &g, void *ws, hipStream_t s)
         }
         return MOE_OK;
     }
-    const GradWs w = grad_ws(g.M, g.N, g.K);
     uint8_t *base = static_cast<uint8_t *>(ws);
     float *parts = reinterpret_cast<float *>(base + w.parts);
     // dy itself is dz where nothing changes it and its rows end on whole pieces
     const bool own = g.act != MOE_ACT_NONE || g.N % 8 || g.lddy % 8 || (uintptr_t)g.dy % 16 ||
                      g.lddy > LIN_MOST_LD;
+    // (without an activation, and through ReLU, dz is fp16 as it is)
+    const bool two = g.act != MOE_ACT_NONE && g.act != MOE_ACT_RELU && w.two && (g.dx || g.dw);
+    const DzTwo rest = {two ? static_cast<f16 *>(ws) : nullptr, reinterpret_cast<f16 *>(base + w.col),
+                        dz_ld(2 * g.N), dz_ld(g.N)};
+    const LinPlan &dx = two ? w.dx2 : w.dx, &dw = two ? w.dw2 : w.dw;
     const f16 *dz = own ? static_cast<const f16 *>(ws) : g.dy;
     const int64_t ldd = own ? dz_ld(g.N) : g.lddy;
     const int G = dz_groups(g.M);
     const LinColumns cols = {parts, G, g.N, g.dbias};
     // the bias gradient's last step joins the launch that joins dw's parts, if there is one
-    const bool late = g.dw && linear_plan(g.N, g.K, g.M, true).splits > 1;
+    const bool late = g.dw && dw.splits > 1;
     if ((own && (g.dx || g.dw)) || g.dbias) {
         int lt = 0;   // threads of a row: up to 32
         while (lt < 5 && (8 << lt) < g.N)
             ++lt;
         auto rows16 = [](const void *p, int64_t ld) { return (uintptr_t)p % 16 == 0 && ld % 8 == 0; };
         hipLaunchKernelGGL(linear_dz_kernel, dim3((g.N + (8 << lt) - 1) / (8 << lt), G), dim3(256), 0,
-                           s, g, own && (g.dx || g.dw) ? static_cast<f16 *>(ws) : nullptr, ldd,
+                           s, g, own && !two && (g.dx || g.dw) ? static_cast<f16 *>(ws) : nullptr, ldd,
                            g.dbias ? parts : nullptr, rows16(g.dy, g.lddy), rows16(g.z, g.ldz), lt,
-                           dz_rows(g.M));
+                           dz_rows(g.M), rest);
         MOE_LAUNCH_CHECK("linear_dz_kernel");
         if (g.dbias && !late) {
             hipLaunchKernelGGL(linear_dbias_kernel, dim3((g.N + 63) / 64), dim3(1024), 0, s, cols);
@@ -236,9 +287,14 @@ int launch_linear_backward(const LinGrads &g, void *ws, hipStream_t s)
         a.ldb = g.ldw;
         a.M = g.M;
         a.K = g.N;
+        if (two) {
+            a.lda = rest.ld_row;
+            a.K = 2 * g.N;
+            a.wrap = g.N;
+        }
         a.out = g.dx;
         a.ldo = g.lddx;
-        const int rc = launch_linear(a, base + w.products, s);
+        const int rc = launch_linear(a, dx, base + w.products, s);
         if (rc)
             return rc;
     }
@@ -248,11 +304,17 @@ int launch_linear_backward(const LinGrads &g, void *ws, hipStream_t s)
         a.ldb = g.ldx;
         a.M = g.N;
         a.K = g.M;
+        if (two) {
+            a.a = rest.col;
+            a.lda = rest.ld_col;
+            a.K = 2 * g.M;
+            a.wrap = g.M;
+        }
         a.out = g.dw;
         a.ldo = g.lddw;
         if (g.dbias && late)
             a.columns = cols;
-        return launch_linear(a, base + w.products, s);
+        return launch_linear(a, dw, base + w.products, s);
     }
     return MOE_OK;
 }

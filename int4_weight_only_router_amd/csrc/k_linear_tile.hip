@@ -59,7 +59,8 @@ struct LtForm {
 };
 
 // One operand of a workgroup of NTH threads: R rows (of A or B) from row r0 on.
-template <int R, bool KS, int NTH>
+// WRAP: its k starts over at `wrap`, counted from k0 before its base.
+template <int R, bool KS, int NTH, bool WRAP = false>
 struct LtOperand {
     static constexpr int LOADS = R * LT_BK * 2 / (NTH * 16);   // 16-byte loads a thread and block
     static constexpr int RB = KS ? R * 2 : LT_BK * 2;          // bytes of an LDS row
@@ -70,7 +71,7 @@ struct LtOperand {
     static constexpr int LROWS = EVEN ? NTH / PIECES : 0, OWN = EVEN ? 1 : LOADS;
     const unsigned char *base;
     uint32_t ld, last;    // bytes: of a row; kc: of the last row (512 ld < 2^32)
-    int K;
+    int K, k0, wrap;
     uint32_t off[OWN];    // of this thread's (first) row
     uint32_t col[KS ? OWN : 1];   // ks: of its column
 
@@ -120,6 +121,11 @@ struct LtOperand {
             const uint32_t k = min(kb * LT_BK + piece(0) * 8, ((K + 7) & ~7) - 8) * 2;
             dma16(base + (min(row, last) + k), to);
         } else {
+            if constexpr (WRAP) {
+                const int k = k0 + min(kb * LT_BK + lrow(i), K - 1);
+                dma16(base + (int64_t)(k < wrap ? k : k - wrap) * ld + col[EVEN ? 0 : i], to);
+                return;
+            }
             const uint32_t end = (uint32_t)min(K - 1 - kb * LT_BK, LT_BK - 1) * ld;
             dma16(base + (int64_t)kb * LT_BK * ld + (min(row, end) + col[EVEN ? 0 : i]), to);
         }
@@ -350,12 +356,12 @@ __device__ __forceinline__ void lt_epilogue_f32(const LinArgs &a, LtAcc<F> &acc,
     }
 }
 
-template <typename F, bool AKS, bool BKS>
+template <typename F, bool AKS, bool BKS, bool WRAP>
 __global__ __launch_bounds__(F::THREADS, 2) void linear_tile_kernel(LinArgs a)
 {
     constexpr int BM = F::BM, BN = F::BN, NS = F::NS, STAGE = F::STAGE, FM = F::FM, FN = F::FN;
     typedef LtOperand<BM, AKS, F::NTH> OA;
-    typedef LtOperand<BN, BKS, F::NTH> OB;
+    typedef LtOperand<BN, BKS, F::NTH, WRAP> OB;
     constexpr int P = OA::LOADS + OB::LOADS;
     constexpr int AB = BM * LT_BK * 2;          // B's place in a stage
     // Of the row fragments the first ROLL are read into the registers that their own
@@ -386,7 +392,9 @@ __global__ __launch_bounds__(F::THREADS, 2) void linear_tile_kernel(LinArgs a)
     OB ob;
     const int64_t k0 = (int64_t)min(kb0, kall - 1) * LT_BK;
     oa.init(a.a + k0 * (AKS ? a.lda : 1), a.lda, m0, a.M, K);
-    ob.init(a.b + k0 * (BKS ? a.ldb : 1), a.ldb, n0, a.N, K);
+    ob.init(a.b + (WRAP ? 0 : k0 * (BKS ? a.ldb : 1)), a.ldb, n0, a.N, K);
+    ob.k0 = (int)k0;
+    ob.wrap = a.wrap;
 
     LtAcc<F> acc;
 #pragma unroll
@@ -571,18 +579,18 @@ __global__ __launch_bounds__(256) void linear_join_kernel(LinArgs a, const float
     }
 }
 
-template <typename F, bool AKS, bool BKS>
+template <typename F, bool AKS, bool BKS, bool WRAP>
 static int launch_tile_t(const LinArgs &a, hipStream_t s)
 {
     static LdsLimit limit;
     const int64_t items =
         (int64_t)((a.M + F::BM - 1) / F::BM) * ((a.N + F::BN - 1) / F::BN) * a.splits;
-    const int rc = limit.raise((const void *)linear_tile_kernel<F, AKS, BKS>, 160 * 1024);
+    const int rc = limit.raise((const void *)linear_tile_kernel<F, AKS, BKS, WRAP>, 160 * 1024);
     if (rc)
         return rc;
     const unsigned grid = (unsigned)((items + LT_NXCD - 1) / LT_NXCD * LT_NXCD);
-    hipLaunchKernelGGL((linear_tile_kernel<F, AKS, BKS>), dim3(grid), dim3(F::THREADS), F::lds(), s,
-                       a);
+    hipLaunchKernelGGL((linear_tile_kernel<F, AKS, BKS, WRAP>), dim3(grid), dim3(F::THREADS),
+                       F::lds(), s, a);
     MOE_LAUNCH_CHECK("linear_tile_kernel");
     return MOE_OK;
 }
@@ -591,8 +599,16 @@ template <typename F>
 static int launch_tile(const LinArgs &a, hipStream_t s)
 {
     if (a.a_ks)
-        return launch_tile_t<F, true, true>(a, s);
-    return a.b_ks ? launch_tile_t<F, false, true>(a, s) : launch_tile_t<F, false, false>(a, s);
+        return launch_tile_t<F, true, true, false>(a, s);
+    return a.b_ks ? launch_tile_t<F, false, true, false>(a, s)
+                  : launch_tile_t<F, false, false, false>(a, s);
+}
+template <typename F>
+static int launch_small(const LinArgs &a, hipStream_t s)
+{
+    if (!a.wrap)
+        return launch_tile<F>(a, s);
+    return a.a_ks ? launch_tile_t<F, true, true, true>(a, s) : launch_tile_t<F, false, true, true>(a, s);
 }
 
 // The forms in the order of LinPlan::form (what each is for: linear_plan).
@@ -625,10 +641,10 @@ int launch_linear_tile(LinArgs a, const LinPlan &p, void *ws, hipStream_t s)
     }
     int rc;
     switch (p.form) {
-    case 0: rc = launch_tile<LtF0>(part, s); break;
-    case 1: rc = launch_tile<LtF1>(part, s); break;
-    case 2: rc = launch_tile<LtF2>(part, s); break;
-    case 3: rc = launch_tile<LtF3>(part, s); break;
+    case 0: rc = launch_small<LtF0>(part, s); break;   // LIN_SMALL of them
+    case 1: rc = launch_small<LtF1>(part, s); break;
+    case 2: rc = launch_small<LtF2>(part, s); break;
+    case 3: rc = launch_small<LtF3>(part, s); break;
     case 4: rc = launch_tile<LtF4>(part, s); break;
     case 5: rc = launch_tile<LtF5>(part, s); break;
     case 6: rc = launch_tile<LtF6>(part, s); break;

@@ -230,6 +230,52 @@ def test_backward(m, n, k, dtype, act):
         assert torch.equal(alone[i], (dx, dw, db)[i])
 
 
+@pytest.mark.parametrize("act", ["silu", "gelu", "relu"])
+@pytest.mark.parametrize("m,n,k", [(1, 5632, 2048), (3, 17, 24), (4, 1407, 520), (100, 63, 520),
+                                   (127, 64, 1000), (4099, 16, 32), (20, 1000, 64)])
+def test_backward_few_values(m, n, k, act):
+    """No rounding but the gradients' own where few values are: dz carries its rest."""
+    say("linear backward, few values: %dx%dx%d %s" % (m, n, k, act))
+    g = torch.Generator().manual_seed(m + n)
+    x, w = put(rand(g, m, k), 0), put(0.05 * rand(g, n, k), 8)
+    dy, z = put(rand(g, m, n), 1), put(2 * rand(g, m, n), 3)
+    dx, dw = (torch.full((r, k + 5), -3.0, dtype=torch.float16, device=DEV) for r in (m, n))
+    backward(dy, z, act, x, w, m, n, k, "f16", dx, dw, None)
+    torch.cuda.synchronize()
+    zv = f64(z, n)
+    dz = f64(dy, n) * R.act_grad_ref(zv, act)
+    # dz in fp32 (16 half steps of dy as elsewhere) and the rest's own rounding: the first
+    # fp16 lies up to a whole step before dz, the rest is up to 2^-10 of it and rounded
+    # by 2^-11 of itself, or to the smallest subnormal
+    ez = 16 * U * f64(dy, n).abs() + 2.0 ** -21 * dz.abs() + R.tiny(torch.float16)
+    h, t = R.half_step(torch.float16), R.tiny(torch.float16)
+    for got, want, size, es, terms in (
+            (dx, dz @ f64(w, k), dz.abs() @ f64(w, k).abs(), ez @ f64(w, k).abs(), 2 * n),
+            (dw, dz.t() @ f64(x, k), dz.abs().t() @ f64(x, k).abs(), ez.t() @ f64(x, k).abs(), 2 * m)):
+        e = sum_bound(terms) * (size + es) + es
+        check(got[:, :k], want, e + h * (want.abs() + e) + t, l2_bound("f16", terms) + 8 * U,
+              "dx" if terms == 2 * n else "dw")
+        assert (got[:, k:] == -3.0).all()
+
+
+def test_backward_few_values_not_finite():
+    """An infinite weight and a gradient beyond fp16 stay infinities, with their signs."""
+    n, k = 70, 64
+    g = torch.Generator().manual_seed(3)
+    x, w = put(rand(g, 2, k), 0), put(rand(g, n, k), 0)
+    dy, z = put(rand(g, 2, n).abs() + 0.5, 0), put(rand(g, 2, n).abs() + 4, 0)   # act' about one
+    w[n - 1, 5], w[3, 9] = float("inf"), -float("inf")
+    dy[1, 7] = float("inf")
+    dx, dw = torch.empty_like(x), torch.empty_like(w)
+    backward(dy, z, "silu", x, w, 2, n, k, "f16", dx, dw, None)
+    assert dx[0, 5] == float("inf") and dx[0, 9] == -float("inf")
+    cols = [i for i in range(k) if i not in (5, 9)]
+    assert torch.isfinite(dx[0, cols]).all()
+    assert torch.equal(dx[1, cols], torch.sign(w[7, cols].float()).half() * float("inf"))
+    assert torch.isinf(dw[7]).all() and torch.isfinite(dw[:7]).all() and torch.isfinite(dw[8:]).all()
+
+
+
 @pytest.mark.parametrize("act", list(R.ACTS))
 def test_activation_gradients(act):
     """dz through the unit matrix: every act' over z from -20 to 20, against the
