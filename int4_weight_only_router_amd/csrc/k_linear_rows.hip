@@ -5,7 +5,7 @@
 // of the row an instruction, four in flight), each lane multiplying its eight k with
 // those of the tokens (v_dot2_f32_f16, fp32 sums); the lanes meet at the end.  No
 // LDS, no barrier.  Out of memory, in a captured run of calls: one row of 5632 x 2048
-// 6.0 us (3.8 TB/s), of 11264 x 2048 9.6 (4.8), two rows 6.7 and 10.8; for more rows
+// 5.9 us (3.9 TB/s), of 11264 x 2048 9.8 (4.7), two rows 6.5 and 10.6; for more rows
 // the tokens' loads and sums outweigh the stream (four 8.9, eight 11, sixteen 17),
 // and the 16-row tiles (8.4 for any of them) are faster.
 #include <algorithm>
