@@ -113,6 +113,16 @@ class BlockNorms:
             raise ValueError("norm weights must all be fp16 or all fp32")
         self.w_dtype = A.MOE_DTYPE_F32 if torch.float32 in types else A.MOE_DTYPE_F16
 
+    def check(self, H):
+        """ValueError where a weight or the gate is not of rows of H."""
+        for w in (self.pre_w, self.pre_b, self.post_w, self.post_b, self.gate):
+            if w is not None and (w.numel() != H or not w.is_contiguous()):
+                raise ValueError("norm weights and gates must be contiguous, of %d values" % H)
+        if self.gate is not None and self.gate.dtype != torch.float16:
+            raise ValueError("the gate must be fp16")
+        if not self.post and (self.post_w is not None or self.post_b is not None):
+            raise ValueError("post-norm weights without post")
+
     @property
     def form(self):
         """What the norms of a stack have in common."""
@@ -212,6 +222,8 @@ class MoELayer:
             raise ValueError("a shared-expert gate needs a shared expert")
         self.flags = A.MOE_RENORM if renorm else 0
         self.routing = routing
+        if norms is not None:
+            norms.check(H)
         self.norms = norms
         self.device = device
 
@@ -444,6 +456,13 @@ class MoELayer:
         leaves, and the logits' gradient times d_loss (fp32 [1] device, such as a loss
         scale: the gradient is fp16), into g.  Scores as the layer's router forms
         them, without the selection's bias.  Returns g.losses."""
+        if g.dlogits.shape[0] != b.T:
+            raise ValueError("balance buffers of %d tokens, not %d" % (g.dlogits.shape[0], b.T))
+        if mask is not None and (mask.numel() != b.T or mask.element_size() != 1
+                                 or not mask.is_contiguous()):
+            raise ValueError("the mask must hold %d bytes" % b.T)
+        if d_loss is not None and (d_loss.dtype != torch.float32 or d_loss.numel() != 1):
+            raise ValueError("d_loss must be one fp32 value")
         logits = b.logits
         if logits is None:
             logits = g.logits
@@ -457,6 +476,8 @@ class MoELayer:
     def router_backward(self, x, g: BalanceBuffers, stream=None):
         """Gradients of the router's weights, of its bias and of x from g.dlogits (from
         balance), into g.d_router, g.d_bias and g.dx: fp32, times balance's d_loss."""
+        if x.shape[0] != g.dlogits.shape[0]:
+            raise ValueError("x has %d rows, the buffers %d" % (x.shape[0], g.dlogits.shape[0]))
         A.moe_linear_f16_backward(g.dlogits, self.E, None, 0, A.MOE_ACT_NONE, x, self.H,
                                   self.router, self.H, g.dlogits.shape[0], self.E, self.H, g.dx,
                                   self.H, g.d_router, self.H, A.MOE_DTYPE_F32, g.d_bias, g.ws,

@@ -61,3 +61,30 @@ def test_buffers():
     need = M.moe_linear_f16_workspace_bytes(3, 4, 2560)
     ws = wide.buffers(3).router_ws
     assert (0 if ws is None else ws.numel()) == need
+
+
+@pytest.mark.parametrize("norms,match", [
+    (BlockNorms(torch.ones(H - 1, dtype=torch.float16)), "values"),
+    (BlockNorms(w(), gate=torch.ones(2 * H, dtype=torch.float16)), "values"),
+    (BlockNorms(torch.ones(2 * H, dtype=torch.float16)[::2]), "contiguous"),
+    (BlockNorms(w(), gate=w(torch.float32)), "gate"),
+    (BlockNorms(w(), post_w=w()), "post")])
+def test_layer_refuses_norms(norms, match):
+    with pytest.raises(ValueError, match=match):
+        _layer(norms)
+
+
+def test_balance_refusals():
+    lay = _layer(None)
+    b, g = lay.buffers(3), lay.balance_buffers(3)
+    x = torch.zeros((3, H), dtype=torch.float16)
+    with pytest.raises(ValueError, match="tokens"):
+        lay.balance(x, b, lay.balance_buffers(2), 0.1)
+    for mask in (torch.ones(2, dtype=torch.uint8), torch.ones(3, dtype=torch.int32),
+                 torch.ones(6, dtype=torch.uint8)[::2]):
+        with pytest.raises(ValueError, match="mask"):
+            lay.balance(x, b, g, 0.1, mask=mask)
+    with pytest.raises(ValueError, match="d_loss"):
+        lay.balance(x, b, g, 0.1, d_loss=torch.ones(1, dtype=torch.float16))
+    with pytest.raises(ValueError, match="rows"):
+        lay.router_backward(x[:2], g)
