@@ -75,22 +75,32 @@ __device__ __forceinline__ float wave_max(float v)
 }
 
 // Choices and unmasked tokens of the tokens t0 <= t < t1 into hist (LDS [E]) and
-// the return value (this thread's share).
+// the return value (this thread's share).  (T k < 2^31; a choice and its token's mask
+// are loaded together, several of them before the first is counted.)
 template <int THREADS>
-__device__ __forceinline__ int count_tokens(const BalanceArgs &a, int64_t t0, int64_t t1, int *hist)
+__device__ __forceinline__ int count_tokens(const BalanceArgs &a, int t0, int t1, int *hist)
 {
     int n = 0;
     if (a.mask)
-        for (int64_t t = t0 + threadIdx.x; t < t1; t += THREADS)
+        for (int64_t t = t0 + (int)threadIdx.x; t < t1; t += THREADS)
             n += a.mask[t] != 0;
-    if (a.idx) {
-        const int64_t i1 = t1 * a.k;
-#pragma unroll 4
-        for (int64_t i = t0 * a.k + threadIdx.x; i < i1; i += THREADS) {
-            const int e = a.idx[i];
-            if ((unsigned)e < (unsigned)a.E && (!a.mask || a.mask[i / a.k]))
-                atomicAdd(&hist[e], 1);
+    if (!a.idx)
+        return n;
+    constexpr int U = 4;
+    const unsigned i1 = (unsigned)t1 * a.k, k = a.k;
+    for (unsigned i0 = (unsigned)t0 * k + threadIdx.x; i0 < i1; i0 += U * THREADS) {
+        int e[U];
+        uint8_t on[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const unsigned i = min(i0 + u * THREADS, i1 - 1);
+            e[u] = a.idx[i];
+            on[u] = a.mask ? a.mask[i / k] : 1;
         }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (i0 + u * THREADS < i1 && (unsigned)e[u] < (unsigned)a.E && on[u])
+                atomicAdd(&hist[e[u]], 1);
     }
     return n;
 }
@@ -275,8 +285,8 @@ __global__ __launch_bounds__(BL_THREADS) void balance_count_kernel(BalanceArgs a
         hist[e] = 0;
     __syncthreads();
     const int64_t each = ((int64_t)a.T + gridDim.x - 1) / gridDim.x;
-    const int64_t t0 = blockIdx.x * each;
-    const int own = wave_sum_int(count_tokens<BL_THREADS>(a, t0, min(t0 + each, (int64_t)a.T), hist));
+    const int t0 = (int)min(blockIdx.x * each, (int64_t)a.T), t1 = (int)min(t0 + each, (int64_t)a.T);
+    const int own = wave_sum_int(count_tokens<BL_THREADS>(a, t0, t1, hist));
     if ((threadIdx.x & 63) == 0)
         s[threadIdx.x >> 6] = own;
     __syncthreads();
