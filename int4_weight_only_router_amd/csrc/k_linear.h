@@ -77,7 +77,7 @@ struct LinPlan {
 constexpr int64_t LIN_MOST_ITEMS = (1 << 22) - 8;   // a launch has fewer than 2^32 threads
 constexpr int LIN_MOST_LD = 1 << 22;                // offsets inside a tile are 32 bits wide
 // across: operands whose rows run across k (b, then a too); small: by one of the first
-// LIN_SMALL forms
+// LIN_SMALL forms (those that can start over in b)
 constexpr int LIN_SMALL = 4;
 LinPlan linear_plan(int M, int N, int K, int across, bool small = false);
 int launch_linear_tile(LinArgs, const LinPlan &, void *ws, hipStream_t);

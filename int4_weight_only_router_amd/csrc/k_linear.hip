@@ -15,8 +15,9 @@ namespace moe {
 // compute units busy with one to eight workgroups each): a workgroup `end` for its
 // first loads and its results and `one` for a block of 64 k (of its group, where
 // groups share k); two workgroups on a compute unit together `two` for a block of each.
-// The smallest form reads 32 and 64 bytes at a time of an operand whose rows run across
-// k, and takes across[0] for a block where b is such, across[1] where both are.
+// The smallest form reads 64 bytes at a time of a b whose rows run across k, and takes
+// `across` for a block then; it is not used where a is such too (32 bytes at a time: 64 x
+// 2048 x 4096 14.4 us, 32-row tiles in four parts 11.0).
 //
 // With them the form and the parts of k that take the least time are chosen.  On 90
 // products from 1 x 1024 x 256 to 8192 x 8192 x 8192 the choice was the fastest form
@@ -27,13 +28,13 @@ namespace moe {
 // 154, 192-row 163; at K = 5632 64 x 2048 16-row 9.7, 32-row in four parts 11.1).
 struct LinForm {
     int bm, bn, kg, per_cu;
-    double end, one, two, across[2];
+    double end, one, two, across;
 };
 static const LinForm FORMS[] = {
-    {16, 32, 8, 1, 3.0, 0.50, 0, {0.80, 1.30}},   {32, 64, 2, 1, 2.2, 0.30, 0, {0.30, 0.30}},
-    {64, 64, 2, 1, 2.2, 0.44, 0, {0.44, 0.44}},   {64, 64, 1, 2, 0.9, 0.33, 0.33, {0.33, 0.33}},
-    {128, 128, 1, 1, 3.5, 0.50, 0, {0.50, 0.50}}, {128, 128, 1, 2, 1.8, 0.72, 0.90, {0.72, 0.72}},
-    {192, 256, 1, 1, 6.0, 1.13, 0, {1.13, 1.13}}, {256, 256, 1, 1, 5.0, 1.45, 0, {1.45, 1.45}}};
+    {16, 32, 8, 1, 3.0, 0.50, 0, 0.80},      {32, 64, 2, 1, 2.2, 0.30, 0, 0.30},
+    {64, 64, 2, 1, 2.2, 0.44, 0, 0.44},      {64, 64, 1, 2, 0.9, 0.33, 0.33, 0.33},
+    {128, 128, 1, 1, 3.5, 0.50, 0, 0.50},    {128, 128, 1, 2, 1.8, 0.72, 0.90, 0.72},
+    {192, 256, 1, 1, 6.0, 1.13, 0, 1.13},    {256, 256, 1, 1, 5.0, 1.45, 0, 1.45}};
 
 LinPlan linear_plan(int M, int N, int K, int across, bool small)
 {
@@ -42,7 +43,9 @@ LinPlan linear_plan(int M, int N, int K, int across, bool small)
     const int nkb = (int)(((int64_t)K + 63) / 64);
     for (int f = 0; f < (small ? LIN_SMALL : 8); ++f) {
         const LinForm &o = FORMS[f];
-        const double one = across ? o.across[across - 1] : o.one;
+        if ((f == 0 && across == 2) || (small && f == 2))   // (never the fastest for so few values)
+            continue;
+        const double one = across ? o.across : o.one;
         const int64_t tiles = ((int64_t)M + o.bm - 1) / o.bm * (((int64_t)N + o.bn - 1) / o.bn);
         for (int s = 1; s <= 8; s *= 2) {
             const int each = (nkb + s - 1) / s;

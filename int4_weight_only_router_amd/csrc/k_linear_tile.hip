@@ -602,20 +602,25 @@ static int launch_tile_t(const LinArgs &a, hipStream_t s)
     return MOE_OK;
 }
 
-template <typename F>
+// BOTH: the form takes products both of whose operands run across k, WRAPS: such as start
+// over in b (linear_plan chooses no other form for those).
+template <typename F, bool BOTH, bool WRAPS>
 static int launch_tile(const LinArgs &a, hipStream_t s)
 {
-    if (a.a_ks)
-        return launch_tile_t<F, true, true, false>(a, s);
+    if ((a.a_ks && !BOTH) || (a.wrap && !WRAPS))
+        return set_error(MOE_EUNSUPPORTED, "linear_tile_kernel: no such form");
+    if constexpr (WRAPS)
+        if (a.wrap) {
+            if constexpr (BOTH)
+                if (a.a_ks)
+                    return launch_tile_t<F, true, true, true>(a, s);
+            return launch_tile_t<F, false, true, true>(a, s);
+        }
+    if constexpr (BOTH)
+        if (a.a_ks)
+            return launch_tile_t<F, true, true, false>(a, s);
     return a.b_ks ? launch_tile_t<F, false, true, false>(a, s)
                   : launch_tile_t<F, false, false, false>(a, s);
-}
-template <typename F>
-static int launch_small(const LinArgs &a, hipStream_t s)
-{
-    if (!a.wrap)
-        return launch_tile<F>(a, s);
-    return a.a_ks ? launch_tile_t<F, true, true, true>(a, s) : launch_tile_t<F, false, true, true>(a, s);
 }
 
 // The forms in the order of LinPlan::form (what each is for: linear_plan).
@@ -648,14 +653,14 @@ int launch_linear_tile(LinArgs a, const LinPlan &p, void *ws, hipStream_t s)
     }
     int rc;
     switch (p.form) {
-    case 0: rc = launch_small<LtF0>(part, s); break;   // LIN_SMALL of them
-    case 1: rc = launch_small<LtF1>(part, s); break;
-    case 2: rc = launch_small<LtF2>(part, s); break;
-    case 3: rc = launch_small<LtF3>(part, s); break;
-    case 4: rc = launch_tile<LtF4>(part, s); break;
-    case 5: rc = launch_tile<LtF5>(part, s); break;
-    case 6: rc = launch_tile<LtF6>(part, s); break;
-    default: rc = launch_tile<LtF7>(part, s); break;
+    case 0: rc = launch_tile<LtF0, false, true>(part, s); break;
+    case 1: rc = launch_tile<LtF1, true, true>(part, s); break;
+    case 2: rc = launch_tile<LtF2, true, false>(part, s); break;
+    case 3: rc = launch_tile<LtF3, true, true>(part, s); break;
+    case 4: rc = launch_tile<LtF4, true, false>(part, s); break;
+    case 5: rc = launch_tile<LtF5, true, false>(part, s); break;
+    case 6: rc = launch_tile<LtF6, true, false>(part, s); break;
+    default: rc = launch_tile<LtF7, true, false>(part, s); break;
     }
     if (rc || a.splits == 1)
         return rc;
