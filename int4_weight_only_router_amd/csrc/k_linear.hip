@@ -25,7 +25,8 @@ namespace moe {
 // 32-row 7.6; 333 x 1408 32-row 8.2, 64-row 9.0; 256 x 5632 64-row 13.7, 128-row
 // 17.3; 2048 x 2048 128-row of eight waves 20.8, of four 26.8; 4096 x 2048 the other
 // way round, 35.7 and 39.8; 4096 x 5632 192-row 86, 256-row 95; 4096 x 11264 256-row
-// 154, 192-row 163; at K = 5632 64 x 2048 16-row 9.7, 32-row in four parts 11.1).
+// 154, 192-row 163; at K = 5632 64 x 2048 16-row 9.7, 32-row in four parts 11.1, 4096
+// x 2048 256 x 128 90, 128-row 94).
 struct LinForm {
     int bm, bn, kg, per_cu;
     double end, one, two, across;
@@ -34,16 +35,18 @@ static const LinForm FORMS[] = {
     {16, 32, 8, 1, 3.0, 0.50, 0, 0.80},      {32, 64, 2, 1, 2.2, 0.30, 0, 0.30},
     {64, 64, 2, 1, 2.2, 0.44, 0, 0.44},      {64, 64, 1, 2, 0.9, 0.33, 0.33, 0.33},
     {128, 128, 1, 1, 3.5, 0.50, 0, 0.50},    {128, 128, 1, 2, 1.8, 0.72, 0.90, 0.72},
-    {192, 256, 1, 1, 6.0, 1.13, 0, 1.13},    {256, 256, 1, 1, 5.0, 1.45, 0, 1.45}};
+    {192, 256, 1, 1, 6.0, 1.13, 0, 1.13},    {256, 256, 1, 1, 5.0, 1.45, 0, 1.45},
+    {256, 128, 1, 1, 4.4, 0.875, 0, 0.875}};
+constexpr int NFORMS = sizeof(FORMS) / sizeof(FORMS[0]);
 
 LinPlan linear_plan(int M, int N, int K, int across, bool small)
 {
     LinPlan best{};
     double least = 1e300;
     const int nkb = (int)(((int64_t)K + 63) / 64);
-    for (int f = 0; f < (small ? LIN_SMALL : 8); ++f) {
+    for (int f = 0; f < (small ? LIN_SMALL : NFORMS); ++f) {
         const LinForm &o = FORMS[f];
-        if ((f == 0 && across == 2) || (small && f == 2))   // (never the fastest for so few values)
+        if ((across == 2 && (f == 0 || f == 8)) || (small && f == 2))   // (never the fastest there)
             continue;
         const double one = across ? o.across : o.one;
         const int64_t tiles = ((int64_t)M + o.bm - 1) / o.bm * (((int64_t)N + o.bn - 1) / o.bn);

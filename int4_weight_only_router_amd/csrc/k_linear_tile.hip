@@ -632,6 +632,7 @@ typedef LtForm<128, 128, 2, 4, 1, 4> LtF4;
 typedef LtForm<128, 128, 2, 2, 1, 2> LtF5;
 typedef LtForm<192, 256, 2, 4, 1, 2> LtF6;
 typedef LtForm<256, 256, 2, 4, 1, 2> LtF7;
+typedef LtForm<256, 128, 4, 2, 1, 3> LtF8;
 
 int launch_linear_tile(LinArgs a, const LinPlan &p, void *ws, hipStream_t s)
 {
@@ -660,7 +661,8 @@ int launch_linear_tile(LinArgs a, const LinPlan &p, void *ws, hipStream_t s)
     case 4: rc = launch_tile<LtF4, true, false>(part, s); break;
     case 5: rc = launch_tile<LtF5, true, false>(part, s); break;
     case 6: rc = launch_tile<LtF6, true, false>(part, s); break;
-    default: rc = launch_tile<LtF7, true, false>(part, s); break;
+    case 7: rc = launch_tile<LtF7, true, false>(part, s); break;
+    default: rc = launch_tile<LtF8, false, false>(part, s); break;
     }
     if (rc || a.splits == 1)
         return rc;

@@ -170,7 +170,8 @@ def backward(dy, z, act, x, w, m, n, k, dtype, dx, dw, db, stream=None, ws=None)
 @pytest.mark.parametrize("dtype", ["f16", "f32"])
 @pytest.mark.parametrize("bias", [False, True])
 @pytest.mark.parametrize("m,n,k", [(70, 131, 72), (1000, 1003, 264), (2050, 2054, 136),
-                                   (4100, 5009, 72), (4100, 8200, 64)])
+                                   (4100, 5009, 72), (4100, 8200, 64), (2050, 2055, 2504),
+                                   (4100, 5001, 264)])
 def test_sums_and_bias_only(m, n, k, bias, dtype):
     """Nothing but the sums and a bias leaves: of every tile's form."""
     say("linear sums %dx%dx%d %s" % (m, n, k, dtype))
@@ -191,7 +192,8 @@ def test_sums_and_bias_only(m, n, k, bias, dtype):
 BACKWARD = [(1, 64, 64), (2, 1, 8), (3, 17, 24), (16, 1408, 2048), (33, 300, 520), (64, 60, 2048),
             (65, 1000, 8), (130, 257, 1032), (255, 256, 264), (333, 1408, 2000), (777, 60, 2048),
             (1000, 1000, 1000), (1025, 520, 264), (4096, 64, 2048), (4099, 3, 256),
-            (33000, 24, 64), (70001, 7, 8)]
+            (33000, 24, 64), (70001, 7, 8), (2050, 2505, 2056), (264, 4100, 5000),
+            (4100, 72, 8200)]
 
 
 @pytest.mark.parametrize("dtype,act", [("f16", "silu"), ("f32", "none"), ("f16", "none")])
