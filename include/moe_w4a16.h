@@ -75,6 +75,8 @@ enum { MOE_NORM_POST = 1u, MOE_NORM_UNIT_OFFSET = 2u };
  * tanh form */
 enum { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_SILU = 2, MOE_ACT_GELU = 3,
        MOE_ACT_GELU_TANH = 4 };
+/* OR'd into out_dtype of moe_linear_f16_backward: dz is rounded to fp16. */
+enum { MOE_DZ_F16 = 0x1000 };
 /* OR'd into out_dtype of moe_gemm_fp8 and into the regime of
  * moe_expert_ffn_w8a8(_plan): every sum has fp32 accuracy, whatever the sizes. */
 enum { MOE_ACC_F32 = 0x800 };
@@ -744,12 +746,15 @@ int moe_linear_f16(const void *x_f16, int64_t ldx, const void *w_f16, int64_t ld
  *   dbias   device fp32 [N] or NULL, from the unrounded dz
  *   ws      device scratch of moe_linear_f16_backward_workspace_bytes(M, N, K)
  *           bytes, as above
- * dz is rounded to fp16 for the products (exact with MOE_ACT_NONE and RELU; where dz,
- * dx or dw have few values, it enters as the sum of two fp16), so out_dtype F32 is for
- * MOE_ACT_NONE only (MOE_EUNSUPPORTED).  Gradients that would leave
- * fp16's range belong scaled by the caller.  Limits as above, for the products of
- * dx and dw, whichever is asked for, and N at most 2^22 (MOE_EUNSUPPORTED); lddy, ldz,
- * lddx and lddw are free.  M = 0: dw and dbias are set to zero.
+ * dz enters the products as it is with MOE_ACT_NONE and RELU, else as the sum of two
+ * fp16 (off by 2^-21 of it, or 2^-25), at every size; so the products take twice the
+ * operations.  With MOE_DZ_F16 OR'd into out_dtype it is rounded to one: half the
+ * time, and 1.4 times the error in dx and dw (dbias is not affected).  out_dtype F32
+ * is for MOE_ACT_NONE only (MOE_EUNSUPPORTED), and bits of out_dtype besides are refused.
+ * Gradients that would leave fp16's range belong scaled by the caller.  Limits as above,
+ * for the products of dx and dw, whichever is asked for, N at most 2^22, and M at most
+ * 2^29 where dz is two fp16 (MOE_EUNSUPPORTED); lddy, ldz, lddx and lddw are free.
+ * M = 0: dw and dbias are set to zero.
  */
 size_t moe_linear_f16_backward_workspace_bytes(int M, int N, int K);
 int moe_linear_f16_backward(const void *dy_f16, int64_t lddy, const void *z_f16, int64_t ldz,

@@ -13,7 +13,7 @@ __all__ = [
     "MOE_DTYPE_F16", "MOE_DTYPE_F32", "MOE_DTYPE_F32_PM", "MOE_DTYPE_BF16",
     "MOE_GROUP_TOP2", "MOE_SCORE_SOFTMAX", "MOE_SCORE_SIGMOID", "MOE_SCALE_POW2", "MOE_ACC_F32", "MOE_FMT_SYM", "MOE_FMT_ZP", "MOE_FMT_FP8", "MOE_W4_ZERO_POINT", "EXPORTS",
     "MOE_NORM_RMS", "MOE_NORM_LAYER", "MOE_NORM_POST", "MOE_NORM_UNIT_OFFSET", "MOE_ACT_NONE",
-    "MOE_ACT_RELU", "MOE_ACT_SILU", "MOE_ACT_GELU", "MOE_ACT_GELU_TANH",
+    "MOE_ACT_RELU", "MOE_ACT_SILU", "MOE_ACT_GELU", "MOE_ACT_GELU_TANH", "MOE_DZ_F16",
     "moe_blob_layout_fmt", "moe_quantize_experts_fmt", "moe_prepack_experts_fmt",
     "moe_unpack_experts_fmt", "moe_prepack_expert_host", "moe_unpack_expert_host",
     "moe_last_error", "moe_workspace_clear", "moe_blob_layout", "moe_quantize_experts",
@@ -54,6 +54,7 @@ MOE_ACC_F32 = 0x800         # OR'd into moe_gemm_fp8's out_dtype and a w8a8 regi
 MOE_NORM_RMS, MOE_NORM_LAYER = 0, 1
 MOE_NORM_POST, MOE_NORM_UNIT_OFFSET = 1, 2   # moe_block_norm flags
 MOE_ACT_NONE, MOE_ACT_RELU, MOE_ACT_SILU, MOE_ACT_GELU, MOE_ACT_GELU_TANH = 0, 1, 2, 3, 4
+MOE_DZ_F16 = 0x1000         # OR'd into moe_linear_f16_backward's out_dtype: dz in one fp16
 MOE_FMT_SYM, MOE_FMT_ZP = 0, 1   # expert blob formats (zero point per group)
 MOE_FMT_FP8 = 2                  # e4m3 blobs (moe_fp8_blob_layout); no argument of the _fmt calls
 MOE_W4_ZERO_POINT = 0x200        # OR'd into a regime: the blobs are MOE_FMT_ZP

@@ -320,6 +320,8 @@ int moe_linear_f16_backward(const void *dy_f16, int64_t lddy, const void *z_f16,
     MOE_API_RANGE();
     clear_error();
     const char *fn = "moe_linear_f16_backward";
+    const bool rounded = out_dtype & MOE_DZ_F16;
+    out_dtype &= ~MOE_DZ_F16;
     int rc = check_linear(fn, M, N, K, act, out_dtype);
     if (rc)
         return rc;
@@ -331,15 +333,16 @@ int moe_linear_f16_backward(const void *dy_f16, int64_t lddy, const void *z_f16,
                          "%s: K, ldx and ldw must be multiples of 8 (K=%d ldx=%lld ldw=%lld)", fn, K,
                          (long long)ldx, (long long)ldw);
     const bool far = (dw && ldx > LIN_MOST_LD) || (dx && ldw > LIN_MOST_LD) || N > LIN_MOST_LD;
+    const bool two = !rounded && !linear_dz_exact(act);
     const LinGradPlan plan = far || M == 0 ? LinGradPlan{} : linear_grad_plan(M, N, K);
-    if (far || (M > 0 && !plan.fits))
+    if (far || (M > 0 && !(two ? plan.fits2 : plan.fits)))
         return set_error(MOE_EUNSUPPORTED,
                          "%s: rows of at most %d elements and %lld tiles (M=%d N=%d K=%d ldx=%lld "
                          "ldw=%lld)", fn, LIN_MOST_LD, (long long)LIN_MOST_ITEMS, M, N, K,
                          (long long)ldx, (long long)ldw);
     if (act != MOE_ACT_NONE && out_dtype == MOE_DTYPE_F32)
         return set_error(MOE_EUNSUPPORTED,
-                         "%s: fp32 gradients through an activation (dz is rounded to fp16)", fn);
+                         "%s: fp32 gradients through an activation", fn);
     if (!dx && !dw && !dbias)
         return set_error(MOE_EINVAL, "%s: no gradient asked for", fn);
     if (M > 0 && (!dy_f16 || (act != MOE_ACT_NONE && !z_f16) || (dw && !x_f16) || (dx && !w_f16)))
@@ -372,6 +375,7 @@ int moe_linear_f16_backward(const void *dy_f16, int64_t lddy, const void *z_f16,
     g.dw = dw;
     g.lddw = lddw;
     g.odt = out_dtype;
+    g.two = two;
     g.dbias = dbias;
     return launch_linear_backward(g, plan, ws, stream);
 }

@@ -50,7 +50,9 @@ struct LinArgs {
     const f16 *a, *b;
     int64_t lda, ldb;
     bool a_ks, b_ks;
-    int wrap;   // b_ks: k from here on starts over in b (0: nowhere)
+    // b_ks: every k of b twice, for the two fp16 of a's; a_ks: one after the other, else
+    // all of them over again
+    bool twice;
     int M, N, K;
     const float *bias;
     int act;
@@ -75,11 +77,12 @@ struct LinPlan {
     int64_t items;   // workgroups
 };
 constexpr int64_t LIN_MOST_ITEMS = (1 << 22) - 8;   // a launch has fewer than 2^32 threads
-constexpr int LIN_MOST_LD = 1 << 22;                // offsets inside a tile are 32 bits wide
-// across: operands whose rows run across k (b, then a too); small: by one of the first
-// LIN_SMALL forms (those that can start over in b)
-constexpr int LIN_SMALL = 4;
-LinPlan linear_plan(int M, int N, int K, int across, bool small = false);
+// Offsets inside a tile of up to 256 rows are 32 bits wide; dz's rows hold two values for
+// each of its columns.
+constexpr int LIN_MOST_LD = 1 << 22;
+constexpr int LIN_MOST_TWICE = 1 << 29;             // rows whose every k is passed twice
+// across: operands whose rows run across k (b, then a too)
+LinPlan linear_plan(int M, int N, int K, int across);
 int launch_linear_tile(LinArgs, const LinPlan &, void *ws, hipStream_t);
 constexpr int LIN_FEW_ROWS = 2;
 int launch_linear_rows(const LinArgs &, hipStream_t);   // so many rows, both operands along k
@@ -165,11 +168,13 @@ int launch_linear(const LinArgs &, const LinPlan &, void *ws, hipStream_t);
 struct LinGradPlan {
     LinPlan dx, dw;
     bool fits;
-    bool two;   // dz as the sum of two fp16 where an activation changes it
+    bool fits2;   // the products with dz as the sum of two fp16
     LinPlan dx2, dw2;
     int64_t col, parts, products, total;   // workspace (dz, or its form for dx, stands first)
 };
 LinGradPlan linear_grad_plan(int M, int N, int K);
+// Whether an activation leaves dz an fp16 as it is.
+inline bool linear_dz_exact(int act) { return act == MOE_ACT_NONE || act == MOE_ACT_RELU; }
 struct LinGrads {
     const f16 *dy, *z, *x, *w;
     int64_t lddy, ldz, ldx, ldw;
@@ -177,6 +182,7 @@ struct LinGrads {
     void *dx, *dw;
     int64_t lddx, lddw;
     int odt;
+    bool two;   // dz as the sum of two fp16
     float *dbias;
 };
 int launch_linear_backward(const LinGrads &, const LinGradPlan &, void *ws, hipStream_t);

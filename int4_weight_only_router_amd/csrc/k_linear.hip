@@ -39,14 +39,14 @@ static const LinForm FORMS[] = {
     {256, 128, 1, 1, 4.4, 0.875, 0, 0.875}};
 constexpr int NFORMS = sizeof(FORMS) / sizeof(FORMS[0]);
 
-LinPlan linear_plan(int M, int N, int K, int across, bool small)
+LinPlan linear_plan(int M, int N, int K, int across)
 {
     LinPlan best{};
     double least = 1e300;
     const int nkb = (int)(((int64_t)K + 63) / 64);
-    for (int f = 0; f < (small ? LIN_SMALL : NFORMS); ++f) {
+    for (int f = 0; f < NFORMS; ++f) {
         const LinForm &o = FORMS[f];
-        if ((across == 2 && (f == 0 || f == 8)) || (small && f == 2))   // (never the fastest there)
+        if (across == 2 && (f == 0 || f == 8))   // (never the fastest there)
             continue;
         const double one = across ? o.across : o.one;
         const int64_t tiles = ((int64_t)M + o.bm - 1) / o.bm * (((int64_t)N + o.bn - 1) / o.bn);
@@ -92,11 +92,10 @@ int launch_linear(const LinArgs &a, const LinPlan &p, void *ws, hipStream_t s)
 
 // ------------------------------------------------------------------ gradients
 
-// dz as the sum of two fp16, where it, dx or dw have few values: its rounding to one
-// adds as much to the errors of dx and dw as their own, and among few values by chance
-// much more (1 x 5632 x 2048: 1.48 of their rounding's, with two 1.00).  The products take
-// twice the k (4 x 1408 x 2048: 19.5 us against 14.1).
-constexpr int64_t DZ_FEW = 1 << 13, DZ_FEW_OUT = 1 << 11, DZ_FEW_MOST = 1 << 20;
+// dz as the sum of two fp16.  Rounded to one it adds as much to the errors of dx and dw as
+// their own rounding (1.41 of it together, among few values by chance much more); as two
+// it is off by 2^-21 of itself at most, and they by 1.00.  The products take twice the k
+// for it (4096 x 5632 x 2048, SiLU: 396 us), so a caller may ask for one (214).
 // Both have dz's sign and neither is zero (but for values that fp16 hardly holds), so
 // that an infinity in x or w meets no zero and no other sign: hi is the last fp16 before
 // dz, lo the rest of up to a step.
@@ -112,8 +111,11 @@ __device__ __forceinline__ void split_f16(float v, float &hi, float &lo)
     if (fabsf(hi) > 65504.0f)
         lo = hi;
 }
-struct DzTwo {      // null: one fp16 each
-    f16 *row, *col;  // [M][dz, rest] for dx and [dz, rest][M] for dw
+// A row of dz for dx: its values, then their rests (k starts over in w).  For dw: the
+// values, and the rests as the next row (x is taken twice a row); where a row has whole
+// pieces of 8 that is the same memory.
+struct DzTwo {       // null: one fp16 each
+    f16 *row, *col;  // [M][dz, rest] and [M][2][dz or rest]; col null: row's
     int64_t ld_row, ld_col;
 };
 
@@ -155,8 +157,10 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(LinGrads g, f16 *dz, int
             const bool vec = g.N % 8 == 0;
             store_piece<f16, 8>(two.row + m * two.ld_row + n, 0, cols, vec, hi);
             store_piece<f16, 8>(two.row + m * two.ld_row + g.N + n, 0, cols, vec, lo);
-            store_piece<f16, 8>(two.col + m * two.ld_col + n, 0, 8, true, hi);
-            store_piece<f16, 8>(two.col + (g.M + m) * two.ld_col + n, 0, 8, true, lo);
+            if (two.col) {
+                store_piece<f16, 8>(two.col + 2 * m * two.ld_col + n, 0, 8, true, hi);
+                store_piece<f16, 8>(two.col + (2 * m + 1) * two.ld_col + n, 0, 8, true, lo);
+            }
             if (n + 8 >= g.N)   // zeros up to the next multiple of 8
                 for (int64_t k = 2 * (int64_t)g.N; k < two.ld_row; ++k)
                     two.row[m * two.ld_row + k] = (f16)0.0f;
@@ -214,17 +218,16 @@ LinGradPlan linear_grad_plan(int M, int N, int K)
     p.dx = linear_plan(M, K, N, 1);
     p.dw = linear_plan(N, K, M, 2);
     p.fits = p.dx.items <= LIN_MOST_ITEMS && p.dw.items <= LIN_MOST_ITEMS;
-    const int64_t values = (int64_t)M * N, out = (int64_t)std::min(M, N) * K;
-    if (values <= DZ_FEW || (out <= DZ_FEW_OUT && values <= DZ_FEW_MOST)) {
-        p.dx2 = linear_plan(M, K, 2 * N, 1, true);
-        p.dw2 = linear_plan(N, K, 2 * M, 2, true);
-        p.two = p.dx2.items <= LIN_MOST_ITEMS && p.dw2.items <= LIN_MOST_ITEMS;
+    if (M <= LIN_MOST_TWICE) {
+        p.dx2 = linear_plan(M, K, 2 * N, 1);
+        p.dw2 = linear_plan(N, K, 2 * M, 2);
+        p.fits2 = p.dx2.items <= LIN_MOST_ITEMS && p.dw2.items <= LIN_MOST_ITEMS;
     }
     size_t most = std::max(plan_ws(p.dx, M, K), plan_ws(p.dw, N, K));
-    if (p.two)
+    if (p.fits2)
         most = std::max({most, plan_ws(p.dx2, M, K), plan_ws(p.dw2, N, K)});
-    p.col = al256((int64_t)M * dz_ld(p.two ? 2 * N : N) * 2);
-    p.parts = p.col + (p.two ? al256(2 * (int64_t)M * dz_ld(N) * 2) : 0);
+    p.col = al256((int64_t)M * dz_ld(p.fits2 ? 2 * N : N) * 2);
+    p.parts = p.col + (p.fits2 && N % 8 ? al256(2 * (int64_t)M * dz_ld(N) * 2) : 0);
     p.products = p.parts + al256((int64_t)dz_groups(M) * N * 4);
     p.total = p.products + (int64_t)most;
     return p;
@@ -256,10 +259,10 @@ int launch_linear_backward(const LinGrads &g, const LinGradPlan &w, void *ws, hi
     // dy itself is dz where nothing changes it and its rows end on whole pieces
     const bool own = g.act != MOE_ACT_NONE || g.N % 8 || g.lddy % 8 || (uintptr_t)g.dy % 16 ||
                      g.lddy > LIN_MOST_LD;
-    // (without an activation, and through ReLU, dz is fp16 as it is)
-    const bool two = g.act != MOE_ACT_NONE && g.act != MOE_ACT_RELU && w.two && (g.dx || g.dw);
-    const DzTwo rest = {two ? static_cast<f16 *>(ws) : nullptr, reinterpret_cast<f16 *>(base + w.col),
-                        dz_ld(2 * g.N), dz_ld(g.N)};
+    const bool two = g.two && (g.dx || g.dw);
+    const DzTwo rest = {two ? static_cast<f16 *>(ws) : nullptr,
+                        g.N % 8 ? reinterpret_cast<f16 *>(base + w.col) : nullptr, dz_ld(2 * g.N),
+                        dz_ld(g.N)};
     const LinPlan &dx = two ? w.dx2 : w.dx, &dw = two ? w.dw2 : w.dw;
     const f16 *dz = own ? static_cast<const f16 *>(ws) : g.dy;
     const int64_t ldd = own ? dz_ld(g.N) : g.lddy;
@@ -297,7 +300,7 @@ int launch_linear_backward(const LinGrads &g, const LinGradPlan &w, void *ws, hi
         if (two) {
             a.lda = rest.ld_row;
             a.K = 2 * g.N;
-            a.wrap = g.N;
+            a.twice = true;
         }
         a.out = g.dx;
         a.ldo = g.lddx;
@@ -312,10 +315,10 @@ int launch_linear_backward(const LinGrads &g, const LinGradPlan &w, void *ws, hi
         a.M = g.N;
         a.K = g.M;
         if (two) {
-            a.a = rest.col;
+            a.a = rest.col ? rest.col : rest.row;
             a.lda = rest.ld_col;
             a.K = 2 * g.M;
-            a.wrap = g.M;
+            a.twice = true;
         }
         a.out = g.dw;
         a.ldo = g.lddw;

@@ -64,9 +64,13 @@ struct LtForm {
     static_assert(FM > 0 && FN > 0 && lds() <= 160 * 1024, "a tile's fragments and LDS");
 };
 
+// Which of its k an operand that runs across k gives: as they come; all of them twice
+// over, starting again at `wrap`; or each of them twice in a row.
+enum LtAgain { ONCE, OVER, EACH };
+
 // One operand of a workgroup of NTH threads: R rows (of A or B) from row r0 on.
-// WRAP: its k starts over at `wrap`, counted from k0 before its base.
-template <int R, bool KS, int NTH, bool WRAP = false>
+// AGAIN: not ONCE: k counts from k0 on, before the base.
+template <int R, bool KS, int NTH, LtAgain AGAIN = ONCE>
 struct LtOperand {
     static constexpr int LOADS = R * LT_BK * 2 / (NTH * 16);   // 16-byte loads a thread and block
     static constexpr int RB = KS ? R * 2 : LT_BK * 2;          // bytes of an LDS row
@@ -76,7 +80,7 @@ struct LtOperand {
     static constexpr bool EVEN = NTH % PIECES == 0;
     static constexpr int LROWS = EVEN ? NTH / PIECES : 0, OWN = EVEN ? 1 : LOADS;
     const unsigned char *base;
-    uint32_t ld, last;    // bytes: of a row; kc: of the last row (512 ld < 2^32)
+    uint32_t ld, last;    // bytes: of a row; kc: of the last row (R <= 256, ld <= 2^24)
     int K, k0, wrap;
     uint32_t off[OWN];    // of this thread's (first) row
     uint32_t col[KS ? OWN : 1];   // ks: of its column
@@ -127,9 +131,10 @@ struct LtOperand {
             const uint32_t k = min(kb * LT_BK + piece(0) * 8, ((K + 7) & ~7) - 8) * 2;
             dma16(base + (min(row, last) + k), to);
         } else {
-            if constexpr (WRAP) {
+            if constexpr (AGAIN != ONCE) {
                 const int k = k0 + min(kb * LT_BK + lrow(i), K - 1);
-                dma16(base + (int64_t)(k < wrap ? k : k - wrap) * ld + col[EVEN ? 0 : i], to);
+                const int of = AGAIN == EACH ? k >> 1 : k < wrap ? k : k - wrap;
+                dma16(base + (int64_t)of * ld + col[EVEN ? 0 : i], to);
                 return;
             }
             const uint32_t end = (uint32_t)min(K - 1 - kb * LT_BK, LT_BK - 1) * ld;
@@ -363,12 +368,12 @@ __device__ __forceinline__ void lt_epilogue_f32(const LinArgs &a, LtAcc<F> &acc,
     }
 }
 
-template <typename F, bool AKS, bool BKS, bool WRAP>
+template <typename F, bool AKS, bool BKS, LtAgain AGAIN>
 __global__ __launch_bounds__(F::THREADS, 2) void linear_tile_kernel(LinArgs a)
 {
     constexpr int BM = F::BM, BN = F::BN, NS = F::NS, STAGE = F::STAGE, FM = F::FM, FN = F::FN;
     typedef LtOperand<BM, AKS, F::NTH> OA;
-    typedef LtOperand<BN, BKS, F::NTH, WRAP> OB;
+    typedef LtOperand<BN, BKS, F::NTH, AGAIN> OB;
     constexpr int P = OA::LOADS + OB::LOADS;
     constexpr int AB = BM * LT_BK * 2;          // B's place in a stage
     // Of the row fragments the first ROLL are read into the registers that their own
@@ -399,9 +404,9 @@ __global__ __launch_bounds__(F::THREADS, 2) void linear_tile_kernel(LinArgs a)
     OB ob;
     const int64_t k0 = (int64_t)min(kb0, kall - 1) * LT_BK;
     oa.init(a.a + k0 * (AKS ? a.lda : 1), a.lda, m0, a.M, K);
-    ob.init(a.b + (WRAP ? 0 : k0 * (BKS ? a.ldb : 1)), a.ldb, n0, a.N, K);
+    ob.init(a.b + (AGAIN != ONCE ? 0 : k0 * (BKS ? a.ldb : 1)), a.ldb, n0, a.N, K);
     ob.k0 = (int)k0;
-    ob.wrap = a.wrap;
+    ob.wrap = a.K / 2;
 
     LtAcc<F> acc;
 #pragma unroll
@@ -586,41 +591,37 @@ __global__ __launch_bounds__(256) void linear_join_kernel(LinArgs a, const float
     }
 }
 
-template <typename F, bool AKS, bool BKS, bool WRAP>
+template <typename F, bool AKS, bool BKS, LtAgain AGAIN>
 static int launch_tile_t(const LinArgs &a, hipStream_t s)
 {
     static LdsLimit limit;
     const int64_t items =
         (int64_t)((a.M + F::BM - 1) / F::BM) * ((a.N + F::BN - 1) / F::BN) * a.splits;
-    const int rc = limit.raise((const void *)linear_tile_kernel<F, AKS, BKS, WRAP>, 160 * 1024);
+    const int rc = limit.raise((const void *)linear_tile_kernel<F, AKS, BKS, AGAIN>, 160 * 1024);
     if (rc)
         return rc;
     const unsigned grid = (unsigned)((items + LT_NXCD - 1) / LT_NXCD * LT_NXCD);
-    hipLaunchKernelGGL((linear_tile_kernel<F, AKS, BKS, WRAP>), dim3(grid), dim3(F::THREADS),
+    hipLaunchKernelGGL((linear_tile_kernel<F, AKS, BKS, AGAIN>), dim3(grid), dim3(F::THREADS),
                        F::lds(), s, a);
     MOE_LAUNCH_CHECK("linear_tile_kernel");
     return MOE_OK;
 }
 
-// BOTH: the form takes products both of whose operands run across k, WRAPS: such as start
-// over in b (linear_plan chooses no other form for those).
-template <typename F, bool BOTH, bool WRAPS>
+// BOTH: the form takes products both of whose operands run across k (linear_plan chooses
+// no other form for those).
+template <typename F, bool BOTH>
 static int launch_tile(const LinArgs &a, hipStream_t s)
 {
-    if ((a.a_ks && !BOTH) || (a.wrap && !WRAPS))
+    if (a.a_ks) {
+        if constexpr (BOTH)
+            return a.twice ? launch_tile_t<F, true, true, EACH>(a, s)
+                           : launch_tile_t<F, true, true, ONCE>(a, s);
         return set_error(MOE_EUNSUPPORTED, "linear_tile_kernel: no such form");
-    if constexpr (WRAPS)
-        if (a.wrap) {
-            if constexpr (BOTH)
-                if (a.a_ks)
-                    return launch_tile_t<F, true, true, true>(a, s);
-            return launch_tile_t<F, false, true, true>(a, s);
-        }
-    if constexpr (BOTH)
-        if (a.a_ks)
-            return launch_tile_t<F, true, true, false>(a, s);
-    return a.b_ks ? launch_tile_t<F, false, true, false>(a, s)
-                  : launch_tile_t<F, false, false, false>(a, s);
+    }
+    if (a.b_ks)
+        return a.twice ? launch_tile_t<F, false, true, OVER>(a, s)
+                       : launch_tile_t<F, false, true, ONCE>(a, s);
+    return launch_tile_t<F, false, false, ONCE>(a, s);
 }
 
 // The forms in the order of LinPlan::form (what each is for: linear_plan).
@@ -654,15 +655,15 @@ int launch_linear_tile(LinArgs a, const LinPlan &p, void *ws, hipStream_t s)
     }
     int rc;
     switch (p.form) {
-    case 0: rc = launch_tile<LtF0, false, true>(part, s); break;
-    case 1: rc = launch_tile<LtF1, true, true>(part, s); break;
-    case 2: rc = launch_tile<LtF2, true, false>(part, s); break;
-    case 3: rc = launch_tile<LtF3, true, true>(part, s); break;
-    case 4: rc = launch_tile<LtF4, true, false>(part, s); break;
-    case 5: rc = launch_tile<LtF5, true, false>(part, s); break;
-    case 6: rc = launch_tile<LtF6, true, false>(part, s); break;
-    case 7: rc = launch_tile<LtF7, true, false>(part, s); break;
-    default: rc = launch_tile<LtF8, false, false>(part, s); break;
+    case 0: rc = launch_tile<LtF0, false>(part, s); break;
+    case 1: rc = launch_tile<LtF1, true>(part, s); break;
+    case 2: rc = launch_tile<LtF2, true>(part, s); break;
+    case 3: rc = launch_tile<LtF3, true>(part, s); break;
+    case 4: rc = launch_tile<LtF4, true>(part, s); break;
+    case 5: rc = launch_tile<LtF5, true>(part, s); break;
+    case 6: rc = launch_tile<LtF6, true>(part, s); break;
+    case 7: rc = launch_tile<LtF7, true>(part, s); break;
+    default: rc = launch_tile<LtF8, false>(part, s); break;
     }
     if (rc || a.splits == 1)
         return rc;
