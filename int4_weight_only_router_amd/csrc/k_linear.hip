@@ -96,20 +96,28 @@ int launch_linear(const LinArgs &a, const LinPlan &p, void *ws, hipStream_t s)
 // their own rounding (1.41 of it together, among few values by chance much more); as two
 // it is off by 2^-21 of itself at most, and they by 1.00.  The products take twice the k
 // for it (4096 x 5632 x 2048, SiLU: 396 us), so a caller may ask for one (214).
-// Both have dz's sign and neither is zero (but for values that fp16 hardly holds), so
-// that an infinity in x or w meets no zero and no other sign: hi is the last fp16 before
-// dz, lo the rest of up to a step.
-__device__ __forceinline__ void split_f16(float v, float &hi, float &lo)
+// Both have dz's sign and neither is zero (but for what fp16's smallest step cannot be
+// divided into), so that an infinity in x or w meets no zero and no other sign: hi is the
+// last fp16 up to dz, by the conversion towards zero, and lo the rest of up to a step;
+// where the rest is zero or rounds to it, hi is the fp16 before and lo the step between
+// the two, whose sum is exact.  So they are off by 2^-11 of lo, or by 2^-25.
+__device__ __forceinline__ void split_f16(const float (&v)[8], float (&hi)[8], float (&lo)[8])
 {
-    f16 h = (f16)v;
-    if (fabsf((float)h) >= fabsf(v) && fabsf((float)h) > 0x1p-23f && fabsf((float)h) <= 65504.0f)
-        h = __builtin_bit_cast(f16, (uint16_t)(__builtin_bit_cast(uint16_t, h) - 1));
-    hi = (float)h;
-    lo = (float)(f16)(v - hi);
-    if (lo == 0.0f && fabsf(hi) >= 0x1p-23f)
-        lo = copysignf(0x1p-24f, v);
-    if (fabsf(hi) > 65504.0f)
-        lo = hi;
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+        const half2_t pair = __builtin_bit_cast(half2_t, __builtin_amdgcn_cvt_pkrtz(v[j], v[j + 1]));
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            f16 a = pair[i], b = (f16)(v[j + i] - (float)a);
+            if (b == (f16)0.0f && a != (f16)0.0f) {
+                const f16 h = a;
+                a = __builtin_bit_cast(f16, (uint16_t)(__builtin_bit_cast(uint16_t, h) - 1));
+                b = h - a;
+            }
+            hi[j + i] = (float)a;
+            lo[j + i] = fabsf((float)a) > 65504.0f ? (float)a : (float)b;
+        }
+    }
 }
 // A row of dz for dx: its values, then their rests (k starts over in w).  For dw: the
 // values, and the rests as the next row (x is taken twice a row); where a row has whole
@@ -151,9 +159,7 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(LinGrads g, f16 *dz, int
             store_piece<f16, 8>(dz + m * ldd + n, 0, 8, true, v);
         if (two.row) {
             float hi[8], lo[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                split_f16(v[j], hi[j], lo[j]);
+            split_f16(v, hi, lo);
             const bool vec = g.N % 8 == 0;
             store_piece<f16, 8>(two.row + m * two.ld_row + n, 0, cols, vec, hi);
             store_piece<f16, 8>(two.row + m * two.ld_row + g.N + n, 0, cols, vec, lo);

@@ -112,6 +112,41 @@ def test_within_the_bound(m, n, k, act):
         assert (off <= e + h * (want.abs() + e) + R.tiny(F16)).all()
 
 
+@pytest.mark.parametrize("act", SOFT)
+@pytest.mark.parametrize("scale", [2.0 ** -10, 2.0 ** -13, 1e-5, 2.0 ** -22])
+@pytest.mark.parametrize("m", [3, 200])
+def test_small_gradients(m, scale, act):
+    """dz below fp16's normal values, through the unit matrix: the sum of the two fp16 is
+    the multiple of 2^-24 next to it, off by 2^-25 (and dz in fp32 by 16 half steps of
+    dy), and dx rounds that once more where it is 2^-13 or above."""
+    n = 256
+    dy, z, x, _ = inputs(m, n, n, scale)
+    z[:, :n] = (z[:, :n].float().abs() + 4).half()   # act' about one
+    eye = put(torch.eye(n))
+    dx, dw, _ = backward(dy, z, act, x, eye, m, n, n, outputs(m, n, n))
+    dz, want, want_w = definition(dy, z, act, x, eye, m, n, n)
+    bound = 2.0 ** -25 + 17 * U * wide(dy, n).abs() + R.half_step(F16) * want.abs()
+    small = want.abs() < 2.0 ** -13
+    bound[small] -= R.half_step(F16) * want.abs()[small]
+    assert ((dx[:, :n].double() - want).abs() <= bound).all()
+    es = (2.0 ** -25 + 17 * U * wide(dy, n).abs()).t() @ wide(x, n).abs()
+    e = es + (2 * m + 16) * U * (dz.abs().t() @ wide(x, n).abs() + es)
+    assert ((dw[:, :n].double() - want_w).abs()
+            <= e + R.half_step(F16) * (want_w.abs() + e) + R.tiny(F16)).all()
+
+
+@pytest.mark.parametrize("act", SOFT)
+def test_steps_of_the_smallest_values(act):
+    """Every multiple of 2^-24 up to 2^-13 comes through as it is."""
+    m, n = 32, 64
+    steps = torch.arange(1, m * n + 1).reshape(m, n).double() * 2.0 ** -24
+    steps[::2] *= -1
+    dy, z = put(steps.float()), put(torch.full((m, n), 60.0))   # act' is one
+    eye, x = put(torch.eye(n)), put(torch.zeros((m, n)))
+    dx, _, _ = backward(dy, z, act, x, eye, m, n, n, outputs(m, n, n))
+    assert torch.equal(dx[:, :n].double().cpu(), steps)
+
+
 @pytest.mark.parametrize("m,n,k", [(2, 70, 64), (300, 1000, 264), (300, 1001, 264), (4096, 512, 2048)])
 def test_infinite_weights(m, n, k):
     """An infinite weight and a gradient beyond fp16 stay infinities, with their signs."""
