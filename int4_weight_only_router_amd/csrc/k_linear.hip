@@ -131,6 +131,7 @@ struct DzTwo {       // null: one fp16 each
 // column N), where dz is not null, and its column sums over `tall` rows, from the
 // unrounded values, where parts is not null.  2^lt threads a row, eight columns each.
 // Bound by memory (4096 x 5632, SiLU: 30 us, 4.6 TB/s).
+template <bool TWO>
 __global__ __launch_bounds__(256) void linear_dz_kernel(LinGrads g, f16 *dz, int64_t ldd,
                                                         float *parts, bool vec_y, bool vec_z, int lt, int tall,
                                                         DzTwo two)
@@ -155,9 +156,9 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(LinGrads g, f16 *dz, int
             for (int j = 0; j < 8; ++j)
                 v[j] = j < cols ? v[j] * act_grad(z[j], g.act) : 0.0f;
         }
-        if (dz)
+        if (!TWO && dz)
             store_piece<f16, 8>(dz + m * ldd + n, 0, 8, true, v);
-        if (two.row) {
+        if constexpr (TWO) {
             float hi[8], lo[8];
             split_f16(v, hi, lo);
             const bool vec = g.N % 8 == 0;
@@ -281,8 +282,9 @@ int launch_linear_backward(const LinGrads &g, const LinGradPlan &w, void *ws, hi
         while (lt < 5 && (8 << lt) < g.N)
             ++lt;
         auto rows16 = [](const void *p, int64_t ld) { return (uintptr_t)p % 16 == 0 && ld % 8 == 0; };
-        hipLaunchKernelGGL(linear_dz_kernel, dim3((g.N + (8 << lt) - 1) / (8 << lt), G), dim3(256), 0,
-                           s, g, own && !two && (g.dx || g.dw) ? static_cast<f16 *>(ws) : nullptr, ldd,
+        hipLaunchKernelGGL(two ? linear_dz_kernel<true> : linear_dz_kernel<false>,
+                           dim3((g.N + (8 << lt) - 1) / (8 << lt), G), dim3(256), 0, s, g,
+                           own && (g.dx || g.dw) ? static_cast<f16 *>(ws) : nullptr, ldd,
                            g.dbias ? parts : nullptr, rows16(g.dy, g.lddy), rows16(g.z, g.ldz), lt,
                            dz_rows(g.M), rest);
         MOE_LAUNCH_CHECK("linear_dz_kernel");
