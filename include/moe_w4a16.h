@@ -725,7 +725,7 @@ int moe_block_norm_backward(const void *dout, int64_t ldo, const void *dn, int64
  *             not overlap
  * The order of the fp32 additions depends on M, N and K only.  K, ldx and ldw are
  * multiples of 8, rows lie at most 2^22 elements apart, M and N are at most 2^30 and
- * small enough for a launch (tiles of 256 x 256: fewer than 2^22); else
+ * small enough for a launch (at most 2^22 - 8 tiles of 256 x 256); else
  * MOE_EUNSUPPORTED.  M = 0: no-op.
  */
 size_t moe_linear_f16_workspace_bytes(int M, int N, int K);

@@ -41,7 +41,7 @@ constexpr int NFORMS = sizeof(FORMS) / sizeof(FORMS[0]);
 
 LinPlan linear_plan(int M, int N, int K, int across)
 {
-    LinPlan best{};
+    LinPlan best{0, 1, LIN_MOST_ITEMS + 1};   // (where no form fits a launch)
     double least = 1e300;
     const int nkb = (int)(((int64_t)K + 63) / 64);
     for (int f = 0; f < NFORMS; ++f) {
@@ -50,6 +50,8 @@ LinPlan linear_plan(int M, int N, int K, int across)
             continue;
         const double one = across ? o.across : o.one;
         const int64_t tiles = ((int64_t)M + o.bm - 1) / o.bm * (((int64_t)N + o.bn - 1) / o.bn);
+        if (tiles > LIN_MOST_ITEMS)
+            continue;
         for (int s = 1; s <= 8; s *= 2) {
             const int each = (nkb + s - 1) / s;
             if (s > 1 && (tiles * s > 256 || (nkb + each - 1) / each != s))

@@ -24,3 +24,15 @@ def test_flag():
     with pytest.raises(M.MoEError) as ei:   # no flag of the forward call
         M.moe_linear_f16(P, 64, P, 64, None, 0, None, 0, 4, 32, 64, P, F16 | DZ, 32, stream=0)
     assert ei.value.code == M.MOE_EINVAL
+
+
+@pytest.mark.parametrize("act", [M.MOE_ACT_SILU, M.MOE_ACT_GELU, M.MOE_ACT_GELU_TANH])
+def test_rows_of_a_dz_of_two(act):
+    """k of dw is passed twice: half as many rows, or dz rounded."""
+    m = 1 << 29
+    assert _code(m, 8, 8, act, F16) == M.MOE_ENOMEM
+    assert _code(m + 1, 8, 8, act, F16) == M.MOE_EUNSUPPORTED
+    assert _code(m + 1, 8, 8, act, F16 | DZ) == M.MOE_ENOMEM
+    for free in (M.MOE_ACT_NONE, M.MOE_ACT_RELU):
+        assert _code(m + 1, 8, 8, free, F16) == M.MOE_ENOMEM
+    assert _code(2, 1 << 22, 8, act, F16) == M.MOE_ENOMEM
