@@ -739,7 +739,8 @@ int moe_linear_f16(const void *x_f16, int64_t ldx, const void *w_f16, int64_t ld
  * residual's):
  *   dz = dy * act'(z),   dx = dz w,   dw = dz^T x,   dbias = sum over rows of dz
  *   dy_f16  device fp16 [M] rows of N values, lddy apart
- *   z_f16   as the forward call wrote it; not read with MOE_ACT_NONE
+ *   z_f16   as the forward call wrote it (an infinity: beyond fp16, with the
+ *           derivative's limit); not read with MOE_ACT_NONE
  *   x_f16, w_f16  as in the forward call (x is read for dw only, w for dx only)
  *   dx      device [M] rows of K values of out_dtype, lddx apart, or NULL
  *   dw      device [N] rows of K values of out_dtype, lddw apart, or NULL

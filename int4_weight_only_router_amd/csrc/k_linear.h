@@ -138,8 +138,11 @@ __device__ __forceinline__ float act_value(float z, int act)
     }
 }
 
+// (z comes as fp16: one that left its range is an infinity, where the products of zero
+// and z below would be NaN; the derivatives there are those of fp16's last value)
 __device__ __forceinline__ float act_grad(float z, int act)
 {
+    z = fabsf(z) > 65504.0f ? copysignf(65504.0f, z) : z;   // (NaN stays)
     switch (act) {
     case MOE_ACT_RELU:
         return z > 0.0f ? 1.0f : 0.0f;

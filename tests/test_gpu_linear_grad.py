@@ -166,6 +166,26 @@ def test_infinite_weights(m, n, k):
     assert torch.isfinite(dw[:7]).all() and torch.isfinite(dw[8:]).all()
 
 
+@pytest.mark.parametrize("act", SOFT + ["relu"])
+@pytest.mark.parametrize("m", [4, 200])
+def test_z_beyond_fp16(act, m):
+    """A z that left fp16's range arrives as an infinity; the derivative there is its
+    limit, one or zero, and spoils no other value of the row.  NaN stays NaN."""
+    n = 64
+    dy, z = torch.full((m, n), 0.5), torch.full((m, n), 30.0)
+    z[1, 3], z[1, 4], z[2, 7] = float("inf"), -float("inf"), float("nan")
+    z[3, 0], z[3, 1] = 65504.0, -65504.0
+    want = torch.full((m, n), 0.5)
+    want[1, 4], want[3, 1] = 0.0, 0.0
+    eye, x = put(torch.eye(n)), put(torch.zeros((m, n)))
+    dx, _, db = backward(put(dy), put(z), act, x, eye, m, n, n, outputs(m, n, n))
+    keep = [i for i in range(m) if i != 2]
+    assert torch.equal(dx[keep][:, :n].cpu().float(), want[keep])
+    if act != "relu":
+        assert torch.isnan(dx[2, :n]).all()   # (NaN times the unit matrix's zeros)
+        assert torch.isnan(db[7]) and torch.isfinite(db[[i for i in range(n) if i != 7]]).all()
+
+
 @pytest.mark.parametrize("act", list(R.ACTS))
 @pytest.mark.parametrize("m,n,k", [(3, 17, 24), (333, 1408, 2000), (2050, 2505, 2056)])
 def test_rounded_dz(m, n, k, act):
