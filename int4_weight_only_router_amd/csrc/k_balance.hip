@@ -7,7 +7,9 @@
 //   dbalance/dl_te = coef / n p_te (d_e - sum_j p_tj d_j) [(1 - s_te) for sigmoid scores]
 //   dz/dl_te = zcoef / n 2 lse_t softmax_te
 // with d_e = E f_e - 1: p sums to one, so the one drops out, and with it the
-// cancellation of a load that is nearly even (d_e is formed from whole numbers).
+// cancellation of a load that is nearly even (d_e is formed from whole numbers).  The
+// loss itself is the sum of E f_e P_e, whose terms are positive: formed from the d_e it
+// would cancel where the load lies on unlikely experts, and count a load of zero as even.
 // The counts are needed before any gradient, the logits only once: a wave takes a
 // row, holds it in registers and writes its gradient at once.
 //
@@ -175,12 +177,11 @@ __device__ __forceinline__ void store_row(const BalanceArgs &a, int64_t t, const
     }
 }
 
-// The row: its p added to psum[], its share of the balance loss and lse^2 added up,
-// its gradient written.
+// The row: its p added to psum[], its lse^2 to zsum, its gradient written.
 template <int NE>
-__device__ __forceinline__ void balance_row(const BalanceArgs &a, int64_t t, bool on,
+__device__ __forceinline__ void balance_row(const BalanceArgs &a, int64_t t,
                                             const float (&l)[NE], const float (&d)[NE], float per_n,
-                                            float up, float (&psum)[NE], float &loss, float &zsum)
+                                            float up, float (&psum)[NE], float &zsum)
 {
     float top = l[0];
 #pragma unroll
@@ -242,11 +243,10 @@ __device__ __forceinline__ void balance_row(const BalanceArgs &a, int64_t t, boo
         psum[i] += p[i];
         dot = __builtin_fmaf(p[i], d[i], dot);
     }
-    dot = wave_sum_f32(dot);
-    loss += some ? dot + 1.0f : 0.0f;   // sum p (d + 1)
     zsum = __builtin_fmaf(lse, lse, zsum);
     if (!a.dlogits)
         return;
+    dot = wave_sum_f32(dot);
     const float cb = up * a.coef * per_n, cz = a.zcoef != 0.0f ? up * a.zcoef * per_n * 2.0f * lse : 0.0f;
     float g[NE];
 #pragma unroll
@@ -378,13 +378,15 @@ __global__ __launch_bounds__(64 * bl_waves<NE>()) void balance_rows_kernel(Balan
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         const int e = threadIdx.x + i * THREADS;
-        if (e < 64 * NE)
+        if (e < 64 * NE) {
             dev[e] = e < a.E ? deviation(c[i], a.E, total, inv) : 0.0f;
+            hist[e] = c[i];   // (this thread's own to here)
+        }
         if (blockIdx.x == 0 && e < a.E && a.idx)
             a.counts[e] = c[i];
     }
     lds_barrier();
-    float d[NE], psum[NE], loss = 0.0f, zsum = 0.0f;
+    float d[NE], psum[NE], zsum = 0.0f;
 #pragma unroll
     for (int i = 0; i < NE; ++i) {
         d[i] = dev[lane + 64 * i];
@@ -400,8 +402,14 @@ __global__ __launch_bounds__(64 * bl_waves<NE>()) void balance_rows_kernel(Balan
         if (t < a.T)
             row.load(a, t);
         if (on || a.dlogits)
-            balance_row<NE>(a, t0, on, l, d, per_n, up, psum, loss, zsum);
+            balance_row<NE>(a, t0, l, d, per_n, up, psum, zsum);
     }
+    float loss = 0.0f;   // sum E f_e p_e of the wave's rows
+    const float each = (float)a.E * inv;
+#pragma unroll
+    for (int i = 0; i < NE; ++i)
+        loss = __builtin_fmaf(psum[i], (float)hist[lane + 64 * i] * each, loss);
+    loss = wave_sum_f32(loss);
     // the waves' sums: the upper half's onto the lower half's, then those
     if (wave >= HALF) {
 #pragma unroll
