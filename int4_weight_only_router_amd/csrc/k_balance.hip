@@ -256,10 +256,10 @@ __device__ __forceinline__ void balance_row(const BalanceArgs &a, int64_t t,
 #pragma unroll
         for (int i = 0; i < NE; ++i)
             g[i] *= rest[i];
-    // (zeros without a score, also where up is not finite)
+    // (zeros for masked experts and tokens, also where up is not finite)
 #pragma unroll
     for (int i = 0; i < NE; ++i)
-        g[i] = some ? __builtin_fmaf(cz, soft[i], g[i]) : 0.0f;
+        g[i] = l[i] > -__builtin_inff() ? __builtin_fmaf(cz, soft[i], g[i]) : 0.0f;
     if (a.gtype == MOE_DTYPE_F32)
         store_row<NE, float>(a, t, g);
     else if (a.gtype == MOE_DTYPE_F16)

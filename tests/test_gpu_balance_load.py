@@ -1,5 +1,6 @@
-"""moe_balance_loss where the load and the probabilities lie apart, and where no
-choice counts."""
+"""moe_balance_loss where the load and the probabilities lie apart, where no choice
+counts, and with gradients scaled beyond fp32."""
+import numpy as np
 import pytest
 import torch
 
@@ -71,6 +72,23 @@ def test_load_on_unlikely_experts(T, E, far, score):
     assert abs(float(got[2][0]) - want[2][0]) <= room(l) * want[2][0]
     given = call(l, None, mask, 2, score, 0.5, counts=got[0].to(DEV))
     assert torch.equal(given[2], got[2])
+
+
+@pytest.mark.parametrize("up", [float("inf"), -float("inf"), float("nan")])
+@pytest.mark.parametrize("score", list(SCORES))
+@pytest.mark.parametrize("T", [5, 130])
+def test_masked_stays_zero_whatever_the_scale(T, score, up):
+    """A loss scale that overflowed reaches no masked expert and no masked token."""
+    E, k = 70, 4
+    l = logits(T, E)
+    idx = torch.sort(l, dim=1, descending=True)[1][:, :k].int().contiguous()
+    l[0, 3], l[0, 69], l[1, :], l[2, 1:] = -np.inf, np.nan, -np.inf, -np.inf
+    mask = torch.ones(T, dtype=torch.uint8)
+    mask[4] = 0
+    grad = call(l, idx, mask, k, score, 0.01, 0.01, up=torch.tensor([up], device=DEV))[3]
+    assert grad[0, 3] == 0 and grad[0, 69] == 0 and (grad[1] == 0).all()
+    assert (grad[2, 1:] == 0).all() and (grad[4] == 0).all()
+    assert not torch.isfinite(grad[3]).any()
 
 
 @pytest.mark.parametrize("T", [5, 200])
