@@ -247,7 +247,7 @@ __device__ __forceinline__ void balance_row(const BalanceArgs &a, int64_t t,
     if (!a.dlogits)
         return;
     dot = wave_sum_f32(dot);
-    const float cb = up * a.coef * per_n, cz = a.zcoef != 0.0f ? up * a.zcoef * per_n * 2.0f * lse : 0.0f;
+    const float cb = up * a.coef * per_n, cz = a.zcoef != 0.0f ? up * a.zcoef * per_n * 2.0f : 0.0f;
     float g[NE];
 #pragma unroll
     for (int i = 0; i < NE; ++i)
@@ -256,10 +256,11 @@ __device__ __forceinline__ void balance_row(const BalanceArgs &a, int64_t t,
 #pragma unroll
         for (int i = 0; i < NE; ++i)
             g[i] *= rest[i];
-    // (zeros for masked experts and tokens, also where up is not finite)
+    // (zeros for masked experts and tokens, also where up is not finite; lse times the
+    // rest, as by itself it can take cz out of fp32's range)
 #pragma unroll
     for (int i = 0; i < NE; ++i)
-        g[i] = l[i] > -__builtin_inff() ? __builtin_fmaf(cz, soft[i], g[i]) : 0.0f;
+        g[i] = l[i] > -__builtin_inff() ? __builtin_fmaf(cz * soft[i], lse, g[i]) : 0.0f;
     if (a.gtype == MOE_DTYPE_F32)
         store_row<NE, float>(a, t, g);
     else if (a.gtype == MOE_DTYPE_F16)

@@ -98,3 +98,23 @@ def test_given_counts_are_not_written(T):
     got = call(logits(T, 40), None, torch.zeros(T, dtype=torch.uint8), 2, "softmax", 0.1,
                counts=counts.clone())
     assert torch.equal(got[0], counts.cpu()) and all((t == 0).all() for t in got[1:])
+
+
+@pytest.mark.parametrize("score", list(SCORES))
+@pytest.mark.parametrize("T", [1, 70])
+@pytest.mark.parametrize("zcoef", [0.001, 1.0])
+def test_largest_logit_with_z_loss(T, score, zcoef):
+    """+inf counts as the largest finite value, whose z loss leaves fp32; its gradient
+    may too, the other experts' is none of that."""
+    E = 40
+    l = logits(T, E)
+    l[0, 7] = np.inf
+    idx = torch.zeros((T, 2), dtype=torch.int32)
+    _, _, _, want = R.balance_ref(l, idx, None, E, SCORES[score], 0.0, zcoef)
+    counts, mean, losses, grad = call(l, idx, None, 2, score, 0.0, zcoef)
+    assert torch.isfinite(mean).all() and losses[0] == 0 and torch.isposinf(losses[1])
+    assert (grad[0, :7] == 0).all() and (grad[0, 8:] == 0).all()
+    big = float(want[0, 7])
+    assert float(grad[0, 7]) == pytest.approx(big, rel=1e-5) if big < 3.4e38 else \
+        torch.isposinf(grad[0, 7])
+    assert torch.isfinite(grad[1:]).all()
