@@ -783,7 +783,8 @@ int moe_linear_f16_backward(const void *dy_f16, int64_t lddy, const void *z_f16,
  *               outside [0, E) does not count), or NULL: counts is an input, such
  *               as moe_route_select_permute's
  *   token_mask  device uint8 [T], zero: masked; or NULL
- *   counts      device int32 [E];  mean_prob device fp32 [E] or NULL
+ *   counts      device int32 [E]: written, or with topk_idx NULL read only, unless T
+ *               is 0;  mean_prob device fp32 [E] or NULL
  *   losses      device fp32 [2] or NULL
  *   d_loss      device fp32 [1] or NULL (one): the losses' gradient, such as a
  *               loss scale
@@ -795,7 +796,10 @@ int moe_linear_f16_backward(const void *dy_f16, int64_t lddy, const void *z_f16,
  * Counts are exact, sums fp32 in an order that depends on T and E only.
  * Errors: MOE_EINVAL for bad sizes, types, coefficients that are not finite, null
  * or misaligned pointers; MOE_EUNSUPPORTED for E > 1024 or T*k >= 2^31; MOE_ENOMEM.
- * T = 0, or every token masked: everything is zero.
+ * No choice counted, or given counts of zero: the balance loss and its gradient are
+ * zero.  Every token masked: everything is zero but given counts, which stay.  T = 0:
+ * everything is set to zero, counts too, also where topk_idx is NULL (counts summed up
+ * over several calls are not passed to one without tokens).
  */
 size_t moe_balance_loss_workspace_bytes(int T, int E);
 int moe_balance_loss(const void *logits, int logits_dtype, int64_t ld, const int32_t *topk_idx,
