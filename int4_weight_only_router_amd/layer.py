@@ -90,11 +90,19 @@ class ScoreRouting:
     scale: float = 1.0
 
 
+def _types(*weights):
+    return {w.dtype for w in weights if w is not None}
+
+
+def _w_dtype(types):
+    return A.MOE_DTYPE_F32 if torch.float32 in types else A.MOE_DTYPE_F16
+
+
 @dataclass
 class BlockNorms:
     """The norms, gate and residual scale around a layer's block (moe_block_norm):
     h' = h + scale * gate * post(MoE(pre(h))).  Weights fp16 or fp32 [H] device (all
-    of one type), gate fp16 [H] device."""
+    of one type, in a stack too; any may be absent), gate fp16 [H] device."""
     pre_w: torch.Tensor | None = None
     pre_b: torch.Tensor | None = None
     post: bool = False                        # norm the block's output too
@@ -107,11 +115,17 @@ class BlockNorms:
     unit_offset: bool = False                 # weights count as 1 + w
 
     def __post_init__(self):
-        types = {w.dtype for w in (self.pre_w, self.pre_b, self.post_w, self.post_b)
-                 if w is not None}
-        if len(types) > 1 or types - {torch.float16, torch.float32}:
+        if len(self.types) > 1 or self.types - {torch.float16, torch.float32}:
             raise ValueError("norm weights must all be fp16 or all fp32")
-        self.w_dtype = A.MOE_DTYPE_F32 if torch.float32 in types else A.MOE_DTYPE_F16
+
+    @property
+    def types(self):
+        """Types of the weights that there are."""
+        return _types(self.pre_w, self.pre_b, self.post_w, self.post_b)
+
+    @property
+    def w_dtype(self):
+        return _w_dtype(self.types)
 
     def check(self, H):
         """ValueError where a weight or the gate is not of rows of H."""
@@ -137,8 +151,6 @@ def block_norm(y, h, end, start, out, n, stream=None):
     if end is not None and start is not None:
         if end.form != start.form:
             raise ValueError("the norms of a stack must have one kind, eps and unit_offset")
-        if end.w_dtype != start.w_dtype and (end.post_w is not None or end.post_b is not None):
-            raise ValueError("the norms of a stack must have weights of one type")
     T, H = h.shape
     flags = A.MOE_NORM_UNIT_OFFSET if norms.unit_offset else 0
     gate = post_w = post_b = None
@@ -148,8 +160,11 @@ def block_norm(y, h, end, start, out, n, stream=None):
         if end.post:
             post_w, post_b, flags = end.post_w, end.post_b, flags | A.MOE_NORM_POST
     pre_w, pre_b = (None, None) if start is None else (start.pre_w, start.pre_b)
+    types = _types(post_w, post_b, pre_w, pre_b)
+    if len(types) > 1:
+        raise ValueError("the norms of a stack must have weights of one type")
     A.moe_block_norm(y, H, h, H, gate, 0, scale, post_w, post_b, pre_w, pre_b, A.MOE_DTYPE_F16,
-                     norms.w_dtype, norms.kind, flags, norms.eps, T, H, out, H, n, H, stream)
+                     _w_dtype(types), norms.kind, flags, norms.eps, T, H, out, H, n, H, stream)
 
 
 def blob_table(blobs: torch.Tensor) -> torch.Tensor:
@@ -589,10 +604,11 @@ def stack_forward(layers, bufs, acts, stream=None, fuse=True, parts=None):
 def _stack_normed(layers, bufs, acts, stream):
     if any(lay.norms is None for lay in layers):
         raise ValueError("a stack's layers must all have norms, or none")
-    for a, b in zip(layers, layers[1:]):   # before anything is launched
-        if a.norms.form != b.norms.form or a.norms.w_dtype != b.norms.w_dtype:
-            raise ValueError("the norms of a stack must have one kind, eps, unit_offset and "
-                             "weights of one type")
+    # before anything is launched
+    if len({lay.norms.form for lay in layers}) > 1 or \
+            len(set().union(*(lay.norms.types for lay in layers))) > 1:
+        raise ValueError("the norms of a stack must have one kind, eps, unit_offset and "
+                         "weights of one type")
     L = len(layers)
     block_norm(None, acts[0], None, layers[0].norms, None, bufs[0].normed, stream)
     for l, lay in enumerate(layers):
