@@ -464,6 +464,14 @@ class MoELayer:
             dlogits=e(T, self.E, t=torch.float16), d_router=e(self.E, self.H), d_bias=e(self.E),
             dx=e(T, self.H), ws=e(n, t=torch.uint8))
 
+    def _check_balance(self, x, g: BalanceBuffers):
+        """ValueError for buffers of other layers, and for x of other rows than theirs."""
+        if g.d_router.shape != (self.E, self.H):
+            raise ValueError("balance buffers of %d experts of %d, not %d of %d" %
+                             (*g.d_router.shape, self.E, self.H))
+        if x.numel() != g.dx.numel() or x.shape[-1] != self.H:
+            raise ValueError("x must hold %d rows of %d" % g.dx.shape)
+
     def balance(self, x, b: LayerBuffers, g: BalanceBuffers, coef, z_coef=0.0, mask=None,
                 d_loss=None, stream=None):
         """After route_permute of x into b: the routing's balance loss, z loss, counts
@@ -473,11 +481,14 @@ class MoELayer:
         them, without the selection's bias.  Returns g.losses."""
         if g.dlogits.shape[0] != b.T:
             raise ValueError("balance buffers of %d tokens, not %d" % (g.dlogits.shape[0], b.T))
+        self._check_balance(x, g)
         if mask is not None and (mask.numel() != b.T or mask.element_size() != 1
                                  or not mask.is_contiguous()):
             raise ValueError("the mask must hold %d bytes" % b.T)
         if d_loss is not None and (d_loss.dtype != torch.float32 or d_loss.numel() != 1):
             raise ValueError("d_loss must be one fp32 value")
+        if any(t is not None and t.device != x.device for t in (mask, d_loss)):
+            raise ValueError("the mask and d_loss must be on the device of x")
         logits = b.logits
         if logits is None:
             logits = g.logits
@@ -491,8 +502,7 @@ class MoELayer:
     def router_backward(self, x, g: BalanceBuffers, stream=None):
         """Gradients of the router's weights, of its bias and of x from g.dlogits (from
         balance), into g.d_router, g.d_bias and g.dx: fp32, times balance's d_loss."""
-        if x.shape[0] != g.dlogits.shape[0]:
-            raise ValueError("x has %d rows, the buffers %d" % (x.shape[0], g.dlogits.shape[0]))
+        self._check_balance(x, g)
         A.moe_linear_f16_backward(g.dlogits, self.E, None, 0, A.MOE_ACT_NONE, x, self.H,
                                   self.router, self.H, g.dlogits.shape[0], self.E, self.H, g.dx,
                                   self.H, g.d_router, self.H, A.MOE_DTYPE_F32, g.d_bias, g.ws,
