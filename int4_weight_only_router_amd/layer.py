@@ -205,11 +205,12 @@ class BalanceBuffers:
     counts: torch.Tensor       # int32 [E]
     mean_prob: torch.Tensor    # fp32 [E]
     losses: torch.Tensor       # fp32 [2]: balance loss, z loss
-    dlogits: torch.Tensor      # fp16 [T, E]
+    dlogits: torch.Tensor      # fp16 [T, E], times balance's d_loss
     d_router: torch.Tensor     # fp32 [E, H]
     d_bias: torch.Tensor       # fp32 [E]
     dx: torch.Tensor           # fp32 [T, H]
     ws: torch.Tensor
+    formed: bool = False       # whether the last balance call formed dlogits
 
 
 class MoELayer:
@@ -476,9 +477,12 @@ class MoELayer:
                 d_loss=None, stream=None):
         """After route_permute of x into b: the routing's balance loss, z loss, counts
         and mean probabilities over the tokens that `mask` (uint8 [T], zero: padding)
-        leaves, and the logits' gradient times d_loss (fp32 [1] device, such as a loss
-        scale: the gradient is fp16), into g.  Scores as the layer's router forms
-        them, without the selection's bias.  Returns g.losses."""
+        leaves, and with d_loss (fp32 [1] device) the logits' gradient times it, into g.
+        That gradient is fp16, and by itself mostly below fp16's smallest step (coef 0.01
+        over 4096 tokens and 64 experts: 5e-8 at most): d_loss is a loss scale, such as
+        65536, which router_backward's results carry.  Without it no gradient is formed.
+        Scores as the layer's router forms them, without the selection's bias.  Returns
+        g.losses."""
         if g.dlogits.shape[0] != b.T:
             raise ValueError("balance buffers of %d tokens, not %d" % (g.dlogits.shape[0], b.T))
         self._check_balance(x, g)
@@ -496,13 +500,18 @@ class MoELayer:
         score = A.MOE_SCORE_SOFTMAX if self.routing is None else self.routing.score
         A.moe_balance_loss(logits, A.MOE_DTYPE_F32, self.E, b.topk_idx, mask, b.T, self.E, self.k,
                            score, coef, z_coef, g.counts, g.mean_prob, g.losses, d_loss,
-                           g.dlogits, A.MOE_DTYPE_F16, self.E, g.ws, g.ws.numel(), stream)
+                           None if d_loss is None else g.dlogits, A.MOE_DTYPE_F16, self.E, g.ws,
+                           g.ws.numel(), stream)
+        g.formed = d_loss is not None
         return g.losses
 
     def router_backward(self, x, g: BalanceBuffers, stream=None):
         """Gradients of the router's weights, of its bias and of x from g.dlogits (from
-        balance), into g.d_router, g.d_bias and g.dx: fp32, times balance's d_loss."""
+        balance), into g.d_router, g.d_bias and g.dx: fp32, times balance's d_loss.
+        ValueError where the last balance call had none."""
         self._check_balance(x, g)
+        if not g.formed:
+            raise ValueError("no gradient to go back from: balance was given no d_loss")
         A.moe_linear_f16_backward(g.dlogits, self.E, None, 0, A.MOE_ACT_NONE, x, self.H,
                                   self.router, self.H, g.dlogits.shape[0], self.E, self.H, g.dx,
                                   self.H, g.d_router, self.H, A.MOE_DTYPE_F32, g.d_bias, g.ws,
