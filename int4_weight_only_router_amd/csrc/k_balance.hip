@@ -26,6 +26,7 @@
 #include <algorithm>
 
 #include "k_balance.h"
+#include "k_block.h"
 
 namespace moe {
 
@@ -119,15 +120,6 @@ __device__ __forceinline__ int64_t wave_sum_counts(int64_t v)
 {
     return (int64_t)wave_sum_f32((float)(v & 0xffff)) +
            ((int64_t)wave_sum_f32((float)(v >> 16)) << 16);
-}
-
-// A row of E values by buffer instructions, whose range check does without masks: zeros
-// are read past its end, and nothing is written there.
-template <typename T>
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t row_rsrc(const T *row, int E)
-{
-    constexpr int RAW = 0x00020000;   // 32-bit data, no swizzle
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<T *>(row), 0, E * (int)sizeof(T), RAW);
 }
 
 // A row's logits and its token's mask in registers, as they were loaded: lane l holds

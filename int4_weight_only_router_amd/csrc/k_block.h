@@ -1,5 +1,5 @@
 // k_block.h -- what the kernels around a routed block share: loads and stores of
-// eight columns in any activation type, and the norms' arguments.
+// columns in any activation type, rows as buffers, and the norms' arguments.
 #pragma once
 
 #include "moe_common.h"
@@ -55,6 +55,16 @@ __device__ __forceinline__ void store_piece(T *row, int c, int cols, bool vec, c
             if (c + i < cols)
                 row[c + i] = (T)v[i];
     }
+}
+
+// A row of `cols` values for buffer instructions, whose range check does without a
+// branch, and without a lane mask, for every value: zeros are read past the row's end,
+// and nothing is written there.
+template <typename T>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t row_rsrc(const T *row, int cols)
+{
+    constexpr int RAW = 0x00020000;   // 32-bit data, no swizzle
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<T *>(row), 0, cols * (int)sizeof(T), RAW);
 }
 
 // Rows of T x H.  vec: H a multiple of 8 and every tensor's rows 16-byte aligned.

@@ -14,14 +14,7 @@
 
 namespace moe {
 
-// One value of a row of H, zero past its end (`at` in bytes), by buffer instructions:
-// their range check does without a branch, and without a lane mask, for every value.
-template <typename T>
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t row_rsrc(const T *row, int H)
-{
-    constexpr int RAW = 0x00020000;   // 32-bit data, no swizzle
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<T *>(row), 0, H * (int)sizeof(T), RAW);
-}
+// One value of a row, zero past its end (`at` in bytes).
 template <typename T>
 __device__ __forceinline__ float row_load(__amdgpu_buffer_rsrc_t r, int at)
 {
