@@ -103,7 +103,7 @@ int launch_linear(const LinArgs &a, const LinPlan &p, void *ws, hipStream_t s)
 // last fp16 up to dz, by the conversion towards zero, and lo the rest of up to a step;
 // where the rest is zero or rounds to it, hi is the fp16 before and lo the step between
 // the two, whose sum is exact.  So they are off by 2^-11 of lo, or by 2^-25.
-__device__ __forceinline__ void split_f16(const float (&v)[8], float (&hi)[8], float (&lo)[8])
+__device__ __forceinline__ void split_f16(const float (&v)[8], half8_t &hi, half8_t &lo)
 {
 #pragma unroll
     for (int j = 0; j < 8; j += 2) {
@@ -116,9 +116,21 @@ __device__ __forceinline__ void split_f16(const float (&v)[8], float (&hi)[8], f
                 a = __builtin_bit_cast(f16, (uint16_t)(__builtin_bit_cast(uint16_t, h) - 1));
                 b = h - a;
             }
-            hi[j + i] = (float)a;
-            lo[j + i] = fabsf((float)a) > 65504.0f ? (float)a : (float)b;
+            hi[j + i] = a;
+            lo[j + i] = __builtin_isinf(a) ? a : b;
         }
+    }
+}
+// Its first `cols` values.
+__device__ __forceinline__ void store_half8(f16 *p, int cols, bool vec, half8_t v)
+{
+    if (vec && cols >= 8) {
+        *reinterpret_cast<half8_t *>(p) = v;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j < cols)
+                p[j] = v[j];
     }
 }
 // A row of dz for dx: its values, then their rests (k starts over in w).  For dw: the
@@ -161,14 +173,14 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(LinGrads g, f16 *dz, int
         if (!TWO && dz)
             store_piece<f16, 8>(dz + m * ldd + n, 0, 8, true, v);
         if constexpr (TWO) {
-            float hi[8], lo[8];
+            half8_t hi, lo;
             split_f16(v, hi, lo);
             const bool vec = g.N % 8 == 0;
-            store_piece<f16, 8>(two.row + m * two.ld_row + n, 0, cols, vec, hi);
-            store_piece<f16, 8>(two.row + m * two.ld_row + g.N + n, 0, cols, vec, lo);
+            store_half8(two.row + m * two.ld_row + n, cols, vec, hi);
+            store_half8(two.row + m * two.ld_row + g.N + n, cols, vec, lo);
             if (two.col) {
-                store_piece<f16, 8>(two.col + 2 * m * two.ld_col + n, 0, 8, true, hi);
-                store_piece<f16, 8>(two.col + (2 * m + 1) * two.ld_col + n, 0, 8, true, lo);
+                store_half8(two.col + 2 * m * two.ld_col + n, 8, true, hi);
+                store_half8(two.col + (2 * m + 1) * two.ld_col + n, 8, true, lo);
             }
             if (n + 8 >= g.N)   // zeros up to the next multiple of 8
                 for (int64_t k = 2 * (int64_t)g.N; k < two.ld_row; ++k)
