@@ -21,8 +21,9 @@
 // wave each, 16 waves a workgroup, sums of p over them to the workspace) and the joining
 // of their sums, and before them the counts where every workgroup counting all choices
 // for itself would take longer.  Bound by the launches and their dependent steps: 4096 x
-// 512 with sigmoid scores, z loss and gradient 15.4 us, of which the counts 3.8, the
-// rows 9.7 (17 MB, 1.7 TB/s; half of it vector instructions, 730 a row), the joining 3.4.
+// 512 with sigmoid scores, z loss and gradient 15.5 us, of which the counts 3.8, the
+// rows 10.2 (17 MB, 1.7 TB/s; half of it vector instructions, 760 a row), the
+// joining 3.5.
 #include <algorithm>
 
 #include "k_balance.h"

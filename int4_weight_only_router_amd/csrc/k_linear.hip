@@ -19,9 +19,12 @@ namespace moe {
 // `across` for a block then; it is not used where a is such too (32 bytes at a time: 64 x
 // 2048 x 4096 14.4 us, 32-row tiles in four parts 11.0).
 //
-// With them the form and the parts of k that take the least time are chosen.  On 90
-// products from 1 x 1024 x 256 to 8192 x 8192 x 8192 the choice was the fastest form
-// or within 8% of it (at K = 2048, chosen / next best: 16 x 5632 16-row tiles 7.4 us,
+// With them the form and the parts of k that take the least time are chosen, among those
+// whose workgroups a launch holds.  On 90 products from 1 x 1024 x 256 to 8192 x 8192 x
+// 8192 the choice was the fastest form or within 8% of it.  These times are of the kernel
+// alone on the same operands again and again, on one card, and tell the forms apart; a
+// call on changing inputs takes up to a tenth more (4096 x 11264 x 2048: 163 us on the
+// same, 174 to 179 on changing ones; 16 x 5632 x 2048 7.4 and 9.0).  (At K = 2048, chosen / next best: 16 x 5632 16-row tiles 7.4 us,
 // 32-row 7.6; 333 x 1408 32-row 8.2, 64-row 9.0; 256 x 5632 64-row 13.7, 128-row
 // 17.3; 2048 x 2048 128-row of eight waves 20.8, of four 26.8; 4096 x 2048 the other
 // way round, 35.7 and 39.8; 4096 x 5632 192-row 86, 256-row 95; 4096 x 11264 256-row
@@ -97,7 +100,7 @@ int launch_linear(const LinArgs &a, const LinPlan &p, void *ws, hipStream_t s)
 // dz as the sum of two fp16.  Rounded to one it adds as much to the errors of dx and dw as
 // their own rounding (1.41 of it together, among few values by chance much more); as two
 // it is off by 2^-21 of itself at most, and they by 1.00.  The products take twice the k
-// for it (4096 x 5632 x 2048, SiLU: 396 us), so a caller may ask for one (214).
+// for it (4096 x 5632 x 2048, SiLU: 400 us), so a caller may ask for one (214).
 // Both have dz's sign and neither is zero (but for what fp16's smallest step cannot be
 // divided into), so that an infinity in x or w meets no zero and no other sign: hi is the
 // last fp16 up to dz, by the conversion towards zero, and lo the rest of up to a step;
@@ -144,7 +147,8 @@ struct DzTwo {       // null: one fp16 each
 // dz = dy act'(z) in fp16 (rows of ldd, zeros up to the next multiple of 8 behind
 // column N), where dz is not null, and its column sums over `tall` rows, from the
 // unrounded values, where parts is not null.  2^lt threads a row, eight columns each.
-// Bound by memory (4096 x 5632, SiLU: 30 us, 4.6 TB/s).
+// 4096 x 5632, SiLU: to one fp16 30 us, bound by memory (4.6 TB/s); to two 51 to 60, the
+// splitting and twice the bytes written (184 MB in all, 3.1 to 3.6 TB/s).
 template <bool TWO>
 __global__ __launch_bounds__(256) void linear_dz_kernel(LinGrads g, f16 *dz, int64_t ldd,
                                                         float *parts, bool vec_y, bool vec_z, int lt, int tall,

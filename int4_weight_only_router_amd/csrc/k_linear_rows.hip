@@ -7,7 +7,7 @@
 // LDS, no barrier.  Out of memory, in a captured run of calls: one row of 5632 x 2048
 // 5.9 us (3.9 TB/s), of 11264 x 2048 9.8 (4.7), two rows 6.5 and 10.6; for more rows
 // the tokens' loads and sums outweigh the stream (four 8.9, eight 11, sixteen 17),
-// and the 16-row tiles (8.4 for any of them) are faster.
+// and the 16-row tiles (8.4 to 9.2 for any of them, out of memory too) are faster.
 #include <algorithm>
 #include <type_traits>
 

@@ -18,9 +18,9 @@
 // are in registers: one barrier a block, behind which the stage takes the loads of
 // the block NS later and the next block's first fragments are read.
 //
-// Bound by the matrix pipe where the tiles fill the card (4096 x 11264 x 2048: 172 us,
-// 1.10 PFLOP/s, the pipe at work half of the cycles and the clock down to 2 GHz; the
-// library's product 174), by the first loads and the results where they are a single
+// Bound by the matrix pipe where the tiles fill the card (4096 x 11264 x 2048: 174 us,
+// 1.09 PFLOP/s, the pipe at work half of the cycles and the clock down to 2 GHz; the
+// library's product 166 to 174), by the first loads and the results where they are a single
 // round (333 x 1408 x 2000: 11 us), by bytes where K is short (4096 x 2048 x 64 to fp32:
 // 10.8 us, 3.1 TB/s).
 #include <algorithm>
@@ -283,7 +283,8 @@ __device__ __forceinline__ void lt_epilogue(const LinArgs &a, LtAcc<F> &acc, con
 }
 
 // The same where nothing but fp16 results leave: rounded before they pass through LDS,
-// in one part (256 x 256: 4096 x 11264 x 2048 in 159 us against 168).
+// in one part (256 x 256, the same operands again and again: 4096 x 11264 x 2048 in 159
+// us against 168).
 template <typename F>
 __device__ __forceinline__ void lt_epilogue_f16(const LinArgs &a, LtAcc<F> &acc, int m0, int n0,
                                                 int mw, int nw, unsigned char *smem)

@@ -219,7 +219,8 @@ class MoELayer:
     unused), routed by softmax top-k or, with `routing`, by scores and groups.
     The softmax router takes H in {256, 512, 1024, 2048}; with `routing` the
     logits of other H come from moe_linear_f16 (any multiple of 8).  `norms`: the
-    norms around the block, which stack_forward applies."""
+    norms around the block, which stack_forward applies, also to a stack of one
+    layer; forward and the other methods of a layer are the block itself."""
 
     def __init__(self, H, I, E, k, group, router, table, bias=None, shared=None,
                  renorm=False, device="cuda", shared_gate=None, overlap_shared=False,
@@ -544,10 +545,11 @@ class MoELayer:
 
     def forward(self, x, b: LayerBuffers, residual=None, out=None, stream=None,
                 overlap_shared=None):
-        """One layer.  With overlap_shared (default: the layer's setting) the
-        shared expert runs on a side stream, forked at the layer's start and
-        joined before the combine: it reads only x, so it overlaps routing and
-        the routed experts.  That pays when the shared weights are large
+        """One layer's block, of x as it is (its `norms` are stack_forward's).
+        With overlap_shared (default: the layer's setting) the shared expert
+        runs on a side stream, forked at the layer's start and joined before
+        the combine: it reads only x, so it overlaps routing and the routed
+        experts.  That pays when the shared weights are large
         (60-expert layer, 69 MB: -12% per layer at T = 8..256) and costs when
         they are small (512-expert layer, 6 MB: +17% at T = 1, the shared
         kernels then delay the latency-bound router)."""
@@ -586,7 +588,8 @@ def stack_forward(layers, bufs, acts, stream=None, fuse=True, parts=None):
     Layers with `norms` (all of the stack or none; ValueError otherwise) compute
     x_{l+1} = x_l + scale_l * gate_l * post_l(MoE_l(pre_l(x_l))): the end of a block
     and the start of the next are one moe_block_norm call between a layer's combine
-    and the next layer's routing, which then are not fused."""
+    and the next layer's routing, which then are not fused (`fuse` and `parts` do not
+    apply); MoE_l's output is rounded to fp16 between the two calls."""
     L = len(layers)
     if any(lay.norms is not None for lay in layers):
         return _stack_normed(layers, bufs, acts, stream)
